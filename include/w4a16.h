@@ -314,6 +314,64 @@ int w4a16_linear_noalloc(const uint16_t *x, const uint32_t *qweight, const uint1
 int w4a16_dense_linear(const uint16_t *x, const uint16_t *w, int M, int N, int K, int dtype,
                        uint16_t *y, void *stream);
 
+/* ---- layers whose weights come in 8 bits (the Z100 thread, section 六: FP8
+ * checkpoints, which that GPU had to dequantise to 16 bits; here the tensor
+ * cores take the 8-bit data).  e4m3 is the 8-bit type with 4 exponent and 3
+ * mantissa bits (bias 7, largest value 448, no Inf; torch.float8_e4m3fn), one
+ * byte per element.
+ *   rows     q [M, K] e4m3 and scales [M, ceil(K/128)] fp32: element k of row m
+ *            is q[m, k] * scales[m, k / 128]
+ *   weights  w [N, K] e4m3 and scales [ceil(N/128), ceil(K/128)] fp32: element
+ *            (n, k) is w[n, k] * scales[n / 128, k / 128]
+ * The last group of a row, and the last blocks of a weight, may be partial.
+ * In these calls M = 0 is an empty batch: nothing is read, written or
+ * launched, and pointers may be NULL. */
+
+/* y [M, N] = rows @ weights^T, + residual [M, N] with W4A16_EPILOGUE_RESIDUAL
+ * (which may be y itself, and must not overlap it otherwise; NULL with
+ * W4A16_EPILOGUE_NONE):
+ *     y[m, n] = sum_b x_scales[m, b] * w_scales[n / 128, b] *
+ *               sum_{k in block b} x[m, k] * w[n, k]   (+ residual[m, n])
+ * y and residual have the 16-bit type `dtype` (w4a16_dtype).  Sums are fp32, y is
+ * rounded once (nearest even).  One kernel; K may be split between CTAs, whose
+ * partial sums go through the w4a16_init workspace and are added in a fixed
+ * order (a workspace too small for that means no split, not an error).  K a
+ * multiple of 16 (16..2^22), 1 <= N < 2^31, 0 <= M <= 65535; x and w 16-byte
+ * aligned, scales 4-byte, y and residual 2-byte.  W4A16_EPILOGUE_SILU_MUL is
+ * W4A16_ERR_UNSUPPORTED (w4a16_fp8_quant applies it to gate+up's rows).  Needs
+ * w4a16_init; allocates nothing and may be captured. */
+int w4a16_fp8_linear(const uint8_t *x, const float *x_scales, const uint8_t *w,
+                     const float *w_scales, int M, int N, int K, int dtype, int epilogue,
+                     const uint16_t *residual, uint16_t *y, void *stream);
+
+/* The norm before a linear, of rows of H elements in the 16-bit type `dtype`:
+ *     h = x (+ residual),   v = h / sqrt(mean(h^2) + eps) * weight
+ * computed in fp32 from the unrounded h.  Written where the pointer is not NULL:
+ *   sum_out    [M, H] h rounded once (only with a residual; it may be the
+ *              residual itself: the stream is updated in place);
+ *   y          [M, H] v rounded once (the input of a w4a16_linear);
+ *   q, scales  v as 8-bit rows (both or neither): a group's scale is
+ *              max(a, 2^-100) / 448, a its largest finite |v|, an element
+ *              e4m3(v / scale), nearest even; Inf and NaN become e4m3's NaN and
+ *              do not enter a.
+ * At least one of y and q.  1 <= H <= 32768 (W4A16_ERR_UNSUPPORTED above),
+ * 0 <= M <= 65535, eps >= 0; 16-bit pointers 2-byte aligned, scales 4-byte (with H
+ * a multiple of 8 and 16-byte aligned pointers the accesses are 16 bytes wide).
+ * Outputs overlap neither the inputs (but sum_out, as said) nor one another.
+ * Needs no w4a16_init. */
+int w4a16_rmsnorm(const uint16_t *x, const uint16_t *residual, const uint16_t *weight, int M, int H,
+                  float eps, int dtype, uint16_t *sum_out, uint16_t *y, uint8_t *q, float *scales,
+                  void *stream);
+
+/* 16-bit rows x [M, cols] -> 8-bit rows, with w4a16_rmsnorm's rule for scales and
+ * elements.  W4A16_EPILOGUE_NONE: of x itself, q [M, cols].
+ * W4A16_EPILOGUE_SILU_MUL: of silu(x[:, :cols/2]) * x[:, cols/2:] (fp32, silu(g) =
+ * g / (1 + e^-g)), q [M, cols/2]; cols even.  W4A16_EPILOGUE_RESIDUAL:
+ * W4A16_ERR_UNSUPPORTED.  0 <= M <= 65535; x 2-byte aligned, scales 4-byte; q and
+ * scales apart from x and from each other.  Needs no w4a16_init. */
+int w4a16_fp8_quant(const uint16_t *x, int M, int cols, int epilogue, int dtype, uint8_t *q,
+                    float *scales, void *stream);
+
 /* ---- mixture of experts (the Z100 thread, section 七: a router picks k of E
  * experts per token; the tokens are regrouped by expert; a W4A16 small-M GEMV
  * runs over the packed INT4 experts; each token's expert outputs are summed

@@ -87,6 +87,9 @@ _sig("w4a16_linear_noalloc", [_P, _P, _P, _P, _I, _I, _I, _I, _P, _P])
 _sig("w4a16_linear_epilogue", [_P, _P, _P, _P, _I, _I, _I, _I, _I, _P, _P, _P])
 _sig("w4a16_linear_ex", [_P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _P, _P, _P])
 _sig("w4a16_dense_linear", [_P, _P, _I, _I, _I, _I, _P, _P])
+_sig("w4a16_fp8_linear", [_P, _P, _P, _P, _I, _I, _I, _I, _I, _P, _P, _P])
+_sig("w4a16_rmsnorm", [_P, _P, _P, _I, _I, ctypes.c_float, _I, _P, _P, _P, _P, _P])
+_sig("w4a16_fp8_quant", [_P, _I, _I, _I, _I, _P, _P, _P])
 _sig("w4a16_moe_align", [_P, _I, _I, _P, _P, _P, _P])
 _sig("w4a16_moe_create", [_I, _I, _I, _I, _P, _P, _P, _I, _I, _I, ctypes.POINTER(_P)])
 _sig("w4a16_moe_destroy", [_P])
@@ -119,6 +122,7 @@ EXPORTED = ["w4a16_init", "w4a16_shutdown", "w4a16_workspace_bytes", "w4a16_pack
             "w4a16_unpack", "w4a16_dequant", "w4a16_repack_transpose", "w4a16_transpose_f16",
             "w4a16_linear", "w4a16_linear_noalloc",
             "w4a16_linear_epilogue", "w4a16_linear_ex", "w4a16_dense_linear",
+            "w4a16_fp8_linear", "w4a16_rmsnorm", "w4a16_fp8_quant",
             "w4a16_moe_align", "w4a16_moe_create", "w4a16_moe_destroy", "w4a16_moe_linear",
             "w4a16_moe_sum", "w4a16_moe_mlp_create", "w4a16_moe_mlp_destroy", "w4a16_moe_mlp",
             "w4a16_moe_mlp_set_path", "w4a16_moe_mlp_path", "w4a16_moe_mlp_buffers",
@@ -341,6 +345,135 @@ def w4a16_dense_linear(x: torch.Tensor, w: torch.Tensor, y=None, stream=None) ->
                                   _dev(y, dt, "y"), _stream_ptr(stream)),
            "w4a16_dense_linear")
     return y
+
+
+FP8 = torch.float8_e4m3fn
+
+
+def _groups(n: int) -> int:
+    return -(-n // GROUP)
+
+
+def _shaped(t: torch.Tensor, dtype, shape, name: str) -> int:
+    p = _dev(t, dtype, name)
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    return p
+
+
+def _dtype16(dt) -> int:
+    if dt not in _DTYPE_OF:
+        raise TypeError(f"the 16-bit type must be float16 or bfloat16, got {dt}")
+    return _DTYPE_OF[dt]
+
+
+def _rows2d(t: torch.Tensor, name: str):
+    if not isinstance(t, torch.Tensor) or t.dim() != 2:
+        raise ValueError(f"{name} must be a 2-D torch tensor")
+    return t.shape
+
+
+def _used_on(stream, *tensors) -> None:
+    """Tell torch's allocator of tensors that a call uses on another stream
+    than the current one, so that freed memory is not handed out too early."""
+    if stream is None:
+        return
+    s = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream))
+    if s != torch.cuda.current_stream():
+        for t in tensors:
+            if t is not None:
+                t.record_stream(s)
+
+
+def w4a16_fp8_linear(x: torch.Tensor, x_scales: torch.Tensor, w: torch.Tensor,
+                     w_scales: torch.Tensor, epilogue: int = EPILOGUE_NONE, residual=None,
+                     dtype: torch.dtype = torch.bfloat16, y=None, stream=None) -> torch.Tensor:
+    """y [M, N] (`dtype`) = rows @ weights^T, + residual [M, N] with
+    EPILOGUE_RESIDUAL (which may be y itself): 8-bit rows x [M, K] with x_scales
+    [M, ceil(K/128)] (w4a16_rmsnorm_fp8, w4a16_fp8_quant) and 8-bit weights w
+    [N, K] with one scale per 128 x 128 block, w_scales [ceil(N/128),
+    ceil(K/128)].  K must be a multiple of 16."""
+    (M, K), (N, Kw) = _rows2d(x, "x"), _rows2d(w, "w")
+    if K != Kw:
+        raise ValueError(f"x has {K} columns and w {Kw}")
+    dt = _dtype16(dtype)
+    xp, wp = _dev(x, FP8, "x"), _dev(w, FP8, "w")
+    xs = _shaped(x_scales, torch.float32, (M, _groups(K)), "x_scales")
+    ws = _shaped(w_scales, torch.float32, (_groups(N), _groups(K)), "w_scales")
+    r = _shaped(residual, dtype, (M, N), "residual") if residual is not None else None
+    if y is None:
+        y = torch.empty((M, N), dtype=dtype, device=x.device)
+    _check(lib.w4a16_fp8_linear(xp, xs, wp, ws, M, N, K, dt, epilogue, r,
+                                _shaped(y, dtype, (M, N), "y"), _stream_ptr(stream)),
+           "w4a16_fp8_linear")
+    _used_on(stream, x, x_scales, w, w_scales, residual, y)
+    return y
+
+
+def _norm(x, weight, residual, eps, sum_out, y, q, scales, stream, what):
+    M, H = x.shape
+    dt = _dtype16(x.dtype)
+    xp = _dev(x, x.dtype, "x")
+    wp = _shaped(weight, x.dtype, (H,), "weight")
+    r = _shaped(residual, x.dtype, (M, H), "residual") if residual is not None else None
+    if sum_out is None:
+        if residual is not None:
+            sum_out = torch.empty_like(x)
+    elif residual is None:
+        raise ValueError("sum_out needs a residual")
+    _check(lib.w4a16_rmsnorm(
+        xp, r, wp, M, H, eps, dt,
+        _shaped(sum_out, x.dtype, (M, H), "sum_out") if sum_out is not None else None,
+        _shaped(y, x.dtype, (M, H), "y") if y is not None else None,
+        _shaped(q, FP8, (M, H), "q") if q is not None else None,
+        _shaped(scales, torch.float32, (M, _groups(H)), "scales") if scales is not None else None,
+        _stream_ptr(stream)), what)
+    _used_on(stream, x, weight, residual, sum_out, y, q, scales)
+    return sum_out
+
+
+def w4a16_rmsnorm(x: torch.Tensor, weight: torch.Tensor, residual=None, eps: float = 1e-6,
+                  sum_out=None, y=None, stream=None):
+    """y [M, H] = h / sqrt(mean(h^2) + eps) * weight with h = x (+ residual).
+    Returns y, or (y, sum_out) when a residual is given: sum_out is h rounded to
+    the 16-bit type (sum_out=residual updates the residual in place)."""
+    _rows2d(x, "x")
+    if y is None:
+        y = torch.empty_like(x)
+    s = _norm(x, weight, residual, eps, sum_out, y, None, None, stream, "w4a16_rmsnorm")
+    return y if s is None else (y, s)
+
+
+def w4a16_rmsnorm_fp8(x: torch.Tensor, weight: torch.Tensor, residual=None, eps: float = 1e-6,
+                      sum_out=None, q=None, scales=None, stream=None):
+    """w4a16_rmsnorm with its rows in 8 bits: (q [M, H], scales [M, ceil(H/128)]),
+    and sum_out third when a residual is given."""
+    M, H = _rows2d(x, "x")
+    if q is None:
+        q = torch.empty((M, H), dtype=FP8, device=x.device)
+    if scales is None:
+        scales = torch.empty((M, _groups(H)), dtype=torch.float32, device=x.device)
+    s = _norm(x, weight, residual, eps, sum_out, None, q, scales, stream, "w4a16_rmsnorm_fp8")
+    return (q, scales) if s is None else (q, scales, s)
+
+
+def w4a16_fp8_quant(x: torch.Tensor, epilogue: int = EPILOGUE_NONE, q=None, scales=None,
+                    stream=None):
+    """8-bit rows (q, scales) of x [M, cols], or with EPILOGUE_SILU_MUL of
+    silu(x[:, :cols/2]) * x[:, cols/2:]."""
+    M, cols = _rows2d(x, "x")
+    dt = _dtype16(x.dtype)
+    N = cols // 2 if epilogue == EPILOGUE_SILU_MUL else cols
+    xp = _dev(x, x.dtype, "x")
+    if q is None:
+        q = torch.empty((M, N), dtype=FP8, device=x.device)
+    if scales is None:
+        scales = torch.empty((M, _groups(N)), dtype=torch.float32, device=x.device)
+    _check(lib.w4a16_fp8_quant(xp, M, cols, epilogue, dt, _shaped(q, FP8, (M, N), "q"),
+                               _shaped(scales, torch.float32, (M, _groups(N)), "scales"),
+                               _stream_ptr(stream)), "w4a16_fp8_quant")
+    _used_on(stream, x, q, scales)
+    return q, scales
 
 
 def w4a16_moe_align(topk_ids: torch.Tensor, E: int, stream=None):

@@ -617,6 +617,7 @@ int w4a16_init(int device, size_t workspace_bytes) {
     if (e == cudaSuccess) e = mma_init(dev);
     if (e == cudaSuccess) e = dense_init(dev);
     if (e == cudaSuccess) e = moe_decode_init(dev);
+    if (e == cudaSuccess) e = fp8_init(dev);
     if (e == cudaSuccess) e = cudaDeviceSynchronize();
     if (e != cudaSuccess) {
         cudaFree(base);
@@ -761,6 +762,103 @@ int w4a16_dense_linear(const uint16_t *x, const uint16_t *w, int M, int N, int K
     if (st.log)
         fprintf(stderr, "[w4a16] dense linear M=%d N=%d K=%d dtype=%d\n", M, N, K, dtype);
     return e == cudaSuccess ? W4A16_OK : cuda_fail(e);
+}
+
+int w4a16_fp8_linear(const uint8_t *x, const float *x_scales, const uint8_t *w,
+                     const float *w_scales, int M, int N, int K, int dtype, int epilogue,
+                     const uint16_t *residual, uint16_t *y, void *stream) {
+    if (M < 0 || M > kMaxM || N < 1 || K < 1 || K > kMaxK) return W4A16_ERR_INVALID_ARG;
+    if (K % 16 != 0) return W4A16_ERR_INVALID_ARG;
+    if (dtype != W4A16_DTYPE_F16 && dtype != W4A16_DTYPE_BF16) return W4A16_ERR_INVALID_ARG;
+    if (epilogue == W4A16_EPILOGUE_SILU_MUL) return W4A16_ERR_UNSUPPORTED;
+    if (epilogue != W4A16_EPILOGUE_NONE && epilogue != W4A16_EPILOGUE_RESIDUAL)
+        return W4A16_ERR_INVALID_ARG;
+    if (M == 0) return W4A16_OK;
+    if (!x || !x_scales || !w || !w_scales || !y) return W4A16_ERR_INVALID_ARG;
+    if ((epilogue == W4A16_EPILOGUE_RESIDUAL) != (residual != nullptr))
+        return W4A16_ERR_INVALID_ARG;
+    if (!aligned(x, 16) || !aligned(w, 16) || !aligned(x_scales, 4) || !aligned(w_scales, 4) ||
+        !aligned(y, 2) || !aligned(residual, 2))
+        return W4A16_ERR_MISALIGNED;
+    const size_t G = ((size_t)K + kGroup - 1) / kGroup, NB = ((size_t)N + kGroup - 1) / kGroup;
+    const size_t ybytes = (size_t)M * N * 2;
+    if (overlaps(x, (size_t)M * K, y, ybytes) || overlaps(w, (size_t)N * K, y, ybytes) ||
+        overlaps(x_scales, M * G * 4, y, ybytes) || overlaps(w_scales, NB * G * 4, y, ybytes))
+        return W4A16_ERR_INVALID_ARG;
+    // the residual is y itself (y += x W^T) or lies apart from it
+    if (residual && residual != y && overlaps(residual, ybytes, y, ybytes))
+        return W4A16_ERR_INVALID_ARG;
+    const State &st = g_state;
+    if (!st.initialized) return W4A16_ERR_NOT_INITIALIZED;
+    const Fp8Plan p = plan_fp8(M, N, K, st.dev, st.ws);
+    const Fp8Args a{x, x_scales, w, w_scales, residual, y, M, N, K, dtype == W4A16_DTYPE_BF16};
+    const cudaError_t e = launch_fp8(a, p, st.ws, (cudaStream_t)stream);
+    if (e != cudaSuccess) return cuda_fail(e);
+    g_launches.fetch_add(1, std::memory_order_relaxed);
+    if (st.log)
+        fprintf(stderr, "[w4a16] fp8 linear M=%d N=%d K=%d dtype=%d T=%d grid=%d\n", M, N, K, dtype,
+                p.T, p.grid);
+    return W4A16_OK;
+}
+
+int w4a16_rmsnorm(const uint16_t *x, const uint16_t *residual, const uint16_t *weight, int M, int H,
+                  float eps, int dtype, uint16_t *sum_out, uint16_t *y, uint8_t *q, float *scales,
+                  void *stream) {
+    if (M < 0 || M > kMaxM || H < 1) return W4A16_ERR_INVALID_ARG;
+    if (H > kMaxNormWidth) return W4A16_ERR_UNSUPPORTED;
+    if (!(eps >= 0.f)) return W4A16_ERR_INVALID_ARG;
+    if (dtype != W4A16_DTYPE_F16 && dtype != W4A16_DTYPE_BF16) return W4A16_ERR_INVALID_ARG;
+    if (M == 0) return W4A16_OK;
+    // an output at least, codes and scales together, a sum only of two
+    if (!x || !weight || (!y && !q) || (q != nullptr) != (scales != nullptr) ||
+        (sum_out && !residual))
+        return W4A16_ERR_INVALID_ARG;
+    if (!aligned(x, 2) || !aligned(residual, 2) || !aligned(weight, 2) || !aligned(sum_out, 2) ||
+        !aligned(y, 2) || !aligned(scales, 4))
+        return W4A16_ERR_MISALIGNED;
+    const size_t n = (size_t)M * H, G = ((size_t)H + kGroup - 1) / kGroup;
+    const struct { const void *p; size_t bytes; } in[] = {{x, n * 2}, {residual, n * 2},
+                                                          {weight, (size_t)H * 2}},
+        out[] = {{sum_out, n * 2}, {y, n * 2}, {q, n}, {scales, (size_t)M * G * 4}};
+    for (int o = 0; o < 4; ++o) {
+        if (!out[o].p) continue;
+        for (const auto &i : in)  // the sum may replace the residual
+            if (i.p && !(o == 0 && i.p == residual && i.p == out[o].p) &&
+                overlaps(i.p, i.bytes, out[o].p, out[o].bytes))
+                return W4A16_ERR_INVALID_ARG;
+        for (int k = 0; k < o; ++k)
+            if (out[k].p && overlaps(out[k].p, out[k].bytes, out[o].p, out[o].bytes))
+                return W4A16_ERR_INVALID_ARG;
+    }
+    const NormArgs a{x, residual, weight, sum_out, y, q, scales, M, H, eps};
+    const cudaError_t e =
+        launch_rmsnorm(a, dtype == W4A16_DTYPE_BF16, (cudaStream_t)stream);
+    if (e != cudaSuccess) return cuda_fail(e);
+    g_launches.fetch_add(1, std::memory_order_relaxed);
+    return W4A16_OK;
+}
+
+int w4a16_fp8_quant(const uint16_t *x, int M, int cols, int epilogue, int dtype, uint8_t *q,
+                    float *scales, void *stream) {
+    const bool silu = epilogue == W4A16_EPILOGUE_SILU_MUL;
+    if (M < 0 || M > kMaxM || cols < 1) return W4A16_ERR_INVALID_ARG;
+    if (dtype != W4A16_DTYPE_F16 && dtype != W4A16_DTYPE_BF16) return W4A16_ERR_INVALID_ARG;
+    if (epilogue == W4A16_EPILOGUE_RESIDUAL) return W4A16_ERR_UNSUPPORTED;
+    if (!silu && epilogue != W4A16_EPILOGUE_NONE) return W4A16_ERR_INVALID_ARG;
+    if (silu && cols % 2 != 0) return W4A16_ERR_INVALID_ARG;
+    if (M == 0) return W4A16_OK;
+    if (!x || !q || !scales) return W4A16_ERR_INVALID_ARG;
+    if (!aligned(x, 2) || !aligned(scales, 4)) return W4A16_ERR_MISALIGNED;
+    const int N = silu ? cols / 2 : cols, G = (int)(((long long)N + kGroup - 1) / kGroup);
+    const size_t xb = (size_t)M * cols * 2, qb = (size_t)M * N, sb = (size_t)M * G * 4;
+    if (overlaps(x, xb, q, qb) || overlaps(x, xb, scales, sb) || overlaps(q, qb, scales, sb))
+        return W4A16_ERR_INVALID_ARG;
+    const QuantArgs a{x, q, scales, M, N, G};
+    const cudaError_t e =
+        launch_quant(a, dtype == W4A16_DTYPE_BF16, silu, (cudaStream_t)stream);
+    if (e != cudaSuccess) return cuda_fail(e);
+    g_launches.fetch_add(1, std::memory_order_relaxed);
+    return W4A16_OK;
 }
 
 int w4a16_moe_create(int E, int N, int K, int group, const uint32_t *qweight,

@@ -1,0 +1,276 @@
+// The steps around the 8-bit linear of w4a16_fp8.cu that are done row by row:
+//
+//   rmsnorm   h = x + residual,  v = h / sqrt(mean(h^2) + eps) * weight
+//   quant     v = x,  or  v = silu(x[:, :n]) * x[:, n:],  silu(g) = g / (1 + e^-g)
+//
+// (forum.sourcefind.cn thread "vLLM on Hygon Z100", section 二, names RMSNorm
+// and SiLU-and-mul among the operators between a decoder layer's linears), with
+// v written in 16 bits (rmsnorm) or as an 8-bit row: per group of 128
+// consecutive elements one scale s = max(a, 2^-100) / 448, a the group's
+// largest finite magnitude, and per element e4m3(v / s), nearest even.
+//
+// Everything before the stores is fp32; the sum h is rounded to 16 bits only
+// where it is stored (the norm reads the unrounded sum), v once where it is
+// stored.  v / s is the correctly rounded fp32 quotient, from the correctly
+// rounded reciprocal r = 1 / s and one correction (Markstein, "Computation of
+// elementary functions on the IBM RISC System/6000 processor", 1990): q0 = v r,
+// q = q0 + (v - q0 s) r, so a tie of e4m3 falls as it does for IEEE division.
+// Inf and NaN elements do not enter a and become e4m3's NaN, so that one of
+// them does not take its group with it.
+//
+// Layout: a lane holds 8 consecutive elements (a 16-byte load), so 16 lanes
+// hold a group and four shuffles give its largest magnitude.  Rows whose width
+// or address does not allow 16-byte accesses are read and written element by
+// element by the same code (kVec false).
+#include <float.h>
+
+#include "w4a16_internal.h"
+
+namespace w4a16 {
+namespace {
+
+constexpr int kLaneElems = 8;                             // elements of a row per lane and step
+constexpr int kGroupLanes = kGroup / kLaneElems;          // 16 lanes hold a scale group
+constexpr float kE4m3Max = 448.f;
+constexpr float kScaleFloor = 7.8886090522101180541e-31f;  // 2^-100
+
+// lets the next kernel's CTAs start while this one drains, then waits for the
+// kernel before (whose outputs this one may read)
+__device__ __forceinline__ void chain_start() {
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+
+template <bool kBf16>
+__device__ __forceinline__ float to_float(uint16_t h) {
+    if constexpr (kBf16) return __uint_as_float((uint32_t)h << 16);
+    else return __half2float(__ushort_as_half(h));
+}
+template <bool kBf16>
+__device__ __forceinline__ uint16_t to_16(float v) {  // nearest, ties to even
+    if constexpr (kBf16) return __bfloat16_as_ushort(__float2bfloat16_rn(v));
+    else return __half_as_ushort(__float2half_rn(v));
+}
+
+// Elements c .. c + 7 of a row (zeros past its n elements).
+template <bool kBf16, bool kVec>
+__device__ __forceinline__ void load8(const uint16_t *row, int c, int n, float (&v)[8]) {
+    if constexpr (kVec) {  // n is a multiple of 8
+        uint4 u = make_uint4(0, 0, 0, 0);
+        if (c < n) u = *reinterpret_cast<const uint4 *>(row + c);
+        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            v[2 * i] = to_float<kBf16>((uint16_t)w[i]);
+            v[2 * i + 1] = to_float<kBf16>((uint16_t)(w[i] >> 16));
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = c + i < n ? to_float<kBf16>(row[c + i]) : 0.f;
+    }
+}
+
+template <bool kBf16, bool kVec>
+__device__ __forceinline__ void store8(uint16_t *row, int c, int n, const float (&v)[8]) {
+    if constexpr (kVec) {
+        if (c < n) {
+            uint32_t w[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                w[i] = (uint32_t)to_16<kBf16>(v[2 * i]) |
+                       (uint32_t)to_16<kBf16>(v[2 * i + 1]) << 16;
+            *reinterpret_cast<uint4 *>(row + c) = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (c + i < n) row[c + i] = to_16<kBf16>(v[i]);
+    }
+}
+
+// two fp32 values -> two e4m3 codes (lo in the low byte), nearest even
+__device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
+    uint16_t d;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(d) : "f"(hi), "f"(lo));
+    return d;
+}
+
+// A lane's 8 elements of its group -> 8 codes of row q and, from the group's
+// first lane, the group's scale.  All 16 lanes of the group call it together.
+template <bool kVec>
+__device__ __forceinline__ void quant8(float (&v)[8], uint8_t *q, float *scale, int c, int n) {
+    float a = 0.f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        v[i] += v[i] - v[i];  // Inf and NaN become NaN, which fmaxf passes over
+        a = fmaxf(a, fabsf(v[i]));
+    }
+#pragma unroll
+    for (int o = kGroupLanes / 2; o > 0; o >>= 1)
+        a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
+    const float s = __fdiv_rn(fmaxf(a, kScaleFloor), kE4m3Max);
+    const float r = __frcp_rn(s);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const float q0 = v[i] * r;
+        v[i] = fmaf(fmaf(-q0, s, v[i]), r, q0);
+    }
+    if (c >= n) return;
+    if (c % kGroup == 0) *scale = s;
+    const uint32_t lo = e4m3x2(v[0], v[1]) | e4m3x2(v[2], v[3]) << 16;
+    const uint32_t hi = e4m3x2(v[4], v[5]) | e4m3x2(v[6], v[7]) << 16;
+    if constexpr (kVec) {
+        *reinterpret_cast<uint2 *>(q + c) = make_uint2(lo, hi);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (c + i < n) q[c + i] = (uint8_t)((i < 4 ? lo : hi) >> (8 * (i & 3)));
+    }
+}
+
+// ---------------------------------------------------------------------------
+// rmsnorm: a CTA per row, V steps of 8 elements per thread, the row in
+// registers between the sum of squares and the outputs (one pass over memory)
+// ---------------------------------------------------------------------------
+template <bool kBf16, bool kVec, int V>
+__global__ void __launch_bounds__(1024) rmsnorm_kernel(NormArgs a) {
+    __shared__ float warp_sums[32];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const size_t row = blockIdx.x;
+    const uint16_t *x = a.x + row * a.H;
+    chain_start();
+    float h[V][8], w[V][8];
+    float sum = 0.f;
+#pragma unroll
+    for (int s = 0; s < V; ++s) {
+        const int c = (s * (int)blockDim.x + (int)threadIdx.x) * kLaneElems;
+        load8<kBf16, kVec>(x, c, a.H, h[s]);
+        if (a.residual) {
+            float r[8];
+            load8<kBf16, kVec>(a.residual + row * a.H, c, a.H, r);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) h[s][i] += r[i];
+        }
+        load8<kBf16, kVec>(a.weight, c, a.H, w[s]);
+    }
+#pragma unroll
+    for (int s = 0; s < V; ++s) {
+        const int c = (s * (int)blockDim.x + (int)threadIdx.x) * kLaneElems;
+        if (a.sum_out) store8<kBf16, kVec>(a.sum_out + row * a.H, c, a.H, h[s]);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) sum = fmaf(h[s][i], h[s][i], sum);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    if (lane == 0) warp_sums[warp] = sum;
+    __syncthreads();
+    // every warp adds the warps' sums in the same tree
+    sum = lane < (int)(blockDim.x >> 5) ? warp_sums[lane] : 0.f;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    const float rstd = __frcp_rn(__fsqrt_rn(__fdiv_rn(sum, (float)a.H) + a.eps));
+#pragma unroll
+    for (int s = 0; s < V; ++s) {
+        const int c = (s * (int)blockDim.x + (int)threadIdx.x) * kLaneElems;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) h[s][i] = h[s][i] * rstd * w[s][i];
+        if (a.y) store8<kBf16, kVec>(a.y + row * a.H, c, a.H, h[s]);
+        if (a.q)
+            quant8<kVec>(h[s], a.q + row * a.H,
+                         a.scales + row * ((a.H + kGroup - 1) / kGroup) + c / kGroup, c, a.H);
+    }
+}
+
+// ---------------------------------------------------------------------------
+// quant: 16 lanes per (row, group)
+// ---------------------------------------------------------------------------
+constexpr int kQuantThreads = 256;
+
+template <bool kBf16, bool kVec, bool kSilu>
+__global__ void __launch_bounds__(kQuantThreads) quant_kernel(QuantArgs a) {
+    chain_start();
+    const long long n_items = (long long)a.M * a.G;
+    // whole warps go round together (the shuffles of quant8): a warp's second
+    // half may be past the end, and then reads and writes nothing
+    const long long first = ((long long)blockIdx.x * kQuantThreads + threadIdx.x) / kGroupLanes;
+    const long long step = (long long)gridDim.x * (kQuantThreads / kGroupLanes);
+    for (long long it = first; (it & ~1ll) < n_items; it += step) {
+        const bool live = it < n_items;
+        const long long row = live ? it / a.G : 0;
+        const int g = live ? (int)(it - row * a.G) : 0;
+        const int c = live ? g * kGroup + (threadIdx.x % kGroupLanes) * kLaneElems : a.N;
+        float v[8];
+        const uint16_t *x = a.x + row * (size_t)(kSilu ? 2 * (size_t)a.N : a.N);
+        load8<kBf16, kVec>(x, c, a.N, v);
+        if constexpr (kSilu) {
+            float u[8];
+            load8<kBf16, kVec>(x + a.N, c, a.N, u);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] = v[i] / (1.f + expf(-v[i])) * u[i];
+        }
+        quant8<kVec>(v, a.q + row * a.N, a.scales + row * a.G + g, c, a.N);
+    }
+}
+
+cudaLaunchConfig_t chained(int grid, int threads, cudaStream_t stream, cudaLaunchAttribute *attr) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(threads);
+    cfg.stream = stream;
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cfg;
+}
+
+bool aligned16(const void *p) { return ((uintptr_t)p & 15) == 0; }
+
+template <bool kBf16, bool kVec>
+cudaError_t launch_norm_v(const NormArgs &a, int steps, int threads, cudaStream_t stream) {
+    cudaLaunchAttribute attr[1];
+    const cudaLaunchConfig_t cfg = chained(a.M, threads, stream, attr);
+    switch (steps) {
+        case 1: return cudaLaunchKernelEx(&cfg, rmsnorm_kernel<kBf16, kVec, 1>, a);
+        case 2: return cudaLaunchKernelEx(&cfg, rmsnorm_kernel<kBf16, kVec, 2>, a);
+        default: return cudaLaunchKernelEx(&cfg, rmsnorm_kernel<kBf16, kVec, 4>, a);
+    }
+}
+
+template <bool kBf16, bool kVec>
+cudaError_t launch_quant_v(const QuantArgs &a, bool silu, int grid, cudaStream_t stream) {
+    cudaLaunchAttribute attr[1];
+    const cudaLaunchConfig_t cfg = chained(grid, kQuantThreads, stream, attr);
+    return silu ? cudaLaunchKernelEx(&cfg, quant_kernel<kBf16, kVec, true>, a)
+                : cudaLaunchKernelEx(&cfg, quant_kernel<kBf16, kVec, false>, a);
+}
+
+}  // namespace
+
+cudaError_t launch_rmsnorm(const NormArgs &a, bool bf16, cudaStream_t stream) {
+    const bool vec = a.H % kLaneElems == 0 && aligned16(a.x) && aligned16(a.residual) &&
+                     aligned16(a.weight) && aligned16(a.sum_out) && aligned16(a.y) &&
+                     aligned16(a.q);
+    const int lanes = (a.H + kLaneElems - 1) / kLaneElems;
+    int steps = 1;
+    while (lanes > 1024 * steps) steps *= 2;
+    const int threads = ((lanes + steps - 1) / steps + 31) / 32 * 32;
+    if (vec) return bf16 ? launch_norm_v<true, true>(a, steps, threads, stream)
+                         : launch_norm_v<false, true>(a, steps, threads, stream);
+    return bf16 ? launch_norm_v<true, false>(a, steps, threads, stream)
+                : launch_norm_v<false, false>(a, steps, threads, stream);
+}
+
+cudaError_t launch_quant(const QuantArgs &a, bool bf16, bool silu, cudaStream_t stream) {
+    const bool vec = a.N % kLaneElems == 0 && aligned16(a.x) && aligned16(a.q);
+    const long long items = (long long)a.M * a.G;
+    const long long per = kQuantThreads / kGroupLanes;
+    long long grid = (items + per - 1) / per;
+    if (grid > (1 << 20)) grid = 1 << 20;
+    if (vec) return bf16 ? launch_quant_v<true, true>(a, silu, (int)grid, stream)
+                         : launch_quant_v<false, true>(a, silu, (int)grid, stream);
+    return bf16 ? launch_quant_v<true, false>(a, silu, (int)grid, stream)
+                : launch_quant_v<false, false>(a, silu, (int)grid, stream);
+}
+
+}  // namespace w4a16

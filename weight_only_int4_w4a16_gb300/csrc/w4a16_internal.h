@@ -273,6 +273,57 @@ cudaError_t launch_dense(const __half *x, const __half *w, __half *y, int M, int
                          cudaStream_t stream);
 cudaError_t dense_init(const DeviceInfo &dev);
 
+// ---- 8-bit linear (w4a16_fp8.cu) --------------------------------------------
+// y [M, N] = x [M, K] w [N, K]^T (+ residual): e4m3 x with scales xs [M, G], e4m3
+// w with scales ws [ceil(N/128), G], G = ceil(K/128); 16-bit y and residual.
+struct Fp8Args {
+    const uint8_t *x;
+    const float *xs;
+    const uint8_t *w;
+    const float *ws;
+    const uint16_t *residual;
+    uint16_t *y;
+    int M, N, K;
+    bool bf16;
+};
+struct Fp8Plan {
+    int T;             // tokens per tile (the MMA's N): 16, 32, 64 or 128
+    int G;             // blocks of 128 along K
+    int tiles_m;       // token tiles
+    long long tiles;   // all tiles
+    bool streamk;      // CTAs take equal runs of (tile, block) work, not whole tiles
+    int grid;
+    int stages;
+    size_t ws_bytes;   // partial sums of split tiles
+};
+// ws: splits nothing that does not fit it
+Fp8Plan plan_fp8(int M, int N, int K, const DeviceInfo &dev, const Workspace &ws);
+cudaError_t launch_fp8(const Fp8Args &a, const Fp8Plan &plan, const Workspace &ws,
+                       cudaStream_t stream);
+cudaError_t fp8_init(const DeviceInfo &dev);
+
+// ---- row steps around it (w4a16_fp8_rows.cu) ---------------------------------
+constexpr int kMaxNormWidth = 32768;
+// h = x (+ residual), v = h / sqrt(mean(h^2) + eps) * weight per row of H;
+// outputs that are null are not written
+struct NormArgs {
+    const uint16_t *x, *residual, *weight;
+    uint16_t *sum_out, *y;
+    uint8_t *q;
+    float *scales;
+    int M, H;
+    float eps;
+};
+cudaError_t launch_rmsnorm(const NormArgs &a, bool bf16, cudaStream_t stream);
+// x [M, N] ([M, 2N] with silu: silu(first N) * last N) -> q [M, N], scales [M, G]
+struct QuantArgs {
+    const uint16_t *x;
+    uint8_t *q;
+    float *scales;
+    int M, N, G;
+};
+cudaError_t launch_quant(const QuantArgs &a, bool bf16, bool silu, cudaStream_t stream);
+
 // ---- mixture of experts (w4a16_moe.cu) -------------------------------------
 constexpr int kMaxMoeExperts = 1024;
 constexpr int kMaxMoeTiles = 2048;  // tiles of up to 8 slots per launch
