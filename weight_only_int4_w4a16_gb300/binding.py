@@ -350,15 +350,20 @@ def w4a16_dense_linear(x: torch.Tensor, w: torch.Tensor, y=None, stream=None) ->
 FP8 = torch.float8_e4m3fn
 
 
-def _groups(n: int) -> int:
-    return -(-n // GROUP)
+def _rows2d(t: torch.Tensor, name: str):
+    if not isinstance(t, torch.Tensor) or t.dim() != 2:
+        raise ValueError(f"{name} must be a 2-D torch tensor")
+    return t.shape
 
 
 def _shaped(t: torch.Tensor, dtype, shape, name: str) -> int:
-    p = _dev(t, dtype, name)
-    if tuple(t.shape) != tuple(shape):
+    """The address of a contiguous CUDA tensor of this type and shape (the checks
+    of a good tensor come first and are cheap: a small call's time is mostly the host's)."""
+    if not (isinstance(t, torch.Tensor) and t.is_cuda and t.dtype is dtype and
+            t.shape == shape and t.is_contiguous()):
+        _dev(t, dtype, name)
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    return p
+    return t.data_ptr()
 
 
 def _dtype16(dt) -> int:
@@ -367,22 +372,20 @@ def _dtype16(dt) -> int:
     return _DTYPE_OF[dt]
 
 
-def _rows2d(t: torch.Tensor, name: str):
-    if not isinstance(t, torch.Tensor) or t.dim() != 2:
-        raise ValueError(f"{name} must be a 2-D torch tensor")
-    return t.shape
-
-
-def _used_on(stream, *tensors) -> None:
-    """Tell torch's allocator of tensors that a call uses on another stream
-    than the current one, so that freed memory is not handed out too early."""
+def _stream_for(t: torch.Tensor, stream, *used) -> int:
+    """The stream of a call on t's device.  For a stream other than the current
+    one, torch's allocator is told of the tensors used on it, so that memory
+    freed after the call is not handed out too early."""
+    current = torch._C._cuda_getCurrentRawStream(t.get_device())
     if stream is None:
-        return
-    s = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream))
-    if s != torch.cuda.current_stream():
-        for t in tensors:
-            if t is not None:
-                t.record_stream(s)
+        return current
+    raw = _stream_ptr(stream)
+    if raw != current:
+        s = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(raw)
+        for u in used:
+            if u is not None:
+                u.record_stream(s)
+    return raw
 
 
 def w4a16_fp8_linear(x: torch.Tensor, x_scales: torch.Tensor, w: torch.Tensor,
@@ -396,39 +399,41 @@ def w4a16_fp8_linear(x: torch.Tensor, x_scales: torch.Tensor, w: torch.Tensor,
     (M, K), (N, Kw) = _rows2d(x, "x"), _rows2d(w, "w")
     if K != Kw:
         raise ValueError(f"x has {K} columns and w {Kw}")
-    dt = _dtype16(dtype)
-    xp, wp = _dev(x, FP8, "x"), _dev(w, FP8, "w")
-    xs = _shaped(x_scales, torch.float32, (M, _groups(K)), "x_scales")
-    ws = _shaped(w_scales, torch.float32, (_groups(N), _groups(K)), "w_scales")
-    r = _shaped(residual, dtype, (M, N), "residual") if residual is not None else None
+    dt, G = _dtype16(dtype), (K + GROUP - 1) // GROUP
+    xp, wp = _shaped(x, FP8, (M, K), "x"), _shaped(w, FP8, (N, K), "w")
+    xs = _shaped(x_scales, torch.float32, (M, G), "x_scales")
+    ws = _shaped(w_scales, torch.float32, ((N + GROUP - 1) // GROUP, G), "w_scales")
+    r = None if residual is None else _shaped(residual, dtype, (M, N), "residual")
     if y is None:
         y = torch.empty((M, N), dtype=dtype, device=x.device)
-    _check(lib.w4a16_fp8_linear(xp, xs, wp, ws, M, N, K, dt, epilogue, r,
-                                _shaped(y, dtype, (M, N), "y"), _stream_ptr(stream)),
+    yp = _shaped(y, dtype, (M, N), "y")
+    _check(lib.w4a16_fp8_linear(xp, xs, wp, ws, M, N, K, dt, epilogue, r, yp,
+                                _stream_for(x, stream, x, x_scales, w, w_scales, residual, y)),
            "w4a16_fp8_linear")
-    _used_on(stream, x, x_scales, w, w_scales, residual, y)
     return y
 
 
 def _norm(x, weight, residual, eps, sum_out, y, q, scales, stream, what):
     M, H = x.shape
-    dt = _dtype16(x.dtype)
-    xp = _dev(x, x.dtype, "x")
-    wp = _shaped(weight, x.dtype, (H,), "weight")
-    r = _shaped(residual, x.dtype, (M, H), "residual") if residual is not None else None
-    if sum_out is None:
-        if residual is not None:
-            sum_out = torch.empty_like(x)
-    elif residual is None:
+    dt = x.dtype
+    code = _dtype16(dt)
+    xp, wp = _shaped(x, dt, (M, H), "x"), _shaped(weight, dt, (H,), "weight")
+    rp = sp = yp = qp = cp = None
+    if residual is not None:
+        rp = _shaped(residual, dt, (M, H), "residual")
+        if sum_out is None:
+            sum_out = torch.empty((M, H), dtype=dt, device=x.device)
+        sp = _shaped(sum_out, dt, (M, H), "sum_out")
+    elif sum_out is not None:
         raise ValueError("sum_out needs a residual")
-    _check(lib.w4a16_rmsnorm(
-        xp, r, wp, M, H, eps, dt,
-        _shaped(sum_out, x.dtype, (M, H), "sum_out") if sum_out is not None else None,
-        _shaped(y, x.dtype, (M, H), "y") if y is not None else None,
-        _shaped(q, FP8, (M, H), "q") if q is not None else None,
-        _shaped(scales, torch.float32, (M, _groups(H)), "scales") if scales is not None else None,
-        _stream_ptr(stream)), what)
-    _used_on(stream, x, weight, residual, sum_out, y, q, scales)
+    if y is not None:
+        yp = _shaped(y, dt, (M, H), "y")
+    if q is not None:
+        qp = _shaped(q, FP8, (M, H), "q")
+        cp = _shaped(scales, torch.float32, (M, (H + GROUP - 1) // GROUP), "scales")
+    _check(lib.w4a16_rmsnorm(xp, rp, wp, M, H, eps, code, sp, yp, qp, cp,
+                             _stream_for(x, stream, x, weight, residual, sum_out, y, q, scales)),
+           what)
     return sum_out
 
 
@@ -437,9 +442,9 @@ def w4a16_rmsnorm(x: torch.Tensor, weight: torch.Tensor, residual=None, eps: flo
     """y [M, H] = h / sqrt(mean(h^2) + eps) * weight with h = x (+ residual).
     Returns y, or (y, sum_out) when a residual is given: sum_out is h rounded to
     the 16-bit type (sum_out=residual updates the residual in place)."""
-    _rows2d(x, "x")
+    M, H = _rows2d(x, "x")
     if y is None:
-        y = torch.empty_like(x)
+        y = torch.empty((M, H), dtype=x.dtype, device=x.device)
     s = _norm(x, weight, residual, eps, sum_out, y, None, None, stream, "w4a16_rmsnorm")
     return y if s is None else (y, s)
 
@@ -452,7 +457,7 @@ def w4a16_rmsnorm_fp8(x: torch.Tensor, weight: torch.Tensor, residual=None, eps:
     if q is None:
         q = torch.empty((M, H), dtype=FP8, device=x.device)
     if scales is None:
-        scales = torch.empty((M, _groups(H)), dtype=torch.float32, device=x.device)
+        scales = torch.empty((M, (H + GROUP - 1) // GROUP), dtype=torch.float32, device=x.device)
     s = _norm(x, weight, residual, eps, sum_out, None, q, scales, stream, "w4a16_rmsnorm_fp8")
     return (q, scales) if s is None else (q, scales, s)
 
@@ -464,15 +469,15 @@ def w4a16_fp8_quant(x: torch.Tensor, epilogue: int = EPILOGUE_NONE, q=None, scal
     M, cols = _rows2d(x, "x")
     dt = _dtype16(x.dtype)
     N = cols // 2 if epilogue == EPILOGUE_SILU_MUL else cols
-    xp = _dev(x, x.dtype, "x")
+    G = (N + GROUP - 1) // GROUP
+    xp = _shaped(x, x.dtype, (M, cols), "x")
     if q is None:
         q = torch.empty((M, N), dtype=FP8, device=x.device)
     if scales is None:
-        scales = torch.empty((M, _groups(N)), dtype=torch.float32, device=x.device)
-    _check(lib.w4a16_fp8_quant(xp, M, cols, epilogue, dt, _shaped(q, FP8, (M, N), "q"),
-                               _shaped(scales, torch.float32, (M, _groups(N)), "scales"),
-                               _stream_ptr(stream)), "w4a16_fp8_quant")
-    _used_on(stream, x, q, scales)
+        scales = torch.empty((M, G), dtype=torch.float32, device=x.device)
+    qp, cp = _shaped(q, FP8, (M, N), "q"), _shaped(scales, torch.float32, (M, G), "scales")
+    _check(lib.w4a16_fp8_quant(xp, M, cols, epilogue, dt, qp, cp,
+                               _stream_for(x, stream, x, q, scales)), "w4a16_fp8_quant")
     return q, scales
 
 

@@ -131,6 +131,15 @@ bool gemv_small(int M, int N, int K) {
     return M <= kMmaMaxTokens && w <= lim;
 }
 
+// The 8-bit linear's kernel for M tokens: CTA pairs on 256-token tiles, or
+// 128-row weight tiles by up to 128 tokens.
+bool fp8_takes_wide(int M, int N, int K) {
+    (void)N;
+    (void)K;
+    const char *e = getenv("FP8_WIDE_FROM");
+    return M >= (e ? atoi(e) : 257);
+}
+
 Decision decide(int M, int N, int K, const DeviceInfo &dev, int forced, int epi = kEpiNone,
                 int dtype = kDtypeF16) {
     const int Mt = M < kGemvMaxTokens ? M : kGemvMaxTokens;
@@ -618,6 +627,7 @@ int w4a16_init(int device, size_t workspace_bytes) {
     if (e == cudaSuccess) e = dense_init(dev);
     if (e == cudaSuccess) e = moe_decode_init(dev);
     if (e == cudaSuccess) e = fp8_init(dev);
+    if (e == cudaSuccess) e = fp8_wide_init(dev);
     if (e == cudaSuccess) e = cudaDeviceSynchronize();
     if (e != cudaSuccess) {
         cudaFree(base);
@@ -790,14 +800,16 @@ int w4a16_fp8_linear(const uint8_t *x, const float *x_scales, const uint8_t *w,
         return W4A16_ERR_INVALID_ARG;
     const State &st = g_state;
     if (!st.initialized) return W4A16_ERR_NOT_INITIALIZED;
-    const Fp8Plan p = plan_fp8(M, N, K, st.dev, st.ws);
     const Fp8Args a{x, x_scales, w, w_scales, residual, y, M, N, K, dtype == W4A16_DTYPE_BF16};
-    const cudaError_t e = launch_fp8(a, p, st.ws, (cudaStream_t)stream);
+    const bool wide = fp8_takes_wide(M, N, K);
+    const cudaError_t e =
+        wide ? launch_fp8_wide(a, plan_fp8_wide(M, N, K, st.dev, st.ws), st.ws, (cudaStream_t)stream)
+             : launch_fp8(a, plan_fp8(M, N, K, st.dev, st.ws), st.ws, (cudaStream_t)stream);
     if (e != cudaSuccess) return cuda_fail(e);
     g_launches.fetch_add(1, std::memory_order_relaxed);
     if (st.log)
-        fprintf(stderr, "[w4a16] fp8 linear M=%d N=%d K=%d dtype=%d T=%d grid=%d\n", M, N, K, dtype,
-                p.T, p.grid);
+        fprintf(stderr, "[w4a16] fp8 linear M=%d N=%d K=%d dtype=%d -> %s\n", M, N, K, dtype,
+                wide ? "wide" : "narrow");
     return W4A16_OK;
 }
 

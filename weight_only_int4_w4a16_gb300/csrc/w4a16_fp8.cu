@@ -30,6 +30,7 @@
 // and exits.
 #include <cstring>
 
+#include "w4a16_fp8_common.cuh"
 #include "w4a16_internal.h"
 #include "w4a16_tcgen05.cuh"
 
@@ -48,10 +49,6 @@ constexpr int kMaxStages = 12;
 constexpr int kSmemBudget = 216 * 1024;       // the stages
 constexpr int kDBufs = 4;                     // block sums in tensor memory
 constexpr int kTmemCols = 512;
-
-// device status bits
-constexpr int kErrStageWait = 1 << 17, kErrSumWait = 1 << 18, kErrSlotWait = 1 << 19,
-              kErrDrain = 1 << 20;
 
 struct Fp8Params {
     CUtensorMap wmap;  // w: (K bytes, N rows), box {128, 128}, 128-byte swizzle
@@ -132,15 +129,7 @@ __device__ __forceinline__ int slot_of(const Fp8Params &p, int b, long long tile
     return 2 * b + (Walk::begin(p, b) > tile0 ? 0 : 1);
 }
 
-__device__ __forceinline__ float half_bits_to_float(uint16_t h, int bf16) {
-    return bf16 ? __uint_as_float((uint32_t)h << 16) : __half2float(__ushort_as_half(h));
-}
-__device__ __forceinline__ uint16_t float_to_half_bits(float v, int bf16) {
-    return bf16 ? __bfloat16_as_ushort(__float2bfloat16_rn(v))
-                : __half_as_ushort(__float2half_rn(v));
-}
-
-// y[m0 + t0 .. + 15][n] = v (+ residual), one rounding each.  The residual may be
+// y[m0 .. m0 + 15][n] = v (+ residual), one rounding each.  The residual may be
 // y itself: its 16 values are read before any of the 16 outputs is written.
 __device__ __forceinline__ void store16(const Fp8Params &p, int m0, int n, const float *v) {
     float r[16];
@@ -307,9 +296,12 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_kernel(const __grid_constant_
                 const float sw = sc[T];
 #pragma unroll
                 for (int i0 = 0; i0 < T; i0 += 16) {
+                    uint32_t u[16];
                     float v[16];
-                    tmem_ld16(tmem + lanes + d * T + i0, v);
-                    tmem_wait_ld();
+                    tmem_ld(tmem + lanes + d * T + i0, u);
+                    tmem_wait_ld(u);
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(u[i]);
 #pragma unroll
                     for (int i = 0; i < 16; i += 4) {
                         const float4 sx = *reinterpret_cast<const float4 *>(sc + i0 + i);
@@ -386,18 +378,6 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_kernel(const __grid_constant_
 // ---------------------------------------------------------------------------
 // host side
 // ---------------------------------------------------------------------------
-bool encode_rows(CUtensorMap *map, const void *base, int rows, int K, int box_rows) {
-    const EncodeTiledFn encode = tensor_map_encoder();
-    const cuuint64_t dims[2] = {(cuuint64_t)K, (cuuint64_t)rows};
-    const cuuint64_t strides[1] = {(cuuint64_t)K};
-    const cuuint32_t box[2] = {(cuuint32_t)kGroup, (cuuint32_t)box_rows};
-    const cuuint32_t estr[2] = {1, 1};
-    return encode && encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void *>(base), dims,
-                            strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
 template <int T>
 cudaError_t launch_t(const Fp8Params &p, int grid, cudaStream_t stream) {
     cudaLaunchConfig_t cfg = {};
@@ -455,7 +435,7 @@ cudaError_t launch_fp8(const Fp8Args &a, const Fp8Plan &plan, const Workspace &w
                        cudaStream_t stream) {
     Fp8Params p;
     memset(&p, 0, sizeof(p));
-    if (!encode_rows(&p.wmap, a.w, a.N, a.K, kTileN) || !encode_rows(&p.xmap, a.x, a.M, a.K, plan.T))
+    if (!encode_fp8_rows(&p.wmap, a.w, a.N, a.K, kTileN) || !encode_fp8_rows(&p.xmap, a.x, a.M, a.K, plan.T))
         return cudaErrorInvalidValue;
     p.xs = a.xs;
     p.ws = a.ws;

@@ -1,0 +1,525 @@
+// The 8-bit linear for many tokens (the operation of w4a16_fp8.cu):
+//
+//   y[m, n] = sum_b sx[m, b] sw[n / 128, b] * (sum_{k in block b} x[m, k] w[n, k])
+//
+// MMA shape: a pair of CTAs (cta_group::2) computes 256 tokens x 256 weight rows,
+// the tokens as the MMA's M = 256 (128 per CTA, a token per tensor-memory lane),
+// the weight rows as its N = 256 (each CTA loads half of them, the tensor cores
+// read both halves): per block of 128 k a CTA loads 32 KB for 4.2 MFLOP x 2, half
+// of what a CTA alone would.  A lane is a token, so a block's scale is one number
+// per thread and 128-column half, sx sw, and adding a block to the sums costs one
+// multiply-add per element.
+//
+//   Roles (320 threads per CTA): warps 0..7 (lane = token, warp / 4 = half of the
+//   256 columns) scale and add the blocks' sums and write y; warp 8 streams the
+//   CTA's 128 rows of x and its 128 rows of w per block by TMA and copies the
+//   scales; warp 9 of the leading CTA issues the pair's products.  Two block sums
+//   of 256 columns fill the tensor memory: while the tensor cores run one, the
+//   other is read.
+//
+//   Outputs go through shared memory to TMA stores (rows of 64 columns), or
+//   straight from registers where N or y's address does not allow TMA.
+//
+//   Work: whole tiles in turn while every pair has one; what remains beyond the
+//   last full round (and that round with it) is cut into equal runs of blocks
+//   ("stream-K"), so that no pair waits; a tile that is split is summed in K
+//   order by its last pair.
+//
+// Every mbarrier wait is bounded, as in w4a16_fp8.cu.  The two cluster barriers
+// (after the setup, before the exit) are reached by every thread: all that comes
+// before them is bounded.
+#include <cstring>
+
+#include "w4a16_fp8_common.cuh"
+#include "w4a16_internal.h"
+#include "w4a16_tcgen05.cuh"
+
+namespace w4a16 {
+namespace {
+
+using namespace dev;
+
+constexpr int kTileM = 256, kTileN = 256;      // of a pair
+constexpr int kHalf = 128;                     // rows of x, and of w, per CTA
+constexpr int kStageX = kHalf * kGroup, kStageW = kHalf * kGroup;
+constexpr int kStage = kStageX + kStageW;      // 32 KB
+constexpr int kScales = kHalf + 4;             // floats per stage: the tokens', two weight blocks'
+constexpr int kStages = 5;
+constexpr int kSumWarps = 8;
+constexpr int kTmaWarp = 8, kMmaWarp = 9;
+constexpr int kThreads = 320;
+constexpr int kDBufs = 2;
+constexpr int kTmemCols = 512;
+constexpr int kStoreCols = 64;                 // columns per TMA store (a 128-byte row)
+constexpr int kStoreBytes = 32 * kStoreCols * 2;  // a warp's staging: 4 KB
+constexpr int kGroupM = 16;                    // token tiles that share a pass over the weights
+constexpr int kBarBytes = (3 * kStages + 2 * kDBufs) * 8 + 16;
+constexpr int kSmem = 1024 + kStages * (kStage + kScales * 4) + kSumWarps * kStoreBytes + kBarBytes;
+constexpr uint32_t kIdesc =  // D f32, A and B e4m3 (0), N = 256, M = 256
+    (1u << 4) | ((uint32_t)(kTileN >> 3) << 17) | ((uint32_t)(kTileM >> 4) << 24);
+
+struct WideParams {
+    CUtensorMap xmap;  // x: (K bytes, M rows), box {128, 128}, 128-byte swizzle
+    CUtensorMap wmap;  // w: (K bytes, N rows), the same
+    CUtensorMap ymap;  // y: (N, M) of 16 bits, box {64, 32}, 128-byte swizzle (tma_store)
+    const float *xs, *ws;
+    const uint16_t *residual;
+    uint16_t *y;
+    float *partials;     // [2 * pairs][2 CTAs][256 columns][128 tokens] fp32
+    unsigned *counters;  // [tiles], zero between launches
+    int *status;
+    int M, N, G, NB;
+    int tiles_m, tiles_n;
+    int whole;           // tiles that pairs take whole, in turn
+    long long split;     // blocks of the other tiles, cut into equal runs
+    int tma_store, bf16;
+};
+
+// A pair's work, in order: segments (tile t, blocks [j0, j1)).
+struct Walk {
+    int tile, pairs, pair;
+    long long pos, end;
+    __device__ __forceinline__ Walk(const WideParams &p)
+        : pairs(gridDim.x / 2), pair(blockIdx.x / 2) {
+        tile = pair;
+        pos = begin(p, pair);
+        end = begin(p, pair + 1);
+    }
+    __device__ __forceinline__ long long begin(const WideParams &p, int b) const {
+        return (long long)b * p.split / pairs;
+    }
+    // the pair whose run holds block i of the split tiles
+    __device__ __forceinline__ int owner(const WideParams &p, long long i) const {
+        return (int)(((i + 1) * (long long)pairs - 1) / p.split);
+    }
+    __device__ __forceinline__ bool next(const WideParams &p, int &t, int &j0, int &j1) {
+        if (tile < p.whole) {
+            t = tile;
+            j0 = 0;
+            j1 = p.G;
+            tile += pairs;
+            return true;
+        }
+        if (pos >= end) return false;
+        const int i = (int)(pos / p.G);
+        const long long t0 = (long long)i * p.G;
+        t = p.whole + i;
+        j0 = (int)(pos - t0);
+        j1 = (int)((t0 + p.G < end ? t0 + p.G : end) - t0);
+        pos = t0 + j1;
+        return true;
+    }
+};
+
+// Tile t's first token and first weight row: groups of kGroupM token tiles pass
+// over the weights together, so that a weight tile is read from memory once per
+// group and x's rows stay in L2.
+__device__ __forceinline__ void tile_at(const WideParams &p, int t, int &m0, int &n0) {
+    const int per = kGroupM * p.tiles_n, g = t / per, r = t - g * per;
+    const int gm = min(kGroupM, p.tiles_m - g * kGroupM);
+    const int n = r / gm;
+    m0 = (g * kGroupM + r - n * gm) * kTileM;
+    n0 = n * kTileN;
+}
+
+// d += a * b on two packed fp32 values
+__device__ __forceinline__ void fma2(uint64_t &d, uint64_t a, uint64_t b) {
+    asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(d) : "l"(a), "l"(b));
+}
+__device__ __forceinline__ uint64_t pack2(uint32_t lo, uint32_t hi) {
+    uint64_t d;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "r"(lo), "r"(hi));
+    return d;
+}
+__device__ __forceinline__ void unpack2(uint64_t v, float &lo, float &hi) {
+    uint32_t a, b;
+    asm("mov.b64 {%0, %1}, %2;" : "=r"(a), "=r"(b) : "l"(v));
+    lo = __uint_as_float(a);
+    hi = __uint_as_float(b);
+}
+
+__global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
+    fp8_wide_kernel(const __grid_constant__ WideParams p) {
+    extern __shared__ uint8_t smem_raw[];
+    // the same offsets in both CTAs: the products read both shared memories at
+    // the leader's addresses
+    uint8_t *smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
+    uint8_t *sm_store = smem + kStages * kStage;
+    float *sm_scales = reinterpret_cast<float *>(sm_store + kSumWarps * kStoreBytes);
+    uint64_t *full = reinterpret_cast<uint64_t *>(sm_scales + kStages * kScales);  // (leader) tiles landed
+    uint64_t *sfull = full + kStages;      // this CTA's scales landed
+    uint64_t *empty = sfull + kStages;     // this CTA's stage read
+    uint64_t *d_full = empty + kStages;    // a block's sums ready
+    uint64_t *d_empty = d_full + kDBufs;   // (leader) read by both CTAs
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(d_empty + kDBufs);
+    volatile int *abort = reinterpret_cast<volatile int *>(tmem_slot + 1);
+    int *s_last = const_cast<int *>(abort + 1);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = cluster_rank();
+
+    grid_dependents_launch();
+    if (threadIdx.x == kTmaWarp * 32) {
+        for (int i = 0; i < kStages; ++i) {
+            mbar_init(smem_u32(full + i), 1);
+            mbar_init(smem_u32(sfull + i), 32);
+            mbar_init(smem_u32(empty + i), 1 + kSumWarps);  // the products, the scales' readers
+        }
+        for (int i = 0; i < kDBufs; ++i) {
+            mbar_init(smem_u32(d_full + i), 1);
+            mbar_init(smem_u32(d_empty + i), 2 * kSumWarps);
+        }
+        *abort = 0;
+        mbar_init_fence();
+        prefetch_tensormap(&p.xmap);
+        prefetch_tensormap(&p.wmap);
+        if (p.tma_store) prefetch_tensormap(&p.ymap);
+    }
+    if (warp == 0) {
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                         smem_u32(tmem_slot)),
+                     "r"(kTmemCols)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+    }
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    auto fail = [&](int code) {
+        *abort = 1;
+        atomicOr(p.status, code);
+    };
+
+    Walk walk(p);
+    int t, j0, j1, m0, n0;
+    if (warp == kTmaWarp) {
+        // ------------------------------------------------ producer
+        grid_dependency_wait();
+        const uint64_t pol_w = policy_evict_first(), pol_x = policy_evict_last();
+        int c = 0;
+        bool ok = true;
+        while (ok && walk.next(p, t, j0, j1)) {
+            tile_at(p, t, m0, n0);
+            const int mr = m0 + (int)rank * kHalf, nr = n0 + (int)rank * kHalf;
+            for (int j = j0; j < j1; ++j, ++c) {
+                const int s = c % kStages;
+                if (c >= kStages && !__all_sync(0xffffffffu,
+                                                mbar_wait_cluster(smem_u32(empty + s),
+                                                                  ((c / kStages) - 1) & 1, abort))) {
+                    if (lane == 0) fail(kErrSlotWait);
+                    ok = false;
+                    break;
+                }
+                if (lane == 0) {
+                    const uint32_t st = smem_u32(smem + s * kStage);
+                    // both CTAs' bytes count at the leader's barrier
+                    const uint32_t bar = map_to_rank(smem_u32(full + s), 0);
+                    if (rank == 0) mbar_arrive_expect_tx(smem_u32(full + s), 2 * kStage);
+                    tma_load_2d_pair(st, &p.xmap, j * kGroup, mr, bar, pol_x);
+                    tma_load_2d_pair(st + kStageX, &p.wmap, j * kGroup, nr, bar, pol_w);
+                }
+                const uint32_t sc = smem_u32(sm_scales + s * kScales);
+#pragma unroll
+                for (int i = 0; i < kHalf / 32; ++i) {
+                    const int r = lane + 32 * i;
+                    const bool live = mr + r < p.M;
+                    cp_async4(sc + 4 * r, live ? p.xs + (size_t)(mr + r) * p.G + j : p.xs,
+                              live ? 4u : 0u);
+                }
+                if (lane < 2) {  // the tile's two weight blocks (the second may not exist)
+                    const int nb = n0 / kGroup + lane;
+                    cp_async4(sc + 4 * (kHalf + lane), nb < p.NB ? p.ws + (size_t)nb * p.G + j : p.ws,
+                              nb < p.NB ? 4u : 0u);
+                }
+                cp_async_arrive(smem_u32(sfull + s));
+            }
+        }
+        cp_async_wait_all();
+        // every load issued must have landed before the CTA exits: the leader
+        // sees both CTAs' (the other waits for it at the last cluster barrier)
+        if (rank == 0 && lane == 0)
+            for (int i = c - kStages > 0 ? c - kStages : 0; i < c; ++i)
+                if (!mbar_wait_drain(smem_u32(full + i % kStages), (i / kStages) & 1))
+                    atomicOr(p.status, kErrDrain);
+    } else if (warp == kMmaWarp) {
+        // ------------------------------------------------ products
+        if (rank == 0 && lane == 0) {
+            int c = 0;
+            bool ok = true;
+            while (ok && walk.next(p, t, j0, j1)) {
+                for (int j = j0; j < j1; ++j, ++c) {
+                    const int s = c % kStages, d = c % kDBufs;
+                    if (!mbar_wait_cluster(smem_u32(full + s), (c / kStages) & 1, abort)) {
+                        fail(kErrStageWait);
+                        ok = false;
+                        break;
+                    }
+                    if (c >= kDBufs && !mbar_wait_cluster(smem_u32(d_empty + d),
+                                                          ((c / kDBufs) - 1) & 1, abort)) {
+                        fail(kErrSumWait);
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint32_t st = smem_u32(smem + s * kStage);
+#pragma unroll
+                    for (int k = 0; k < kGroup / 32; ++k)
+                        mma_f8_ss_pair(tmem + d * kTileN, smem_desc_sw128(st + 32 * k),
+                                       smem_desc_sw128(st + kStageX + 32 * k), kIdesc, k > 0);
+                    mma_commit_pair(smem_u32(empty + s));
+                    mma_commit_pair(smem_u32(d_full + d));
+                }
+            }
+            // the products issued complete before the tensor memory is freed
+            for (int i = c - kDBufs > 0 ? c - kDBufs : 0; i < c; ++i)
+                if (!mbar_wait_drain(smem_u32(d_full + i % kDBufs), (i / kDBufs) & 1))
+                    atomicOr(p.status, kErrDrain);
+        }
+    } else {
+        // ------------------------------------------------ sums and outputs
+        grid_dependency_wait();
+        const int quarter = warp & 3, half = warp >> 2;
+        const int r = quarter * 32 + lane;  // token within the CTA's 128
+        const uint32_t taddr = tmem + ((uint32_t)(quarter * 32) << 16) + half * kHalf;
+        uint8_t *stage_out = sm_store + warp * kStoreBytes;
+        int c = 0;
+        bool ok = true;
+        while (ok && walk.next(p, t, j0, j1)) {
+            tile_at(p, t, m0, n0);
+            const int m = m0 + (int)rank * kHalf + r, nc = n0 + half * kHalf;
+            uint64_t acc[kHalf / 2];
+#pragma unroll
+            for (int i = 0; i < kHalf / 2; ++i) acc[i] = 0;
+            for (int j = j0; j < j1; ++j, ++c) {
+                const int s = c % kStages, d = c % kDBufs;
+                if (!__all_sync(0xffffffffu,
+                                mbar_wait(smem_u32(sfull + s), (c / kStages) & 1, abort) &&
+                                    mbar_wait_cluster(smem_u32(d_full + d), (c / kDBufs) & 1,
+                                                      abort))) {
+                    if (lane == 0) fail(kErrSumWait);
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                const float *sc = sm_scales + s * kScales;
+                const uint32_t sb = __float_as_uint(sc[r] * sc[kHalf + half]);
+                const uint64_t s2 = pack2(sb, sb);
+#pragma unroll
+                for (int q = 0; q < kHalf / 32; ++q) {
+                    uint32_t v[32];
+                    tmem_ld(taddr + d * kTileN + 32 * q, v);
+                    tmem_wait_ld(v);
+                    if (q == kHalf / 32 - 1) {  // all read: the tensor cores may write again
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) {
+                            mbar_arrive_cluster(map_to_rank(smem_u32(d_empty + d), 0));
+                            mbar_arrive(smem_u32(empty + s));
+                        }
+                    }
+#pragma unroll
+                    for (int i = 0; i < 16; ++i)
+                        fma2(acc[16 * q + i], pack2(v[2 * i], v[2 * i + 1]), s2);
+                }
+            }
+            if (!ok) break;
+            const bool whole = j0 == 0 && j1 == p.G;
+            bool last = whole;
+            const long long tile0 = (long long)(t - p.whole) * p.G;
+            int b0 = 0, b1 = 0;
+            if (!whole) {
+                // part of a tile: the sums go to this pair's slot (0: the run
+                // begins inside the tile, 1: the tile begins inside the run);
+                // the last CTA of this half of the tokens adds them in K order
+                b0 = walk.owner(p, tile0);
+                b1 = walk.owner(p, tile0 + p.G - 1);
+                const int slot = 2 * walk.pair + (walk.begin(p, walk.pair) > tile0 ? 0 : 1);
+                float *part = p.partials +
+                              ((size_t)(2 * slot + rank) * kTileN + half * kHalf) * kHalf + r;
+#pragma unroll
+                for (int i = 0; i < kHalf / 2; ++i) {
+                    float lo, hi;
+                    unpack2(acc[i], lo, hi);
+                    part[(size_t)(2 * i) * kHalf] = lo;
+                    part[(size_t)(2 * i + 1) * kHalf] = hi;
+                }
+                __threadfence();
+                asm volatile("bar.sync 1, %0;" ::"r"(kSumWarps * 32) : "memory");
+                unsigned *counter = p.counters + 2 * (t - p.whole) + rank;
+                if (threadIdx.x == 0)
+                    *s_last = atomicAdd(counter, 1u) == (unsigned)(b1 - b0) ? 1 : 0;
+                asm volatile("bar.sync 1, %0;" ::"r"(kSumWarps * 32) : "memory");
+                last = *s_last != 0;
+                if (last) {
+                    __threadfence();
+                    if (threadIdx.x == 0) *counter = 0u;  // ready for the next launch
+#pragma unroll
+                    for (int i = 0; i < kHalf / 2; ++i) acc[i] = 0;
+                    for (int b = b0; b <= b1; ++b) {
+                        const int sl = 2 * b + (walk.begin(p, b) > tile0 ? 0 : 1);
+                        const float *src = p.partials +
+                                           ((size_t)(2 * sl + rank) * kTileN + half * kHalf) * kHalf +
+                                           r;
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) {
+                            float v[32];
+#pragma unroll
+                            for (int i = 0; i < 32; ++i)
+                                v[i] = __ldcg(src + (size_t)(32 * q + i) * kHalf);
+#pragma unroll
+                            for (int i = 0; i < 16; ++i) {
+                                float lo, hi;
+                                unpack2(acc[16 * q + i], lo, hi);
+                                acc[16 * q + i] = pack2(__float_as_uint(lo + v[2 * i]),
+                                                        __float_as_uint(hi + v[2 * i + 1]));
+                            }
+                        }
+                    }
+                }
+                // s_last is written again only after every thread has read it
+                asm volatile("bar.sync 1, %0;" ::"r"(kSumWarps * 32) : "memory");
+            }
+            if (!last) continue;
+            // y[m][nc .. nc + 127] = sums (+ residual), one rounding each
+            if (p.tma_store) {
+                const uint16_t *res = p.residual && m < p.M ? p.residual + (size_t)m * p.N : nullptr;
+#pragma unroll
+                for (int h = 0; h < kHalf / kStoreCols; ++h) {
+                    const int n = nc + h * kStoreCols;
+                    tma_store_wait_read();  // (lane 0) the staging is free
+                    __syncwarp();
+#pragma unroll
+                    for (int q = 0; q < 8; ++q) {  // 8 columns, 16 bytes
+                        float v[8];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            unpack2(acc[h * 32 + q * 4 + i], v[2 * i], v[2 * i + 1]);
+                        if (res && n + 8 * q < p.N) {  // N is a multiple of 8
+                            const uint4 u = *reinterpret_cast<const uint4 *>(res + n + 8 * q);
+                            const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                v[2 * i] += half_bits_to_float((uint16_t)w[i], p.bf16);
+                                v[2 * i + 1] += half_bits_to_float((uint16_t)(w[i] >> 16), p.bf16);
+                            }
+                        }
+                        uint32_t o[4];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            o[i] = (uint32_t)float_to_half_bits(v[2 * i], p.bf16) |
+                                   (uint32_t)float_to_half_bits(v[2 * i + 1], p.bf16) << 16;
+                        // 128-byte swizzle: chunk q of row `lane`
+                        *reinterpret_cast<uint4 *>(stage_out + lane * 128 + ((q ^ (lane & 7)) << 4)) =
+                            make_uint4(o[0], o[1], o[2], o[3]);
+                    }
+                    fence_async_shared();
+                    __syncwarp();
+                    const int mw = m0 + (int)rank * kHalf + quarter * 32;
+                    if (lane == 0 && n < p.N && mw < p.M)
+                        tma_store_2d(&p.ymap, n, mw, smem_u32(stage_out));
+                }
+            } else if (m < p.M) {
+#pragma unroll
+                for (int i = 0; i < kHalf / 2; ++i) {
+                    float v[2];
+                    unpack2(acc[i], v[0], v[1]);
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const int n = nc + 2 * i + e;
+                        if (n < p.N) {
+                            const size_t o = (size_t)m * p.N + n;
+                            if (p.residual) v[e] += half_bits_to_float(p.residual[o], p.bf16);
+                            p.y[o] = float_to_half_bits(v[e], p.bf16);
+                        }
+                    }
+                }
+            }
+        }
+        tma_store_wait();
+    }
+
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync();  // neither CTA's shared or tensor memory goes while the pair uses it
+    if (warp == 0) {
+        tc_fence_after();
+        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem),
+                     "r"(kTmemCols)
+                     : "memory");
+    }
+}
+
+}  // namespace
+
+Fp8WidePlan plan_fp8_wide(int M, int N, int K, const DeviceInfo &dev, const Workspace &ws) {
+    Fp8WidePlan pl{};
+    pl.G = (K + kGroup - 1) / kGroup;
+    pl.tiles_m = (M + kTileM - 1) / kTileM;
+    pl.tiles_n = (N + kTileN - 1) / kTileN;
+    const long long tiles = (long long)pl.tiles_m * pl.tiles_n;
+    const int pairs = dev.sm_count / 2;
+    pl.pairs = (int)(tiles < pairs ? tiles : pairs);
+    pl.whole = (int)tiles;
+    const long long rest = tiles % pairs;
+    if (rest == 0 || rest * 100 >= (long long)pairs * 90) return pl;
+    // an unfinished last round: it and the full round before it are cut into
+    // equal runs (each longer than half a tile, so that a tile has few pieces)
+    const long long split = tiles < pairs ? tiles : pairs + rest;
+    long long runs = pairs;
+    if (tiles < pairs && split * pl.G < runs * 4)
+        runs = split * pl.G / 4;  // at least four blocks each
+    const size_t need = (size_t)2 * runs * 2 * kTileN * kHalf * sizeof(float);
+    if (tiles < pairs && runs <= tiles) return pl;
+    if (need > ws.partial_bytes || 2 * split > ws.n_counters - kMmaSchedWords) return pl;
+    pl.pairs = (int)runs;
+    pl.whole = (int)(tiles - split);
+    pl.split = split * pl.G;
+    return pl;
+}
+
+cudaError_t launch_fp8_wide(const Fp8Args &a, const Fp8WidePlan &plan, const Workspace &ws,
+                            cudaStream_t stream) {
+    WideParams p;
+    memset(&p, 0, sizeof(p));
+    if (!encode_fp8_rows(&p.xmap, a.x, a.M, a.K, kHalf) ||
+        !encode_fp8_rows(&p.wmap, a.w, a.N, a.K, kHalf))
+        return cudaErrorInvalidValue;
+    p.tma_store = a.N % 8 == 0 && ((uintptr_t)a.y & 15) == 0 && ((uintptr_t)a.residual & 15) == 0;
+    if (p.tma_store && !encode_store16(&p.ymap, a.y, a.M, a.N, 32, kStoreCols))
+        return cudaErrorInvalidValue;
+    p.xs = a.xs;
+    p.ws = a.ws;
+    p.residual = a.residual;
+    p.y = a.y;
+    p.partials = ws.partials;
+    p.counters = ws.counters;
+    p.status = ws.status;
+    p.M = a.M;
+    p.N = a.N;
+    p.G = plan.G;
+    p.NB = (a.N + kGroup - 1) / kGroup;
+    p.tiles_m = plan.tiles_m;
+    p.tiles_n = plan.tiles_n;
+    p.whole = plan.whole;
+    p.split = plan.split;
+    p.bf16 = a.bf16;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(2 * plan.pairs);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = kSmem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, fp8_wide_kernel, p);
+}
+
+cudaError_t fp8_wide_init(const DeviceInfo &) {
+    return cudaFuncSetAttribute((const void *)fp8_wide_kernel,
+                                cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+}
+
+}  // namespace w4a16

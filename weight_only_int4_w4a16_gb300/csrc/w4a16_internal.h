@@ -301,6 +301,17 @@ Fp8Plan plan_fp8(int M, int N, int K, const DeviceInfo &dev, const Workspace &ws
 cudaError_t launch_fp8(const Fp8Args &a, const Fp8Plan &plan, const Workspace &ws,
                        cudaStream_t stream);
 cudaError_t fp8_init(const DeviceInfo &dev);
+// the same for many tokens, CTA pairs on tiles of 256 x 256 (w4a16_fp8_wide.cu)
+struct Fp8WidePlan {
+    int G, tiles_m, tiles_n;
+    int pairs;        // CTA pairs of the launch
+    int whole;        // tiles that pairs take whole, in turn
+    long long split;  // blocks of the remaining tiles, cut into equal runs
+};
+Fp8WidePlan plan_fp8_wide(int M, int N, int K, const DeviceInfo &dev, const Workspace &ws);
+cudaError_t launch_fp8_wide(const Fp8Args &a, const Fp8WidePlan &plan, const Workspace &ws,
+                            cudaStream_t stream);
+cudaError_t fp8_wide_init(const DeviceInfo &dev);
 
 // ---- row steps around it (w4a16_fp8_rows.cu) ---------------------------------
 constexpr int kMaxNormWidth = 32768;
