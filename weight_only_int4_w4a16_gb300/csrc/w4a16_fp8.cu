@@ -157,7 +157,7 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_kernel(const __grid_constant_
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(d_empty + kDBufs);
     volatile int *abort = reinterpret_cast<volatile int *>(tmem_slot + 1);
     int *s_last = const_cast<int *>(abort + 1);
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = (int)uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
 
     grid_dependents_launch();
     if (threadIdx.x == kTmaWarp * 32) {
@@ -236,38 +236,38 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_kernel(const __grid_constant_
         cp_async_wait_all();
     } else if (warp == kMmaWarp) {
         // ------------------------------------------------ products
-        if (lane == 0) {
-            int c = 0;
-            bool ok = true;
-            while (ok && walk.next(p, t, j0, j1)) {
-                for (int j = j0; j < j1; ++j, ++c) {
-                    const int s = c % NS, d = c % kDBufs;
-                    if (!mbar_wait(smem_u32(full + s), (c / NS) & 1, abort)) {
-                        fail(kErrStageWait);
-                        ok = false;
-                        break;
-                    }
-                    if (c >= kDBufs &&
-                        !mbar_wait(smem_u32(d_empty + d), ((c / kDBufs) - 1) & 1, abort)) {
-                        fail(kErrSumWait);
-                        ok = false;
-                        break;
-                    }
-                    tc_fence_after();
-                    const uint32_t st = smem_u32(smem + (size_t)s * C::kStage);
-#pragma unroll
-                    for (int k = 0; k < kGroup / 32; ++k)
-                        mma_f8_ss(tmem + d * T, smem_desc_sw128(st + 32 * k),
-                                  smem_desc_sw128(st + kStageW + 32 * k), C::kIdesc, k > 0);
-                    mma_commit(smem_u32(empty + s));
-                    mma_commit(smem_u32(d_full + d));
+        const uint32_t stages = uniform(smem_u32(smem)), bars = uniform(smem_u32(full));
+        const uint32_t tm = uniform(tmem);
+        int c = 0;
+        bool ok = true;
+        while (ok && walk.next(p, t, j0, j1)) {
+            for (int j = j0; j < j1; ++j, ++c) {
+                const int s = c % NS, d = c % kDBufs;
+                if (!mbar_wait_all(bars + 8 * s, (c / NS) & 1, abort)) {
+                    if (lane == 0) fail(kErrStageWait);
+                    ok = false;
+                    break;
+                }
+                if (c >= kDBufs && !mbar_wait_all(bars + 8 * (2 * kMaxStages + kDBufs + d),
+                                                  ((c / kDBufs) - 1) & 1, abort)) {
+                    if (lane == 0) fail(kErrSumWait);
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                if (elect_one()) {
+                    const uint64_t a = smem_desc_sw128(stages + s * C::kStage);
+                    mma_f8_block(tm + d * T, a, a + (kStageW >> 4), C::kIdesc);
+                    mma_commit(bars + 8 * (2 * kMaxStages + d));
+                    mma_commit(bars + 8 * (kMaxStages + s));
                 }
             }
-            // the products issued complete before the tensor memory is freed
+        }
+        // the products issued complete before the tensor memory is freed
+        if (lane == 0)
             for (int i = c - kDBufs > 0 ? c - kDBufs : 0; i < c; ++i)
                 if (!mbar_wait_drain(smem_u32(d_full + i % kDBufs), (i / kDBufs) & 1))
                     atomicOr(p.status, kErrDrain);
-        }
     } else {
         // ------------------------------------------------ sums and outputs
         grid_dependency_wait();

@@ -10,10 +10,10 @@
 // per thread and 128-column half, sx sw, and adding a block to the sums costs one
 // multiply-add per element.
 //
-//   Roles (320 threads per CTA): warps 0..7 (lane = token, warp / 4 = half of the
-//   256 columns) scale and add the blocks' sums and write y; warp 8 streams the
-//   CTA's 128 rows of x and its 128 rows of w per block by TMA and copies the
-//   scales; warp 9 of the leading CTA issues the pair's products.  Two block sums
+//   Roles (384 threads per CTA): warps 0..7 (lane = token, warp / 4 = half of the
+//   256 columns) scale and add the blocks' sums and write y (the scales come from
+//   global memory into registers, four blocks ahead); warp 8 streams the CTA's 128
+//   rows of x and its 128 rows of w per block by TMA; warp 9 of the leading CTA issues the pair's products.  Two block sums
 //   of 256 columns fill the tensor memory: while the tensor cores run one, the
 //   other is read.
 //
@@ -43,18 +43,20 @@ constexpr int kTileM = 256, kTileN = 256;      // of a pair
 constexpr int kHalf = 128;                     // rows of x, and of w, per CTA
 constexpr int kStageX = kHalf * kGroup, kStageW = kHalf * kGroup;
 constexpr int kStage = kStageX + kStageW;      // 32 KB
-constexpr int kScales = kHalf + 4;             // floats per stage: the tokens', two weight blocks'
-constexpr int kStages = 5;
+constexpr int kStages = 6;
 constexpr int kSumWarps = 8;
 constexpr int kTmaWarp = 8, kMmaWarp = 9;
-constexpr int kThreads = 320;
-constexpr int kDBufs = 2;
+constexpr int kThreads = 384;                  // three warpgroups (warps 10 and 11 only fill the last)
+// registers per thread: the launch's 168 x 384 split between the warpgroups
+constexpr int kSumRegs = 216, kOtherRegs = 72;
+static_assert(2 * kSumRegs + kOtherRegs <= 3 * 168, "the launch's registers");
+constexpr int kDBufs = 2;                      // block sums in tensor memory
 constexpr int kTmemCols = 512;
 constexpr int kStoreCols = 64;                 // columns per TMA store (a 128-byte row)
 constexpr int kStoreBytes = 32 * kStoreCols * 2;  // a warp's staging: 4 KB
 constexpr int kGroupM = 16;                    // token tiles that share a pass over the weights
-constexpr int kBarBytes = (3 * kStages + 2 * kDBufs) * 8 + 16;
-constexpr int kSmem = 1024 + kStages * (kStage + kScales * 4) + kSumWarps * kStoreBytes + kBarBytes;
+constexpr int kBarBytes = (2 * kStages + 2 * kDBufs) * 8 + 16;
+constexpr int kSmem = 1024 + kStages * kStage + kSumWarps * kStoreBytes + kBarBytes;
 constexpr uint32_t kIdesc =  // D f32, A and B e4m3 (0), N = 256, M = 256
     (1u << 4) | ((uint32_t)(kTileN >> 3) << 17) | ((uint32_t)(kTileM >> 4) << 24);
 
@@ -122,22 +124,6 @@ __device__ __forceinline__ void tile_at(const WideParams &p, int t, int &m0, int
     n0 = n * kTileN;
 }
 
-// d += a * b on two packed fp32 values
-__device__ __forceinline__ void fma2(uint64_t &d, uint64_t a, uint64_t b) {
-    asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(d) : "l"(a), "l"(b));
-}
-__device__ __forceinline__ uint64_t pack2(uint32_t lo, uint32_t hi) {
-    uint64_t d;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "r"(lo), "r"(hi));
-    return d;
-}
-__device__ __forceinline__ void unpack2(uint64_t v, float &lo, float &hi) {
-    uint32_t a, b;
-    asm("mov.b64 {%0, %1}, %2;" : "=r"(a), "=r"(b) : "l"(v));
-    lo = __uint_as_float(a);
-    hi = __uint_as_float(b);
-}
-
 __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
     fp8_wide_kernel(const __grid_constant__ WideParams p) {
     extern __shared__ uint8_t smem_raw[];
@@ -145,24 +131,21 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
     // the leader's addresses
     uint8_t *smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
     uint8_t *sm_store = smem + kStages * kStage;
-    float *sm_scales = reinterpret_cast<float *>(sm_store + kSumWarps * kStoreBytes);
-    uint64_t *full = reinterpret_cast<uint64_t *>(sm_scales + kStages * kScales);  // (leader) tiles landed
-    uint64_t *sfull = full + kStages;      // this CTA's scales landed
-    uint64_t *empty = sfull + kStages;     // this CTA's stage read
+    uint64_t *full = reinterpret_cast<uint64_t *>(sm_store + kSumWarps * kStoreBytes);  // (leader)
+    uint64_t *empty = full + kStages;      // this CTA's stage read
     uint64_t *d_full = empty + kStages;    // a block's sums ready
     uint64_t *d_empty = d_full + kDBufs;   // (leader) read by both CTAs
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(d_empty + kDBufs);
     volatile int *abort = reinterpret_cast<volatile int *>(tmem_slot + 1);
     int *s_last = const_cast<int *>(abort + 1);
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = (int)uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
     const uint32_t rank = cluster_rank();
 
     grid_dependents_launch();
     if (threadIdx.x == kTmaWarp * 32) {
         for (int i = 0; i < kStages; ++i) {
             mbar_init(smem_u32(full + i), 1);
-            mbar_init(smem_u32(sfull + i), 32);
-            mbar_init(smem_u32(empty + i), 1 + kSumWarps);  // the products, the scales' readers
+            mbar_init(smem_u32(empty + i), 1);
         }
         for (int i = 0; i < kDBufs; ++i) {
             mbar_init(smem_u32(d_full + i), 1);
@@ -193,25 +176,26 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
 
     Walk walk(p);
     int t, j0, j1, m0, n0;
+    if (warp >= kSumWarps) {
+    regs_dec<kOtherRegs>();
     if (warp == kTmaWarp) {
         // ------------------------------------------------ producer
         grid_dependency_wait();
-        const uint64_t pol_w = policy_evict_first(), pol_x = policy_evict_last();
-        int c = 0;
-        bool ok = true;
-        while (ok && walk.next(p, t, j0, j1)) {
-            tile_at(p, t, m0, n0);
-            const int mr = m0 + (int)rank * kHalf, nr = n0 + (int)rank * kHalf;
-            for (int j = j0; j < j1; ++j, ++c) {
-                const int s = c % kStages;
-                if (c >= kStages && !__all_sync(0xffffffffu,
-                                                mbar_wait_cluster(smem_u32(empty + s),
-                                                                  ((c / kStages) - 1) & 1, abort))) {
-                    if (lane == 0) fail(kErrSlotWait);
-                    ok = false;
-                    break;
-                }
-                if (lane == 0) {
+        if (lane == 0) {
+            const uint64_t pol_w = policy_evict_first(), pol_x = policy_evict_last();
+            int c = 0;
+            bool ok = true;
+            while (ok && walk.next(p, t, j0, j1)) {
+                tile_at(p, t, m0, n0);
+                const int mr = m0 + (int)rank * kHalf, nr = n0 + (int)rank * kHalf;
+                for (int j = j0; j < j1; ++j, ++c) {
+                    const int s = c % kStages;
+                    if (c >= kStages &&
+                        !mbar_wait(smem_u32(empty + s), ((c / kStages) - 1) & 1, abort)) {
+                        fail(kErrSlotWait);
+                        ok = false;
+                        break;
+                    }
                     const uint32_t st = smem_u32(smem + s * kStage);
                     // both CTAs' bytes count at the leader's barrier
                     const uint32_t bar = map_to_rank(smem_u32(full + s), 0);
@@ -219,108 +203,112 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
                     tma_load_2d_pair(st, &p.xmap, j * kGroup, mr, bar, pol_x);
                     tma_load_2d_pair(st + kStageX, &p.wmap, j * kGroup, nr, bar, pol_w);
                 }
-                const uint32_t sc = smem_u32(sm_scales + s * kScales);
-#pragma unroll
-                for (int i = 0; i < kHalf / 32; ++i) {
-                    const int r = lane + 32 * i;
-                    const bool live = mr + r < p.M;
-                    cp_async4(sc + 4 * r, live ? p.xs + (size_t)(mr + r) * p.G + j : p.xs,
-                              live ? 4u : 0u);
-                }
-                if (lane < 2) {  // the tile's two weight blocks (the second may not exist)
-                    const int nb = n0 / kGroup + lane;
-                    cp_async4(sc + 4 * (kHalf + lane), nb < p.NB ? p.ws + (size_t)nb * p.G + j : p.ws,
-                              nb < p.NB ? 4u : 0u);
-                }
-                cp_async_arrive(smem_u32(sfull + s));
             }
+            // every load issued must have landed before the CTA exits: the leader
+            // sees both CTAs' (the other waits for it at the last cluster barrier)
+            if (rank == 0)
+                for (int i = c - kStages > 0 ? c - kStages : 0; i < c; ++i)
+                    if (!mbar_wait_drain(smem_u32(full + i % kStages), (i / kStages) & 1))
+                        atomicOr(p.status, kErrDrain);
         }
-        cp_async_wait_all();
-        // every load issued must have landed before the CTA exits: the leader
-        // sees both CTAs' (the other waits for it at the last cluster barrier)
-        if (rank == 0 && lane == 0)
-            for (int i = c - kStages > 0 ? c - kStages : 0; i < c; ++i)
-                if (!mbar_wait_drain(smem_u32(full + i % kStages), (i / kStages) & 1))
-                    atomicOr(p.status, kErrDrain);
     } else if (warp == kMmaWarp) {
         // ------------------------------------------------ products
-        if (rank == 0 && lane == 0) {
+        if (rank == 0) {
+            const uint32_t stages = uniform(smem_u32(smem));
+            const uint32_t bars = uniform(smem_u32(full));
+            const uint32_t tm = uniform(tmem);
             int c = 0;
             bool ok = true;
             while (ok && walk.next(p, t, j0, j1)) {
                 for (int j = j0; j < j1; ++j, ++c) {
                     const int s = c % kStages, d = c % kDBufs;
-                    if (!mbar_wait_cluster(smem_u32(full + s), (c / kStages) & 1, abort)) {
-                        fail(kErrStageWait);
+                    if (!mbar_wait_all(bars + 8 * s, (c / kStages) & 1, abort)) {
+                        if (lane == 0) fail(kErrStageWait);
                         ok = false;
                         break;
                     }
-                    if (c >= kDBufs && !mbar_wait_cluster(smem_u32(d_empty + d),
-                                                          ((c / kDBufs) - 1) & 1, abort)) {
-                        fail(kErrSumWait);
+                    if (c >= kDBufs && !mbar_wait_all(bars + 8 * (2 * kStages + kDBufs + d),
+                                                      ((c / kDBufs) - 1) & 1, abort)) {
+                        if (lane == 0) fail(kErrSumWait);
                         ok = false;
                         break;
                     }
                     tc_fence_after();
-                    const uint32_t st = smem_u32(smem + s * kStage);
-#pragma unroll
-                    for (int k = 0; k < kGroup / 32; ++k)
-                        mma_f8_ss_pair(tmem + d * kTileN, smem_desc_sw128(st + 32 * k),
-                                       smem_desc_sw128(st + kStageX + 32 * k), kIdesc, k > 0);
-                    mma_commit_pair(smem_u32(empty + s));
-                    mma_commit_pair(smem_u32(d_full + d));
+                    if (elect_one()) {
+                        const uint64_t a = smem_desc_sw128(stages + s * kStage);
+                        mma_f8_block_pair(tm + d * kTileN, a, a + (kStageX >> 4), kIdesc);
+                        mma_commit_pair(bars + 8 * (2 * kStages + d));
+                        mma_commit_pair(bars + 8 * (kStages + s));
+                    }
                 }
             }
             // the products issued complete before the tensor memory is freed
-            for (int i = c - kDBufs > 0 ? c - kDBufs : 0; i < c; ++i)
-                if (!mbar_wait_drain(smem_u32(d_full + i % kDBufs), (i / kDBufs) & 1))
-                    atomicOr(p.status, kErrDrain);
+            if (lane == 0)
+                for (int i = c - kDBufs > 0 ? c - kDBufs : 0; i < c; ++i)
+                    if (!mbar_wait_drain(smem_u32(d_full + i % kDBufs), (i / kDBufs) & 1))
+                        atomicOr(p.status, kErrDrain);
         }
+    }
     } else {
         // ------------------------------------------------ sums and outputs
+        regs_inc<kSumRegs>();
         grid_dependency_wait();
         const int quarter = warp & 3, half = warp >> 2;
         const int r = quarter * 32 + lane;  // token within the CTA's 128
         const uint32_t taddr = tmem + ((uint32_t)(quarter * 32) << 16) + half * kHalf;
         uint8_t *stage_out = sm_store + warp * kStoreBytes;
+        const uint32_t bar_full = smem_u32(d_full), bar_empty = map_to_rank(smem_u32(d_empty), 0);
         int c = 0;
         bool ok = true;
         while (ok && walk.next(p, t, j0, j1)) {
             tile_at(p, t, m0, n0);
             const int m = m0 + (int)rank * kHalf + r, nc = n0 + half * kHalf;
-            uint64_t acc[kHalf / 2];
+            float acc[kHalf];
 #pragma unroll
-            for (int i = 0; i < kHalf / 2; ++i) acc[i] = 0;
-            for (int j = j0; j < j1; ++j, ++c) {
-                const int s = c % kStages, d = c % kDBufs;
-                if (!__all_sync(0xffffffffu,
-                                mbar_wait(smem_u32(sfull + s), (c / kStages) & 1, abort) &&
-                                    mbar_wait_cluster(smem_u32(d_full + d), (c / kDBufs) & 1,
-                                                      abort))) {
-                    if (lane == 0) fail(kErrSumWait);
-                    ok = false;
-                    break;
+            for (int i = 0; i < kHalf; ++i) acc[i] = 0.f;
+            // the scales of four blocks at a time, loaded four blocks ahead (rows
+            // and columns past the end take the last one's: they are not stored)
+            const float *sx = p.xs + (size_t)min(m, p.M - 1) * p.G;
+            const float *sw = p.ws + (size_t)min(nc / kGroup, p.NB - 1) * p.G;
+            float nx[4], nw[4];
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                nx[u] = __ldg(sx + min(j0 + u, j1 - 1));
+                nw[u] = __ldg(sw + min(j0 + u, j1 - 1));
+            }
+            for (int j = j0; j < j1 && ok; j += 4) {
+                float sb[4];
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {
+                    sb[u] = nx[u] * nw[u];
+                    nx[u] = __ldg(sx + min(j + 4 + u, j1 - 1));
+                    nw[u] = __ldg(sw + min(j + 4 + u, j1 - 1));
                 }
-                tc_fence_after();
-                const float *sc = sm_scales + s * kScales;
-                const uint32_t sb = __float_as_uint(sc[r] * sc[kHalf + half]);
-                const uint64_t s2 = pack2(sb, sb);
 #pragma unroll
-                for (int q = 0; q < kHalf / 32; ++q) {
-                    uint32_t v[32];
-                    tmem_ld(taddr + d * kTileN + 32 * q, v);
-                    tmem_wait_ld(v);
-                    if (q == kHalf / 32 - 1) {  // all read: the tensor cores may write again
-                        tc_fence_before();
-                        __syncwarp();
-                        if (lane == 0) {
-                            mbar_arrive_cluster(map_to_rank(smem_u32(d_empty + d), 0));
-                            mbar_arrive(smem_u32(empty + s));
-                        }
+                for (int u = 0; u < 4; ++u) {
+                    if (j + u >= j1) break;
+                    const int d = c % kDBufs;
+                    if (!mbar_wait_all(bar_full + 8 * d, (c / kDBufs) & 1, abort)) {
+                        if (lane == 0) fail(kErrSumWait);
+                        ok = false;
+                        break;
                     }
+                    tc_fence_after();
 #pragma unroll
-                    for (int i = 0; i < 16; ++i)
-                        fma2(acc[16 * q + i], pack2(v[2 * i], v[2 * i + 1]), s2);
+                    for (int q = 0; q < kHalf / 32; ++q) {
+                        uint32_t v[32];
+                        tmem_ld(taddr + d * kTileN + 32 * q, v);
+                        tmem_wait_ld(v);
+                        if (q == kHalf / 32 - 1) {  // all read: the tensor cores may write again
+                            tc_fence_before();
+                            __syncwarp();
+                            if (lane == 0) mbar_arrive_remote(bar_empty + 8 * d);
+                        }
+#pragma unroll
+                        for (int i = 0; i < 32; ++i)
+                            acc[32 * q + i] = fmaf(__uint_as_float(v[i]), sb[u], acc[32 * q + i]);
+                    }
+                    ++c;
                 }
             }
             if (!ok) break;
@@ -338,12 +326,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
                 float *part = p.partials +
                               ((size_t)(2 * slot + rank) * kTileN + half * kHalf) * kHalf + r;
 #pragma unroll
-                for (int i = 0; i < kHalf / 2; ++i) {
-                    float lo, hi;
-                    unpack2(acc[i], lo, hi);
-                    part[(size_t)(2 * i) * kHalf] = lo;
-                    part[(size_t)(2 * i + 1) * kHalf] = hi;
-                }
+                for (int i = 0; i < kHalf; ++i) part[(size_t)i * kHalf] = acc[i];
                 __threadfence();
                 asm volatile("bar.sync 1, %0;" ::"r"(kSumWarps * 32) : "memory");
                 unsigned *counter = p.counters + 2 * (t - p.whole) + rank;
@@ -355,7 +338,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
                     __threadfence();
                     if (threadIdx.x == 0) *counter = 0u;  // ready for the next launch
 #pragma unroll
-                    for (int i = 0; i < kHalf / 2; ++i) acc[i] = 0;
+                    for (int i = 0; i < kHalf; ++i) acc[i] = 0.f;
                     for (int b = b0; b <= b1; ++b) {
                         const int sl = 2 * b + (walk.begin(p, b) > tile0 ? 0 : 1);
                         const float *src = p.partials +
@@ -368,12 +351,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
                             for (int i = 0; i < 32; ++i)
                                 v[i] = __ldcg(src + (size_t)(32 * q + i) * kHalf);
 #pragma unroll
-                            for (int i = 0; i < 16; ++i) {
-                                float lo, hi;
-                                unpack2(acc[16 * q + i], lo, hi);
-                                acc[16 * q + i] = pack2(__float_as_uint(lo + v[2 * i]),
-                                                        __float_as_uint(hi + v[2 * i + 1]));
-                            }
+                            for (int i = 0; i < 32; ++i) acc[32 * q + i] += v[i];
                         }
                     }
                 }
@@ -393,8 +371,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
                     for (int q = 0; q < 8; ++q) {  // 8 columns, 16 bytes
                         float v[8];
 #pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            unpack2(acc[h * 32 + q * 4 + i], v[2 * i], v[2 * i + 1]);
+                        for (int i = 0; i < 8; ++i) v[i] = acc[h * kStoreCols + q * 8 + i];
                         if (res && n + 8 * q < p.N) {  // N is a multiple of 8
                             const uint4 u = *reinterpret_cast<const uint4 *>(res + n + 8 * q);
                             const uint32_t w[4] = {u.x, u.y, u.z, u.w};
@@ -421,17 +398,13 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
                 }
             } else if (m < p.M) {
 #pragma unroll
-                for (int i = 0; i < kHalf / 2; ++i) {
-                    float v[2];
-                    unpack2(acc[i], v[0], v[1]);
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        const int n = nc + 2 * i + e;
-                        if (n < p.N) {
-                            const size_t o = (size_t)m * p.N + n;
-                            if (p.residual) v[e] += half_bits_to_float(p.residual[o], p.bf16);
-                            p.y[o] = float_to_half_bits(v[e], p.bf16);
-                        }
+                for (int i = 0; i < kHalf; ++i) {
+                    const int n = nc + i;
+                    if (n < p.N) {
+                        const size_t o = (size_t)m * p.N + n;
+                        float v = acc[i];
+                        if (p.residual) v += half_bits_to_float(p.residual[o], p.bf16);
+                        p.y[o] = float_to_half_bits(v, p.bf16);
                     }
                 }
             }
