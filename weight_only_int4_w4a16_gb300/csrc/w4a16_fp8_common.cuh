@@ -33,16 +33,17 @@ inline bool encode_fp8_rows(CUtensorMap *map, const void *base, int rows, int K,
                             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// 16-bit rows [rows, cols] (cols a multiple of 8, base 16-byte aligned) stored in
-// boxes of box_rows x box_cols, 128-byte swizzle; what a box has past the end is not stored
-inline bool encode_store16(CUtensorMap *map, void *base, int rows, int cols, int box_rows,
-                           int box_cols) {
+// 16-bit rows [rows, cols] (cols a multiple of 8, base 16-byte aligned) in boxes of
+// box_rows x box_cols, 128-byte swizzle; what a box has past the end is not stored
+// (and comes as zeros)
+inline bool encode_rows16(CUtensorMap *map, const void *base, int rows, int cols, int box_rows,
+                          int box_cols) {
     const EncodeTiledFn encode = tensor_map_encoder();
     const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
     const cuuint64_t strides[1] = {(cuuint64_t)cols * 2};
     const cuuint32_t box[2] = {(cuuint32_t)box_cols, (cuuint32_t)box_rows};
     const cuuint32_t estr[2] = {1, 1};
-    return encode && encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT16, 2, base, dims, strides, box, estr,
+    return encode && encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT16, 2, const_cast<void *>(base), dims, strides, box, estr,
                             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                             CU_TENSOR_MAP_L2_PROMOTION_NONE,
                             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;

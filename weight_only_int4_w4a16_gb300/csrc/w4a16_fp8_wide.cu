@@ -17,8 +17,9 @@
 //   of 256 columns fill the tensor memory: while the tensor cores run one, the
 //   other is read.
 //
-//   Outputs go through shared memory to TMA stores (rows of 64 columns), or
-//   straight from registers where N or y's address does not allow TMA.
+//   Outputs go through shared memory to TMA stores (boxes of 32 tokens x 64
+//   columns), where the residual was loaded by TMA before; where N or an address
+//   does not allow TMA, straight from registers.
 //
 //   Work: whole tiles in turn while every pair has one; what remains beyond the
 //   last full round (and that round with it) is cut into equal runs of blocks
@@ -43,7 +44,7 @@ constexpr int kTileM = 256, kTileN = 256;      // of a pair
 constexpr int kHalf = 128;                     // rows of x, and of w, per CTA
 constexpr int kStageX = kHalf * kGroup, kStageW = kHalf * kGroup;
 constexpr int kStage = kStageX + kStageW;      // 32 KB
-constexpr int kStages = 6;
+constexpr int kStages = 5;
 constexpr int kSumWarps = 8;
 constexpr int kTmaWarp = 8, kMmaWarp = 9;
 constexpr int kThreads = 384;                  // three warpgroups (warps 10 and 11 only fill the last)
@@ -53,10 +54,10 @@ static_assert(2 * kSumRegs + kOtherRegs <= 3 * 168, "the launch's registers");
 constexpr int kDBufs = 2;                      // block sums in tensor memory
 constexpr int kTmemCols = 512;
 constexpr int kStoreCols = 64;                 // columns per TMA store (a 128-byte row)
-constexpr int kStoreBytes = 32 * kStoreCols * 2;  // a warp's staging: 4 KB
+constexpr int kStoreBytes = 32 * kStoreCols * 2;  // 4 KB; a warp has two of them
 constexpr int kGroupM = 16;                    // token tiles that share a pass over the weights
-constexpr int kBarBytes = (2 * kStages + 2 * kDBufs) * 8 + 16;
-constexpr int kSmem = 1024 + kStages * kStage + kSumWarps * kStoreBytes + kBarBytes;
+constexpr int kBarBytes = (2 * kStages + 2 * kDBufs + kSumWarps) * 8 + 16;
+constexpr int kSmem = 1024 + kStages * kStage + 2 * kSumWarps * kStoreBytes + kBarBytes;
 constexpr uint32_t kIdesc =  // D f32, A and B e4m3 (0), N = 256, M = 256
     (1u << 4) | ((uint32_t)(kTileN >> 3) << 17) | ((uint32_t)(kTileM >> 4) << 24);
 
@@ -64,6 +65,7 @@ struct WideParams {
     CUtensorMap xmap;  // x: (K bytes, M rows), box {128, 128}, 128-byte swizzle
     CUtensorMap wmap;  // w: (K bytes, N rows), the same
     CUtensorMap ymap;  // y: (N, M) of 16 bits, box {64, 32}, 128-byte swizzle (tma_store)
+    CUtensorMap rmap;  // the residual, the same
     const float *xs, *ws;
     const uint16_t *residual;
     uint16_t *y;
@@ -74,7 +76,8 @@ struct WideParams {
     int tiles_m, tiles_n;
     int whole;           // tiles that pairs take whole, in turn
     long long split;     // blocks of the other tiles, cut into equal runs
-    int tma_store, bf16;
+    int tma_store;       // y (and the residual) can go by TMA
+    int scales16;        // four blocks' scales of a row are one aligned 16-byte load
 };
 
 // A pair's work, in order: segments (tile t, blocks [j0, j1)).
@@ -124,6 +127,32 @@ __device__ __forceinline__ void tile_at(const WideParams &p, int t, int &m0, int
     n0 = n * kTileN;
 }
 
+// a load that stays where it is written: the compiler may not move it to its use
+__device__ __forceinline__ float load_now(const float *p) {
+    float v;
+    asm volatile("ld.global.nc.f32 %0, [%1];" : "=f"(v) : "l"(p));
+    return v;
+}
+__device__ __forceinline__ float4 load4_now(const float *p) {  // 16-byte aligned
+    float4 v;
+    asm volatile("ld.global.nc.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                 : "l"(p));
+    return v;
+}
+
+template <bool kBf16>
+__device__ __forceinline__ uint32_t pack16(float lo, float hi) {  // one rounding each
+    if constexpr (kBf16) {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+        return *reinterpret_cast<const uint32_t *>(&h);
+    } else {
+        const __half2 h = __floats2half2_rn(lo, hi);
+        return *reinterpret_cast<const uint32_t *>(&h);
+    }
+}
+
+template <bool kBf16>
 __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
     fp8_wide_kernel(const __grid_constant__ WideParams p) {
     extern __shared__ uint8_t smem_raw[];
@@ -131,11 +160,12 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
     // the leader's addresses
     uint8_t *smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
     uint8_t *sm_store = smem + kStages * kStage;
-    uint64_t *full = reinterpret_cast<uint64_t *>(sm_store + kSumWarps * kStoreBytes);  // (leader)
+    uint64_t *full = reinterpret_cast<uint64_t *>(sm_store + 2 * kSumWarps * kStoreBytes);
     uint64_t *empty = full + kStages;      // this CTA's stage read
     uint64_t *d_full = empty + kStages;    // a block's sums ready
     uint64_t *d_empty = d_full + kDBufs;   // (leader) read by both CTAs
-    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(d_empty + kDBufs);
+    uint64_t *r_full = d_empty + kDBufs;   // [sum warp] its residual landed
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(r_full + kSumWarps);
     volatile int *abort = reinterpret_cast<volatile int *>(tmem_slot + 1);
     int *s_last = const_cast<int *>(abort + 1);
     const int warp = (int)uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
@@ -151,11 +181,13 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
             mbar_init(smem_u32(d_full + i), 1);
             mbar_init(smem_u32(d_empty + i), 2 * kSumWarps);
         }
+        for (int i = 0; i < kSumWarps; ++i) mbar_init(smem_u32(r_full + i), 1);
         *abort = 0;
         mbar_init_fence();
         prefetch_tensormap(&p.xmap);
         prefetch_tensormap(&p.wmap);
         if (p.tma_store) prefetch_tensormap(&p.ymap);
+        if (p.tma_store && p.residual) prefetch_tensormap(&p.rmap);
     }
     if (warp == 0) {
         asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
@@ -256,37 +288,63 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
         const int quarter = warp & 3, half = warp >> 2;
         const int r = quarter * 32 + lane;  // token within the CTA's 128
         const uint32_t taddr = tmem + ((uint32_t)(quarter * 32) << 16) + half * kHalf;
-        uint8_t *stage_out = sm_store + warp * kStoreBytes;
+        uint8_t *stage_out = sm_store + 2 * warp * kStoreBytes;
         const uint32_t bar_full = smem_u32(d_full), bar_empty = map_to_rank(smem_u32(d_empty), 0);
-        int c = 0;
-        bool ok = true;
-        while (ok && walk.next(p, t, j0, j1)) {
+        const uint32_t bar_res = smem_u32(r_full + warp);
+        uint32_t res_asked = 0, res_taken = 0;  // residual tiles
+        // the scales of four blocks 4 i .. 4 i + 3 at a time, loaded four blocks ahead
+        // (rows and columns past the end take the last one's: they are not stored)
+        const float *sx = nullptr, *sw = nullptr;
+        float4 nx, nw;
+        auto load_scales = [&](int j) {
+            if (j >= p.G) return;
+            if (p.scales16) {
+                nx = load4_now(sx + j);
+                nw = load4_now(sw + j);
+            } else {
+                const int a = min(j + 1, p.G - 1), b = min(j + 2, p.G - 1), d = min(j + 3, p.G - 1);
+                nx = make_float4(load_now(sx + j), load_now(sx + a), load_now(sx + b), load_now(sx + d));
+                nw = make_float4(load_now(sw + j), load_now(sw + a), load_now(sw + b), load_now(sw + d));
+            }
+        };
+        auto begin_tile = [&]() {
             tile_at(p, t, m0, n0);
-            const int m = m0 + (int)rank * kHalf + r, nc = n0 + half * kHalf;
+            sx = p.xs + (size_t)min(m0 + (int)rank * kHalf + r, p.M - 1) * p.G;
+            sw = p.ws + (size_t)min(n0 / kGroup + half, p.NB - 1) * p.G;
+            load_scales(j0 & ~3);
+        };
+        // the warp's 32 tokens x 128 columns of the residual, into its staging
+        auto ask_residual = [&](int n, int mw) {
+            if (lane == 0) {
+                tma_store_wait_read();  // the staging is free
+                mbar_arrive_expect_tx(bar_res, 2 * kStoreBytes);
+                tma_load_2d(smem_u32(stage_out), &p.rmap, n, mw, bar_res, policy_evict_first());
+                tma_load_2d(smem_u32(stage_out + kStoreBytes), &p.rmap, n + kStoreCols, mw, bar_res,
+                            policy_evict_first());
+            }
+            ++res_asked;
+        };
+        const bool staged_res = p.residual && p.tma_store;
+        int c = 0;
+        bool ok = true, more = walk.next(p, t, j0, j1);
+        if (more) begin_tile();
+        while (more) {
+            // this tile; the next one's place and first scales are fetched before
+            // this one's outputs are written
+            const int mw = m0 + (int)rank * kHalf + quarter * 32, m = mw + lane;
+            const int nc = n0 + half * kHalf, tt = t, end = j1;
+            const bool whole = j0 == 0 && j1 == p.G;
+            if (staged_res && whole) ask_residual(nc, mw);
             float acc[kHalf];
 #pragma unroll
             for (int i = 0; i < kHalf; ++i) acc[i] = 0.f;
-            // the scales of four blocks at a time, loaded four blocks ahead (rows
-            // and columns past the end take the last one's: they are not stored)
-            const float *sx = p.xs + (size_t)min(m, p.M - 1) * p.G;
-            const float *sw = p.ws + (size_t)min(nc / kGroup, p.NB - 1) * p.G;
-            float nx[4], nw[4];
-#pragma unroll
-            for (int u = 0; u < 4; ++u) {
-                nx[u] = __ldg(sx + min(j0 + u, j1 - 1));
-                nw[u] = __ldg(sw + min(j0 + u, j1 - 1));
-            }
-            for (int j = j0; j < j1 && ok; j += 4) {
-                float sb[4];
+            for (int j = j0 & ~3, begin = j0; j < end && ok; j += 4) {
+                const float sb[4] = {nx.x * nw.x, nx.y * nw.y, nx.z * nw.z, nx.w * nw.w};
+                if (j + 4 < end) load_scales(j + 4);
 #pragma unroll
                 for (int u = 0; u < 4; ++u) {
-                    sb[u] = nx[u] * nw[u];
-                    nx[u] = __ldg(sx + min(j + 4 + u, j1 - 1));
-                    nw[u] = __ldg(sw + min(j + 4 + u, j1 - 1));
-                }
-#pragma unroll
-                for (int u = 0; u < 4; ++u) {
-                    if (j + u >= j1) break;
+                    if (j + u < begin) continue;
+                    if (j + u >= end) break;
                     const int d = c % kDBufs;
                     if (!mbar_wait_all(bar_full + 8 * d, (c / kDBufs) & 1, abort)) {
                         if (lane == 0) fail(kErrSumWait);
@@ -312,16 +370,14 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
                 }
             }
             if (!ok) break;
-            const bool whole = j0 == 0 && j1 == p.G;
-            bool last = whole;
-            const long long tile0 = (long long)(t - p.whole) * p.G;
-            int b0 = 0, b1 = 0;
+            more = walk.next(p, t, j0, j1);
+            if (more) begin_tile();
             if (!whole) {
                 // part of a tile: the sums go to this pair's slot (0: the run
                 // begins inside the tile, 1: the tile begins inside the run);
                 // the last CTA of this half of the tokens adds them in K order
-                b0 = walk.owner(p, tile0);
-                b1 = walk.owner(p, tile0 + p.G - 1);
+                const long long tile0 = (long long)(tt - p.whole) * p.G;
+                const int b0 = walk.owner(p, tile0), b1 = walk.owner(p, tile0 + p.G - 1);
                 const int slot = 2 * walk.pair + (walk.begin(p, walk.pair) > tile0 ? 0 : 1);
                 float *part = p.partials +
                               ((size_t)(2 * slot + rank) * kTileN + half * kHalf) * kHalf + r;
@@ -329,14 +385,15 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
                 for (int i = 0; i < kHalf; ++i) part[(size_t)i * kHalf] = acc[i];
                 __threadfence();
                 asm volatile("bar.sync 1, %0;" ::"r"(kSumWarps * 32) : "memory");
-                unsigned *counter = p.counters + 2 * (t - p.whole) + rank;
+                unsigned *counter = p.counters + 2 * (tt - p.whole) + rank;
                 if (threadIdx.x == 0)
                     *s_last = atomicAdd(counter, 1u) == (unsigned)(b1 - b0) ? 1 : 0;
                 asm volatile("bar.sync 1, %0;" ::"r"(kSumWarps * 32) : "memory");
-                last = *s_last != 0;
+                const bool last = *s_last != 0;
                 if (last) {
                     __threadfence();
                     if (threadIdx.x == 0) *counter = 0u;  // ready for the next launch
+                    if (staged_res) ask_residual(nc, mw);
 #pragma unroll
                     for (int i = 0; i < kHalf; ++i) acc[i] = 0.f;
                     for (int b = b0; b <= b1; ++b) {
@@ -357,44 +414,46 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
                 }
                 // s_last is written again only after every thread has read it
                 asm volatile("bar.sync 1, %0;" ::"r"(kSumWarps * 32) : "memory");
+                if (!last) continue;
             }
-            if (!last) continue;
             // y[m][nc .. nc + 127] = sums (+ residual), one rounding each
             if (p.tma_store) {
-                const uint16_t *res = p.residual && m < p.M ? p.residual + (size_t)m * p.N : nullptr;
+                if (staged_res) {
+                    if (!mbar_wait_all(bar_res, res_taken & 1, abort)) {
+                        if (lane == 0) fail(kErrStageWait);
+                        break;
+                    }
+                    ++res_taken;
+                } else {
+                    if (lane == 0) tma_store_wait_read();  // the staging is free
+                    __syncwarp();
+                }
 #pragma unroll
                 for (int h = 0; h < kHalf / kStoreCols; ++h) {
-                    const int n = nc + h * kStoreCols;
-                    tma_store_wait_read();  // (lane 0) the staging is free
-                    __syncwarp();
+                    uint8_t *row = stage_out + h * kStoreBytes + lane * 128;
 #pragma unroll
-                    for (int q = 0; q < 8; ++q) {  // 8 columns, 16 bytes
+                    for (int q = 0; q < 8; ++q) {  // 8 columns, 16 bytes, at the swizzled chunk
+                        uint4 *at = reinterpret_cast<uint4 *>(row + ((q ^ (lane & 7)) << 4));
                         float v[8];
 #pragma unroll
                         for (int i = 0; i < 8; ++i) v[i] = acc[h * kStoreCols + q * 8 + i];
-                        if (res && n + 8 * q < p.N) {  // N is a multiple of 8
-                            const uint4 u = *reinterpret_cast<const uint4 *>(res + n + 8 * q);
+                        if (staged_res) {
+                            const uint4 u = *at;
                             const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
                             for (int i = 0; i < 4; ++i) {
-                                v[2 * i] += half_bits_to_float((uint16_t)w[i], p.bf16);
-                                v[2 * i + 1] += half_bits_to_float((uint16_t)(w[i] >> 16), p.bf16);
+                                v[2 * i] += half_bits_to_float((uint16_t)w[i], kBf16);
+                                v[2 * i + 1] += half_bits_to_float((uint16_t)(w[i] >> 16), kBf16);
                             }
                         }
-                        uint32_t o[4];
-#pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            o[i] = (uint32_t)float_to_half_bits(v[2 * i], p.bf16) |
-                                   (uint32_t)float_to_half_bits(v[2 * i + 1], p.bf16) << 16;
-                        // 128-byte swizzle: chunk q of row `lane`
-                        *reinterpret_cast<uint4 *>(stage_out + lane * 128 + ((q ^ (lane & 7)) << 4)) =
-                            make_uint4(o[0], o[1], o[2], o[3]);
+                        *at = make_uint4(pack16<kBf16>(v[0], v[1]), pack16<kBf16>(v[2], v[3]),
+                                         pack16<kBf16>(v[4], v[5]), pack16<kBf16>(v[6], v[7]));
                     }
                     fence_async_shared();
                     __syncwarp();
-                    const int mw = m0 + (int)rank * kHalf + quarter * 32;
+                    const int n = nc + h * kStoreCols;
                     if (lane == 0 && n < p.N && mw < p.M)
-                        tma_store_2d(&p.ymap, n, mw, smem_u32(stage_out));
+                        tma_store_2d(&p.ymap, n, mw, smem_u32(stage_out + h * kStoreBytes));
                 }
             } else if (m < p.M) {
 #pragma unroll
@@ -403,12 +462,15 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
                     if (n < p.N) {
                         const size_t o = (size_t)m * p.N + n;
                         float v = acc[i];
-                        if (p.residual) v += half_bits_to_float(p.residual[o], p.bf16);
-                        p.y[o] = float_to_half_bits(v, p.bf16);
+                        if (p.residual) v += half_bits_to_float(p.residual[o], kBf16);
+                        p.y[o] = float_to_half_bits(v, kBf16);
                     }
                 }
             }
         }
+        // what was asked for lands, what was stored is written, before the exit
+        if (res_asked != res_taken && lane == 0 && !mbar_wait_drain(bar_res, res_taken & 1))
+            atomicOr(p.status, kErrDrain);
         tma_store_wait();
     }
 
@@ -459,7 +521,8 @@ cudaError_t launch_fp8_wide(const Fp8Args &a, const Fp8WidePlan &plan, const Wor
         !encode_fp8_rows(&p.wmap, a.w, a.N, a.K, kHalf))
         return cudaErrorInvalidValue;
     p.tma_store = a.N % 8 == 0 && ((uintptr_t)a.y & 15) == 0 && ((uintptr_t)a.residual & 15) == 0;
-    if (p.tma_store && !encode_store16(&p.ymap, a.y, a.M, a.N, 32, kStoreCols))
+    if (p.tma_store && (!encode_rows16(&p.ymap, a.y, a.M, a.N, 32, kStoreCols) ||
+                        (a.residual && !encode_rows16(&p.rmap, a.residual, a.M, a.N, 32, kStoreCols))))
         return cudaErrorInvalidValue;
     p.xs = a.xs;
     p.ws = a.ws;
@@ -474,9 +537,9 @@ cudaError_t launch_fp8_wide(const Fp8Args &a, const Fp8WidePlan &plan, const Wor
     p.NB = (a.N + kGroup - 1) / kGroup;
     p.tiles_m = plan.tiles_m;
     p.tiles_n = plan.tiles_n;
+    p.scales16 = plan.G % 4 == 0 && ((uintptr_t)a.xs & 15) == 0 && ((uintptr_t)a.ws & 15) == 0;
     p.whole = plan.whole;
     p.split = plan.split;
-    p.bf16 = a.bf16;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(2 * plan.pairs);
     cfg.blockDim = dim3(kThreads);
@@ -487,11 +550,15 @@ cudaError_t launch_fp8_wide(const Fp8Args &a, const Fp8WidePlan &plan, const Wor
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, fp8_wide_kernel, p);
+    return a.bf16 ? cudaLaunchKernelEx(&cfg, fp8_wide_kernel<true>, p)
+                  : cudaLaunchKernelEx(&cfg, fp8_wide_kernel<false>, p);
 }
 
 cudaError_t fp8_wide_init(const DeviceInfo &) {
-    return cudaFuncSetAttribute((const void *)fp8_wide_kernel,
+    const cudaError_t e = cudaFuncSetAttribute(
+        (const void *)fp8_wide_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+    if (e != cudaSuccess) return e;
+    return cudaFuncSetAttribute((const void *)fp8_wide_kernel<true>,
                                 cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
 }
 
