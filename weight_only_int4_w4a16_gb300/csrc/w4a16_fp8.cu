@@ -16,14 +16,17 @@
 //   instruction, four instructions per block.  A partial last block is filled
 //   with zeros by TMA.
 //
-//   Roles (one CTA per SM, 192 threads): warps 0..3 (thread = weight row) scale
-//   and add the blocks and write y; warp 4 streams a block of weights and of x
-//   per stage by TMA (128-byte swizzled, K-major), its lanes copy the block's
-//   scales next to them; warp 5 issues the products.
+//   Roles (one CTA per SM, 192 threads): warp 4 streams two blocks of weights and
+//   of x per stage by TMA (128-byte swizzled, K-major; 256 consecutive bytes of each
+//   weight row), its lanes copy the blocks' scales next to them; warp 5 issues the
+//   products; warps 0..3 (thread = weight row) scale and add the blocks and write y.
 //
-//   Work: the (tile, block) sequence is cut into equal runs, one per CTA
-//   ("stream-K"); a tile split between CTAs is summed by the last of them in K
-//   order, so results do not depend on which CTA came last.
+//   Work: few tiles (a small N) are split along K between the CTAs of a cluster,
+//   which exchange their sums through distributed shared memory.  Otherwise the
+//   (tile, block) sequence is cut into equal runs, one per CTA ("stream-K"), and a
+//   tile split between CTAs is summed by the last of them from global memory.
+//   Either way the pieces are added in K order: results do not depend on which CTA
+//   came last.
 //
 // Every mbarrier wait is bounded; on expiry the kernel records an error code in
 // the device status word, drains what it has in flight, frees its tensor memory
@@ -40,15 +43,13 @@ namespace {
 using namespace dev;
 
 constexpr int kTileN = 128;                   // weight rows per tile (MMA M)
-constexpr int kStageW = kTileN * kGroup;      // 16 KB of weights per block
-constexpr int kEpiWarps = 4;
-constexpr int kTmaWarp = 4;
-constexpr int kMmaWarp = 5;
-constexpr int kThreads = 192;
-constexpr int kMaxStages = 12;
-constexpr int kSmemBudget = 216 * 1024;       // the stages
-constexpr int kDBufs = 4;                     // block sums in tensor memory
+constexpr int kSub = 2;                       // blocks per stage
+constexpr int kBlockW = kTileN * kGroup;      // 16 KB of weights per block
+constexpr int kMaxStages = 6;
+constexpr int kSmemBudget = 220 * 1024;       // the stages
+constexpr int kDBufs = 2;                     // stages' sums in tensor memory
 constexpr int kTmemCols = 512;
+constexpr int kMaxCluster = 8;
 
 struct Fp8Params {
     CUtensorMap wmap;  // w: (K bytes, N rows), box {128, 128}, 128-byte swizzle
@@ -64,15 +65,24 @@ struct Fp8Params {
     long long total;     // blocks of all tiles
     int tiles;
     int streamk;
+    int ksplit;          // CTAs of a cluster that split each tile along K (1: none)
     int stages;
     int bf16;
 };
 
 template <int T>
 struct Cfg {
-    static constexpr int kStageX = T * kGroup;
-    static constexpr int kStage = kStageW + kStageX;
-    static constexpr int kScales = T + 4;  // floats per stage: T of x, then the weight block's
+    // warps that add the sums: a quarter of the rows each, and from 32 tokens on
+    // half of the tokens (one quarter's four warps alone fall behind the loads: at
+    // 64 tokens 0.36 us a block against 0.30)
+    static constexpr int kSumWarps = T >= 32 ? 8 : 4;
+    static constexpr int kCols = T / (kSumWarps / 4);  // tokens per thread
+    static constexpr int kTmaWarp = kSumWarps, kMmaWarp = kSumWarps + 1;
+    static constexpr int kThreads = (kSumWarps + 2) * 32;
+    static constexpr int kBlockX = T * kGroup;
+    static constexpr int kStage = kSub * (kBlockW + kBlockX);  // weights, then x
+    // floats per stage: per block T scales of x, then per block the weights'
+    static constexpr int kScales = kSub * T + 4;
     static constexpr uint32_t kIdesc =     // D f32, A and B e4m3 (0), N = T, M = 128
         (1u << 4) | ((uint32_t)(T >> 3) << 17) | ((uint32_t)(kTileN >> 4) << 24);
     static int stages() {
@@ -90,7 +100,12 @@ struct Cfg {
 struct Walk {
     long long pos, end;
     __device__ __forceinline__ Walk(const Fp8Params &p) {
-        if (p.streamk) {
+        if (p.ksplit > 1) {  // the CTA's part of its cluster's tile
+            const int r = blockIdx.x % p.ksplit;
+            const long long t0 = (long long)(blockIdx.x / p.ksplit) * p.G;
+            pos = t0 + r * p.G / p.ksplit;
+            end = t0 + (r + 1) * p.G / p.ksplit;
+        } else if (p.streamk) {
             pos = begin(p, blockIdx.x);
             end = begin(p, blockIdx.x + 1);
         } else {
@@ -111,7 +126,7 @@ struct Walk {
         t = (int)(pos / p.G);
         const long long t0 = (long long)t * p.G;
         j0 = (int)(pos - t0);
-        if (p.streamk) {
+        if (p.streamk || p.ksplit > 1) {
             j1 = (int)((t0 + p.G < end ? t0 + p.G : end) - t0);
             pos = t0 + j1;
         } else {
@@ -143,8 +158,45 @@ __device__ __forceinline__ void store16(const Fp8Params &p, int m0, int n, const
         if (m0 + i < p.M) p.y[(size_t)(m0 + i) * p.N + n] = float_to_half_bits(v[i] + r[i], p.bf16);
 }
 
+// four rows' residual of token m (zeros without one, or past N), and their outputs;
+// vec: rows in fours and 8-byte aligned
+__device__ __forceinline__ float4 residual4(const Fp8Params &p, int m, int n, bool vec) {
+    float r[4] = {0.f, 0.f, 0.f, 0.f};
+    if (p.residual) {
+        const uint16_t *src = p.residual + (size_t)m * p.N + n;
+        if (vec) {
+            if (n < p.N) {
+                const uint2 u = *reinterpret_cast<const uint2 *>(src);
+                r[0] = half_bits_to_float((uint16_t)u.x, p.bf16);
+                r[1] = half_bits_to_float((uint16_t)(u.x >> 16), p.bf16);
+                r[2] = half_bits_to_float((uint16_t)u.y, p.bf16);
+                r[3] = half_bits_to_float((uint16_t)(u.y >> 16), p.bf16);
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (n + i < p.N) r[i] = half_bits_to_float(src[i], p.bf16);
+        }
+    }
+    return make_float4(r[0], r[1], r[2], r[3]);
+}
+__device__ __forceinline__ void store4(const Fp8Params &p, int m, int n, bool vec, float4 v) {
+    const uint16_t h[4] = {float_to_half_bits(v.x, p.bf16), float_to_half_bits(v.y, p.bf16),
+                           float_to_half_bits(v.z, p.bf16), float_to_half_bits(v.w, p.bf16)};
+    uint16_t *dst = p.y + (size_t)m * p.N + n;
+    if (vec) {
+        if (n < p.N)
+            *reinterpret_cast<uint2 *>(dst) =
+                make_uint2((uint32_t)h[0] | (uint32_t)h[1] << 16, (uint32_t)h[2] | (uint32_t)h[3] << 16);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (n + i < p.N) dst[i] = h[i];
+    }
+}
+
 template <int T>
-__global__ void __launch_bounds__(kThreads, 1) fp8_kernel(const __grid_constant__ Fp8Params p) {
+__global__ void __launch_bounds__(Cfg<T>::kThreads, 1) fp8_kernel(const __grid_constant__ Fp8Params p) {
     using C = Cfg<T>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
@@ -160,14 +212,14 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_kernel(const __grid_constant_
     const int warp = (int)uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
 
     grid_dependents_launch();
-    if (threadIdx.x == kTmaWarp * 32) {
+    if (threadIdx.x == C::kTmaWarp * 32) {
         for (int i = 0; i < NS; ++i) {
             mbar_init(smem_u32(full + i), 1 + 32);          // the TMA bytes, each lane's scales
-            mbar_init(smem_u32(empty + i), 1 + kEpiWarps);  // the products, each reader of the scales
+            mbar_init(smem_u32(empty + i), 1 + C::kSumWarps);  // the products, each reader of the scales
         }
         for (int i = 0; i < kDBufs; ++i) {
             mbar_init(smem_u32(d_full + i), 1);
-            mbar_init(smem_u32(d_empty + i), kEpiWarps);
+            mbar_init(smem_u32(d_empty + i), C::kSumWarps);
         }
         *abort = 0;
         mbar_init_fence();
@@ -185,6 +237,7 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_kernel(const __grid_constant_
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
+    float *sums = reinterpret_cast<float *>(smem);  // [T][128], once the stages are done
     auto fail = [&](int code) {
         *abort = 1;
         atomicOr(p.status, code);
@@ -192,18 +245,17 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_kernel(const __grid_constant_
 
     Walk walk(p);
     int t, j0, j1;
-    if (warp == kTmaWarp) {
+    if (warp == C::kTmaWarp) {
         // ------------------------------------------------ producer
         grid_dependency_wait();
         const uint64_t pol_w = policy_evict_first(), pol_x = policy_evict_last();
-        int c = 0;
+        int c = 0;  // stages
         bool ok = true;
         while (ok && walk.next(p, t, j0, j1)) {
             const int nt = t / p.tiles_m, m0 = (t - nt * p.tiles_m) * T;
-            for (int j = j0; j < j1; ++j, ++c) {
-                const int s = c % NS;
-                if (c >= NS && !__all_sync(0xffffffffu, mbar_wait(smem_u32(empty + s),
-                                                                  ((c / NS) - 1) & 1, abort))) {
+            for (int j = j0; j < j1; j += kSub, ++c) {
+                const int s = c % NS, nb = min(kSub, j1 - j);
+                if (c >= NS && !mbar_wait_all(smem_u32(empty + s), ((c / NS) - 1) & 1, abort)) {
                     if (lane == 0) fail(kErrSlotWait);
                     ok = false;
                     break;
@@ -211,20 +263,27 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_kernel(const __grid_constant_
                 const uint32_t bar = smem_u32(full + s);
                 if (lane == 0) {
                     const uint32_t st = smem_u32(smem + (size_t)s * C::kStage);
-                    mbar_arrive_expect_tx(bar, C::kStage);
-                    tma_load_2d(st, &p.wmap, j * kGroup, nt * kTileN, bar, pol_w);
-                    tma_load_2d(st + kStageW, &p.xmap, j * kGroup, m0, bar, pol_x);
+                    mbar_arrive_expect_tx(bar, nb * (kBlockW + C::kBlockX));
+                    for (int b = 0; b < nb; ++b)
+                        tma_load_2d(st + b * kBlockW, &p.wmap, (j + b) * kGroup, nt * kTileN, bar,
+                                    pol_w);
+                    for (int b = 0; b < nb; ++b)
+                        tma_load_2d(st + kSub * kBlockW + b * C::kBlockX, &p.xmap, (j + b) * kGroup,
+                                    m0, bar, pol_x);
                 }
                 const uint32_t sc = smem_u32(sm_scales + s * C::kScales);
 #pragma unroll
                 for (int i = 0; i < (T + 31) / 32; ++i) {
                     const int tt = lane + 32 * i;
                     const bool live = tt < T && m0 + tt < p.M;
-                    if (tt < T)
-                        cp_async4(sc + 4 * tt, live ? p.xs + (size_t)(m0 + tt) * p.G + j : p.xs,
-                                  live ? 4u : 0u);
+                    const float *src = live ? p.xs + (size_t)(m0 + tt) * p.G + j : p.xs;
+#pragma unroll
+                    for (int b = 0; b < kSub; ++b)
+                        if (tt < T)
+                            cp_async4(sc + 4 * (b * T + tt), live && b < nb ? src + b : p.xs,
+                                      live && b < nb ? 4u : 0u);
                 }
-                if (lane == 0) cp_async4(sc + 4 * T, p.ws + (size_t)nt * p.G + j, 4u);
+                if (lane < nb) cp_async4(sc + 4 * (kSub * T + lane), p.ws + (size_t)nt * p.G + j + lane, 4u);
                 cp_async_arrive(bar);
             }
         }
@@ -234,15 +293,15 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_kernel(const __grid_constant_
                 if (!mbar_wait_drain(smem_u32(full + i % NS), (i / NS) & 1))
                     atomicOr(p.status, kErrDrain);
         cp_async_wait_all();
-    } else if (warp == kMmaWarp) {
+    } else if (warp == C::kMmaWarp) {
         // ------------------------------------------------ products
         const uint32_t stages = uniform(smem_u32(smem)), bars = uniform(smem_u32(full));
         const uint32_t tm = uniform(tmem);
         int c = 0;
         bool ok = true;
         while (ok && walk.next(p, t, j0, j1)) {
-            for (int j = j0; j < j1; ++j, ++c) {
-                const int s = c % NS, d = c % kDBufs;
+            for (int j = j0; j < j1; j += kSub, ++c) {
+                const int s = c % NS, d = c % kDBufs, nb = min(kSub, j1 - j);
                 if (!mbar_wait_all(bars + 8 * s, (c / NS) & 1, abort)) {
                     if (lane == 0) fail(kErrStageWait);
                     ok = false;
@@ -256,8 +315,12 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_kernel(const __grid_constant_
                 }
                 tc_fence_after();
                 if (elect_one()) {
-                    const uint64_t a = smem_desc_sw128(stages + s * C::kStage);
-                    mma_f8_block(tm + d * T, a, a + (kStageW >> 4), C::kIdesc);
+                    const uint32_t st = stages + s * C::kStage;
+                    const uint64_t a = smem_desc_sw128(st), b = smem_desc_sw128(st + kSub * kBlockW);
+                    mma_f8_block(tm + d * kSub * T, a, b, C::kIdesc);
+                    if (nb > 1)
+                        mma_f8_block(tm + (d * kSub + 1) * T, a + (kBlockW >> 4),
+                                     b + (C::kBlockX >> 4), C::kIdesc);
                     mma_commit(bars + 8 * (2 * kMaxStages + d));
                     mma_commit(bars + 8 * (kMaxStages + s));
                 }
@@ -271,44 +334,52 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_kernel(const __grid_constant_
     } else {
         // ------------------------------------------------ sums and outputs
         grid_dependency_wait();
-        const int r = warp * 32 + lane;  // row within the tile
-        const uint32_t lanes = (uint32_t)(warp * 32) << 16;
+        constexpr int kCols = C::kCols;
+        const int r = (warp & 3) * 32 + lane;   // row within the tile
+        const int cb = (warp >> 2) * kCols;     // first token within the tile
+        const uint32_t taddr = tmem + ((uint32_t)((warp & 3) * 32) << 16) + cb;
         int c = 0;
         bool ok = true;
         while (ok && walk.next(p, t, j0, j1)) {
-            const int nt = t / p.tiles_m, m0 = (t - nt * p.tiles_m) * T;
-            const int n = nt * kTileN + r;
-            float acc[T];
+            const int nt = t / p.tiles_m, m0 = (t - nt * p.tiles_m) * T + cb;
+            const int n = nt * kTileN + r, mt = p.M - m0;  // this thread's tokens: i < mt
+            float acc[kCols];
 #pragma unroll
-            for (int i = 0; i < T; ++i) acc[i] = 0.f;
-            for (int j = j0; j < j1; ++j, ++c) {
+            for (int i = 0; i < kCols; ++i) acc[i] = 0.f;
+            for (int j = j0; j < j1; j += kSub, ++c) {
                 const int s = c % NS, d = c % kDBufs;
-                // the stage's barrier shows its scales, the sum's its products
-                if (!__all_sync(0xffffffffu,
-                                mbar_wait(smem_u32(full + s), (c / NS) & 1, abort) &&
-                                    mbar_wait(smem_u32(d_full + d), (c / kDBufs) & 1, abort))) {
+                // the stage's barrier shows its scales, the sums' its products
+                if (!mbar_wait_all(smem_u32(full + s), (c / NS) & 1, abort) ||
+                    !mbar_wait_all(smem_u32(d_full + d), (c / kDBufs) & 1, abort)) {
                     if (lane == 0) fail(kErrSumWait);
                     ok = false;
                     break;
                 }
                 tc_fence_after();
                 const float *sc = sm_scales + s * C::kScales;
-                const float sw = sc[T];
 #pragma unroll
-                for (int i0 = 0; i0 < T; i0 += 16) {
-                    uint32_t u[16];
-                    float v[16];
-                    tmem_ld(tmem + lanes + d * T + i0, u);
-                    tmem_wait_ld(u);
+                for (int b = 0; b < kSub; ++b) {
+                    if (j + b >= j1) break;
+                    const float sw = sc[kSub * T + b];
+                    constexpr int kLoad = kCols < 32 ? kCols : 32;
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(u[i]);
+                    for (int i0 = 0; i0 < kCols; i0 += kLoad) {
+                        uint32_t u[kLoad];
+                        tmem_ld(taddr + (d * kSub + b) * T + i0, u);
+                        float f[kLoad];
 #pragma unroll
-                    for (int i = 0; i < 16; i += 4) {
-                        const float4 sx = *reinterpret_cast<const float4 *>(sc + i0 + i);
-                        acc[i0 + i] = fmaf(v[i], sx.x * sw, acc[i0 + i]);
-                        acc[i0 + i + 1] = fmaf(v[i + 1], sx.y * sw, acc[i0 + i + 1]);
-                        acc[i0 + i + 2] = fmaf(v[i + 2], sx.z * sw, acc[i0 + i + 2]);
-                        acc[i0 + i + 3] = fmaf(v[i + 3], sx.w * sw, acc[i0 + i + 3]);
+                        for (int i = 0; i < kLoad; i += 4) {
+                            const float4 sx =
+                                *reinterpret_cast<const float4 *>(sc + b * T + cb + i0 + i);
+                            f[i] = sx.x * sw;
+                            f[i + 1] = sx.y * sw;
+                            f[i + 2] = sx.z * sw;
+                            f[i + 3] = sx.w * sw;
+                        }
+                        tmem_wait_ld(u);
+#pragma unroll
+                        for (int i = 0; i < kLoad; ++i)
+                            acc[i0 + i] = fmaf(__uint_as_float(u[i]), f[i], acc[i0 + i]);
                     }
                 }
                 tc_fence_before();
@@ -322,47 +393,103 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_kernel(const __grid_constant_
             if (j0 == 0 && j1 == p.G) {  // a whole tile
                 if (n < p.N) {
 #pragma unroll
-                    for (int i = 0; i < T; i += 16) store16(p, m0 + i, n, acc + i);
+                    for (int i = 0; i < kCols; i += 16) store16(p, m0 + i, n, acc + i);
                 }
                 continue;
+            }
+            if (p.ksplit > 1) {
+                // the cluster's tile: the sums wait in this CTA's stages, which
+                // nothing uses any more, for the exchange below
+#pragma unroll
+                for (int i = 0; i < kCols; ++i)
+                    if (i < mt) sums[(cb + i) * kTileN + r] = acc[i];
+                break;
             }
             // part of a tile: the sums go to this CTA's slot, and the last CTA
             // of the tile adds the slots in K order
             const long long tile0 = (long long)t * p.G;
-            float *part = p.partials + (size_t)slot_of(p, blockIdx.x, tile0) * T * kTileN + r;
-            const int mt = min(T, p.M - m0);
+            const size_t mine = (size_t)cb * kTileN + r;
+            float *part = p.partials + (size_t)slot_of(p, blockIdx.x, tile0) * T * kTileN + mine;
 #pragma unroll
-            for (int i = 0; i < T; ++i)
+            for (int i = 0; i < kCols; ++i)
                 if (i < mt) part[(size_t)i * kTileN] = acc[i];
             __threadfence();
-            asm volatile("bar.sync 1, %0;" ::"r"(kEpiWarps * 32) : "memory");
+            asm volatile("bar.sync 1, %0;" ::"r"(C::kSumWarps * 32) : "memory");
             const int b0 = Walk::owner(p, tile0), b1 = Walk::owner(p, tile0 + p.G - 1);
             if (threadIdx.x == 0)
                 *s_last = atomicAdd(p.counters + t, 1u) == (unsigned)(b1 - b0) ? 1 : 0;
-            asm volatile("bar.sync 1, %0;" ::"r"(kEpiWarps * 32) : "memory");
+            asm volatile("bar.sync 1, %0;" ::"r"(C::kSumWarps * 32) : "memory");
             if (*s_last) {
                 __threadfence();
-                for (int i0 = 0; i0 < mt; i0 += 16) {
-                    float sum[16];
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) sum[i] = 0.f;
-                    for (int b = b0; b <= b1; ++b) {
-                        const float *src = p.partials +
-                                           ((size_t)slot_of(p, b, tile0) * T + i0) * kTileN + r;
-                        float v[16];
-#pragma unroll
-                        for (int i = 0; i < 16; ++i)
-                            v[i] = i0 + i < mt ? __ldcg(src + (size_t)i * kTileN) : 0.f;
-#pragma unroll
-                        for (int i = 0; i < 16; ++i) sum[i] += v[i];
-                    }
-                    if (n < p.N) store16(p, m0 + i0, n, sum);
-                }
                 if (threadIdx.x == 0) p.counters[t] = 0u;  // ready for the next launch
+                // a piece's loads all at once: a round trip per piece
+#pragma unroll
+                for (int i = 0; i < kCols; ++i) acc[i] = 0.f;
+                for (int b = b0; b <= b1; ++b) {
+                    const float *src = p.partials + (size_t)slot_of(p, b, tile0) * T * kTileN + mine;
+                    float v[kCols];
+#pragma unroll
+                    for (int i = 0; i < kCols; ++i)
+                        v[i] = i < mt ? __ldcg(src + (size_t)i * kTileN) : 0.f;
+#pragma unroll
+                    for (int i = 0; i < kCols; ++i) acc[i] += v[i];
+                }
+                if (n < p.N) {
+#pragma unroll
+                    for (int i = 0; i < kCols; i += 16) store16(p, m0 + i, n, acc + i);
+                }
             }
             // s_last is written again only after every thread has read it
-            asm volatile("bar.sync 1, %0;" ::"r"(kEpiWarps * 32) : "memory");
+            asm volatile("bar.sync 1, %0;" ::"r"(C::kSumWarps * 32) : "memory");
         }
+    }
+    if (p.ksplit > 1) {
+        // the exchange: CTA r of the cluster takes every ksplit-th token of the tile,
+        // adds the CTAs' sums in K order (which is rank order) and writes y; a warp
+        // takes a token's 128 rows, four per lane, and four tokens at a time
+        __syncthreads();
+        cluster_sync();
+        if (!*abort) {
+            const int S = p.ksplit, tile = blockIdx.x / S;
+            const int nt = tile / p.tiles_m, m0 = (tile - nt * p.tiles_m) * T;
+            const int n = nt * kTileN + 4 * lane, mt = min(T, p.M - m0);
+            const bool vec = p.N % 4 == 0 && ((uintptr_t)p.y & 7) == 0 &&
+                             ((uintptr_t)p.residual & 7) == 0;
+            const uint32_t mine = smem_u32(sums + 4 * lane);
+            constexpr int kBatch = 4, kWarps = C::kSumWarps + 2;
+            for (int i0 = cluster_rank() + S * warp; i0 < mt; i0 += kBatch * kWarps * S) {
+                float4 v[kBatch][kMaxCluster], res[kBatch];
+#pragma unroll
+                for (int i = 0; i < kBatch; ++i) {
+                    const int m = i0 + i * kWarps * S;
+                    res[i] = m < mt ? residual4(p, m0 + m, n, vec) : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+                    for (int q = 0; q < kMaxCluster; ++q)
+                        if (q < S && m < mt)
+                            v[i][q] = ld4_cluster(map_to_rank(mine, q) + (uint32_t)(m * kTileN * 4));
+                }
+#pragma unroll
+                for (int i = 0; i < kBatch; ++i) {
+                    const int m = i0 + i * kWarps * S;
+                    if (m >= mt) break;
+                    float4 sum = v[i][0];
+#pragma unroll
+                    for (int q = 1; q < kMaxCluster; ++q)
+                        if (q < S) {
+                            sum.x += v[i][q].x;
+                            sum.y += v[i][q].y;
+                            sum.z += v[i][q].z;
+                            sum.w += v[i][q].w;
+                        }
+                    store4(p, m0 + m, n, vec, make_float4(sum.x + res[i].x, sum.y + res[i].y,
+                                                          sum.z + res[i].z, sum.w + res[i].w));
+                }
+            }
+        }
+        // no CTA leaves while another reads its sums: the arrival comes after the
+        // stores of what was read, and orders execution only
+        cluster_arrive_relaxed();
+        cluster_wait();
     }
 
     tc_fence_before();
@@ -379,19 +506,31 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_kernel(const __grid_constant_
 // host side
 // ---------------------------------------------------------------------------
 template <int T>
-cudaError_t launch_t(const Fp8Params &p, int grid, cudaStream_t stream) {
-    cudaLaunchConfig_t cfg = {};
+void config_t(cudaLaunchConfig_t &cfg, cudaLaunchAttribute (&attr)[2], int grid, int ksplit,
+              int stages, cudaStream_t stream) {
+    cfg = {};
     cfg.gridDim = dim3(grid);
-    cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = Cfg<T>::smem(p.stages);
+    cfg.blockDim = dim3(Cfg<T>::kThreads);
+    cfg.dynamicSmemBytes = Cfg<T>::smem(stages);
     cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim = {(unsigned)ksplit, 1, 1};
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = ksplit > 1 ? 2 : 1;
+}
+
+template <int T>
+cudaError_t launch_t(const Fp8Params &p, int grid, cudaStream_t stream) {
+    cudaLaunchConfig_t cfg;
+    cudaLaunchAttribute attr[2];
+    config_t<T>(cfg, attr, grid, p.ksplit, p.stages, stream);
     return cudaLaunchKernelEx(&cfg, fp8_kernel<T>, p);
 }
+
+// clusters of k CTAs that run at the same time, found once per process
+int g_clusters[kMaxCluster + 1];
 
 int stages_of(int T) {
     switch (T) {
@@ -410,24 +549,26 @@ Fp8Plan plan_fp8(int M, int N, int K, const DeviceInfo &dev, const Workspace &ws
     pl.G = (K + kGroup - 1) / kGroup;
     pl.tiles_m = (M + pl.T - 1) / pl.T;
     pl.tiles = (long long)pl.tiles_m * ((N + kTileN - 1) / kTileN);
-    const long long total = pl.tiles * pl.G;
-    // whole tiles when they fill the last wave; else equal runs of blocks, of
-    // at least four blocks each
-    const long long waves = (pl.tiles + dev.sm_count - 1) / dev.sm_count;
-    pl.streamk = pl.tiles * 100 < waves * dev.sm_count * 95;
-    pl.grid = (int)(pl.tiles < dev.sm_count ? pl.tiles : dev.sm_count);
-    if (pl.streamk) {
-        long long g = total / 4 < dev.sm_count ? total / 4 : dev.sm_count;
-        if (g > pl.grid) pl.grid = (int)g;
-        pl.ws_bytes = (size_t)2 * pl.grid * pl.T * kTileN * sizeof(float);
-        if (pl.grid == pl.tiles || pl.ws_bytes > ws.partial_bytes ||
-            pl.tiles > ws.n_counters - kMmaSchedWords) {
-            pl.streamk = false;
-            pl.ws_bytes = 0;
-            pl.grid = (int)(pl.tiles < dev.sm_count ? pl.tiles : dev.sm_count);
-        }
-    }
     pl.stages = stages_of(pl.T);
+    pl.ksplit = 1;
+    pl.grid = (int)(pl.tiles < dev.sm_count ? pl.tiles : dev.sm_count);
+    // few tiles: the largest cluster that keeps every tile in one wave, with at
+    // least two blocks of K per CTA
+    for (int k = kMaxCluster; k > 1; --k)
+        if (pl.tiles <= g_clusters[k] && pl.G >= 2 * k) {
+            pl.ksplit = k;
+            pl.grid = (int)pl.tiles * k;
+            return pl;
+        }
+    // whole tiles when they fill the last wave, else equal runs of blocks
+    const long long waves = (pl.tiles + dev.sm_count - 1) / dev.sm_count;
+    const size_t need = (size_t)2 * dev.sm_count * pl.T * kTileN * sizeof(float);
+    if (pl.tiles * 100 < waves * dev.sm_count * 95 && pl.tiles * pl.G >= 4ll * dev.sm_count &&
+        need <= ws.partial_bytes && pl.tiles <= ws.n_counters - kMmaSchedWords) {
+        pl.streamk = true;
+        pl.grid = dev.sm_count;
+        pl.ws_bytes = need;
+    }
     return pl;
 }
 
@@ -451,6 +592,7 @@ cudaError_t launch_fp8(const Fp8Args &a, const Fp8Plan &plan, const Workspace &w
     p.tiles = (int)plan.tiles;
     p.total = plan.tiles * plan.G;
     p.streamk = plan.streamk;
+    p.ksplit = plan.ksplit;
     p.stages = plan.stages;
     p.bf16 = a.bf16;
     switch (plan.T) {
@@ -471,6 +613,16 @@ cudaError_t fp8_init(const DeviceInfo &) {
     for (const auto &k : fns) {
         cudaError_t e =
             cudaFuncSetAttribute(k.f, cudaFuncAttributeMaxDynamicSharedMemorySize, k.smem);
+        if (e != cudaSuccess) return e;
+    }
+    // one CTA per SM whatever T, so one kernel answers for all
+    for (int k = 2; k <= kMaxCluster; ++k) {
+        cudaLaunchConfig_t cfg;
+        cudaLaunchAttribute attr[2];
+        config_t<64>(cfg, attr, k, k, Cfg<64>::stages(), nullptr);
+        attr[0] = attr[1];
+        cfg.numAttrs = 1;
+        const cudaError_t e = cudaOccupancyMaxActiveClusters(&g_clusters[k], fp8_kernel<64>, &cfg);
         if (e != cudaSuccess) return e;
     }
     return cudaSuccess;

@@ -291,6 +291,7 @@ struct Fp8Plan {
     int G;             // blocks of 128 along K
     int tiles_m;       // token tiles
     long long tiles;   // all tiles
+    int ksplit;        // CTAs of a cluster that split each tile along K (1: none)
     bool streamk;      // CTAs take equal runs of (tile, block) work, not whole tiles
     int grid;
     int stages;
