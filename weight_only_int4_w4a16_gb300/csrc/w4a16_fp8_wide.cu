@@ -13,22 +13,25 @@
 //   Roles (384 threads per CTA): warps 0..7 (lane = token, warp / 4 = half of the
 //   256 columns) scale and add the blocks' sums and write y (the scales come from
 //   global memory into registers, four blocks ahead); warp 8 streams the CTA's 128
-//   rows of x and its 128 rows of w per block by TMA; warp 9 of the leading CTA issues the pair's products.  Two block sums
-//   of 256 columns fill the tensor memory: while the tensor cores run one, the
-//   other is read.
+//   rows of x and its 128 rows of w per block by TMA; warp 9 of the leading CTA
+//   issues the pair's products.  Two block sums of 256 columns fill the tensor
+//   memory: while the tensor cores run one, the other is read.
 //
 //   Outputs go through shared memory to TMA stores (boxes of 32 tokens x 64
 //   columns), where the residual was loaded by TMA before; where N or an address
 //   does not allow TMA, straight from registers.
 //
-//   Work: whole tiles in turn while every pair has one; what remains beyond the
-//   last full round (and that round with it) is cut into equal runs of blocks
-//   ("stream-K"), so that no pair waits; a tile that is split is summed in K
-//   order by its last pair.
+//   Work: few tiles are split along K between the pairs of a cluster, which exchange
+//   their sums through distributed shared memory.  Otherwise whole tiles in turn
+//   while every pair has one; what remains beyond the last full round (and that
+//   round with it) is cut into equal runs of blocks ("stream-K"), so that no pair
+//   waits.  A run is then at least as long as a tile, so a tile has at most two
+//   pieces, and the pair that comes last adds the other's: the order of two terms
+//   does not change their sum.
 //
-// Every mbarrier wait is bounded, as in w4a16_fp8.cu.  The two cluster barriers
-// (after the setup, before the exit) are reached by every thread: all that comes
-// before them is bounded.
+// Every mbarrier wait is bounded, as in w4a16_fp8.cu.  The cluster barriers
+// (after the setup, before the exchange, before the exit) are reached by every
+// thread: all that comes before them is bounded.
 #include <cstring>
 
 #include "w4a16_fp8_common.cuh"
@@ -53,6 +56,7 @@ constexpr int kSumRegs = 216, kOtherRegs = 72;
 static_assert(2 * kSumRegs + kOtherRegs <= 3 * 168, "the launch's registers");
 constexpr int kDBufs = 2;                      // block sums in tensor memory
 constexpr int kTmemCols = 512;
+constexpr int kMaxSplit = 4;                   // pairs of a cluster
 constexpr int kStoreCols = 64;                 // columns per TMA store (a 128-byte row)
 constexpr int kStoreBytes = 32 * kStoreCols * 2;  // 4 KB; a warp has two of them
 constexpr int kGroupM = 16;                    // token tiles that share a pass over the weights
@@ -70,12 +74,13 @@ struct WideParams {
     const uint16_t *residual;
     uint16_t *y;
     float *partials;     // [2 * pairs][2 CTAs][256 columns][128 tokens] fp32
-    unsigned *counters;  // [tiles], zero between launches
+    unsigned *counters;  // [split tiles][2 CTAs], zero between launches
     int *status;
     int M, N, G, NB;
     int tiles_m, tiles_n;
     int whole;           // tiles that pairs take whole, in turn
     long long split;     // blocks of the other tiles, cut into equal runs
+    int ksplit;          // pairs of a cluster that split each tile along K (1: none)
     int tma_store;       // y (and the residual) can go by TMA
     int scales16;        // four blocks' scales of a row are one aligned 16-byte load
 };
@@ -86,9 +91,17 @@ struct Walk {
     long long pos, end;
     __device__ __forceinline__ Walk(const WideParams &p)
         : pairs(gridDim.x / 2), pair(blockIdx.x / 2) {
-        tile = pair;
-        pos = begin(p, pair);
-        end = begin(p, pair + 1);
+        if (p.ksplit > 1) {  // the pair's part of its cluster's tile
+            tile = p.whole;
+            const int i = pair % p.ksplit;
+            pos = (long long)(pair / p.ksplit) * p.G;
+            end = pos + (i + 1) * p.G / p.ksplit;
+            pos += i * p.G / p.ksplit;
+        } else {
+            tile = pair;
+            pos = begin(p, pair);
+            end = begin(p, pair + 1);
+        }
     }
     __device__ __forceinline__ long long begin(const WideParams &p, int b) const {
         return (long long)b * p.split / pairs;
@@ -152,8 +165,49 @@ __device__ __forceinline__ uint32_t pack16(float lo, float hi) {  // one roundin
     }
 }
 
+// y[m][n .. n + 15]: the sums at `sums` (16 columns, kHalf apart) of every CTA of
+// this rank in the cluster's pairs, in K order, + residual, one rounding each
 template <bool kBf16>
-__global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
+__device__ __forceinline__ void exchange16(const WideParams &p, const float *sums, uint32_t rank,
+                                           int m, int n) {
+    float v[kMaxSplit][16];
+#pragma unroll
+    for (int q = 0; q < kMaxSplit; ++q)
+        if (q < p.ksplit) {
+            const uint32_t from = map_to_rank(smem_u32(sums), 2 * q + rank);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) v[q][i] = ld_cluster(from + i * kHalf * 4);
+        }
+    const size_t o = (size_t)m * p.N + n;
+    float res[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+        res[i] = p.residual && m < p.M && n + i < p.N ? half_bits_to_float(p.residual[o + i], kBf16)
+                                                      : 0.f;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+#pragma unroll
+        for (int q = 1; q < kMaxSplit; ++q)
+            if (q < p.ksplit) v[0][i] += v[q][i];
+        v[0][i] += res[i];
+    }
+    if (m >= p.M) return;
+    if (p.tma_store) {  // what allows TMA allows 16-byte stores
+#pragma unroll
+        for (int i = 0; i < 16; i += 8)
+            if (n + i < p.N)
+                *reinterpret_cast<uint4 *>(p.y + o + i) = make_uint4(
+                    pack16<kBf16>(v[0][i], v[0][i + 1]), pack16<kBf16>(v[0][i + 2], v[0][i + 3]),
+                    pack16<kBf16>(v[0][i + 4], v[0][i + 5]), pack16<kBf16>(v[0][i + 6], v[0][i + 7]));
+    } else {
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+            if (n + i < p.N) p.y[o + i] = float_to_half_bits(v[0][i], kBf16);
+    }
+}
+
+template <bool kBf16>
+__global__ void __launch_bounds__(kThreads, 1)
     fp8_wide_kernel(const __grid_constant__ WideParams p) {
     extern __shared__ uint8_t smem_raw[];
     // the same offsets in both CTAs: the products read both shared memories at
@@ -169,7 +223,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
     volatile int *abort = reinterpret_cast<volatile int *>(tmem_slot + 1);
     int *s_last = const_cast<int *>(abort + 1);
     const int warp = (int)uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
-    const uint32_t rank = cluster_rank();
+    const uint32_t crank = cluster_rank(), rank = crank & 1, leader = crank & ~1u;
 
     grid_dependents_launch();
     if (threadIdx.x == kTmaWarp * 32) {
@@ -201,6 +255,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
     cluster_sync();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
+    float *sums = reinterpret_cast<float *>(smem);  // [256 columns][128 tokens], after the stages
     auto fail = [&](int code) {
         *abort = 1;
         atomicOr(p.status, code);
@@ -230,7 +285,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
                     }
                     const uint32_t st = smem_u32(smem + s * kStage);
                     // both CTAs' bytes count at the leader's barrier
-                    const uint32_t bar = map_to_rank(smem_u32(full + s), 0);
+                    const uint32_t bar = map_to_rank(smem_u32(full + s), leader);
                     if (rank == 0) mbar_arrive_expect_tx(smem_u32(full + s), 2 * kStage);
                     tma_load_2d_pair(st, &p.xmap, j * kGroup, mr, bar, pol_x);
                     tma_load_2d_pair(st + kStageX, &p.wmap, j * kGroup, nr, bar, pol_w);
@@ -249,6 +304,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
             const uint32_t stages = uniform(smem_u32(smem));
             const uint32_t bars = uniform(smem_u32(full));
             const uint32_t tm = uniform(tmem);
+            const uint16_t both = (uint16_t)(3u << leader);
             int c = 0;
             bool ok = true;
             while (ok && walk.next(p, t, j0, j1)) {
@@ -269,8 +325,8 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
                     if (elect_one()) {
                         const uint64_t a = smem_desc_sw128(stages + s * kStage);
                         mma_f8_block_pair(tm + d * kTileN, a, a + (kStageX >> 4), kIdesc);
-                        mma_commit_pair(bars + 8 * (2 * kStages + d));
-                        mma_commit_pair(bars + 8 * (kStages + s));
+                        mma_commit_pair(bars + 8 * (2 * kStages + d), both);
+                        mma_commit_pair(bars + 8 * (kStages + s), both);
                     }
                 }
             }
@@ -281,6 +337,8 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
                         atomicOr(p.status, kErrDrain);
         }
     }
+    __syncwarp();
+    if (p.ksplit > 1) cluster_sync();  // with the sum warps', before the exchange
     } else {
         // ------------------------------------------------ sums and outputs
         regs_inc<kSumRegs>();
@@ -289,7 +347,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
         const int r = quarter * 32 + lane;  // token within the CTA's 128
         const uint32_t taddr = tmem + ((uint32_t)(quarter * 32) << 16) + half * kHalf;
         uint8_t *stage_out = sm_store + 2 * warp * kStoreBytes;
-        const uint32_t bar_full = smem_u32(d_full), bar_empty = map_to_rank(smem_u32(d_empty), 0);
+        const uint32_t bar_full = smem_u32(d_full), bar_empty = map_to_rank(smem_u32(d_empty), leader);
         const uint32_t bar_res = smem_u32(r_full + warp);
         uint32_t res_asked = 0, res_taken = 0;  // residual tiles
         // the scales of four blocks 4 i .. 4 i + 3 at a time, loaded four blocks ahead
@@ -372,10 +430,17 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
             if (!ok) break;
             more = walk.next(p, t, j0, j1);
             if (more) begin_tile();
+            if (p.ksplit > 1) {
+                // the cluster's tile: the sums wait in this CTA's stages, which
+                // nothing uses any more, for the exchange below
+#pragma unroll
+                for (int i = 0; i < kHalf; ++i) sums[(half * kHalf + i) * kHalf + r] = acc[i];
+                break;
+            }
             if (!whole) {
                 // part of a tile: the sums go to this pair's slot (0: the run
-                // begins inside the tile, 1: the tile begins inside the run);
-                // the last CTA of this half of the tokens adds them in K order
+                // begins inside the tile, 1: the tile begins inside the run); the
+                // CTA that comes last of the two adds the other's to its own
                 const long long tile0 = (long long)(tt - p.whole) * p.G;
                 const int b0 = walk.owner(p, tile0), b1 = walk.owner(p, tile0 + p.G - 1);
                 const int slot = 2 * walk.pair + (walk.begin(p, walk.pair) > tile0 ? 0 : 1);
@@ -387,29 +452,25 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
                 asm volatile("bar.sync 1, %0;" ::"r"(kSumWarps * 32) : "memory");
                 unsigned *counter = p.counters + 2 * (tt - p.whole) + rank;
                 if (threadIdx.x == 0)
-                    *s_last = atomicAdd(counter, 1u) == (unsigned)(b1 - b0) ? 1 : 0;
+                    *s_last = atomicAdd(counter, 1u) == 1u ? 1 : 0;
                 asm volatile("bar.sync 1, %0;" ::"r"(kSumWarps * 32) : "memory");
                 const bool last = *s_last != 0;
                 if (last) {
                     __threadfence();
                     if (threadIdx.x == 0) *counter = 0u;  // ready for the next launch
                     if (staged_res) ask_residual(nc, mw);
+                    const int b = walk.pair == b0 ? b1 : b0;
+                    const int sl = 2 * b + (walk.begin(p, b) > tile0 ? 0 : 1);
+                    const float *src =
+                        p.partials + ((size_t)(2 * sl + rank) * kTileN + half * kHalf) * kHalf + r;
 #pragma unroll
-                    for (int i = 0; i < kHalf; ++i) acc[i] = 0.f;
-                    for (int b = b0; b <= b1; ++b) {
-                        const int sl = 2 * b + (walk.begin(p, b) > tile0 ? 0 : 1);
-                        const float *src = p.partials +
-                                           ((size_t)(2 * sl + rank) * kTileN + half * kHalf) * kHalf +
-                                           r;
+                    for (int q = 0; q < 2; ++q) {  // a round trip each
+                        float v[64];
 #pragma unroll
-                        for (int q = 0; q < 4; ++q) {
-                            float v[32];
+                        for (int i = 0; i < 64; ++i)
+                            v[i] = __ldcg(src + (size_t)(64 * q + i) * kHalf);
 #pragma unroll
-                            for (int i = 0; i < 32; ++i)
-                                v[i] = __ldcg(src + (size_t)(32 * q + i) * kHalf);
-#pragma unroll
-                            for (int i = 0; i < 32; ++i) acc[32 * q + i] += v[i];
-                        }
+                        for (int i = 0; i < 64; ++i) acc[64 * q + i] += v[i];
                     }
                 }
                 // s_last is written again only after every thread has read it
@@ -472,11 +533,33 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
         if (res_asked != res_taken && lane == 0 && !mbar_wait_drain(bar_res, res_taken & 1))
             atomicOr(p.status, kErrDrain);
         tma_store_wait();
+        __syncwarp();
+        if (p.ksplit > 1) {
+            // the exchange: the cluster's CTAs of these 128 tokens share out the tile's
+            // 16 groups of 16 columns; a warp takes a group for 32 tokens (lane =
+            // token), adds the CTAs' sums in K order (which is rank order) and writes
+            // y.  It stays with these warps: the others keep few registers.
+            cluster_sync();
+            if (!*abort) {
+                const int S = p.ksplit;
+                tile_at(p, blockIdx.x / (2 * S), m0, n0);
+                for (int u = warp; u < 64; u += kSumWarps) {
+                    const int qu = u & 3, g = (u >> 2) * S + (int)(crank >> 1);
+                    const int m = m0 + (int)rank * kHalf + qu * 32 + lane, n = n0 + 16 * g;
+                    if (g >= 16 || n >= p.N) break;
+                    exchange16<kBf16>(p, sums + 16 * g * kHalf + qu * 32 + lane, rank, m, n);
+                }
+            }
+            __syncwarp();
+        }
     }
 
     tc_fence_before();
     __syncthreads();
-    cluster_sync();  // neither CTA's shared or tensor memory goes while the pair uses it
+    // No CTA's shared or tensor memory goes while another uses it.  What was read of
+    // the others' has been used by now; the barrier orders execution only.
+    cluster_arrive_relaxed();
+    cluster_wait();
     if (warp == 0) {
         tc_fence_after();
         asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem),
@@ -484,6 +567,24 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
                      : "memory");
     }
 }
+
+void config(cudaLaunchConfig_t &cfg, cudaLaunchAttribute (&attr)[2], int pairs, int ksplit,
+            cudaStream_t stream) {
+    cfg = {};
+    cfg.gridDim = dim3(2 * pairs);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = kSmem;
+    cfg.stream = stream;
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim = {2u * ksplit, 1, 1};
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+}
+
+// clusters of k pairs that run at the same time, found once per process
+int g_clusters[kMaxSplit + 1];
 
 }  // namespace
 
@@ -496,18 +597,23 @@ Fp8WidePlan plan_fp8_wide(int M, int N, int K, const DeviceInfo &dev, const Work
     const int pairs = dev.sm_count / 2;
     pl.pairs = (int)(tiles < pairs ? tiles : pairs);
     pl.whole = (int)tiles;
+    pl.ksplit = 1;
+    // few tiles: the largest cluster that keeps every tile in one wave, with at
+    // least four blocks of K per pair
+    for (int k = kMaxSplit; k > 1; --k)
+        if (tiles <= g_clusters[k] && pl.G >= 4 * k) {
+            pl.ksplit = k;
+            pl.pairs = (int)tiles * k;
+            pl.whole = 0;
+            return pl;
+        }
     const long long rest = tiles % pairs;
-    if (rest == 0 || rest * 100 >= (long long)pairs * 90) return pl;
-    // an unfinished last round: it and the full round before it are cut into
-    // equal runs (each longer than half a tile, so that a tile has few pieces)
-    const long long split = tiles < pairs ? tiles : pairs + rest;
-    long long runs = pairs;
-    if (tiles < pairs && split * pl.G < runs * 4)
-        runs = split * pl.G / 4;  // at least four blocks each
-    const size_t need = (size_t)2 * runs * 2 * kTileN * kHalf * sizeof(float);
-    if (tiles < pairs && runs <= tiles) return pl;
-    if (need > ws.partial_bytes || 2 * split > ws.n_counters - kMmaSchedWords) return pl;
-    pl.pairs = (int)runs;
+    if (tiles < pairs || rest == 0 || rest * 100 >= (long long)pairs * 90) return pl;
+    // an unfinished last round: it and the full round before it are cut into equal runs
+    const long long split = pairs + rest;
+    if ((size_t)2 * pairs * 2 * kTileN * kHalf * sizeof(float) > ws.partial_bytes ||
+        2 * split > ws.n_counters - kMmaSchedWords)
+        return pl;
     pl.whole = (int)(tiles - split);
     pl.split = split * pl.G;
     return pl;
@@ -539,27 +645,29 @@ cudaError_t launch_fp8_wide(const Fp8Args &a, const Fp8WidePlan &plan, const Wor
     p.tiles_n = plan.tiles_n;
     p.scales16 = plan.G % 4 == 0 && ((uintptr_t)a.xs & 15) == 0 && ((uintptr_t)a.ws & 15) == 0;
     p.whole = plan.whole;
+    p.ksplit = plan.ksplit;
     p.split = plan.split;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(2 * plan.pairs);
-    cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = kSmem;
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    cudaLaunchConfig_t cfg;
+    cudaLaunchAttribute attr[2];
+    config(cfg, attr, plan.pairs, plan.ksplit, stream);
     return a.bf16 ? cudaLaunchKernelEx(&cfg, fp8_wide_kernel<true>, p)
                   : cudaLaunchKernelEx(&cfg, fp8_wide_kernel<false>, p);
 }
 
 cudaError_t fp8_wide_init(const DeviceInfo &) {
-    const cudaError_t e = cudaFuncSetAttribute(
+    cudaError_t e = cudaFuncSetAttribute(
         (const void *)fp8_wide_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
     if (e != cudaSuccess) return e;
-    return cudaFuncSetAttribute((const void *)fp8_wide_kernel<true>,
-                                cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+    e = cudaFuncSetAttribute((const void *)fp8_wide_kernel<true>,
+                             cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+    for (int k = 2; k <= kMaxSplit && e == cudaSuccess; ++k) {
+        cudaLaunchConfig_t cfg;
+        cudaLaunchAttribute attr[2];
+        config(cfg, attr, k, k, nullptr);
+        cfg.numAttrs = 1;
+        e = cudaOccupancyMaxActiveClusters(&g_clusters[k], fp8_wide_kernel<true>, &cfg);
+    }
+    return e;
 }
 
 }  // namespace w4a16

@@ -306,6 +306,7 @@ cudaError_t fp8_init(const DeviceInfo &dev);
 struct Fp8WidePlan {
     int G, tiles_m, tiles_n;
     int pairs;        // CTA pairs of the launch
+    int ksplit;       // pairs of a cluster that split each tile along K (1: none)
     int whole;        // tiles that pairs take whole, in turn
     long long split;  // blocks of the remaining tiles, cut into equal runs
 };

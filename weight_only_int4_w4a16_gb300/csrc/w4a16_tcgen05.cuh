@@ -236,7 +236,13 @@ __device__ __forceinline__ uint32_t map_to_rank(uint32_t addr, uint32_t rank) {
     asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(d) : "r"(addr), "r"(rank));
     return d;
 }
-// 16 bytes of a CTA's shared memory in the cluster (a shared::cluster address)
+// a value, or 16 bytes, of a CTA's shared memory in the cluster (a shared::cluster
+// address)
+__device__ __forceinline__ float ld_cluster(uint32_t addr) {
+    float v;
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+    return v;
+}
 __device__ __forceinline__ float4 ld4_cluster(uint32_t addr) {
     float4 v;
     asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
@@ -279,13 +285,13 @@ __device__ __forceinline__ void mma_f8_block_pair(uint32_t d_tmem, uint64_t a_de
         "l"(a_desc), "l"(b_desc), "r"(idesc)
         : "memory");
 }
-// one arrival at the barrier of this offset in both CTAs once this thread's
-// earlier products are done
-__device__ __forceinline__ void mma_commit_pair(uint32_t bar) {
+// one arrival at the barrier of this offset in the cluster's CTAs of the mask (the
+// pair's two) once this thread's earlier products are done
+__device__ __forceinline__ void mma_commit_pair(uint32_t bar, uint16_t mask) {
     asm volatile(
         "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64"
         " [%0], %1;" ::"r"(bar),
-        "h"((uint16_t)3)
+        "h"(mask)
         : "memory");
 }
 
