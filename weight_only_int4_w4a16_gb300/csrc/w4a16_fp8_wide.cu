@@ -11,11 +11,12 @@
 // multiply-add per element.
 //
 //   Roles (384 threads per CTA): warps 0..7 (lane = token, warp / 4 = half of the
-//   256 columns) scale and add the blocks' sums and write y (the scales come from
-//   global memory into registers, four blocks ahead); warp 8 streams the CTA's 128
-//   rows of x and its 128 rows of w per block by TMA; warp 9 of the leading CTA
-//   issues the pair's products.  Two block sums of 256 columns fill the tensor
-//   memory: while the tensor cores run one, the other is read.
+//   256 columns) scale and add the blocks' sums and write y; warp 8 streams the
+//   CTA's 128 rows of x and its 128 rows of w per block by TMA; warp 9 of the
+//   leading CTA issues the pair's products; warps 10 and 11 bring the scales of four
+//   blocks at a time to shared memory (loaded by the sum warps themselves, their
+//   latency held up the tensor-memory loads).  Two block sums of 256 columns fill the
+//   tensor memory: while the tensor cores run one, the other is read.
 //
 //   Outputs go through shared memory to TMA stores (boxes of 32 tokens x 64
 //   columns), where the residual was loaded by TMA before; where N or an address
@@ -47,10 +48,12 @@ constexpr int kTileM = 256, kTileN = 256;      // of a pair
 constexpr int kHalf = 128;                     // rows of x, and of w, per CTA
 constexpr int kStageX = kHalf * kGroup, kStageW = kHalf * kGroup;
 constexpr int kStage = kStageX + kStageW;      // 32 KB
-constexpr int kStages = 5;
+constexpr int kStages = 4;
 constexpr int kSumWarps = 8;
-constexpr int kTmaWarp = 8, kMmaWarp = 9;
-constexpr int kThreads = 384;                  // three warpgroups (warps 10 and 11 only fill the last)
+constexpr int kTmaWarp = 8, kMmaWarp = 9;       // 10 and 11 load scales
+constexpr int kScaleSlots = 3;                 // batches of four blocks' scales
+constexpr int kScaleSlot = kHalf * 16 + 32;    // the tokens' four each, then the two weight blocks'
+constexpr int kThreads = 384;                  // three warpgroups
 // registers per thread: the launch's 168 x 384 split between the warpgroups
 constexpr int kSumRegs = 216, kOtherRegs = 72;
 static_assert(2 * kSumRegs + kOtherRegs <= 3 * 168, "the launch's registers");
@@ -60,8 +63,9 @@ constexpr int kMaxSplit = 4;                   // pairs of a cluster
 constexpr int kStoreCols = 64;                 // columns per TMA store (a 128-byte row)
 constexpr int kStoreBytes = 32 * kStoreCols * 2;  // 4 KB; a warp has two of them
 constexpr int kGroupM = 16;                    // token tiles that share a pass over the weights
-constexpr int kBarBytes = (2 * kStages + 2 * kDBufs + kSumWarps) * 8 + 16;
-constexpr int kSmem = 1024 + kStages * kStage + 2 * kSumWarps * kStoreBytes + kBarBytes;
+constexpr int kBarBytes = (2 * kStages + 2 * kDBufs + kSumWarps + 2 * kScaleSlots) * 8 + 16;
+constexpr int kSmem = 1024 + kStages * kStage + 2 * kSumWarps * kStoreBytes +
+                      kScaleSlots * kScaleSlot + kBarBytes;
 constexpr uint32_t kIdesc =  // D f32, A and B e4m3 (0), N = 256, M = 256
     (1u << 4) | ((uint32_t)(kTileN >> 3) << 17) | ((uint32_t)(kTileM >> 4) << 24);
 
@@ -140,18 +144,12 @@ __device__ __forceinline__ void tile_at(const WideParams &p, int t, int &m0, int
     n0 = n * kTileN;
 }
 
-// a load that stays where it is written: the compiler may not move it to its use
-__device__ __forceinline__ float load_now(const float *p) {
-    float v;
-    asm volatile("ld.global.nc.f32 %0, [%1];" : "=f"(v) : "l"(p));
-    return v;
-}
-__device__ __forceinline__ float4 load4_now(const float *p) {  // 16-byte aligned
-    float4 v;
-    asm volatile("ld.global.nc.v4.f32 {%0, %1, %2, %3}, [%4];"
-                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
-                 : "l"(p));
-    return v;
+// a row's scales of blocks j .. j + 3 (those past the end are not used)
+__device__ __forceinline__ float4 load4(const WideParams &p, const float *row, int j) {
+    if (p.scales16) return __ldg(reinterpret_cast<const float4 *>(row + j));
+    const int e = p.G - 1;
+    return make_float4(__ldg(row + j), __ldg(row + min(j + 1, e)), __ldg(row + min(j + 2, e)),
+                       __ldg(row + min(j + 3, e)));
 }
 
 template <bool kBf16>
@@ -206,6 +204,13 @@ __device__ __forceinline__ void exchange16(const WideParams &p, const float *sum
     }
 }
 
+// acc[i] += v[i] * s for i in [a, b)
+template <int a, int b>
+__device__ __forceinline__ void add_columns(float *acc, const uint32_t (&v)[32], float s) {
+#pragma unroll
+    for (int i = a; i < b; ++i) acc[i] = fmaf(__uint_as_float(v[i]), s, acc[i]);
+}
+
 template <bool kBf16>
 __global__ void __launch_bounds__(kThreads, 1)
     fp8_wide_kernel(const __grid_constant__ WideParams p) {
@@ -214,12 +219,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     // the leader's addresses
     uint8_t *smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
     uint8_t *sm_store = smem + kStages * kStage;
-    uint64_t *full = reinterpret_cast<uint64_t *>(sm_store + 2 * kSumWarps * kStoreBytes);
+    uint8_t *sm_scales = sm_store + 2 * kSumWarps * kStoreBytes;
+    uint64_t *full = reinterpret_cast<uint64_t *>(sm_scales + kScaleSlots * kScaleSlot);
     uint64_t *empty = full + kStages;      // this CTA's stage read
     uint64_t *d_full = empty + kStages;    // a block's sums ready
     uint64_t *d_empty = d_full + kDBufs;   // (leader) read by both CTAs
     uint64_t *r_full = d_empty + kDBufs;   // [sum warp] its residual landed
-    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(r_full + kSumWarps);
+    uint64_t *sc_full = r_full + kSumWarps;  // [scale slot]
+    uint64_t *sc_empty = sc_full + kScaleSlots;
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(sc_empty + kScaleSlots);
     volatile int *abort = reinterpret_cast<volatile int *>(tmem_slot + 1);
     int *s_last = const_cast<int *>(abort + 1);
     const int warp = (int)uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
@@ -236,6 +244,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(smem_u32(d_empty + i), 2 * kSumWarps);
         }
         for (int i = 0; i < kSumWarps; ++i) mbar_init(smem_u32(r_full + i), 1);
+        for (int i = 0; i < kScaleSlots; ++i) {
+            mbar_init(smem_u32(sc_full + i), 64);
+            mbar_init(smem_u32(sc_empty + i), kSumWarps);
+        }
         *abort = 0;
         mbar_init_fence();
         prefetch_tensormap(&p.xmap);
@@ -336,6 +348,37 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (!mbar_wait_drain(smem_u32(d_full + i % kDBufs), (i / kDBufs) & 1))
                         atomicOr(p.status, kErrDrain);
         }
+    } else if (warp > kMmaWarp) {
+        // ------------------------------------------------ scales
+        // (rows and columns past the end take the last one's: they are not stored)
+        grid_dependency_wait();
+        const int i = (warp - kMmaWarp - 1) * 32 + lane;  // tokens i and i + 64
+        int c = 0;                                        // batches
+        bool ok = true;
+        while (ok && walk.next(p, t, j0, j1)) {
+            tile_at(p, t, m0, n0);
+            const int mr = m0 + (int)rank * kHalf + i;
+            const float *x0 = p.xs + (size_t)min(mr, p.M - 1) * p.G;
+            const float *x1 = p.xs + (size_t)min(mr + 64, p.M - 1) * p.G;
+            const float *w0 = p.ws + (size_t)min(n0 / kGroup + i, p.NB - 1) * p.G;
+            for (int j = j0 & ~3; j < j1; j += 4, ++c) {
+                const int s = c % kScaleSlots;
+                const float4 a = load4(p, x0, j), b = load4(p, x1, j);
+                float4 w = a;
+                if (i < 2) w = load4(p, w0, j);
+                if (c >= kScaleSlots && !mbar_wait_all(smem_u32(sc_empty + s),
+                                                       ((c / kScaleSlots) - 1) & 1, abort)) {
+                    if (lane == 0) fail(kErrSlotWait);
+                    ok = false;
+                    break;
+                }
+                float4 *slot = reinterpret_cast<float4 *>(sm_scales + s * kScaleSlot);
+                slot[i] = a;
+                slot[i + 64] = b;
+                if (i < 2) slot[kHalf + i] = w;
+                mbar_arrive(smem_u32(sc_full + s));
+            }
+        }
     }
     __syncwarp();
     if (p.ksplit > 1) cluster_sync();  // with the sum warps', before the exchange
@@ -350,26 +393,18 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t bar_full = smem_u32(d_full), bar_empty = map_to_rank(smem_u32(d_empty), leader);
         const uint32_t bar_res = smem_u32(r_full + warp);
         uint32_t res_asked = 0, res_taken = 0;  // residual tiles
-        // the scales of four blocks 4 i .. 4 i + 3 at a time, loaded four blocks ahead
-        // (rows and columns past the end take the last one's: they are not stored)
-        const float *sx = nullptr, *sw = nullptr;
-        float4 nx, nw;
-        auto load_scales = [&](int j) {
-            if (j >= p.G) return;
-            if (p.scales16) {
-                nx = load4_now(sx + j);
-                nw = load4_now(sw + j);
-            } else {
-                const int a = min(j + 1, p.G - 1), b = min(j + 2, p.G - 1), d = min(j + 3, p.G - 1);
-                nx = make_float4(load_now(sx + j), load_now(sx + a), load_now(sx + b), load_now(sx + d));
-                nw = make_float4(load_now(sw + j), load_now(sw + a), load_now(sw + b), load_now(sw + d));
-            }
-        };
-        auto begin_tile = [&]() {
-            tile_at(p, t, m0, n0);
-            sx = p.xs + (size_t)min(m0 + (int)rank * kHalf + r, p.M - 1) * p.G;
-            sw = p.ws + (size_t)min(n0 / kGroup + half, p.NB - 1) * p.G;
-            load_scales(j0 & ~3);
+        // the scale products of four blocks 4 i .. 4 i + 3, from the slot
+        int sc = 0;  // batches
+        auto take_scales = [&](float4 &f) {
+            const int s = sc % kScaleSlots;
+            if (!mbar_wait_all(smem_u32(sc_full + s), (sc / kScaleSlots) & 1, abort)) return false;
+            const float4 *slot = reinterpret_cast<const float4 *>(sm_scales + s * kScaleSlot);
+            const float4 a = slot[r], b = slot[kHalf + half];
+            f = make_float4(a.x * b.x, a.y * b.y, a.z * b.z, a.w * b.w);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(sc_empty + s));
+            ++sc;
+            return true;
         };
         // the warp's 32 tokens x 128 columns of the residual, into its staging
         auto ask_residual = [&](int n, int mw) {
@@ -385,10 +420,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         const bool staged_res = p.residual && p.tma_store;
         int c = 0;
         bool ok = true, more = walk.next(p, t, j0, j1);
-        if (more) begin_tile();
         while (more) {
-            // this tile; the next one's place and first scales are fetched before
-            // this one's outputs are written
+            tile_at(p, t, m0, n0);
             const int mw = m0 + (int)rank * kHalf + quarter * 32, m = mw + lane;
             const int nc = n0 + half * kHalf, tt = t, end = j1;
             const bool whole = j0 == 0 && j1 == p.G;
@@ -396,40 +429,57 @@ __global__ void __launch_bounds__(kThreads, 1)
             float acc[kHalf];
 #pragma unroll
             for (int i = 0; i < kHalf; ++i) acc[i] = 0.f;
+            // 32 columns a load, the next one on its way while one is added, across
+            // blocks too: v[0] always holds (or awaits) the next columns to add
+            uint32_t v[2][32];
+            float4 next_scales;
+            ok = take_scales(next_scales) &&
+                 mbar_wait_all(bar_full + 8 * (c % kDBufs), (c / kDBufs) & 1, abort);
+            if (ok) {
+                tc_fence_after();
+                tmem_ld(taddr + (c % kDBufs) * kTileN, v[0]);
+            }
             for (int j = j0 & ~3, begin = j0; j < end && ok; j += 4) {
-                const float sb[4] = {nx.x * nw.x, nx.y * nw.y, nx.z * nw.z, nx.w * nw.w};
-                if (j + 4 < end) load_scales(j + 4);
+                const float sb[4] = {next_scales.x, next_scales.y, next_scales.z, next_scales.w};
+                if (j + 4 < end && !take_scales(next_scales)) {
+                    ok = false;
+                    break;
+                }
 #pragma unroll
                 for (int u = 0; u < 4; ++u) {
                     if (j + u < begin) continue;
                     if (j + u >= end) break;
-                    const int d = c % kDBufs;
-                    if (!mbar_wait_all(bar_full + 8 * d, (c / kDBufs) & 1, abort)) {
-                        if (lane == 0) fail(kErrSumWait);
-                        ok = false;
-                        break;
-                    }
-                    tc_fence_after();
-#pragma unroll
-                    for (int q = 0; q < kHalf / 32; ++q) {
-                        uint32_t v[32];
-                        tmem_ld(taddr + d * kTileN + 32 * q, v);
-                        tmem_wait_ld(v);
-                        if (q == kHalf / 32 - 1) {  // all read: the tensor cores may write again
-                            tc_fence_before();
-                            __syncwarp();
-                            if (lane == 0) mbar_arrive_remote(bar_empty + 8 * d);
-                        }
-#pragma unroll
-                        for (int i = 0; i < 32; ++i)
-                            acc[32 * q + i] = fmaf(__uint_as_float(v[i]), sb[u], acc[32 * q + i]);
-                    }
+                    const uint32_t from = taddr + (c % kDBufs) * kTileN;
+                    const uint32_t freed = bar_empty + 8 * (c % kDBufs);
                     ++c;
+#pragma unroll
+                    for (int q = 0; q < kHalf / 32 - 1; ++q) {
+                        tmem_wait_ld(v[q & 1]);
+                        tmem_ld(from + 32 * (q + 1), v[(q + 1) & 1]);
+                        add_columns<0, 32>(acc + 32 * q, v[q & 1], sb[u]);
+                    }
+                    tmem_wait_ld(v[1]);
+                    tc_fence_before();  // all read: the tensor cores may write again
+                    if (lane == 0) mbar_arrive_remote(freed);
+                    // the next block's barrier and first load amid the last sums
+                    const uint32_t next = bar_full + 8 * (c % kDBufs), parity = (c / kDBufs) & 1;
+                    const bool another = j + u + 1 < end;
+                    const bool ready = another && mbar_try_wait(next, parity);
+                    add_columns<0, 16>(acc + 96, v[1], sb[u]);
+                    if (another) {
+                        if (!__all_sync(0xffffffffu, ready) && !mbar_wait_all(next, parity, abort)) {
+                            ok = false;
+                            break;
+                        }
+                        tc_fence_after();
+                        tmem_ld(taddr + (c % kDBufs) * kTileN, v[0]);
+                    }
+                    add_columns<16, 32>(acc + 96, v[1], sb[u]);
                 }
             }
+            if (!ok && lane == 0) fail(kErrSumWait);
             if (!ok) break;
             more = walk.next(p, t, j0, j1);
-            if (more) begin_tile();
             if (p.ksplit > 1) {
                 // the cluster's tile: the sums wait in this CTA's stages, which
                 // nothing uses any more, for the exchange below
