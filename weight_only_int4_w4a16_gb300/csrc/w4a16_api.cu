@@ -137,7 +137,7 @@ bool fp8_takes_wide(int M, int N, int K) {
     (void)N;
     (void)K;
     const char *e = getenv("FP8_WIDE_FROM");
-    return M >= (e ? atoi(e) : 129);
+    return M >= (e ? atoi(e) : 65);
 }
 
 Decision decide(int M, int N, int K, const DeviceInfo &dev, int forced, int epi = kEpiNone,

@@ -1,4 +1,4 @@
-// The 8-bit linear: y [M, N] = x [M, K] w [N, K]^T (+ residual) for e4m3 rows x
+// The 8-bit linear for up to 64 tokens (more: w4a16_fp8_wide.cu): y [M, N] = x [M, K] w [N, K]^T (+ residual) for e4m3 rows x
 // with one fp32 scale per 128 elements and e4m3 weights with one fp32 scale per
 // block of 128 x 128 (forum.sourcefind.cn thread "vLLM on Hygon Z100", section
 // 六: FP8 checkpoints, dequantised to 16 bits at load there because the GPU has
@@ -12,7 +12,7 @@
 // sums in registers (one fused multiply-add per element and block).
 //
 //   MMA shape (swap AB): the MMA's M = 128 weight rows of one tile, its N = T
-//   tokens (16, 32, 64 or 128; missing tokens are zero rows of x), K = 32 per
+//   tokens (16, 32 or 64; missing tokens are zero rows of x), K = 32 per
 //   instruction, four instructions per block.  A partial last block is filled
 //   with zeros by TMA.
 //
@@ -61,7 +61,6 @@ struct Fp8Params {
     unsigned *counters;  // [tiles], zero between launches
     int *status;
     int M, N, G;
-    int tiles_m;         // token tiles; tile = n_tile * tiles_m + m_tile
     long long total;     // blocks of all tiles
     int tiles;
     int streamk;
@@ -252,7 +251,6 @@ __global__ void __launch_bounds__(Cfg<T>::kThreads, 1) fp8_kernel(const __grid_c
         int c = 0;  // stages
         bool ok = true;
         while (ok && walk.next(p, t, j0, j1)) {
-            const int nt = t / p.tiles_m, m0 = (t - nt * p.tiles_m) * T;
             for (int j = j0; j < j1; j += kSub, ++c) {
                 const int s = c % NS, nb = min(kSub, j1 - j);
                 if (c >= NS && !mbar_wait_all(smem_u32(empty + s), ((c / NS) - 1) & 1, abort)) {
@@ -265,25 +263,25 @@ __global__ void __launch_bounds__(Cfg<T>::kThreads, 1) fp8_kernel(const __grid_c
                     const uint32_t st = smem_u32(smem + (size_t)s * C::kStage);
                     mbar_arrive_expect_tx(bar, nb * (kBlockW + C::kBlockX));
                     for (int b = 0; b < nb; ++b)
-                        tma_load_2d(st + b * kBlockW, &p.wmap, (j + b) * kGroup, nt * kTileN, bar,
+                        tma_load_2d(st + b * kBlockW, &p.wmap, (j + b) * kGroup, t * kTileN, bar,
                                     pol_w);
                     for (int b = 0; b < nb; ++b)
                         tma_load_2d(st + kSub * kBlockW + b * C::kBlockX, &p.xmap, (j + b) * kGroup,
-                                    m0, bar, pol_x);
+                                    0, bar, pol_x);
                 }
                 const uint32_t sc = smem_u32(sm_scales + s * C::kScales);
 #pragma unroll
                 for (int i = 0; i < (T + 31) / 32; ++i) {
                     const int tt = lane + 32 * i;
-                    const bool live = tt < T && m0 + tt < p.M;
-                    const float *src = live ? p.xs + (size_t)(m0 + tt) * p.G + j : p.xs;
+                    const bool live = tt < p.M;
+                    const float *src = live ? p.xs + (size_t)tt * p.G + j : p.xs;
 #pragma unroll
                     for (int b = 0; b < kSub; ++b)
                         if (tt < T)
                             cp_async4(sc + 4 * (b * T + tt), live && b < nb ? src + b : p.xs,
                                       live && b < nb ? 4u : 0u);
                 }
-                if (lane < nb) cp_async4(sc + 4 * (kSub * T + lane), p.ws + (size_t)nt * p.G + j + lane, 4u);
+                if (lane < nb) cp_async4(sc + 4 * (kSub * T + lane), p.ws + (size_t)t * p.G + j + lane, 4u);
                 cp_async_arrive(bar);
             }
         }
@@ -341,8 +339,7 @@ __global__ void __launch_bounds__(Cfg<T>::kThreads, 1) fp8_kernel(const __grid_c
         int c = 0;
         bool ok = true;
         while (ok && walk.next(p, t, j0, j1)) {
-            const int nt = t / p.tiles_m, m0 = (t - nt * p.tiles_m) * T + cb;
-            const int n = nt * kTileN + r, mt = p.M - m0;  // this thread's tokens: i < mt
+            const int n = t * kTileN + r, mt = p.M - cb;  // this thread's tokens: i < mt
             float acc[kCols];
 #pragma unroll
             for (int i = 0; i < kCols; ++i) acc[i] = 0.f;
@@ -393,7 +390,7 @@ __global__ void __launch_bounds__(Cfg<T>::kThreads, 1) fp8_kernel(const __grid_c
             if (j0 == 0 && j1 == p.G) {  // a whole tile
                 if (n < p.N) {
 #pragma unroll
-                    for (int i = 0; i < kCols; i += 16) store16(p, m0 + i, n, acc + i);
+                    for (int i = 0; i < kCols; i += 16) store16(p, cb + i, n, acc + i);
                 }
                 continue;
             }
@@ -436,7 +433,7 @@ __global__ void __launch_bounds__(Cfg<T>::kThreads, 1) fp8_kernel(const __grid_c
                 }
                 if (n < p.N) {
 #pragma unroll
-                    for (int i = 0; i < kCols; i += 16) store16(p, m0 + i, n, acc + i);
+                    for (int i = 0; i < kCols; i += 16) store16(p, cb + i, n, acc + i);
                 }
             }
             // s_last is written again only after every thread has read it
@@ -450,28 +447,26 @@ __global__ void __launch_bounds__(Cfg<T>::kThreads, 1) fp8_kernel(const __grid_c
         __syncthreads();
         cluster_sync();
         if (!*abort) {
-            const int S = p.ksplit, tile = blockIdx.x / S;
-            const int nt = tile / p.tiles_m, m0 = (tile - nt * p.tiles_m) * T;
-            const int n = nt * kTileN + 4 * lane, mt = min(T, p.M - m0);
+            const int S = p.ksplit, n = (int)(blockIdx.x / S) * kTileN + 4 * lane;
             const bool vec = p.N % 4 == 0 && ((uintptr_t)p.y & 7) == 0 &&
                              ((uintptr_t)p.residual & 7) == 0;
             const uint32_t mine = smem_u32(sums + 4 * lane);
             constexpr int kBatch = 4, kWarps = C::kSumWarps + 2;
-            for (int i0 = cluster_rank() + S * warp; i0 < mt; i0 += kBatch * kWarps * S) {
+            for (int i0 = cluster_rank() + S * warp; i0 < p.M; i0 += kBatch * kWarps * S) {
                 float4 v[kBatch][kMaxCluster], res[kBatch];
 #pragma unroll
                 for (int i = 0; i < kBatch; ++i) {
                     const int m = i0 + i * kWarps * S;
-                    res[i] = m < mt ? residual4(p, m0 + m, n, vec) : make_float4(0.f, 0.f, 0.f, 0.f);
+                    res[i] = m < p.M ? residual4(p, m, n, vec) : make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
                     for (int q = 0; q < kMaxCluster; ++q)
-                        if (q < S && m < mt)
+                        if (q < S && m < p.M)
                             v[i][q] = ld4_cluster(map_to_rank(mine, q) + (uint32_t)(m * kTileN * 4));
                 }
 #pragma unroll
                 for (int i = 0; i < kBatch; ++i) {
                     const int m = i0 + i * kWarps * S;
-                    if (m >= mt) break;
+                    if (m >= p.M) break;
                     float4 sum = v[i][0];
 #pragma unroll
                     for (int q = 1; q < kMaxCluster; ++q)
@@ -481,7 +476,7 @@ __global__ void __launch_bounds__(Cfg<T>::kThreads, 1) fp8_kernel(const __grid_c
                             sum.z += v[i][q].z;
                             sum.w += v[i][q].w;
                         }
-                    store4(p, m0 + m, n, vec, make_float4(sum.x + res[i].x, sum.y + res[i].y,
+                    store4(p, m, n, vec, make_float4(sum.x + res[i].x, sum.y + res[i].y,
                                                           sum.z + res[i].z, sum.w + res[i].w));
                 }
             }
@@ -536,8 +531,7 @@ int stages_of(int T) {
     switch (T) {
         case 16: return Cfg<16>::stages();
         case 32: return Cfg<32>::stages();
-        case 64: return Cfg<64>::stages();
-        default: return Cfg<128>::stages();
+        default: return Cfg<64>::stages();
     }
 }
 
@@ -545,25 +539,24 @@ int stages_of(int T) {
 
 Fp8Plan plan_fp8(int M, int N, int K, const DeviceInfo &dev, const Workspace &ws) {
     Fp8Plan pl{};
-    pl.T = M <= 16 ? 16 : M <= 32 ? 32 : M <= 64 ? 64 : 128;
+    pl.T = M <= 16 ? 16 : M <= 32 ? 32 : 64;
     pl.G = (K + kGroup - 1) / kGroup;
-    pl.tiles_m = (M + pl.T - 1) / pl.T;
-    pl.tiles = (long long)pl.tiles_m * ((N + kTileN - 1) / kTileN);
+    pl.tiles = (N + kTileN - 1) / kTileN;
     pl.stages = stages_of(pl.T);
     pl.ksplit = 1;
-    pl.grid = (int)(pl.tiles < dev.sm_count ? pl.tiles : dev.sm_count);
+    pl.grid = pl.tiles < dev.sm_count ? pl.tiles : dev.sm_count;
     // few tiles: the largest cluster that keeps every tile in one wave, with at
     // least two blocks of K per CTA
     for (int k = kMaxCluster; k > 1; --k)
         if (pl.tiles <= g_clusters[k] && pl.G >= 2 * k) {
             pl.ksplit = k;
-            pl.grid = (int)pl.tiles * k;
+            pl.grid = pl.tiles * k;
             return pl;
         }
     // whole tiles when they fill the last wave, else equal runs of blocks
-    const long long waves = (pl.tiles + dev.sm_count - 1) / dev.sm_count;
+    const int waves = (pl.tiles + dev.sm_count - 1) / dev.sm_count;
     const size_t need = (size_t)2 * dev.sm_count * pl.T * kTileN * sizeof(float);
-    if (pl.tiles * 100 < waves * dev.sm_count * 95 && pl.tiles * pl.G >= 4ll * dev.sm_count &&
+    if (pl.tiles * 100ll < waves * dev.sm_count * 95ll && (long long)pl.tiles * pl.G >= 4ll * dev.sm_count &&
         need <= ws.partial_bytes && pl.tiles <= ws.n_counters - kMmaSchedWords) {
         pl.streamk = true;
         pl.grid = dev.sm_count;
@@ -588,9 +581,8 @@ cudaError_t launch_fp8(const Fp8Args &a, const Fp8Plan &plan, const Workspace &w
     p.M = a.M;
     p.N = a.N;
     p.G = plan.G;
-    p.tiles_m = plan.tiles_m;
-    p.tiles = (int)plan.tiles;
-    p.total = plan.tiles * plan.G;
+    p.tiles = plan.tiles;
+    p.total = (long long)plan.tiles * plan.G;
     p.streamk = plan.streamk;
     p.ksplit = plan.ksplit;
     p.stages = plan.stages;
@@ -598,8 +590,7 @@ cudaError_t launch_fp8(const Fp8Args &a, const Fp8Plan &plan, const Workspace &w
     switch (plan.T) {
         case 16: return launch_t<16>(p, plan.grid, stream);
         case 32: return launch_t<32>(p, plan.grid, stream);
-        case 64: return launch_t<64>(p, plan.grid, stream);
-        default: return launch_t<128>(p, plan.grid, stream);
+        default: return launch_t<64>(p, plan.grid, stream);
     }
 }
 
@@ -608,8 +599,7 @@ cudaError_t fp8_init(const DeviceInfo &) {
     const struct { const void *f; int smem; } fns[] = {
         {(const void *)fp8_kernel<16>, Cfg<16>::smem(Cfg<16>::stages())},
         {(const void *)fp8_kernel<32>, Cfg<32>::smem(Cfg<32>::stages())},
-        {(const void *)fp8_kernel<64>, Cfg<64>::smem(Cfg<64>::stages())},
-        {(const void *)fp8_kernel<128>, Cfg<128>::smem(Cfg<128>::stages())}};
+        {(const void *)fp8_kernel<64>, Cfg<64>::smem(Cfg<64>::stages())}};
     for (const auto &k : fns) {
         cudaError_t e =
             cudaFuncSetAttribute(k.f, cudaFuncAttributeMaxDynamicSharedMemorySize, k.smem);

@@ -10,10 +10,10 @@
 // per thread and 128-column half, sx sw, and adding a block to the sums costs one
 // multiply-add per element.
 //
-//   Roles (384 threads per CTA): warps 0..7 (lane = token, warp / 4 = half of the
-//   256 columns) scale and add the blocks' sums and write y; warp 8 streams the
-//   CTA's 128 rows of x and its 128 rows of w per block by TMA; warp 9 of the
-//   leading CTA issues the pair's products; warps 10 and 11 bring the scales of four
+//   Roles (640 threads per CTA): warps 0..15 (lane = token, warp / 4 = quarter of
+//   the 256 columns) scale and add the blocks' sums and write y; warp 16 streams the
+//   CTA's 128 rows of x and its 128 rows of w per block by TMA; warp 17 of the
+//   leading CTA issues the pair's products; warps 18 and 19 bring the scales of four
 //   blocks at a time to shared memory (loaded by the sum warps themselves, their
 //   latency held up the tensor-memory loads).  Two block sums of 256 columns fill the
 //   tensor memory: while the tensor cores run one, the other is read.
@@ -49,22 +49,24 @@ constexpr int kHalf = 128;                     // rows of x, and of w, per CTA
 constexpr int kStageX = kHalf * kGroup, kStageW = kHalf * kGroup;
 constexpr int kStage = kStageX + kStageW;      // 32 KB
 constexpr int kStages = 4;
-constexpr int kSumWarps = 8;
-constexpr int kTmaWarp = 8, kMmaWarp = 9;       // 10 and 11 load scales
+constexpr int kSumWarps = 16;
+constexpr int kCols = 64;                      // columns per sum warp
+constexpr int kTmaWarp = 16, kMmaWarp = 17;     // 18 and 19 load scales
 constexpr int kScaleSlots = 3;                 // batches of four blocks' scales
 constexpr int kScaleSlot = kHalf * 16 + 32;    // the tokens' four each, then the two weight blocks'
-constexpr int kThreads = 384;                  // three warpgroups
-// registers per thread: the launch's 168 x 384 split between the warpgroups
-constexpr int kSumRegs = 216, kOtherRegs = 72;
-static_assert(2 * kSumRegs + kOtherRegs <= 3 * 168, "the launch's registers");
+constexpr int kThreads = 640;                  // five warpgroups
+// registers per thread: the launch's 96 x 640 split between the warpgroups
+constexpr int kSumRegs = 104, kOtherRegs = 64;
+static_assert(4 * kSumRegs + kOtherRegs <= 5 * 96, "the launch's registers");
 constexpr int kDBufs = 2;                      // block sums in tensor memory
 constexpr int kTmemCols = 512;
 constexpr int kMaxSplit = 4;                   // pairs of a cluster
 constexpr int kStoreCols = 64;                 // columns per TMA store (a 128-byte row)
-constexpr int kStoreBytes = 32 * kStoreCols * 2;  // 4 KB; a warp has two of them
+constexpr int kStoreBytes = 32 * kStoreCols * 2;  // a warp's staging: 4 KB
+static_assert(kStoreCols == kCols, "a warp's outputs are one box");
 constexpr int kGroupM = 16;                    // token tiles that share a pass over the weights
 constexpr int kBarBytes = (2 * kStages + 2 * kDBufs + kSumWarps + 2 * kScaleSlots) * 8 + 16;
-constexpr int kSmem = 1024 + kStages * kStage + 2 * kSumWarps * kStoreBytes +
+constexpr int kSmem = 1024 + kStages * kStage + kSumWarps * kStoreBytes +
                       kScaleSlots * kScaleSlot + kBarBytes;
 constexpr uint32_t kIdesc =  // D f32, A and B e4m3 (0), N = 256, M = 256
     (1u << 4) | ((uint32_t)(kTileN >> 3) << 17) | ((uint32_t)(kTileM >> 4) << 24);
@@ -163,27 +165,27 @@ __device__ __forceinline__ uint32_t pack16(float lo, float hi) {  // one roundin
     }
 }
 
-// y[m][n .. n + 15]: the sums at `sums` (16 columns, kHalf apart) of every CTA of
+// y[m][n .. n + 7]: the sums at `sums` (8 columns, kHalf apart) of every CTA of
 // this rank in the cluster's pairs, in K order, + residual, one rounding each
 template <bool kBf16>
-__device__ __forceinline__ void exchange16(const WideParams &p, const float *sums, uint32_t rank,
-                                           int m, int n) {
-    float v[kMaxSplit][16];
+__device__ __forceinline__ void exchange8(const WideParams &p, const float *sums, uint32_t rank,
+                                          int m, int n) {
+    float v[kMaxSplit][8];
 #pragma unroll
     for (int q = 0; q < kMaxSplit; ++q)
         if (q < p.ksplit) {
             const uint32_t from = map_to_rank(smem_u32(sums), 2 * q + rank);
 #pragma unroll
-            for (int i = 0; i < 16; ++i) v[q][i] = ld_cluster(from + i * kHalf * 4);
+            for (int i = 0; i < 8; ++i) v[q][i] = ld_cluster(from + i * kHalf * 4);
         }
     const size_t o = (size_t)m * p.N + n;
-    float res[16];
+    float res[8];
 #pragma unroll
-    for (int i = 0; i < 16; ++i)
+    for (int i = 0; i < 8; ++i)
         res[i] = p.residual && m < p.M && n + i < p.N ? half_bits_to_float(p.residual[o + i], kBf16)
                                                       : 0.f;
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
+    for (int i = 0; i < 8; ++i) {
 #pragma unroll
         for (int q = 1; q < kMaxSplit; ++q)
             if (q < p.ksplit) v[0][i] += v[q][i];
@@ -191,24 +193,14 @@ __device__ __forceinline__ void exchange16(const WideParams &p, const float *sum
     }
     if (m >= p.M) return;
     if (p.tma_store) {  // what allows TMA allows 16-byte stores
-#pragma unroll
-        for (int i = 0; i < 16; i += 8)
-            if (n + i < p.N)
-                *reinterpret_cast<uint4 *>(p.y + o + i) = make_uint4(
-                    pack16<kBf16>(v[0][i], v[0][i + 1]), pack16<kBf16>(v[0][i + 2], v[0][i + 3]),
-                    pack16<kBf16>(v[0][i + 4], v[0][i + 5]), pack16<kBf16>(v[0][i + 6], v[0][i + 7]));
+        *reinterpret_cast<uint4 *>(p.y + o) =
+            make_uint4(pack16<kBf16>(v[0][0], v[0][1]), pack16<kBf16>(v[0][2], v[0][3]),
+                       pack16<kBf16>(v[0][4], v[0][5]), pack16<kBf16>(v[0][6], v[0][7]));
     } else {
 #pragma unroll
-        for (int i = 0; i < 16; ++i)
+        for (int i = 0; i < 8; ++i)
             if (n + i < p.N) p.y[o + i] = float_to_half_bits(v[0][i], kBf16);
     }
-}
-
-// acc[i] += v[i] * s for i in [a, b)
-template <int a, int b>
-__device__ __forceinline__ void add_columns(float *acc, const uint32_t (&v)[32], float s) {
-#pragma unroll
-    for (int i = a; i < b; ++i) acc[i] = fmaf(__uint_as_float(v[i]), s, acc[i]);
 }
 
 template <bool kBf16>
@@ -219,7 +211,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // the leader's addresses
     uint8_t *smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
     uint8_t *sm_store = smem + kStages * kStage;
-    uint8_t *sm_scales = sm_store + 2 * kSumWarps * kStoreBytes;
+    uint8_t *sm_scales = sm_store + kSumWarps * kStoreBytes;
     uint64_t *full = reinterpret_cast<uint64_t *>(sm_scales + kScaleSlots * kScaleSlot);
     uint64_t *empty = full + kStages;      // this CTA's stage read
     uint64_t *d_full = empty + kStages;    // a block's sums ready
@@ -386,10 +378,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         // ------------------------------------------------ sums and outputs
         regs_inc<kSumRegs>();
         grid_dependency_wait();
-        const int quarter = warp & 3, half = warp >> 2;
+        const int quarter = warp & 3, col = (warp >> 2) * kCols;  // its 64 columns
         const int r = quarter * 32 + lane;  // token within the CTA's 128
-        const uint32_t taddr = tmem + ((uint32_t)(quarter * 32) << 16) + half * kHalf;
-        uint8_t *stage_out = sm_store + 2 * warp * kStoreBytes;
+        const uint32_t taddr = tmem + ((uint32_t)(quarter * 32) << 16) + col;
+        uint8_t *stage_out = sm_store + warp * kStoreBytes;
         const uint32_t bar_full = smem_u32(d_full), bar_empty = map_to_rank(smem_u32(d_empty), leader);
         const uint32_t bar_res = smem_u32(r_full + warp);
         uint32_t res_asked = 0, res_taken = 0;  // residual tiles
@@ -399,21 +391,19 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int s = sc % kScaleSlots;
             if (!mbar_wait_all(smem_u32(sc_full + s), (sc / kScaleSlots) & 1, abort)) return false;
             const float4 *slot = reinterpret_cast<const float4 *>(sm_scales + s * kScaleSlot);
-            const float4 a = slot[r], b = slot[kHalf + half];
+            const float4 a = slot[r], b = slot[kHalf + col / kGroup];
             f = make_float4(a.x * b.x, a.y * b.y, a.z * b.z, a.w * b.w);
             __syncwarp();
             if (lane == 0) mbar_arrive(smem_u32(sc_empty + s));
             ++sc;
             return true;
         };
-        // the warp's 32 tokens x 128 columns of the residual, into its staging
+        // the warp's 32 tokens x 64 columns of the residual, into its staging
         auto ask_residual = [&](int n, int mw) {
             if (lane == 0) {
                 tma_store_wait_read();  // the staging is free
-                mbar_arrive_expect_tx(bar_res, 2 * kStoreBytes);
+                mbar_arrive_expect_tx(bar_res, kStoreBytes);
                 tma_load_2d(smem_u32(stage_out), &p.rmap, n, mw, bar_res, policy_evict_first());
-                tma_load_2d(smem_u32(stage_out + kStoreBytes), &p.rmap, n + kStoreCols, mw, bar_res,
-                            policy_evict_first());
             }
             ++res_asked;
         };
@@ -423,58 +413,43 @@ __global__ void __launch_bounds__(kThreads, 1)
         while (more) {
             tile_at(p, t, m0, n0);
             const int mw = m0 + (int)rank * kHalf + quarter * 32, m = mw + lane;
-            const int nc = n0 + half * kHalf, tt = t, end = j1;
+            const int nc = n0 + col, tt = t, end = j1;
             const bool whole = j0 == 0 && j1 == p.G;
             if (staged_res && whole) ask_residual(nc, mw);
-            float acc[kHalf];
+            float acc[kCols];
 #pragma unroll
-            for (int i = 0; i < kHalf; ++i) acc[i] = 0.f;
-            // 32 columns a load, the next one on its way while one is added, across
-            // blocks too: v[0] always holds (or awaits) the next columns to add
-            uint32_t v[2][32];
-            float4 next_scales;
-            ok = take_scales(next_scales) &&
-                 mbar_wait_all(bar_full + 8 * (c % kDBufs), (c / kDBufs) & 1, abort);
-            if (ok) {
-                tc_fence_after();
-                tmem_ld(taddr + (c % kDBufs) * kTileN, v[0]);
-            }
+            for (int i = 0; i < kCols; ++i) acc[i] = 0.f;
             for (int j = j0 & ~3, begin = j0; j < end && ok; j += 4) {
-                const float sb[4] = {next_scales.x, next_scales.y, next_scales.z, next_scales.w};
-                if (j + 4 < end && !take_scales(next_scales)) {
-                    ok = false;
-                    break;
-                }
+                float4 f;
+                ok = take_scales(f);
+                if (!ok) break;
+                const float sb[4] = {f.x, f.y, f.z, f.w};
 #pragma unroll
                 for (int u = 0; u < 4; ++u) {
                     if (j + u < begin) continue;
                     if (j + u >= end) break;
                     const uint32_t from = taddr + (c % kDBufs) * kTileN;
-                    const uint32_t freed = bar_empty + 8 * (c % kDBufs);
-                    ++c;
+                    ok = mbar_wait_all(bar_full + 8 * (c % kDBufs), (c / kDBufs) & 1, abort);
+                    if (!ok) break;
+                    tc_fence_after();
+                    // 16 columns a load, the next on its way while one is added
+                    uint32_t v[2][16];
+                    tmem_ld(from, v[0]);
 #pragma unroll
-                    for (int q = 0; q < kHalf / 32 - 1; ++q) {
+                    for (int q = 0; q < kCols / 16; ++q) {
                         tmem_wait_ld(v[q & 1]);
-                        tmem_ld(from + 32 * (q + 1), v[(q + 1) & 1]);
-                        add_columns<0, 32>(acc + 32 * q, v[q & 1], sb[u]);
-                    }
-                    tmem_wait_ld(v[1]);
-                    tc_fence_before();  // all read: the tensor cores may write again
-                    if (lane == 0) mbar_arrive_remote(freed);
-                    // the next block's barrier and first load amid the last sums
-                    const uint32_t next = bar_full + 8 * (c % kDBufs), parity = (c / kDBufs) & 1;
-                    const bool another = j + u + 1 < end;
-                    const bool ready = another && mbar_try_wait(next, parity);
-                    add_columns<0, 16>(acc + 96, v[1], sb[u]);
-                    if (another) {
-                        if (!__all_sync(0xffffffffu, ready) && !mbar_wait_all(next, parity, abort)) {
-                            ok = false;
-                            break;
+                        if (q + 1 < kCols / 16) {
+                            tmem_ld(from + 16 * (q + 1), v[(q + 1) & 1]);
+                        } else {  // all read: the tensor cores may write again
+                            tc_fence_before();
+                            if (lane == 0) mbar_arrive_remote(bar_empty + 8 * (c % kDBufs));
                         }
-                        tc_fence_after();
-                        tmem_ld(taddr + (c % kDBufs) * kTileN, v[0]);
+#pragma unroll
+                        for (int i = 0; i < 16; ++i)
+                            acc[16 * q + i] =
+                                fmaf(__uint_as_float(v[q & 1][i]), sb[u], acc[16 * q + i]);
                     }
-                    add_columns<16, 32>(acc + 96, v[1], sb[u]);
+                    ++c;
                 }
             }
             if (!ok && lane == 0) fail(kErrSumWait);
@@ -484,50 +459,54 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // the cluster's tile: the sums wait in this CTA's stages, which
                 // nothing uses any more, for the exchange below
 #pragma unroll
-                for (int i = 0; i < kHalf; ++i) sums[(half * kHalf + i) * kHalf + r] = acc[i];
+                for (int i = 0; i < kCols; ++i) sums[(col + i) * kHalf + r] = acc[i];
                 break;
             }
             if (!whole) {
-                // part of a tile: the sums go to this pair's slot (0: the run
-                // begins inside the tile, 1: the tile begins inside the run); the
-                // CTA that comes last of the two adds the other's to its own
+                // part of a tile: if the other piece is in its pair's slot by now, it
+                // is added to this one; else this one goes to this pair's slot (0: the
+                // run begins inside the tile, 1: the tile begins inside the run), and
+                // whoever of the two sees the other's there finishes the tile
                 const long long tile0 = (long long)(tt - p.whole) * p.G;
                 const int b0 = walk.owner(p, tile0), b1 = walk.owner(p, tile0 + p.G - 1);
-                const int slot = 2 * walk.pair + (walk.begin(p, walk.pair) > tile0 ? 0 : 1);
-                float *part = p.partials +
-                              ((size_t)(2 * slot + rank) * kTileN + half * kHalf) * kHalf + r;
+                const int b = walk.pair == b0 ? b1 : b0;
+                auto slot = [&](int pair) {
+                    const int s = 2 * pair + (walk.begin(p, pair) > tile0 ? 0 : 1);
+                    return p.partials + ((size_t)(2 * s + rank) * kTileN + col) * kHalf + r;
+                };
+                unsigned *there = p.counters + 2 * (tt - p.whole) + rank;  // pieces in slots
+                if (threadIdx.x == 0) *s_last = atomicAdd(there, 0u) != 0u;
+                asm volatile("bar.sync 1, %0;" ::"r"(kSumWarps * 32) : "memory");
+                if (!*s_last) {
+                    float *part = slot(walk.pair);
 #pragma unroll
-                for (int i = 0; i < kHalf; ++i) part[(size_t)i * kHalf] = acc[i];
-                __threadfence();
-                asm volatile("bar.sync 1, %0;" ::"r"(kSumWarps * 32) : "memory");
-                unsigned *counter = p.counters + 2 * (tt - p.whole) + rank;
-                if (threadIdx.x == 0)
-                    *s_last = atomicAdd(counter, 1u) == 1u ? 1 : 0;
-                asm volatile("bar.sync 1, %0;" ::"r"(kSumWarps * 32) : "memory");
+                    for (int i = 0; i < kCols; ++i) part[(size_t)i * kHalf] = acc[i];
+                    __threadfence();
+                    asm volatile("bar.sync 1, %0;" ::"r"(kSumWarps * 32) : "memory");
+                    if (threadIdx.x == 0) *s_last = atomicAdd(there, 1u) != 0u;
+                    asm volatile("bar.sync 1, %0;" ::"r"(kSumWarps * 32) : "memory");
+                }
                 const bool last = *s_last != 0;
                 if (last) {
                     __threadfence();
-                    if (threadIdx.x == 0) *counter = 0u;  // ready for the next launch
+                    if (threadIdx.x == 0) *there = 0u;  // ready for the next launch
                     if (staged_res) ask_residual(nc, mw);
-                    const int b = walk.pair == b0 ? b1 : b0;
-                    const int sl = 2 * b + (walk.begin(p, b) > tile0 ? 0 : 1);
-                    const float *src =
-                        p.partials + ((size_t)(2 * sl + rank) * kTileN + half * kHalf) * kHalf + r;
+                    const float *src = slot(b);
 #pragma unroll
                     for (int q = 0; q < 2; ++q) {  // a round trip each
-                        float v[64];
+                        float v[32];
 #pragma unroll
-                        for (int i = 0; i < 64; ++i)
-                            v[i] = __ldcg(src + (size_t)(64 * q + i) * kHalf);
+                        for (int i = 0; i < 32; ++i)
+                            v[i] = __ldcg(src + (size_t)(32 * q + i) * kHalf);
 #pragma unroll
-                        for (int i = 0; i < 64; ++i) acc[64 * q + i] += v[i];
+                        for (int i = 0; i < 32; ++i) acc[32 * q + i] += v[i];
                     }
                 }
                 // s_last is written again only after every thread has read it
                 asm volatile("bar.sync 1, %0;" ::"r"(kSumWarps * 32) : "memory");
                 if (!last) continue;
             }
-            // y[m][nc .. nc + 127] = sums (+ residual), one rounding each
+            // y[m][nc .. nc + 63] = sums (+ residual), one rounding each
             if (p.tma_store) {
                 if (staged_res) {
                     if (!mbar_wait_all(bar_res, res_taken & 1, abort)) {
@@ -539,36 +518,30 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (lane == 0) tma_store_wait_read();  // the staging is free
                     __syncwarp();
                 }
+                uint8_t *row = stage_out + lane * 128;
 #pragma unroll
-                for (int h = 0; h < kHalf / kStoreCols; ++h) {
-                    uint8_t *row = stage_out + h * kStoreBytes + lane * 128;
+                for (int q = 0; q < 8; ++q) {  // 8 columns, 16 bytes, at the swizzled chunk
+                    uint4 *at = reinterpret_cast<uint4 *>(row + ((q ^ (lane & 7)) << 4));
+                    float *v = acc + q * 8;
+                    if (staged_res) {
+                        const uint4 u = *at;
+                        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
-                    for (int q = 0; q < 8; ++q) {  // 8 columns, 16 bytes, at the swizzled chunk
-                        uint4 *at = reinterpret_cast<uint4 *>(row + ((q ^ (lane & 7)) << 4));
-                        float v[8];
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) v[i] = acc[h * kStoreCols + q * 8 + i];
-                        if (staged_res) {
-                            const uint4 u = *at;
-                            const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-                            for (int i = 0; i < 4; ++i) {
-                                v[2 * i] += half_bits_to_float((uint16_t)w[i], kBf16);
-                                v[2 * i + 1] += half_bits_to_float((uint16_t)(w[i] >> 16), kBf16);
-                            }
+                        for (int i = 0; i < 4; ++i) {
+                            v[2 * i] += half_bits_to_float((uint16_t)w[i], kBf16);
+                            v[2 * i + 1] += half_bits_to_float((uint16_t)(w[i] >> 16), kBf16);
                         }
-                        *at = make_uint4(pack16<kBf16>(v[0], v[1]), pack16<kBf16>(v[2], v[3]),
-                                         pack16<kBf16>(v[4], v[5]), pack16<kBf16>(v[6], v[7]));
                     }
-                    fence_async_shared();
-                    __syncwarp();
-                    const int n = nc + h * kStoreCols;
-                    if (lane == 0 && n < p.N && mw < p.M)
-                        tma_store_2d(&p.ymap, n, mw, smem_u32(stage_out + h * kStoreBytes));
+                    *at = make_uint4(pack16<kBf16>(v[0], v[1]), pack16<kBf16>(v[2], v[3]),
+                                     pack16<kBf16>(v[4], v[5]), pack16<kBf16>(v[6], v[7]));
                 }
+                fence_async_shared();
+                __syncwarp();
+                if (lane == 0 && nc < p.N && mw < p.M)
+                    tma_store_2d(&p.ymap, nc, mw, smem_u32(stage_out));
             } else if (m < p.M) {
 #pragma unroll
-                for (int i = 0; i < kHalf; ++i) {
+                for (int i = 0; i < kCols; ++i) {
                     const int n = nc + i;
                     if (n < p.N) {
                         const size_t o = (size_t)m * p.N + n;
@@ -586,18 +559,18 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
         if (p.ksplit > 1) {
             // the exchange: the cluster's CTAs of these 128 tokens share out the tile's
-            // 16 groups of 16 columns; a warp takes a group for 32 tokens (lane =
-            // token), adds the CTAs' sums in K order (which is rank order) and writes
-            // y.  It stays with these warps: the others keep few registers.
+            // 32 groups of 8 columns; a warp takes a group for 32 tokens (lane = token),
+            // adds the CTAs' sums in K order (which is rank order) and writes y.  It
+            // stays with these warps: the others keep few registers.
             cluster_sync();
             if (!*abort) {
                 const int S = p.ksplit;
                 tile_at(p, blockIdx.x / (2 * S), m0, n0);
-                for (int u = warp; u < 64; u += kSumWarps) {
+                for (int u = warp;; u += kSumWarps) {
                     const int qu = u & 3, g = (u >> 2) * S + (int)(crank >> 1);
-                    const int m = m0 + (int)rank * kHalf + qu * 32 + lane, n = n0 + 16 * g;
-                    if (g >= 16 || n >= p.N) break;
-                    exchange16<kBf16>(p, sums + 16 * g * kHalf + qu * 32 + lane, rank, m, n);
+                    const int m = m0 + (int)rank * kHalf + qu * 32 + lane, n = n0 + 8 * g;
+                    if (g >= kTileN / 8 || n >= p.N) break;
+                    exchange8<kBf16>(p, sums + 8 * g * kHalf + qu * 32 + lane, rank, m, n);
                 }
             }
             __syncwarp();

@@ -287,16 +287,16 @@ struct Fp8Args {
     bool bf16;
 };
 struct Fp8Plan {
-    int T;             // tokens per tile (the MMA's N): 16, 32, 64 or 128
+    int T;             // the MMA's N: 16, 32 or 64 tokens
     int G;             // blocks of 128 along K
-    int tiles_m;       // token tiles
-    long long tiles;   // all tiles
+    int tiles;         // of 128 weight rows
     int ksplit;        // CTAs of a cluster that split each tile along K (1: none)
     bool streamk;      // CTAs take equal runs of (tile, block) work, not whole tiles
     int grid;
     int stages;
     size_t ws_bytes;   // partial sums of split tiles
 };
+constexpr int kFp8MaxTokens = 64;  // per launch of this kernel
 // ws: splits nothing that does not fit it
 Fp8Plan plan_fp8(int M, int N, int K, const DeviceInfo &dev, const Workspace &ws);
 cudaError_t launch_fp8(const Fp8Args &a, const Fp8Plan &plan, const Workspace &ws,
