@@ -367,7 +367,7 @@ int w4a16_rmsnorm(const uint16_t *x, const uint16_t *residual, const uint16_t *w
  * elements.  W4A16_EPILOGUE_NONE: of x itself, q [M, cols].
  * W4A16_EPILOGUE_SILU_MUL: of silu(x[:, :cols/2]) * x[:, cols/2:] (fp32, silu(g) =
  * g / (1 + e^-g)), q [M, cols/2]; cols even.  W4A16_EPILOGUE_RESIDUAL:
- * W4A16_ERR_UNSUPPORTED.  0 <= M <= 65535; x 2-byte aligned, scales 4-byte; q and
+ * W4A16_ERR_UNSUPPORTED.  0 <= M <= 65535, 1 <= cols <= 2^30; x 2-byte aligned, scales 4-byte; q and
  * scales apart from x and from each other.  Needs no w4a16_init. */
 int w4a16_fp8_quant(const uint16_t *x, int M, int cols, int epilogue, int dtype, uint8_t *q,
                     float *scales, void *stream);

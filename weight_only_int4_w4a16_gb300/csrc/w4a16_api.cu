@@ -131,14 +131,15 @@ bool gemv_small(int M, int N, int K) {
     return M <= kMmaMaxTokens && w <= lim;
 }
 
-// The 8-bit linear's kernel for M tokens: CTA pairs on 256-token tiles, or
-// 128-row weight tiles by up to 128 tokens.
-bool fp8_takes_wide(int M, int N, int K) {
-    (void)N;
-    (void)K;
-    const char *e = getenv("FP8_WIDE_FROM");
-    return M >= (e ? atoi(e) : 65);
-}
+// The 8-bit linear's kernel for M tokens: up to 64 run in one pass over the weights
+// with 128 weight rows as the MMA's M and the tokens as its N, split finely over the
+// SMs (fp8_kernel); more run on pairs of CTAs, 256 tokens by 256 weight rows at a time
+// (fp8_wide_kernel).  At 64 tokens, L2 evicted (one GB300): N 8192, K 5120 19.1
+// against 25.3 us, N 5120, K 17408 29.3 against 35.5, N 34816, K 5120 47.7 against
+// 57.0; with a 128-token tile of the first kernel 128 tokens took 18.6 against 19.0 us
+// on N 8192, K 5120, but 57.2 against 52.2 on N 34816, K 5120, and 192 tokens, in two
+// such passes, 33.2 against 19.2.
+bool fp8_takes_wide(int M) { return M > kFp8MaxTokens; }
 
 Decision decide(int M, int N, int K, const DeviceInfo &dev, int forced, int epi = kEpiNone,
                 int dtype = kDtypeF16) {
@@ -801,7 +802,7 @@ int w4a16_fp8_linear(const uint8_t *x, const float *x_scales, const uint8_t *w,
     const State &st = g_state;
     if (!st.initialized) return W4A16_ERR_NOT_INITIALIZED;
     const Fp8Args a{x, x_scales, w, w_scales, residual, y, M, N, K, dtype == W4A16_DTYPE_BF16};
-    const bool wide = fp8_takes_wide(M, N, K);
+    const bool wide = fp8_takes_wide(M);
     const cudaError_t e =
         wide ? launch_fp8_wide(a, plan_fp8_wide(M, N, K, st.dev, st.ws), st.ws, (cudaStream_t)stream)
              : launch_fp8(a, plan_fp8(M, N, K, st.dev, st.ws), st.ws, (cudaStream_t)stream);
@@ -853,7 +854,7 @@ int w4a16_rmsnorm(const uint16_t *x, const uint16_t *residual, const uint16_t *w
 int w4a16_fp8_quant(const uint16_t *x, int M, int cols, int epilogue, int dtype, uint8_t *q,
                     float *scales, void *stream) {
     const bool silu = epilogue == W4A16_EPILOGUE_SILU_MUL;
-    if (M < 0 || M > kMaxM || cols < 1) return W4A16_ERR_INVALID_ARG;
+    if (M < 0 || M > kMaxM || cols < 1 || cols > 1 << 30) return W4A16_ERR_INVALID_ARG;
     if (dtype != W4A16_DTYPE_F16 && dtype != W4A16_DTYPE_BF16) return W4A16_ERR_INVALID_ARG;
     if (epilogue == W4A16_EPILOGUE_RESIDUAL) return W4A16_ERR_UNSUPPORTED;
     if (!silu && epilogue != W4A16_EPILOGUE_NONE) return W4A16_ERR_INVALID_ARG;

@@ -20,7 +20,7 @@
 //
 //   Outputs go through shared memory to TMA stores (boxes of 32 tokens x 64
 //   columns), where the residual was loaded by TMA before; where N or an address
-//   does not allow TMA, straight from registers.
+//   does not allow TMA, the warps copy the same boxes row by row.
 //
 //   Work: few tiles are split along K between the pairs of a cluster, which exchange
 //   their sums through distributed shared memory.  Otherwise whole tiles in turn
@@ -74,7 +74,7 @@ constexpr uint32_t kIdesc =  // D f32, A and B e4m3 (0), N = 256, M = 256
 struct WideParams {
     CUtensorMap xmap;  // x: (K bytes, M rows), box {128, 128}, 128-byte swizzle
     CUtensorMap wmap;  // w: (K bytes, N rows), the same
-    CUtensorMap ymap;  // y: (N, M) of 16 bits, box {64, 32}, 128-byte swizzle (tma_store)
+    CUtensorMap ymap;  // y: (N, M) of 16 bits, box {64, 32}, 128-byte swizzle (kTma)
     CUtensorMap rmap;  // the residual, the same
     const float *xs, *ws;
     const uint16_t *residual;
@@ -87,7 +87,6 @@ struct WideParams {
     int whole;           // tiles that pairs take whole, in turn
     long long split;     // blocks of the other tiles, cut into equal runs
     int ksplit;          // pairs of a cluster that split each tile along K (1: none)
-    int tma_store;       // y (and the residual) can go by TMA
     int scales16;        // four blocks' scales of a row are one aligned 16-byte load
 };
 
@@ -165,9 +164,64 @@ __device__ __forceinline__ uint32_t pack16(float lo, float hi) {  // one roundin
     }
 }
 
+// Rows m .. m + 31, columns n .. n + 63 of the residual into a warp's staging (kIn), or
+// of y out of it, for rows that TMA cannot address: 32-bit words where N is even and
+// the address allows it, else single elements, 8 rows at a time (their loads together).
+template <bool kIn>
+__device__ __forceinline__ void copy_rows(const WideParams &p, uint8_t *staging, int lane, int m,
+                                          int n) {
+    const bool words = p.N % 2 == 0 && ((uintptr_t)(kIn ? p.residual : p.y) & 3) == 0;
+    const int rows = min(32, p.M - m), cols = min(kStoreCols, p.N - n);
+    // element (r, c) of the staging, 128-byte swizzled
+    auto at = [&](int r, int c) { return staging + r * 128 + (((c >> 3) ^ (r & 7)) << 4) + (c & 7) * 2; };
+    __syncwarp();
+    for (int r0 = 0; r0 < rows; r0 += 8) {
+        const size_t o = (size_t)(m + r0) * p.N + n;
+        if (words) {
+            const int c = 2 * lane;
+            if (c >= cols) continue;
+            uint32_t v[8];
+#pragma unroll
+            for (int r = 0; r < 8; ++r)
+                if (r0 + r < rows) {
+                    if constexpr (kIn)
+                        v[r] = *reinterpret_cast<const uint32_t *>(p.residual + o + (size_t)r * p.N + c);
+                    else
+                        v[r] = *reinterpret_cast<const uint32_t *>(at(r0 + r, c));
+                }
+#pragma unroll
+            for (int r = 0; r < 8; ++r)
+                if (r0 + r < rows) {
+                    if constexpr (kIn) *reinterpret_cast<uint32_t *>(at(r0 + r, c)) = v[r];
+                    else *reinterpret_cast<uint32_t *>(p.y + o + (size_t)r * p.N + c) = v[r];
+                }
+        } else {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int c = lane + 32 * h;
+                if (c >= cols) continue;
+                uint16_t v[8];
+#pragma unroll
+                for (int r = 0; r < 8; ++r)
+                    if (r0 + r < rows) {
+                        if constexpr (kIn) v[r] = p.residual[o + (size_t)r * p.N + c];
+                        else v[r] = *reinterpret_cast<const uint16_t *>(at(r0 + r, c));
+                    }
+#pragma unroll
+                for (int r = 0; r < 8; ++r)
+                    if (r0 + r < rows) {
+                        if constexpr (kIn) *reinterpret_cast<uint16_t *>(at(r0 + r, c)) = v[r];
+                        else p.y[o + (size_t)r * p.N + c] = v[r];
+                    }
+            }
+        }
+    }
+    __syncwarp();
+}
+
 // y[m][n .. n + 7]: the sums at `sums` (8 columns, kHalf apart) of every CTA of
 // this rank in the cluster's pairs, in K order, + residual, one rounding each
-template <bool kBf16>
+template <bool kBf16, bool kTma>
 __device__ __forceinline__ void exchange8(const WideParams &p, const float *sums, uint32_t rank,
                                           int m, int n) {
     float v[kMaxSplit][8];
@@ -192,7 +246,7 @@ __device__ __forceinline__ void exchange8(const WideParams &p, const float *sums
         v[0][i] += res[i];
     }
     if (m >= p.M) return;
-    if (p.tma_store) {  // what allows TMA allows 16-byte stores
+    if constexpr (kTma) {  // what allows TMA allows 16-byte stores
         *reinterpret_cast<uint4 *>(p.y + o) =
             make_uint4(pack16<kBf16>(v[0][0], v[0][1]), pack16<kBf16>(v[0][2], v[0][3]),
                        pack16<kBf16>(v[0][4], v[0][5]), pack16<kBf16>(v[0][6], v[0][7]));
@@ -203,7 +257,9 @@ __device__ __forceinline__ void exchange8(const WideParams &p, const float *sums
     }
 }
 
-template <bool kBf16>
+// kTma: y (and the residual) can go by TMA.  The copies of the other case stay out of
+// this one's registers: in one kernel they cost its products 17%.
+template <bool kBf16, bool kTma>
 __global__ void __launch_bounds__(kThreads, 1)
     fp8_wide_kernel(const __grid_constant__ WideParams p) {
     extern __shared__ uint8_t smem_raw[];
@@ -244,8 +300,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_init_fence();
         prefetch_tensormap(&p.xmap);
         prefetch_tensormap(&p.wmap);
-        if (p.tma_store) prefetch_tensormap(&p.ymap);
-        if (p.tma_store && p.residual) prefetch_tensormap(&p.rmap);
+        if (kTma) prefetch_tensormap(&p.ymap);
+        if (kTma && p.residual) prefetch_tensormap(&p.rmap);
     }
     if (warp == 0) {
         asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
@@ -407,15 +463,15 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             ++res_asked;
         };
-        const bool staged_res = p.residual && p.tma_store;
+        const bool staged_res = kTma && p.residual;
         int c = 0;
         bool ok = true, more = walk.next(p, t, j0, j1);
         while (more) {
             tile_at(p, t, m0, n0);
-            const int mw = m0 + (int)rank * kHalf + quarter * 32, m = mw + lane;
+            const int mw = m0 + (int)rank * kHalf + quarter * 32;
             const int nc = n0 + col, tt = t, end = j1;
             const bool whole = j0 == 0 && j1 == p.G;
-            if (staged_res && whole) ask_residual(nc, mw);
+            if (whole && staged_res) ask_residual(nc, mw);
             float acc[kCols];
 #pragma unroll
             for (int i = 0; i < kCols; ++i) acc[i] = 0.f;
@@ -506,50 +562,45 @@ __global__ void __launch_bounds__(kThreads, 1)
                 asm volatile("bar.sync 1, %0;" ::"r"(kSumWarps * 32) : "memory");
                 if (!last) continue;
             }
-            // y[m][nc .. nc + 63] = sums (+ residual), one rounding each
-            if (p.tma_store) {
-                if (staged_res) {
-                    if (!mbar_wait_all(bar_res, res_taken & 1, abort)) {
-                        if (lane == 0) fail(kErrStageWait);
-                        break;
-                    }
-                    ++res_taken;
-                } else {
-                    if (lane == 0) tma_store_wait_read();  // the staging is free
-                    __syncwarp();
+            // y[m][nc .. nc + 63] = sums (+ residual), one rounding each, by way of the
+            // warp's staging: the residual comes there, and the outputs leave from
+            // there, by TMA or (rows that TMA cannot address) by the warp's own copies
+            if (staged_res) {
+                if (!mbar_wait_all(bar_res, res_taken & 1, abort)) {
+                    if (lane == 0) fail(kErrStageWait);
+                    break;
                 }
-                uint8_t *row = stage_out + lane * 128;
+                ++res_taken;
+            } else if constexpr (kTma) {
+                if (lane == 0) tma_store_wait_read();  // the staging is free
+                __syncwarp();
+            } else if (p.residual) {
+                copy_rows<true>(p, stage_out, lane, mw, nc);
+            }
+            uint8_t *row = stage_out + lane * 128;
 #pragma unroll
-                for (int q = 0; q < 8; ++q) {  // 8 columns, 16 bytes, at the swizzled chunk
-                    uint4 *at = reinterpret_cast<uint4 *>(row + ((q ^ (lane & 7)) << 4));
-                    float *v = acc + q * 8;
-                    if (staged_res) {
-                        const uint4 u = *at;
-                        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+            for (int q = 0; q < 8; ++q) {  // 8 columns, 16 bytes, at the swizzled chunk
+                uint4 *at = reinterpret_cast<uint4 *>(row + ((q ^ (lane & 7)) << 4));
+                float *v = acc + q * 8;
+                if (p.residual) {
+                    const uint4 u = *at;
+                    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            v[2 * i] += half_bits_to_float((uint16_t)w[i], kBf16);
-                            v[2 * i + 1] += half_bits_to_float((uint16_t)(w[i] >> 16), kBf16);
-                        }
+                    for (int i = 0; i < 4; ++i) {
+                        v[2 * i] += half_bits_to_float((uint16_t)w[i], kBf16);
+                        v[2 * i + 1] += half_bits_to_float((uint16_t)(w[i] >> 16), kBf16);
                     }
-                    *at = make_uint4(pack16<kBf16>(v[0], v[1]), pack16<kBf16>(v[2], v[3]),
-                                     pack16<kBf16>(v[4], v[5]), pack16<kBf16>(v[6], v[7]));
                 }
+                *at = make_uint4(pack16<kBf16>(v[0], v[1]), pack16<kBf16>(v[2], v[3]),
+                                 pack16<kBf16>(v[4], v[5]), pack16<kBf16>(v[6], v[7]));
+            }
+            if constexpr (kTma) {
                 fence_async_shared();
                 __syncwarp();
                 if (lane == 0 && nc < p.N && mw < p.M)
                     tma_store_2d(&p.ymap, nc, mw, smem_u32(stage_out));
-            } else if (m < p.M) {
-#pragma unroll
-                for (int i = 0; i < kCols; ++i) {
-                    const int n = nc + i;
-                    if (n < p.N) {
-                        const size_t o = (size_t)m * p.N + n;
-                        float v = acc[i];
-                        if (p.residual) v += half_bits_to_float(p.residual[o], kBf16);
-                        p.y[o] = float_to_half_bits(v, kBf16);
-                    }
-                }
+            } else {
+                copy_rows<false>(p, stage_out, lane, mw, nc);
             }
         }
         // what was asked for lands, what was stored is written, before the exit
@@ -570,7 +621,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const int qu = u & 3, g = (u >> 2) * S + (int)(crank >> 1);
                     const int m = m0 + (int)rank * kHalf + qu * 32 + lane, n = n0 + 8 * g;
                     if (g >= kTileN / 8 || n >= p.N) break;
-                    exchange8<kBf16>(p, sums + 8 * g * kHalf + qu * 32 + lane, rank, m, n);
+                    exchange8<kBf16, kTma>(p, sums + 8 * g * kHalf + qu * 32 + lane, rank, m, n);
                 }
             }
             __syncwarp();
@@ -649,9 +700,9 @@ cudaError_t launch_fp8_wide(const Fp8Args &a, const Fp8WidePlan &plan, const Wor
     if (!encode_fp8_rows(&p.xmap, a.x, a.M, a.K, kHalf) ||
         !encode_fp8_rows(&p.wmap, a.w, a.N, a.K, kHalf))
         return cudaErrorInvalidValue;
-    p.tma_store = a.N % 8 == 0 && ((uintptr_t)a.y & 15) == 0 && ((uintptr_t)a.residual & 15) == 0;
-    if (p.tma_store && (!encode_rows16(&p.ymap, a.y, a.M, a.N, 32, kStoreCols) ||
-                        (a.residual && !encode_rows16(&p.rmap, a.residual, a.M, a.N, 32, kStoreCols))))
+    const bool tma = a.N % 8 == 0 && ((uintptr_t)a.y & 15) == 0 && ((uintptr_t)a.residual & 15) == 0;
+    if (tma && (!encode_rows16(&p.ymap, a.y, a.M, a.N, 32, kStoreCols) ||
+                (a.residual && !encode_rows16(&p.rmap, a.residual, a.M, a.N, 32, kStoreCols))))
         return cudaErrorInvalidValue;
     p.xs = a.xs;
     p.ws = a.ws;
@@ -673,22 +724,26 @@ cudaError_t launch_fp8_wide(const Fp8Args &a, const Fp8WidePlan &plan, const Wor
     cudaLaunchConfig_t cfg;
     cudaLaunchAttribute attr[2];
     config(cfg, attr, plan.pairs, plan.ksplit, stream);
-    return a.bf16 ? cudaLaunchKernelEx(&cfg, fp8_wide_kernel<true>, p)
-                  : cudaLaunchKernelEx(&cfg, fp8_wide_kernel<false>, p);
+    if (tma) return a.bf16 ? cudaLaunchKernelEx(&cfg, fp8_wide_kernel<true, true>, p)
+                           : cudaLaunchKernelEx(&cfg, fp8_wide_kernel<false, true>, p);
+    return a.bf16 ? cudaLaunchKernelEx(&cfg, fp8_wide_kernel<true, false>, p)
+                  : cudaLaunchKernelEx(&cfg, fp8_wide_kernel<false, false>, p);
 }
 
 cudaError_t fp8_wide_init(const DeviceInfo &) {
-    cudaError_t e = cudaFuncSetAttribute(
-        (const void *)fp8_wide_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
-    if (e != cudaSuccess) return e;
-    e = cudaFuncSetAttribute((const void *)fp8_wide_kernel<true>,
-                             cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+    const void *kernels[] = {
+        (const void *)fp8_wide_kernel<false, false>, (const void *)fp8_wide_kernel<false, true>,
+        (const void *)fp8_wide_kernel<true, false>, (const void *)fp8_wide_kernel<true, true>};
+    cudaError_t e = cudaSuccess;
+    for (const void *k : kernels)
+        if (e == cudaSuccess)
+            e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
     for (int k = 2; k <= kMaxSplit && e == cudaSuccess; ++k) {
         cudaLaunchConfig_t cfg;
         cudaLaunchAttribute attr[2];
         config(cfg, attr, k, k, nullptr);
         cfg.numAttrs = 1;
-        e = cudaOccupancyMaxActiveClusters(&g_clusters[k], fp8_wide_kernel<true>, &cfg);
+        e = cudaOccupancyMaxActiveClusters(&g_clusters[k], fp8_wide_kernel<true, true>, &cfg);
     }
     return e;
 }
