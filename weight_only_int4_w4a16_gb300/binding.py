@@ -366,6 +366,14 @@ def _shaped(t: torch.Tensor, dtype, shape, name: str) -> int:
     return t.data_ptr()
 
 
+def _output(t, shape, dtype, like: torch.Tensor, name: str):
+    """(t, its address), checked, or a new tensor on like's device."""
+    if t is None:
+        t = torch.empty(shape, dtype=dtype, device=like.device)
+        return t, t.data_ptr()
+    return t, _shaped(t, dtype, shape, name)
+
+
 def _dtype16(dt) -> int:
     if dt not in _DTYPE_OF:
         raise TypeError(f"the 16-bit type must be float16 or bfloat16, got {dt}")
@@ -404,37 +412,26 @@ def w4a16_fp8_linear(x: torch.Tensor, x_scales: torch.Tensor, w: torch.Tensor,
     xs = _shaped(x_scales, torch.float32, (M, G), "x_scales")
     ws = _shaped(w_scales, torch.float32, ((N + GROUP - 1) // GROUP, G), "w_scales")
     r = None if residual is None else _shaped(residual, dtype, (M, N), "residual")
-    if y is None:
-        y = torch.empty((M, N), dtype=dtype, device=x.device)
-    yp = _shaped(y, dtype, (M, N), "y")
+    y, yp = _output(y, (M, N), dtype, x, "y")
     _check(lib.w4a16_fp8_linear(xp, xs, wp, ws, M, N, K, dt, epilogue, r, yp,
                                 _stream_for(x, stream, x, x_scales, w, w_scales, residual, y)),
            "w4a16_fp8_linear")
     return y
 
 
-def _norm(x, weight, residual, eps, sum_out, y, q, scales, stream, what):
-    M, H = x.shape
+def _norm_inputs(x, weight, residual, sum_out):
+    """(M, H, dtype code, addresses of x, weight, residual; sum_out and its address)."""
+    M, H = _rows2d(x, "x")
     dt = x.dtype
     code = _dtype16(dt)
     xp, wp = _shaped(x, dt, (M, H), "x"), _shaped(weight, dt, (H,), "weight")
-    rp = sp = yp = qp = cp = None
-    if residual is not None:
-        rp = _shaped(residual, dt, (M, H), "residual")
-        if sum_out is None:
-            sum_out = torch.empty((M, H), dtype=dt, device=x.device)
-        sp = _shaped(sum_out, dt, (M, H), "sum_out")
-    elif sum_out is not None:
-        raise ValueError("sum_out needs a residual")
-    if y is not None:
-        yp = _shaped(y, dt, (M, H), "y")
-    if q is not None:
-        qp = _shaped(q, FP8, (M, H), "q")
-        cp = _shaped(scales, torch.float32, (M, (H + GROUP - 1) // GROUP), "scales")
-    _check(lib.w4a16_rmsnorm(xp, rp, wp, M, H, eps, code, sp, yp, qp, cp,
-                             _stream_for(x, stream, x, weight, residual, sum_out, y, q, scales)),
-           what)
-    return sum_out
+    if residual is None:
+        if sum_out is not None:
+            raise ValueError("sum_out needs a residual")
+        return M, H, code, xp, wp, None, None, None
+    rp = _shaped(residual, dt, (M, H), "residual")
+    sum_out, sp = _output(sum_out, (M, H), dt, x, "sum_out")
+    return M, H, code, xp, wp, rp, sum_out, sp
 
 
 def w4a16_rmsnorm(x: torch.Tensor, weight: torch.Tensor, residual=None, eps: float = 1e-6,
@@ -442,24 +439,25 @@ def w4a16_rmsnorm(x: torch.Tensor, weight: torch.Tensor, residual=None, eps: flo
     """y [M, H] = h / sqrt(mean(h^2) + eps) * weight with h = x (+ residual).
     Returns y, or (y, sum_out) when a residual is given: sum_out is h rounded to
     the 16-bit type (sum_out=residual updates the residual in place)."""
-    M, H = _rows2d(x, "x")
-    if y is None:
-        y = torch.empty((M, H), dtype=x.dtype, device=x.device)
-    s = _norm(x, weight, residual, eps, sum_out, y, None, None, stream, "w4a16_rmsnorm")
-    return y if s is None else (y, s)
+    M, H, code, xp, wp, rp, sum_out, sp = _norm_inputs(x, weight, residual, sum_out)
+    y, yp = _output(y, (M, H), x.dtype, x, "y")
+    _check(lib.w4a16_rmsnorm(xp, rp, wp, M, H, eps, code, sp, yp, None, None,
+                             _stream_for(x, stream, x, weight, residual, sum_out, y)),
+           "w4a16_rmsnorm")
+    return y if residual is None else (y, sum_out)
 
 
 def w4a16_rmsnorm_fp8(x: torch.Tensor, weight: torch.Tensor, residual=None, eps: float = 1e-6,
                       sum_out=None, q=None, scales=None, stream=None):
     """w4a16_rmsnorm with its rows in 8 bits: (q [M, H], scales [M, ceil(H/128)]),
     and sum_out third when a residual is given."""
-    M, H = _rows2d(x, "x")
-    if q is None:
-        q = torch.empty((M, H), dtype=FP8, device=x.device)
-    if scales is None:
-        scales = torch.empty((M, (H + GROUP - 1) // GROUP), dtype=torch.float32, device=x.device)
-    s = _norm(x, weight, residual, eps, sum_out, None, q, scales, stream, "w4a16_rmsnorm_fp8")
-    return (q, scales) if s is None else (q, scales, s)
+    M, H, code, xp, wp, rp, sum_out, sp = _norm_inputs(x, weight, residual, sum_out)
+    q, qp = _output(q, (M, H), FP8, x, "q")
+    scales, cp = _output(scales, (M, (H + GROUP - 1) // GROUP), torch.float32, x, "scales")
+    _check(lib.w4a16_rmsnorm(xp, rp, wp, M, H, eps, code, sp, None, qp, cp,
+                             _stream_for(x, stream, x, weight, residual, sum_out, q, scales)),
+           "w4a16_rmsnorm_fp8")
+    return (q, scales) if residual is None else (q, scales, sum_out)
 
 
 def w4a16_fp8_quant(x: torch.Tensor, epilogue: int = EPILOGUE_NONE, q=None, scales=None,
@@ -469,13 +467,9 @@ def w4a16_fp8_quant(x: torch.Tensor, epilogue: int = EPILOGUE_NONE, q=None, scal
     M, cols = _rows2d(x, "x")
     dt = _dtype16(x.dtype)
     N = cols // 2 if epilogue == EPILOGUE_SILU_MUL else cols
-    G = (N + GROUP - 1) // GROUP
     xp = _shaped(x, x.dtype, (M, cols), "x")
-    if q is None:
-        q = torch.empty((M, N), dtype=FP8, device=x.device)
-    if scales is None:
-        scales = torch.empty((M, G), dtype=torch.float32, device=x.device)
-    qp, cp = _shaped(q, FP8, (M, N), "q"), _shaped(scales, torch.float32, (M, G), "scales")
+    q, qp = _output(q, (M, N), FP8, x, "q")
+    scales, cp = _output(scales, (M, (N + GROUP - 1) // GROUP), torch.float32, x, "scales")
     _check(lib.w4a16_fp8_quant(xp, M, cols, epilogue, dt, qp, cp,
                                _stream_for(x, stream, x, q, scales)), "w4a16_fp8_quant")
     return q, scales
