@@ -150,16 +150,22 @@ __device__ __forceinline__ void quant8(float (&v)[8], uint8_t *q, float *scale, 
 
 // silu(g) * u = g / (1 + e^-g) * u for a 16-bit g.  e^-g = 2^(-g L), L = log2(e) =
 // H + R with H the 13 leading bits of L: -g H is exact in fp32 (11 + 13 bits), and
-// 2^(-g R) = 1 - g R ln 2 to first order (|g R| is at most 4e-5 |g|, and where |g| is
+// 2^(-g R) = 1 - g R ln 2 to first order (|g R| is at most 7e-5 |g|, and where |g| is
 // large the other factor makes the sum 1, or the result nothing).  So the
 // exponential's argument carries no rounding error, which |g| would magnify, at the
 // price of a product and an addition.  R > 0: an infinite 2^(-g H) stays infinite.
+// The quotient is corrected like quant8's; its divisor stops at 2^126, whose
+// reciprocal is still a normal number (the quotient is then below any scale).
 __device__ __forceinline__ float silu_mul(float g, float u) {
     constexpr float kH = 1.442626953125f, kRLn2 = 4.719484162e-05f;
     float e;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(-g * kH));
     e = fmaf(e, -g * kRLn2, e);
-    return __fdividef(g, 1.f + e) * u;
+    const float s = fminf(1.f + e, 8.50705917e37f);
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(s));
+    const float q = g * r;
+    return fmaf(fmaf(-s, q, g), r, q) * u;
 }
 
 // ---------------------------------------------------------------------------
