@@ -41,6 +41,35 @@ __device__ __forceinline__ void chain_start() {
     asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
+// Two fp32 values in one 64-bit register: the packed instructions round each as the
+// scalar ones do and take half their issue slots, which is what bounds these kernels
+// beside memory.
+typedef unsigned long long f2;
+__device__ __forceinline__ f2 pack(float lo, float hi) {
+    f2 d;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(lo), "f"(hi));
+    return d;
+}
+__device__ __forceinline__ f2 both(float v) { return pack(v, v); }
+__device__ __forceinline__ float lo(f2 v) { return __uint_as_float((uint32_t)v); }
+__device__ __forceinline__ float hi(f2 v) { return __uint_as_float((uint32_t)(v >> 32)); }
+__device__ __forceinline__ f2 add2(f2 a, f2 b) {
+    f2 d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ __forceinline__ f2 mul2(f2 a, f2 b) {
+    f2 d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c) {
+    f2 d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+__device__ __forceinline__ f2 neg2(f2 a) { return a ^ 0x8000000080000000ull; }
+
 template <bool kBf16>
 __device__ __forceinline__ float to_float(uint16_t h) {
     if constexpr (kBf16) return __uint_as_float((uint32_t)h << 16);
@@ -52,39 +81,38 @@ __device__ __forceinline__ uint16_t to_16(float v) {  // nearest, ties to even
     else return __half_as_ushort(__float2half_rn(v));
 }
 
-// Elements c .. c + 7 of a row (zeros past its n elements).
+// Elements c .. c + 7 of a row (zeros past its n elements), in pairs.
 template <bool kBf16, bool kVec>
-__device__ __forceinline__ void load8(const uint16_t *row, int c, int n, float (&v)[8]) {
+__device__ __forceinline__ void load8(const uint16_t *row, int c, int n, f2 (&v)[4]) {
     if constexpr (kVec) {  // n is a multiple of 8
         uint4 u = make_uint4(0, 0, 0, 0);
         if (c < n) u = *reinterpret_cast<const uint4 *>(row + c);
         const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            v[2 * i] = to_float<kBf16>((uint16_t)w[i]);
-            v[2 * i + 1] = to_float<kBf16>((uint16_t)(w[i] >> 16));
-        }
+        for (int i = 0; i < 4; ++i)
+            v[i] = pack(to_float<kBf16>((uint16_t)w[i]), to_float<kBf16>((uint16_t)(w[i] >> 16)));
     } else {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = c + i < n ? to_float<kBf16>(row[c + i]) : 0.f;
+        for (int i = 0; i < 8; i += 2)
+            v[i / 2] = pack(c + i < n ? to_float<kBf16>(row[c + i]) : 0.f,
+                            c + i + 1 < n ? to_float<kBf16>(row[c + i + 1]) : 0.f);
     }
 }
 
 template <bool kBf16, bool kVec>
-__device__ __forceinline__ void store8(uint16_t *row, int c, int n, const float (&v)[8]) {
+__device__ __forceinline__ void store8(uint16_t *row, int c, int n, const f2 (&v)[4]) {
     if constexpr (kVec) {
         if (c < n) {
             uint32_t w[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-                w[i] = (uint32_t)to_16<kBf16>(v[2 * i]) |
-                       (uint32_t)to_16<kBf16>(v[2 * i + 1]) << 16;
+                w[i] = (uint32_t)to_16<kBf16>(lo(v[i])) | (uint32_t)to_16<kBf16>(hi(v[i])) << 16;
             *reinterpret_cast<uint4 *>(row + c) = make_uint4(w[0], w[1], w[2], w[3]);
         }
     } else {
 #pragma unroll
         for (int i = 0; i < 8; ++i)
-            if (c + i < n) row[c + i] = to_16<kBf16>(v[i]);
+            if (c + i < n) row[c + i] = to_16<kBf16>(i & 1 ? hi(v[i / 2]) : lo(v[i / 2]));
     }
 }
 
@@ -112,39 +140,39 @@ __device__ __forceinline__ float group_max(float a) {
 // A lane's 8 elements of its group -> 8 codes of row q and, from the group's
 // first lane, the group's scale.  All lanes of the warp call it together.
 template <bool kVec>
-__device__ __forceinline__ void quant8(float (&v)[8], uint8_t *q, float *scale, int c, int n) {
+__device__ __forceinline__ void quant8(f2 (&v)[4], uint8_t *q, float *scale, int c, int n) {
     float a = 0.f;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) a = max_abs_nan(a, v[i]);
+    for (int i = 0; i < 4; ++i) a = max_abs_nan(max_abs_nan(a, lo(v[i])), hi(v[i]));
     a = group_max(a);
     if (__any_sync(0xffffffffu, !(a <= FLT_MAX))) {
         // an Inf or NaN in one of the warp's groups: make it NaN, and the largest
         // magnitude that of the others
         a = 0.f;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            v[i] += v[i] - v[i];
-            a = fmaxf(a, fabsf(v[i]));  // fmaxf passes over NaN
+        for (int i = 0; i < 4; ++i) {
+            v[i] = add2(v[i], add2(v[i], neg2(v[i])));
+            a = fmaxf(fmaxf(a, fabsf(lo(v[i]))), fabsf(hi(v[i])));  // fmaxf passes over NaN
         }
         a = group_max(a);
     }
     const float s = __fdiv_rn(fmaxf(a, kScaleFloor), kE4m3Max);
-    const float r = __frcp_rn(s);
+    const f2 r = both(__frcp_rn(s)), ns = both(-s);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const float q0 = v[i] * r;
-        v[i] = fmaf(fmaf(-q0, s, v[i]), r, q0);
+    for (int i = 0; i < 4; ++i) {
+        const f2 q0 = mul2(v[i], r);
+        v[i] = fma2(fma2(q0, ns, v[i]), r, q0);
     }
     if (c >= n) return;
     if (c % kGroup == 0) *scale = s;
-    const uint32_t lo = e4m3x2(v[0], v[1]) | e4m3x2(v[2], v[3]) << 16;
-    const uint32_t hi = e4m3x2(v[4], v[5]) | e4m3x2(v[6], v[7]) << 16;
+    const uint32_t c0 = e4m3x2(lo(v[0]), hi(v[0])) | e4m3x2(lo(v[1]), hi(v[1])) << 16;
+    const uint32_t c1 = e4m3x2(lo(v[2]), hi(v[2])) | e4m3x2(lo(v[3]), hi(v[3])) << 16;
     if constexpr (kVec) {
-        *reinterpret_cast<uint2 *>(q + c) = make_uint2(lo, hi);
+        *reinterpret_cast<uint2 *>(q + c) = make_uint2(c0, c1);
     } else {
 #pragma unroll
         for (int i = 0; i < 8; ++i)
-            if (c + i < n) q[c + i] = (uint8_t)((i < 4 ? lo : hi) >> (8 * (i & 3)));
+            if (c + i < n) q[c + i] = (uint8_t)((i < 4 ? c0 : c1) >> (8 * (i & 3)));
     }
 }
 
@@ -156,16 +184,19 @@ __device__ __forceinline__ void quant8(float (&v)[8], uint8_t *q, float *scale, 
 // price of a product and an addition.  R > 0: an infinite 2^(-g H) stays infinite.
 // The quotient is corrected like quant8's; its divisor stops at 2^126, whose
 // reciprocal is still a normal number (the quotient is then below any scale).
-__device__ __forceinline__ float silu_mul(float g, float u) {
-    constexpr float kH = 1.442626953125f, kRLn2 = 4.719484162e-05f;
-    float e;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(-g * kH));
-    e = fmaf(e, -g * kRLn2, e);
-    const float s = fminf(1.f + e, 8.50705917e37f);
-    float r;
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(s));
-    const float q = g * r;
-    return fmaf(fmaf(-s, q, g), r, q) * u;
+__device__ __forceinline__ f2 silu_mul(f2 g, f2 u) {
+    constexpr float kH = 1.442626953125f, kRLn2 = 4.719484150e-05f, kTop = 8.50705917e37f;
+    const f2 t = mul2(g, both(-kH));
+    float e0, e1, r0, r1;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e0) : "f"(lo(t)));
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e1) : "f"(hi(t)));
+    f2 s = pack(e0, e1);
+    s = add2(fma2(s, mul2(g, both(-kRLn2)), s), both(1.f));
+    s = pack(fminf(lo(s), kTop), fminf(hi(s), kTop));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r0) : "f"(lo(s)));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r1) : "f"(hi(s)));
+    const f2 r = pack(r0, r1), q = mul2(g, r);
+    return mul2(fma2(fma2(neg2(s), q, g), r, q), u);
 }
 
 // ---------------------------------------------------------------------------
@@ -181,17 +212,16 @@ __global__ void __launch_bounds__(1024) rmsnorm_kernel(NormArgs a) {
     const size_t row = blockIdx.x;
     const uint16_t *x = a.x + row * a.H;
     chain_start();
-    float h[V][8];
-    float sum = 0.f;
+    f2 h[V][4], sums = both(0.f);
 #pragma unroll
     for (int s = 0; s < V; ++s) {
         const int c = (s * (int)blockDim.x + (int)threadIdx.x) * kLaneElems;
         load8<kBf16, kVec>(x, c, a.H, h[s]);
         if (a.residual) {
-            float r[8];
+            f2 r[4];
             load8<kBf16, kVec>(a.residual + row * a.H, c, a.H, r);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) h[s][i] += r[i];
+            for (int i = 0; i < 4; ++i) h[s][i] = add2(h[s][i], r[i]);
         }
     }
 #pragma unroll
@@ -199,8 +229,9 @@ __global__ void __launch_bounds__(1024) rmsnorm_kernel(NormArgs a) {
         const int c = (s * (int)blockDim.x + (int)threadIdx.x) * kLaneElems;
         if (a.sum_out) store8<kBf16, kVec>(a.sum_out + row * a.H, c, a.H, h[s]);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) sum = fmaf(h[s][i], h[s][i], sum);
+        for (int i = 0; i < 4; ++i) sums = fma2(h[s][i], h[s][i], sums);
     }
+    float sum = lo(sums) + hi(sums);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
     if (lane == 0) warp_sums[warp] = sum;
@@ -213,10 +244,10 @@ __global__ void __launch_bounds__(1024) rmsnorm_kernel(NormArgs a) {
 #pragma unroll
     for (int s = 0; s < V; ++s) {
         const int c = (s * (int)blockDim.x + (int)threadIdx.x) * kLaneElems;
-        float w[8];  // every row's: it comes from L1 or L2
+        f2 w[4];  // every row's: it comes from L1 or L2
         load8<kBf16, kVec>(a.weight, c, a.H, w);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) h[s][i] = h[s][i] * rstd * w[i];
+        for (int i = 0; i < 4; ++i) h[s][i] = mul2(mul2(h[s][i], both(rstd)), w[i]);
         if (a.y) store8<kBf16, kVec>(a.y + row * a.H, c, a.H, h[s]);
         if (a.q)
             quant8<kVec>(h[s], a.q + row * a.H,
@@ -241,7 +272,7 @@ __global__ void __launch_bounds__(kQuantThreads) quant_kernel(QuantArgs a) {
     const size_t row = blockIdx.y;
     const uint16_t *x = a.x + row * (kSilu ? 2 * (size_t)a.N : (size_t)a.N);
     const int first = (int)(blockIdx.x * U * kQuantThreads + threadIdx.x) * kLaneElems;
-    float v[U][8], u[U][8];
+    f2 v[U][4], u[U][4];
 #pragma unroll
     for (int s = 0; s < U; ++s) {  // all loads, then the arithmetic
         const int c = first + s * kQuantThreads * kLaneElems;
@@ -253,7 +284,7 @@ __global__ void __launch_bounds__(kQuantThreads) quant_kernel(QuantArgs a) {
         const int c = first + s * kQuantThreads * kLaneElems;
         if constexpr (kSilu) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) v[s][i] = silu_mul(v[s][i], u[s][i]);
+            for (int i = 0; i < 4; ++i) v[s][i] = silu_mul(v[s][i], u[s][i]);
         }
         quant8<kVec>(v[s], a.q + row * a.N, a.scales + row * a.G + c / kGroup, c, a.N);
     }
