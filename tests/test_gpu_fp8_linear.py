@@ -93,6 +93,32 @@ def test_linear_matches_definition(w4, M, N, K, dtype, residual):
     check(y, want, A, K, f"M={M} N={N} K={K}")
 
 
+# one shape or two for every way the work is cut: up to 64 tokens, whole tiles, clusters
+# of 2 .. 8 CTAs per tile, runs of blocks with tiles in two and three pieces; more
+# tokens, whole tiles, clusters of 2, 3 and 4 pairs, whole tiles and then runs; each
+# with rows that TMA can address (N a multiple of 8) and cannot, and with scale rows
+# of whole 16-byte pieces (K / 128 a multiple of 4) and not
+PLANS = [
+    (2, 19456, 256), (2, 300, 384), (40, 384, 1152), (50, 1023, 2048), (7, 5120, 2304),
+    (16, 9000, 1024), (5, 12800, 1280), (33, 12801, 1024), (64, 34816, 256),
+    (70, 19456, 128), (128, 384, 1152), (512, 3840, 1024), (256, 5120, 1536), (256, 5121, 1664),
+    (100, 704, 2048), (100, 701, 2048), (1100, 8200, 640), (1100, 8201, 512), (1100, 8202, 640),
+    (900, 10240, 384),
+]
+
+
+@pytest.mark.parametrize("M,N,K", PLANS)
+@pytest.mark.parametrize("dtype,residual", [(BF16, True), (F16, False)])
+def test_every_way_to_cut_the_work(w4, M, N, K, dtype, residual):
+    ops = ref.make_linear(M + N * 3 + K, M, N, K, dtype, residual)
+    y = torch.full((M, N), float("nan"), dtype=dtype, device=DEV)
+    call(w4, ops, dtype, y=y)
+    again = call(w4, ops, dtype)
+    assert torch.equal(y.view(torch.int16), again.view(torch.int16))
+    want, A = ref.linear(*ops)
+    check(y, want, A, K, f"M={M} N={N} K={K}")
+
+
 @pytest.mark.parametrize("M,N,K", [(1, 200, 272), (20, 300, 1152), (130, 520, 640),
                                    (700, 1100, 528), (4, 1024, 8192)])
 def test_integer_operands_are_exact(w4, M, N, K):
