@@ -71,6 +71,8 @@ constexpr int kSmem = 1024 + kStages * kStage + kSumWarps * kStoreBytes +
 constexpr uint32_t kIdesc =  // D f32, A and B e4m3 (0), N = 256, M = 256
     (1u << 4) | ((uint32_t)(kTileN >> 3) << 17) | ((uint32_t)(kTileM >> 4) << 24);
 
+static_assert(kHalf * kTileN * 4 <= kStages * kStage, "a split tile's sums fit the stages");
+
 struct WideParams {
     CUtensorMap xmap;  // x: (K bytes, M rows), box {128, 128}, 128-byte swizzle
     CUtensorMap wmap;  // w: (K bytes, N rows), the same
@@ -174,15 +176,16 @@ __device__ __forceinline__ void copy_rows(const WideParams &p, uint8_t *staging,
     const int rows = min(32, p.M - m), cols = min(kStoreCols, p.N - n);
     // element (r, c) of the staging, 128-byte swizzled
     auto at = [&](int r, int c) { return staging + r * 128 + (((c >> 3) ^ (r & 7)) << 4) + (c & 7) * 2; };
+    constexpr int kRows = 8;
     __syncwarp();
-    for (int r0 = 0; r0 < rows; r0 += 8) {
+    for (int r0 = 0; r0 < rows; r0 += kRows) {
         const size_t o = (size_t)(m + r0) * p.N + n;
         if (words) {
             const int c = 2 * lane;
             if (c >= cols) continue;
-            uint32_t v[8];
+            uint32_t v[kRows];
 #pragma unroll
-            for (int r = 0; r < 8; ++r)
+            for (int r = 0; r < kRows; ++r)
                 if (r0 + r < rows) {
                     if constexpr (kIn)
                         v[r] = *reinterpret_cast<const uint32_t *>(p.residual + o + (size_t)r * p.N + c);
@@ -190,7 +193,7 @@ __device__ __forceinline__ void copy_rows(const WideParams &p, uint8_t *staging,
                         v[r] = *reinterpret_cast<const uint32_t *>(at(r0 + r, c));
                 }
 #pragma unroll
-            for (int r = 0; r < 8; ++r)
+            for (int r = 0; r < kRows; ++r)
                 if (r0 + r < rows) {
                     if constexpr (kIn) *reinterpret_cast<uint32_t *>(at(r0 + r, c)) = v[r];
                     else *reinterpret_cast<uint32_t *>(p.y + o + (size_t)r * p.N + c) = v[r];
@@ -200,15 +203,15 @@ __device__ __forceinline__ void copy_rows(const WideParams &p, uint8_t *staging,
             for (int h = 0; h < 2; ++h) {
                 const int c = lane + 32 * h;
                 if (c >= cols) continue;
-                uint16_t v[8];
+                uint16_t v[kRows];
 #pragma unroll
-                for (int r = 0; r < 8; ++r)
+                for (int r = 0; r < kRows; ++r)
                     if (r0 + r < rows) {
                         if constexpr (kIn) v[r] = p.residual[o + (size_t)r * p.N + c];
                         else v[r] = *reinterpret_cast<const uint16_t *>(at(r0 + r, c));
                     }
 #pragma unroll
-                for (int r = 0; r < 8; ++r)
+                for (int r = 0; r < kRows; ++r)
                     if (r0 + r < rows) {
                         if constexpr (kIn) *reinterpret_cast<uint16_t *>(at(r0 + r, c)) = v[r];
                         else p.y[o + (size_t)r * p.N + c] = v[r];
@@ -219,41 +222,85 @@ __device__ __forceinline__ void copy_rows(const WideParams &p, uint8_t *staging,
     __syncwarp();
 }
 
-// y[m][n .. n + 7]: the sums at `sums` (8 columns, kHalf apart) of every CTA of
-// this rank in the cluster's pairs, in K order, + residual, one rounding each
-template <bool kBf16, bool kTma>
-__device__ __forceinline__ void exchange8(const WideParams &p, const float *sums, uint32_t rank,
-                                          int m, int n) {
-    float v[kMaxSplit][8];
+// 32 tokens' kC columns of y (8 or 16), m = the warp's first token, n = the first
+// column: the sums at `sums` (this lane's token, columns kHalf apart) of the CTAs of
+// this rank in the cluster's up to kS pairs, loaded all at once and added in K order,
+// + residual, one rounding each.  Rows that 16-byte accesses do not fit go through
+// `staging` (1 KB of the warp's own), so that they are read and written along the rows.
+template <bool kBf16, bool kTma, int kC, int kS>
+__device__ __forceinline__ void exchange(const WideParams &p, const float *sums, uint4 *staging,
+                                         uint32_t rank, int lane, int m, int n) {
+    constexpr int kQ = kC / 8;      // 16-byte pieces per row
+    constexpr int kStep = 32 / kC;  // rows per step of the copies along the rows
+    const int rows = min(32, p.M - m), cols = min(kC, p.N - n);
+    const size_t o = (size_t)(m + lane) * p.N + n;
+    uint16_t *cells = reinterpret_cast<uint16_t *>(staging);  // [32 tokens][kC columns]
+    const int row0 = lane / kC, col = lane % kC;
+    uint4 r[kQ];
+    if (p.residual) {
+        if constexpr (kTma) {
 #pragma unroll
-    for (int q = 0; q < kMaxSplit; ++q)
+            for (int h = 0; h < kQ; ++h) {
+                r[h] = make_uint4(0, 0, 0, 0);
+                if (lane < rows && 8 * h < cols)
+                    r[h] = *reinterpret_cast<const uint4 *>(p.residual + o + 8 * h);
+            }
+        } else {
+            uint16_t c[kC];
+#pragma unroll
+            for (int i = 0; i < kC; ++i)
+                if (kStep * i + row0 < rows && col < cols)
+                    c[i] = p.residual[(size_t)(m + kStep * i + row0) * p.N + n + col];
+#pragma unroll
+            for (int i = 0; i < kC; ++i) cells[(kStep * i + row0) * kC + col] = c[i];
+            __syncwarp();
+#pragma unroll
+            for (int h = 0; h < kQ; ++h) r[h] = staging[kQ * lane + h];
+            __syncwarp();
+        }
+    }
+    float v[kS][kC];
+#pragma unroll
+    for (int q = 0; q < kS; ++q)
         if (q < p.ksplit) {
             const uint32_t from = map_to_rank(smem_u32(sums), 2 * q + rank);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) v[q][i] = ld_cluster(from + i * kHalf * 4);
+            for (int i = 0; i < kC; ++i) v[q][i] = ld_cluster(from + i * kHalf * 4);
         }
-    const size_t o = (size_t)m * p.N + n;
-    float res[8];
+    uint32_t out[kC / 2];
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-        res[i] = p.residual && m < p.M && n + i < p.N ? half_bits_to_float(p.residual[o + i], kBf16)
-                                                      : 0.f;
+    for (int i = 0; i < kC / 2; ++i) {
+        float lo = v[0][2 * i], hi = v[0][2 * i + 1];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-#pragma unroll
-        for (int q = 1; q < kMaxSplit; ++q)
-            if (q < p.ksplit) v[0][i] += v[q][i];
-        v[0][i] += res[i];
+        for (int q = 1; q < kS; ++q)
+            if (q < p.ksplit) {
+                lo += v[q][2 * i];
+                hi += v[q][2 * i + 1];
+            }
+        if (p.residual) {
+            const uint4 w = r[i / 4];
+            const uint32_t e = i % 4 == 0 ? w.x : i % 4 == 1 ? w.y : i % 4 == 2 ? w.z : w.w;
+            lo += half_bits_to_float((uint16_t)e, kBf16);
+            hi += half_bits_to_float((uint16_t)(e >> 16), kBf16);
+        }
+        out[i] = pack16<kBf16>(lo, hi);
     }
-    if (m >= p.M) return;
-    if constexpr (kTma) {  // what allows TMA allows 16-byte stores
-        *reinterpret_cast<uint4 *>(p.y + o) =
-            make_uint4(pack16<kBf16>(v[0][0], v[0][1]), pack16<kBf16>(v[0][2], v[0][3]),
-                       pack16<kBf16>(v[0][4], v[0][5]), pack16<kBf16>(v[0][6], v[0][7]));
-    } else {
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-            if (n + i < p.N) p.y[o + i] = float_to_half_bits(v[0][i], kBf16);
+    for (int h = 0; h < kQ; ++h) {
+        const uint4 y = make_uint4(out[4 * h], out[4 * h + 1], out[4 * h + 2], out[4 * h + 3]);
+        if constexpr (!kTma)
+            staging[kQ * lane + h] = y;
+        else if (lane < rows && 8 * h < cols)  // what allows TMA allows 16-byte stores
+            *reinterpret_cast<uint4 *>(p.y + o + 8 * h) = y;
+    }
+    if constexpr (!kTma) {
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < kC; ++i)
+            if (kStep * i + row0 < rows && col < cols)
+                p.y[(size_t)(m + kStep * i + row0) * p.N + n + col] =
+                    cells[(kStep * i + row0) * kC + col];
+        __syncwarp();
     }
 }
 
@@ -315,7 +362,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     cluster_sync();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
-    float *sums = reinterpret_cast<float *>(smem);  // [256 columns][128 tokens], after the stages
+    // a split tile's sums, [256 columns][128 tokens], over the stages
+    float *sums = reinterpret_cast<float *>(smem);
     auto fail = [&](int code) {
         *abort = 1;
         atomicOr(p.status, code);
@@ -610,18 +658,21 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
         if (p.ksplit > 1) {
             // the exchange: the cluster's CTAs of these 128 tokens share out the tile's
-            // 32 groups of 8 columns; a warp takes a group for 32 tokens (lane = token),
-            // adds the CTAs' sums in K order (which is rank order) and writes y.  It
-            // stays with these warps: the others keep few registers.
+            // columns, in groups of 16 (two pairs) or 8; a warp takes a group for 32
+            // tokens (lane = token).  It stays with these warps: the others keep few
+            // registers.
             cluster_sync();
             if (!*abort) {
-                const int S = p.ksplit;
+                const int S = p.ksplit, width = S == 2 ? 16 : 8;
+                uint4 *own = reinterpret_cast<uint4 *>(stage_out);
                 tile_at(p, blockIdx.x / (2 * S), m0, n0);
                 for (int u = warp;; u += kSumWarps) {
-                    const int qu = u & 3, g = (u >> 2) * S + (int)(crank >> 1);
-                    const int m = m0 + (int)rank * kHalf + qu * 32 + lane, n = n0 + 8 * g;
-                    if (g >= kTileN / 8 || n >= p.N) break;
-                    exchange8<kBf16, kTma>(p, sums + 8 * g * kHalf + qu * 32 + lane, rank, m, n);
+                    const int qu = u & 3, c = ((u >> 2) * S + (int)(crank >> 1)) * width;
+                    const int m = m0 + (int)rank * kHalf + qu * 32, n = n0 + c;
+                    if (c >= kTileN || n >= p.N) break;
+                    const float *from = sums + c * kHalf + qu * 32 + lane;
+                    if (S == 2) exchange<kBf16, kTma, 16, 2>(p, from, own, rank, lane, m, n);
+                    else exchange<kBf16, kTma, 8, kMaxSplit>(p, from, own, rank, lane, m, n);
                 }
             }
             __syncwarp();
