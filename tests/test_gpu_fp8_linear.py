@@ -104,6 +104,8 @@ PLANS = [
     (70, 19456, 128), (128, 384, 1152), (512, 3840, 1024), (256, 5120, 1536), (256, 5121, 1664),
     (100, 704, 2048), (100, 701, 2048), (1100, 8200, 640), (1100, 8201, 512), (1100, 8202, 640),
     (900, 10240, 384),
+    # long tiles in equal runs: the last wave would be mostly empty
+    (3, 10300, 5648), (20, 20480, 2816), (50, 21001, 2704), (300, 10240, 3328), (500, 10241, 3216),
 ]
 
 

@@ -802,10 +802,11 @@ int w4a16_fp8_linear(const uint8_t *x, const float *x_scales, const uint8_t *w,
     const State &st = g_state;
     if (!st.initialized) return W4A16_ERR_NOT_INITIALIZED;
     const Fp8Args a{x, x_scales, w, w_scales, residual, y, M, N, K, dtype == W4A16_DTYPE_BF16};
+    const cudaStream_t s = (cudaStream_t)stream;
     const bool wide = fp8_takes_wide(M);
     const cudaError_t e =
-        wide ? launch_fp8_wide(a, plan_fp8_wide(M, N, K, st.dev, st.ws), st.ws, (cudaStream_t)stream)
-             : launch_fp8(a, plan_fp8(M, N, K, st.dev, st.ws), st.ws, (cudaStream_t)stream);
+        wide ? launch_fp8_wide(a, plan_fp8_wide(M, N, K, st.dev, st.ws), st.ws, s)
+             : launch_fp8(a, plan_fp8(M, N, K, st.dev, st.ws), st.ws, s);
     if (e != cudaSuccess) return cuda_fail(e);
     g_launches.fetch_add(1, std::memory_order_relaxed);
     if (st.log)

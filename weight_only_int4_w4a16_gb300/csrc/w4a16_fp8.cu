@@ -72,8 +72,9 @@ struct Fp8Params {
 template <int T>
 struct Cfg {
     // warps that add the sums: a quarter of the rows each, and from 32 tokens on
-    // half of the tokens (one quarter's four warps alone fall behind the loads: at
-    // 64 tokens 0.36 us a block against 0.30)
+    // half of the tokens, so that a tile's outputs are written by twice the threads
+    // (64 tokens, N 20480: K 2048 23.2 us against 25.2 with four warps, K 5120 43.3
+    // against 43.6, K 17408 119.4 against 116.2)
     static constexpr int kSumWarps = T >= 32 ? 8 : 4;
     static constexpr int kCols = T / (kSumWarps / 4);  // tokens per thread
     static constexpr int kTmaWarp = kSumWarps, kMmaWarp = kSumWarps + 1;
@@ -186,7 +187,8 @@ __device__ __forceinline__ void store4(const Fp8Params &p, int m, int n, bool ve
     if (vec) {
         if (n < p.N)
             *reinterpret_cast<uint2 *>(dst) =
-                make_uint2((uint32_t)h[0] | (uint32_t)h[1] << 16, (uint32_t)h[2] | (uint32_t)h[3] << 16);
+                make_uint2((uint32_t)h[0] | (uint32_t)h[1] << 16,
+                           (uint32_t)h[2] | (uint32_t)h[3] << 16);
     } else {
 #pragma unroll
         for (int i = 0; i < 4; ++i)
@@ -195,7 +197,8 @@ __device__ __forceinline__ void store4(const Fp8Params &p, int m, int n, bool ve
 }
 
 template <int T>
-__global__ void __launch_bounds__(Cfg<T>::kThreads, 1) fp8_kernel(const __grid_constant__ Fp8Params p) {
+__global__ void __launch_bounds__(Cfg<T>::kThreads, 1)
+    fp8_kernel(const __grid_constant__ Fp8Params p) {
     using C = Cfg<T>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
@@ -213,8 +216,9 @@ __global__ void __launch_bounds__(Cfg<T>::kThreads, 1) fp8_kernel(const __grid_c
     grid_dependents_launch();
     if (threadIdx.x == C::kTmaWarp * 32) {
         for (int i = 0; i < NS; ++i) {
-            mbar_init(smem_u32(full + i), 1 + 32);          // the TMA bytes, each lane's scales
-            mbar_init(smem_u32(empty + i), 1 + C::kSumWarps);  // the products, each reader of the scales
+            mbar_init(smem_u32(full + i), 1 + 32);  // the TMA bytes, each lane's scales
+            // the products, each reader of the scales
+            mbar_init(smem_u32(empty + i), 1 + C::kSumWarps);
         }
         for (int i = 0; i < kDBufs; ++i) {
             mbar_init(smem_u32(d_full + i), 1);
@@ -281,7 +285,8 @@ __global__ void __launch_bounds__(Cfg<T>::kThreads, 1) fp8_kernel(const __grid_c
                             cp_async4(sc + 4 * (b * T + tt), live && b < nb ? src + b : p.xs,
                                       live && b < nb ? 4u : 0u);
                 }
-                if (lane < nb) cp_async4(sc + 4 * (kSub * T + lane), p.ws + (size_t)t * p.G + j + lane, 4u);
+                if (lane < nb)
+                    cp_async4(sc + 4 * (kSub * T + lane), p.ws + (size_t)t * p.G + j + lane, 4u);
                 cp_async_arrive(bar);
             }
         }
@@ -314,7 +319,8 @@ __global__ void __launch_bounds__(Cfg<T>::kThreads, 1) fp8_kernel(const __grid_c
                 tc_fence_after();
                 if (elect_one()) {
                     const uint32_t st = stages + s * C::kStage;
-                    const uint64_t a = smem_desc_sw128(st), b = smem_desc_sw128(st + kSub * kBlockW);
+                    const uint64_t a = smem_desc_sw128(st);
+                    const uint64_t b = smem_desc_sw128(st + kSub * kBlockW);
                     mma_f8_block(tm + d * kSub * T, a, b, C::kIdesc);
                     if (nb > 1)
                         mma_f8_block(tm + (d * kSub + 1) * T, a + (kBlockW >> 4),
@@ -423,7 +429,8 @@ __global__ void __launch_bounds__(Cfg<T>::kThreads, 1) fp8_kernel(const __grid_c
 #pragma unroll
                 for (int i = 0; i < kCols; ++i) acc[i] = 0.f;
                 for (int b = b0; b <= b1; ++b) {
-                    const float *src = p.partials + (size_t)slot_of(p, b, tile0) * T * kTileN + mine;
+                    const float *src =
+                        p.partials + (size_t)slot_of(p, b, tile0) * T * kTileN + mine;
                     float v[kCols];
 #pragma unroll
                     for (int i = 0; i < kCols; ++i)
@@ -461,7 +468,8 @@ __global__ void __launch_bounds__(Cfg<T>::kThreads, 1) fp8_kernel(const __grid_c
 #pragma unroll
                     for (int q = 0; q < kMaxCluster; ++q)
                         if (q < S && m < p.M)
-                            v[i][q] = ld4_cluster(map_to_rank(mine, q) + (uint32_t)(m * kTileN * 4));
+                            v[i][q] =
+                                ld4_cluster(map_to_rank(mine, q) + (uint32_t)(m * kTileN * 4));
                 }
 #pragma unroll
                 for (int i = 0; i < kBatch; ++i) {
@@ -545,22 +553,31 @@ Fp8Plan plan_fp8(int M, int N, int K, const DeviceInfo &dev, const Workspace &ws
     pl.stages = stages_of(pl.T);
     pl.ksplit = 1;
     pl.grid = pl.tiles < dev.sm_count ? pl.tiles : dev.sm_count;
-    // few tiles: the largest cluster that keeps every tile in one wave, with at
-    // least two blocks of K per CTA
+    // few tiles: the largest cluster that keeps every tile in one wave (N 5120: M 8,
+    // K 5120 15.0 us against 19.1 in equal runs; M 64, K 17408 29.3 against 33.4), with
+    // at least two blocks of K per CTA (M 8, N 512, K 1024: 8.8 us, 10.9 with four)
     for (int k = kMaxCluster; k > 1; --k)
         if (pl.tiles <= g_clusters[k] && pl.G >= 2 * k) {
             pl.ksplit = k;
             pl.grid = pl.tiles * k;
             return pl;
         }
-    // whole tiles when they fill the last wave, else equal runs of blocks
+    // whole tiles in turn, or equal runs of blocks.  Whole tiles leave the last wave
+    // partly empty, equal runs add and read back the pieces of split tiles, which
+    // costs what about 20 blocks do.  Microseconds, whole against equal runs:
+    //   empty blocks per CTA   M 8           M 64
+    //   N 20480, K 2048   15   19.1   21.1   23.2   23.2
+    //   N 34048, K 5120   10   37.5   41.6   43.6   45.7
+    //   N 29184, K 5120   20   37.5   35.5   43.6   39.5
+    //   N 20480, K 5120   38   35.7   30.4   43.3   34.2
+    //   N 10752, K 17408  61   49.8   45.7   64.1   49.2
     const int waves = (pl.tiles + dev.sm_count - 1) / dev.sm_count;
+    const long long empty = ((long long)waves * dev.sm_count - pl.tiles) * pl.G;
     const size_t need = (size_t)2 * dev.sm_count * pl.T * kTileN * sizeof(float);
-    if (pl.tiles * 100ll < waves * dev.sm_count * 95ll && (long long)pl.tiles * pl.G >= 4ll * dev.sm_count &&
+    if (empty >= 20ll * dev.sm_count && (long long)pl.tiles * pl.G >= 4ll * dev.sm_count &&
         need <= ws.partial_bytes && pl.tiles <= ws.n_counters - kMmaSchedWords) {
         pl.streamk = true;
         pl.grid = dev.sm_count;
-        pl.ws_bytes = need;
     }
     return pl;
 }
@@ -569,7 +586,8 @@ cudaError_t launch_fp8(const Fp8Args &a, const Fp8Plan &plan, const Workspace &w
                        cudaStream_t stream) {
     Fp8Params p;
     memset(&p, 0, sizeof(p));
-    if (!encode_fp8_rows(&p.wmap, a.w, a.N, a.K, kTileN) || !encode_fp8_rows(&p.xmap, a.x, a.M, a.K, plan.T))
+    if (!encode_fp8_rows(&p.wmap, a.w, a.N, a.K, kTileN) ||
+        !encode_fp8_rows(&p.xmap, a.x, a.M, a.K, plan.T))
         return cudaErrorInvalidValue;
     p.xs = a.xs;
     p.ws = a.ws;

@@ -175,7 +175,9 @@ __device__ __forceinline__ void copy_rows(const WideParams &p, uint8_t *staging,
     const bool words = p.N % 2 == 0 && ((uintptr_t)(kIn ? p.residual : p.y) & 3) == 0;
     const int rows = min(32, p.M - m), cols = min(kStoreCols, p.N - n);
     // element (r, c) of the staging, 128-byte swizzled
-    auto at = [&](int r, int c) { return staging + r * 128 + (((c >> 3) ^ (r & 7)) << 4) + (c & 7) * 2; };
+    auto at = [&](int r, int c) {
+        return staging + r * 128 + (((c >> 3) ^ (r & 7)) << 4) + (c & 7) * 2;
+    };
     constexpr int kRows = 8;
     __syncwarp();
     for (int r0 = 0; r0 < rows; r0 += kRows) {
@@ -188,7 +190,8 @@ __device__ __forceinline__ void copy_rows(const WideParams &p, uint8_t *staging,
             for (int r = 0; r < kRows; ++r)
                 if (r0 + r < rows) {
                     if constexpr (kIn)
-                        v[r] = *reinterpret_cast<const uint32_t *>(p.residual + o + (size_t)r * p.N + c);
+                        v[r] = *reinterpret_cast<const uint32_t *>(
+                            p.residual + o + (size_t)r * p.N + c);
                     else
                         v[r] = *reinterpret_cast<const uint32_t *>(at(r0 + r, c));
                 }
@@ -372,112 +375,112 @@ __global__ void __launch_bounds__(kThreads, 1)
     Walk walk(p);
     int t, j0, j1, m0, n0;
     if (warp >= kSumWarps) {
-    regs_dec<kOtherRegs>();
-    if (warp == kTmaWarp) {
-        // ------------------------------------------------ producer
-        grid_dependency_wait();
-        if (lane == 0) {
-            const uint64_t pol_w = policy_evict_first(), pol_x = policy_evict_last();
-            int c = 0;
+        regs_dec<kOtherRegs>();
+        if (warp == kTmaWarp) {
+            // ------------------------------------------------ producer
+            grid_dependency_wait();
+            if (lane == 0) {
+                const uint64_t pol_w = policy_evict_first(), pol_x = policy_evict_last();
+                int c = 0;
+                bool ok = true;
+                while (ok && walk.next(p, t, j0, j1)) {
+                    tile_at(p, t, m0, n0);
+                    const int mr = m0 + (int)rank * kHalf, nr = n0 + (int)rank * kHalf;
+                    for (int j = j0; j < j1; ++j, ++c) {
+                        const int s = c % kStages;
+                        if (c >= kStages &&
+                            !mbar_wait(smem_u32(empty + s), ((c / kStages) - 1) & 1, abort)) {
+                            fail(kErrSlotWait);
+                            ok = false;
+                            break;
+                        }
+                        const uint32_t st = smem_u32(smem + s * kStage);
+                        // both CTAs' bytes count at the leader's barrier
+                        const uint32_t bar = map_to_rank(smem_u32(full + s), leader);
+                        if (rank == 0) mbar_arrive_expect_tx(smem_u32(full + s), 2 * kStage);
+                        tma_load_2d_pair(st, &p.xmap, j * kGroup, mr, bar, pol_x);
+                        tma_load_2d_pair(st + kStageX, &p.wmap, j * kGroup, nr, bar, pol_w);
+                    }
+                }
+                // every load issued must have landed before the CTA exits: the leader
+                // sees both CTAs' (the other waits for it at the last cluster barrier)
+                if (rank == 0)
+                    for (int i = c - kStages > 0 ? c - kStages : 0; i < c; ++i)
+                        if (!mbar_wait_drain(smem_u32(full + i % kStages), (i / kStages) & 1))
+                            atomicOr(p.status, kErrDrain);
+            }
+        } else if (warp == kMmaWarp) {
+            // ------------------------------------------------ products
+            if (rank == 0) {
+                const uint32_t stages = uniform(smem_u32(smem));
+                const uint32_t bars = uniform(smem_u32(full));
+                const uint32_t tm = uniform(tmem);
+                const uint16_t both = (uint16_t)(3u << leader);
+                int c = 0;
+                bool ok = true;
+                while (ok && walk.next(p, t, j0, j1)) {
+                    for (int j = j0; j < j1; ++j, ++c) {
+                        const int s = c % kStages, d = c % kDBufs;
+                        if (!mbar_wait_all(bars + 8 * s, (c / kStages) & 1, abort)) {
+                            if (lane == 0) fail(kErrStageWait);
+                            ok = false;
+                            break;
+                        }
+                        if (c >= kDBufs && !mbar_wait_all(bars + 8 * (2 * kStages + kDBufs + d),
+                                                          ((c / kDBufs) - 1) & 1, abort)) {
+                            if (lane == 0) fail(kErrSumWait);
+                            ok = false;
+                            break;
+                        }
+                        tc_fence_after();
+                        if (elect_one()) {
+                            const uint64_t a = smem_desc_sw128(stages + s * kStage);
+                            mma_f8_block_pair(tm + d * kTileN, a, a + (kStageX >> 4), kIdesc);
+                            mma_commit_pair(bars + 8 * (2 * kStages + d), both);
+                            mma_commit_pair(bars + 8 * (kStages + s), both);
+                        }
+                    }
+                }
+                // the products issued complete before the tensor memory is freed
+                if (lane == 0)
+                    for (int i = c - kDBufs > 0 ? c - kDBufs : 0; i < c; ++i)
+                        if (!mbar_wait_drain(smem_u32(d_full + i % kDBufs), (i / kDBufs) & 1))
+                            atomicOr(p.status, kErrDrain);
+            }
+        } else if (warp > kMmaWarp) {
+            // ------------------------------------------------ scales
+            // (rows and columns past the end take the last one's: they are not stored)
+            grid_dependency_wait();
+            const int i = (warp - kMmaWarp - 1) * 32 + lane;  // tokens i and i + 64
+            int c = 0;                                        // batches
             bool ok = true;
             while (ok && walk.next(p, t, j0, j1)) {
                 tile_at(p, t, m0, n0);
-                const int mr = m0 + (int)rank * kHalf, nr = n0 + (int)rank * kHalf;
-                for (int j = j0; j < j1; ++j, ++c) {
-                    const int s = c % kStages;
-                    if (c >= kStages &&
-                        !mbar_wait(smem_u32(empty + s), ((c / kStages) - 1) & 1, abort)) {
-                        fail(kErrSlotWait);
+                const int mr = m0 + (int)rank * kHalf + i;
+                const float *x0 = p.xs + (size_t)min(mr, p.M - 1) * p.G;
+                const float *x1 = p.xs + (size_t)min(mr + 64, p.M - 1) * p.G;
+                const float *w0 = p.ws + (size_t)min(n0 / kGroup + i, p.NB - 1) * p.G;
+                for (int j = j0 & ~3; j < j1; j += 4, ++c) {
+                    const int s = c % kScaleSlots;
+                    const float4 a = load4(p, x0, j), b = load4(p, x1, j);
+                    float4 w = a;
+                    if (i < 2) w = load4(p, w0, j);
+                    if (c >= kScaleSlots && !mbar_wait_all(smem_u32(sc_empty + s),
+                                                           ((c / kScaleSlots) - 1) & 1, abort)) {
+                        if (lane == 0) fail(kErrSlotWait);
                         ok = false;
                         break;
                     }
-                    const uint32_t st = smem_u32(smem + s * kStage);
-                    // both CTAs' bytes count at the leader's barrier
-                    const uint32_t bar = map_to_rank(smem_u32(full + s), leader);
-                    if (rank == 0) mbar_arrive_expect_tx(smem_u32(full + s), 2 * kStage);
-                    tma_load_2d_pair(st, &p.xmap, j * kGroup, mr, bar, pol_x);
-                    tma_load_2d_pair(st + kStageX, &p.wmap, j * kGroup, nr, bar, pol_w);
+                    float4 *slot = reinterpret_cast<float4 *>(sm_scales + s * kScaleSlot);
+                    slot[i] = a;
+                    slot[i + 64] = b;
+                    if (i < 2) slot[kHalf + i] = w;
+                    mbar_arrive(smem_u32(sc_full + s));
                 }
             }
-            // every load issued must have landed before the CTA exits: the leader
-            // sees both CTAs' (the other waits for it at the last cluster barrier)
-            if (rank == 0)
-                for (int i = c - kStages > 0 ? c - kStages : 0; i < c; ++i)
-                    if (!mbar_wait_drain(smem_u32(full + i % kStages), (i / kStages) & 1))
-                        atomicOr(p.status, kErrDrain);
         }
-    } else if (warp == kMmaWarp) {
-        // ------------------------------------------------ products
-        if (rank == 0) {
-            const uint32_t stages = uniform(smem_u32(smem));
-            const uint32_t bars = uniform(smem_u32(full));
-            const uint32_t tm = uniform(tmem);
-            const uint16_t both = (uint16_t)(3u << leader);
-            int c = 0;
-            bool ok = true;
-            while (ok && walk.next(p, t, j0, j1)) {
-                for (int j = j0; j < j1; ++j, ++c) {
-                    const int s = c % kStages, d = c % kDBufs;
-                    if (!mbar_wait_all(bars + 8 * s, (c / kStages) & 1, abort)) {
-                        if (lane == 0) fail(kErrStageWait);
-                        ok = false;
-                        break;
-                    }
-                    if (c >= kDBufs && !mbar_wait_all(bars + 8 * (2 * kStages + kDBufs + d),
-                                                      ((c / kDBufs) - 1) & 1, abort)) {
-                        if (lane == 0) fail(kErrSumWait);
-                        ok = false;
-                        break;
-                    }
-                    tc_fence_after();
-                    if (elect_one()) {
-                        const uint64_t a = smem_desc_sw128(stages + s * kStage);
-                        mma_f8_block_pair(tm + d * kTileN, a, a + (kStageX >> 4), kIdesc);
-                        mma_commit_pair(bars + 8 * (2 * kStages + d), both);
-                        mma_commit_pair(bars + 8 * (kStages + s), both);
-                    }
-                }
-            }
-            // the products issued complete before the tensor memory is freed
-            if (lane == 0)
-                for (int i = c - kDBufs > 0 ? c - kDBufs : 0; i < c; ++i)
-                    if (!mbar_wait_drain(smem_u32(d_full + i % kDBufs), (i / kDBufs) & 1))
-                        atomicOr(p.status, kErrDrain);
-        }
-    } else if (warp > kMmaWarp) {
-        // ------------------------------------------------ scales
-        // (rows and columns past the end take the last one's: they are not stored)
-        grid_dependency_wait();
-        const int i = (warp - kMmaWarp - 1) * 32 + lane;  // tokens i and i + 64
-        int c = 0;                                        // batches
-        bool ok = true;
-        while (ok && walk.next(p, t, j0, j1)) {
-            tile_at(p, t, m0, n0);
-            const int mr = m0 + (int)rank * kHalf + i;
-            const float *x0 = p.xs + (size_t)min(mr, p.M - 1) * p.G;
-            const float *x1 = p.xs + (size_t)min(mr + 64, p.M - 1) * p.G;
-            const float *w0 = p.ws + (size_t)min(n0 / kGroup + i, p.NB - 1) * p.G;
-            for (int j = j0 & ~3; j < j1; j += 4, ++c) {
-                const int s = c % kScaleSlots;
-                const float4 a = load4(p, x0, j), b = load4(p, x1, j);
-                float4 w = a;
-                if (i < 2) w = load4(p, w0, j);
-                if (c >= kScaleSlots && !mbar_wait_all(smem_u32(sc_empty + s),
-                                                       ((c / kScaleSlots) - 1) & 1, abort)) {
-                    if (lane == 0) fail(kErrSlotWait);
-                    ok = false;
-                    break;
-                }
-                float4 *slot = reinterpret_cast<float4 *>(sm_scales + s * kScaleSlot);
-                slot[i] = a;
-                slot[i + 64] = b;
-                if (i < 2) slot[kHalf + i] = w;
-                mbar_arrive(smem_u32(sc_full + s));
-            }
-        }
-    }
-    __syncwarp();
-    if (p.ksplit > 1) cluster_sync();  // with the sum warps', before the exchange
+        __syncwarp();
+        if (p.ksplit > 1) cluster_sync();  // with the sum warps', before the exchange
     } else {
         // ------------------------------------------------ sums and outputs
         regs_inc<kSumRegs>();
@@ -486,7 +489,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int r = quarter * 32 + lane;  // token within the CTA's 128
         const uint32_t taddr = tmem + ((uint32_t)(quarter * 32) << 16) + col;
         uint8_t *stage_out = sm_store + warp * kStoreBytes;
-        const uint32_t bar_full = smem_u32(d_full), bar_empty = map_to_rank(smem_u32(d_empty), leader);
+        const uint32_t bar_full = smem_u32(d_full);
+        const uint32_t bar_empty = map_to_rank(smem_u32(d_empty), leader);
         const uint32_t bar_res = smem_u32(r_full + warp);
         uint32_t res_asked = 0, res_taken = 0;  // residual tiles
         // the scale products of four blocks 4 i .. 4 i + 3, from the slot
@@ -723,18 +727,28 @@ Fp8WidePlan plan_fp8_wide(int M, int N, int K, const DeviceInfo &dev, const Work
     pl.pairs = (int)(tiles < pairs ? tiles : pairs);
     pl.whole = (int)tiles;
     pl.ksplit = 1;
-    // few tiles: the largest cluster that keeps every tile in one wave, with at
-    // least four blocks of K per pair
+    // few tiles: the largest cluster that keeps every tile in one wave (M 256, N 5120:
+    // K 5120 23.2 us, 27.3 unsplit; K 17408 37.5, 68.3), with at least eight blocks of
+    // K per pair (M 256, N 1024, K 1024: 12.9 us, 15.0 with four; K 1536 the same)
     for (int k = kMaxSplit; k > 1; --k)
-        if (tiles <= g_clusters[k] && pl.G >= 4 * k) {
+        if (tiles <= g_clusters[k] && pl.G >= 8 * k) {
             pl.ksplit = k;
             pl.pairs = (int)tiles * k;
             pl.whole = 0;
             return pl;
         }
-    const long long rest = tiles % pairs;
-    if (tiles < pairs || rest == 0 || rest * 100 >= (long long)pairs * 90) return pl;
-    // an unfinished last round: it and the full round before it are cut into equal runs
+    // an unfinished last round: it and the full round before it are cut into equal
+    // runs where that saves more than the pieces cost, about 24 blocks and, in long
+    // tiles, a third of a round.  M 512, microseconds, whole against equal runs:
+    //   empty blocks per pair, of a round's
+    //   N 10240, K 2048    15 of 16    27.3   28.1
+    //   N 16896, K 5120    11 of 40    47.7   56.0
+    //   N 14592, K 5120    20 of 40    47.7   47.7
+    //   N 20480, K 5120    36 of 40    66.2   62.0
+    //   N 16896, K 17408   36 of 136  129.7  138.1
+    //   N 14592, K 17408   68 of 136  129.7  117.4
+    const long long rest = tiles % pairs, empty = (pairs - rest) * pl.G;
+    if (tiles < pairs || rest == 0 || empty < 24ll * pairs || (pairs - rest) * 3 < pairs) return pl;
     const long long split = pairs + rest;
     if ((size_t)2 * pairs * 2 * kTileN * kHalf * sizeof(float) > ws.partial_bytes ||
         2 * split > ws.n_counters - kMmaSchedWords)
@@ -751,7 +765,8 @@ cudaError_t launch_fp8_wide(const Fp8Args &a, const Fp8WidePlan &plan, const Wor
     if (!encode_fp8_rows(&p.xmap, a.x, a.M, a.K, kHalf) ||
         !encode_fp8_rows(&p.wmap, a.w, a.N, a.K, kHalf))
         return cudaErrorInvalidValue;
-    const bool tma = a.N % 8 == 0 && ((uintptr_t)a.y & 15) == 0 && ((uintptr_t)a.residual & 15) == 0;
+    const bool tma = a.N % 8 == 0 && ((uintptr_t)a.y & 15) == 0 &&
+                     ((uintptr_t)a.residual & 15) == 0;
     if (tma && (!encode_rows16(&p.ymap, a.y, a.M, a.N, 32, kStoreCols) ||
                 (a.residual && !encode_rows16(&p.rmap, a.residual, a.M, a.N, 32, kStoreCols))))
         return cudaErrorInvalidValue;

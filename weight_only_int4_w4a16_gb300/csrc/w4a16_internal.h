@@ -294,7 +294,6 @@ struct Fp8Plan {
     bool streamk;      // CTAs take equal runs of (tile, block) work, not whole tiles
     int grid;
     int stages;
-    size_t ws_bytes;   // partial sums of split tiles
 };
 constexpr int kFp8MaxTokens = 64;  // per launch of this kernel
 // ws: splits nothing that does not fit it
