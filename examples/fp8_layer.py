@@ -56,7 +56,8 @@ class Fp8Layer:
             return (torch.empty((M, n), dtype=FP8, device=dev),
                     torch.empty((M, -(-n // BLOCK)), dtype=torch.float32, device=dev))
 
-        self.q_hidden, self.q_heads, self.q_inter = rows(self.hidden), rows(self.heads), rows(self.inter)
+        self.q_hidden, self.q_heads = rows(self.hidden), rows(self.heads)
+        self.q_inter = rows(self.inter)
         self.qkv = torch.empty((M, wqkv.shape[0]), dtype=dt, device=dev)
         self.gate_up = torch.empty((M, wgate_up.shape[0]), dtype=dt, device=dev)
 

@@ -333,7 +333,8 @@ int w4a16_dense_linear(const uint16_t *x, const uint16_t *w, int M, int N, int K
  *     y[m, n] = sum_b x_scales[m, b] * w_scales[n / 128, b] *
  *               sum_{k in block b} x[m, k] * w[n, k]   (+ residual[m, n])
  * y and residual have the 16-bit type `dtype` (w4a16_dtype).  Sums are fp32, y is
- * rounded once (nearest even).  One kernel; K may be split between CTAs, whose
+ * rounded once (nearest even); the two scales are multiplied first, so their
+ * product has to be finite in fp32.  One kernel; K may be split between CTAs, whose
  * partial sums go through the w4a16_init workspace and are added in a fixed
  * order (a workspace too small for that means no split, not an error).  K a
  * multiple of 16 (16..2^22), 1 <= N < 2^31, 0 <= M <= 65535; x and w 16-byte
@@ -367,8 +368,9 @@ int w4a16_rmsnorm(const uint16_t *x, const uint16_t *residual, const uint16_t *w
  * elements.  W4A16_EPILOGUE_NONE: of x itself, q [M, cols].
  * W4A16_EPILOGUE_SILU_MUL: of silu(x[:, :cols/2]) * x[:, cols/2:] (fp32, silu(g) =
  * g / (1 + e^-g)), q [M, cols/2]; cols even.  W4A16_EPILOGUE_RESIDUAL:
- * W4A16_ERR_UNSUPPORTED.  0 <= M <= 65535, 1 <= cols <= 2^30; x 2-byte aligned, scales 4-byte; q and
- * scales apart from x and from each other.  Needs no w4a16_init. */
+ * W4A16_ERR_UNSUPPORTED.  0 <= M <= 65535, 1 <= cols <= 2^30; x 2-byte aligned,
+ * scales 4-byte; q and scales apart from x and from each other.  Needs no
+ * w4a16_init. */
 int w4a16_fp8_quant(const uint16_t *x, int M, int cols, int epilogue, int dtype, uint8_t *q,
                     float *scales, void *stream);
 

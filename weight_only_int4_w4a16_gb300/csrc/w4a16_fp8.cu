@@ -1,6 +1,7 @@
-// The 8-bit linear for up to 64 tokens (more: w4a16_fp8_wide.cu): y [M, N] = x [M, K] w [N, K]^T (+ residual) for e4m3 rows x
-// with one fp32 scale per 128 elements and e4m3 weights with one fp32 scale per
-// block of 128 x 128 (forum.sourcefind.cn thread "vLLM on Hygon Z100", section
+// The 8-bit linear for up to 64 tokens (more: w4a16_fp8_wide.cu):
+// y [M, N] = x [M, K] w [N, K]^T (+ residual) for e4m3 rows x with one fp32 scale
+// per 128 elements and e4m3 weights with one fp32 scale per block of 128 x 128
+// (forum.sourcefind.cn thread "vLLM on Hygon Z100", section
 // 六: FP8 checkpoints, dequantised to 16 bits at load there because the GPU has
 // no FP8 arithmetic; here the tensor cores take the 8-bit data):
 //
@@ -8,18 +9,21 @@
 //
 // The scales change every 128 elements of K, so the tensor cores' accumulator
 // holds one block's sum only: per block b a fresh product of 128 weight rows by
-// T tokens lands in tensor memory, and four warps add it, times sx sw, to fp32
-// sums in registers (one fused multiply-add per element and block).
+// T tokens lands in tensor memory, and the sum warps add it, times sx sw, to fp32
+// sums in registers (one fused multiply-add per element and block).  A product of two
+// e4m3 numbers is exact, the tensor cores add 128 of them in fp32; a block's addition
+// rounds once, and y once, to its 16 bits.
 //
 //   MMA shape (swap AB): the MMA's M = 128 weight rows of one tile, its N = T
 //   tokens (16, 32 or 64; missing tokens are zero rows of x), K = 32 per
 //   instruction, four instructions per block.  A partial last block is filled
 //   with zeros by TMA.
 //
-//   Roles (one CTA per SM, 192 threads): warp 4 streams two blocks of weights and
-//   of x per stage by TMA (128-byte swizzled, K-major; 256 consecutive bytes of each
-//   weight row), its lanes copy the blocks' scales next to them; warp 5 issues the
-//   products; warps 0..3 (thread = weight row) scale and add the blocks and write y.
+//   Roles (one CTA per SM): four sum warps, eight from 32 tokens on (thread = weight
+//   row), scale and add the blocks and write y; the next warp streams two blocks of
+//   weights and of x per stage by TMA (128-byte swizzled, K-major; 256 consecutive
+//   bytes of each weight row), its lanes copy the blocks' scales next to them; the
+//   last warp issues the products.
 //
 //   Work: few tiles (a small N) are split along K between the CTAs of a cluster,
 //   which exchange their sums through distributed shared memory.  Otherwise the
@@ -27,6 +31,12 @@
 //   tile split between CTAs is summed by the last of them from global memory.
 //   Either way the pieces are added in K order: results do not depend on which CTA
 //   came last.
+//
+//   Bound by the weights' bytes and, in short calls, by the start (about 3 us to the
+//   first weights) and the exchange of split tiles (about 2 us).  N 34816, K 5120
+//   (178 MB) at 8 tokens: 29.5 us, 6.07 TB/s, 89% of the measured copy rate;
+//   N 5120, K 17408 (89 MB) at 64 tokens: 24.0 us, 3.8 TB/s; N 8192, K 5120 (42 MB)
+//   at 1 token: 10.9 us, 3.9 TB/s.
 //
 // Every mbarrier wait is bounded; on expiry the kernel records an error code in
 // the device status word, drains what it has in flight, frees its tensor memory
@@ -364,26 +374,21 @@ __global__ void __launch_bounds__(Cfg<T>::kThreads, 1)
                 for (int b = 0; b < kSub; ++b) {
                     if (j + b >= j1) break;
                     const float sw = sc[kSub * T + b];
-                    constexpr int kLoad = kCols < 32 ? kCols : 32;
+                    uint32_t u[kCols];
+                    tmem_ld(taddr + (d * kSub + b) * T, u);
+                    float f[kCols];
 #pragma unroll
-                    for (int i0 = 0; i0 < kCols; i0 += kLoad) {
-                        uint32_t u[kLoad];
-                        tmem_ld(taddr + (d * kSub + b) * T + i0, u);
-                        float f[kLoad];
-#pragma unroll
-                        for (int i = 0; i < kLoad; i += 4) {
-                            const float4 sx =
-                                *reinterpret_cast<const float4 *>(sc + b * T + cb + i0 + i);
-                            f[i] = sx.x * sw;
-                            f[i + 1] = sx.y * sw;
-                            f[i + 2] = sx.z * sw;
-                            f[i + 3] = sx.w * sw;
-                        }
-                        tmem_wait_ld(u);
-#pragma unroll
-                        for (int i = 0; i < kLoad; ++i)
-                            acc[i0 + i] = fmaf(__uint_as_float(u[i]), f[i], acc[i0 + i]);
+                    for (int i = 0; i < kCols; i += 4) {
+                        const float4 sx = *reinterpret_cast<const float4 *>(sc + b * T + cb + i);
+                        f[i] = sx.x * sw;
+                        f[i + 1] = sx.y * sw;
+                        f[i + 2] = sx.z * sw;
+                        f[i + 3] = sx.w * sw;
                     }
+                    tmem_wait_ld(u);
+#pragma unroll
+                    for (int i = 0; i < kCols; ++i)
+                        acc[i] = fmaf(__uint_as_float(u[i]), f[i], acc[i]);
                 }
                 tc_fence_before();
                 __syncwarp();

@@ -203,7 +203,7 @@ __device__ __forceinline__ f2 silu_mul(f2 g, f2 u) {
 // rmsnorm: a CTA per row, V steps of 8 elements per thread, the row in
 // registers between the sum of squares and the outputs (one pass over memory).
 // Bound by memory: 8192 rows of 5120 with the residual's sum, bf16 to 8 bits, take
-// 45.7 us (6.45 TB/s, 95% of the measured copy rate).
+// 43.7 us (6.75 TB/s, 99% of the measured copy rate; 45.7 with scalar arithmetic).
 // ---------------------------------------------------------------------------
 template <bool kBf16, bool kVec, int V>
 __global__ void __launch_bounds__(1024) rmsnorm_kernel(NormArgs a) {
@@ -258,9 +258,9 @@ __global__ void __launch_bounds__(1024) rmsnorm_kernel(NormArgs a) {
 // ---------------------------------------------------------------------------
 // quant: 16 lanes per (row, group), two groups each, both loaded before either is
 // computed; a CTA has 16 consecutive groups of a row.  Bound by memory: silu-and-mul
-// of 4096 x 17408 takes 60.3 us (5.95 TB/s, 88% of the measured copy rate; 67.1 with
-// 256 threads and one group each, 63.9 with 256 and two), of which the arithmetic
-// alone would take about 46.
+// of 4096 x 17408 takes 57.6 us (6.23 TB/s, 92% of the measured copy rate; with scalar
+// arithmetic 60.3, then 67.1 with 256 threads and one group each, 63.9 with 256 and
+// two).
 // ---------------------------------------------------------------------------
 constexpr int kQuantThreads = 128;
 constexpr int kQuantU = 2;
@@ -333,8 +333,8 @@ cudaError_t launch_rmsnorm(const NormArgs &a, bool bf16, cudaStream_t stream) {
                      aligned16(a.q);
     const int lanes = (a.H + kLaneElems - 1) / kLaneElems;
     // up to four steps per thread before more than 128 threads: small CTAs keep more
-    // rows in flight (8192 rows of 5120: 61.3 us in one step, 49.1 in two, 45.7 in
-    // four; of 2048: 23.7 in one step, 19.9 in two)
+    // rows in flight (8192 rows of 5120, with scalar arithmetic: 61.3 us in one step,
+    // 49.1 in two, 45.7 in four; of 2048: 23.7 in one step, 19.9 in two)
     int steps = 1;
     while (steps < 4 && lanes > 128 * steps) steps *= 2;
     const int threads = ((lanes + steps - 1) / steps + 31) / 32 * 32;
