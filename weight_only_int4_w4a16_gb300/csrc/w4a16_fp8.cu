@@ -26,11 +26,11 @@
 //   last warp issues the products.
 //
 //   Work: few tiles (a small N) are split along K between the CTAs of a cluster,
-//   which exchange their sums through distributed shared memory.  Otherwise the
-//   (tile, block) sequence is cut into equal runs, one per CTA ("stream-K"), and a
-//   tile split between CTAs is summed by the last of them from global memory.
-//   Either way the pieces are added in K order: results do not depend on which CTA
-//   came last.
+//   which exchange their sums through distributed shared memory.  More take whole
+//   tiles in turn; where that would leave much of the last wave empty, the (tile,
+//   block) sequence is cut into equal runs, one per CTA ("stream-K"), and a tile
+//   split between CTAs is summed by the last of them from global memory.  Pieces are
+//   added in K order either way: results do not depend on which CTA came last.
 //
 //   Bound by the weights' bytes and, in short calls, by the start (about 3 us to the
 //   first weights) and the exchange of split tiles (about 2 us).  N 34816, K 5120
