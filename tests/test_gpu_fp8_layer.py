@@ -84,3 +84,33 @@ def test_layer_step_by_step(example, M):
     off = float((h.float() - want).norm() / (want - h0.float()).norm())
     assert off <= 0.11, off
     assert w4.w4a16_device_status() == 0
+
+
+def test_new_outputs_on_another_stream_are_its_own_memory(example):
+    # memory that the current stream has just freed may still be in use there: a call on
+    # another stream has to take its outputs from elsewhere, and to leave them whole for
+    # the current stream after they are freed
+    w4 = example.w4
+    s = torch.cuda.Stream()
+    M, H = 256, 2048
+    x = torch.randn((M, H), device="cuda").to(torch.bfloat16)
+    weight = torch.ones(H, dtype=torch.bfloat16, device="cuda")
+    w = torch.ones((H, H), device="cuda").to(torch.float8_e4m3fn)
+    ws = torch.ones((H // 128, H // 128), device="cuda")
+    q, sc = w4.w4a16_fp8_quant(x)
+    torch.cuda.synchronize()
+    calls = [lambda: w4.w4a16_fp8_linear(q, sc, w, ws, stream=s),
+             lambda: w4.w4a16_rmsnorm(x, weight, stream=s),
+             lambda: w4.w4a16_rmsnorm(x, weight, residual=x, stream=s),
+             lambda: w4.w4a16_rmsnorm_fp8(x, weight, stream=s),
+             lambda: w4.w4a16_fp8_quant(x, stream=s)]
+    for f in calls:
+        freed = [torch.empty(n, dtype=torch.uint8, device="cuda")
+                 for n in (2 * M * H, 2 * M * H, M * H, M * H, M * H // 32)]
+        spans = [(t.data_ptr(), t.data_ptr() + t.numel()) for t in freed]
+        del freed
+        out = f()
+        for t in out if isinstance(out, tuple) else (out,):
+            a, b = t.data_ptr(), t.data_ptr() + t.numel() * t.element_size()
+            assert all(b <= lo or a >= hi for lo, hi in spans)
+        s.synchronize()

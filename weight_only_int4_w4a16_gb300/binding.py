@@ -366,12 +366,19 @@ def _shaped(t: torch.Tensor, dtype, shape, name: str) -> int:
     return t.data_ptr()
 
 
-def _output(t, shape, dtype, like: torch.Tensor, name: str):
-    """(t, its address), checked, or a new tensor on like's device."""
-    if t is None:
+def _output(t, shape, dtype, like: torch.Tensor, side, name: str):
+    """(t, its address), checked, or a new tensor on like's device: of the stream
+    `side`'s memory when there is one, as memory of the current stream may still be
+    in use there, and kept for what the current stream does with it afterwards."""
+    if t is not None:
+        return t, _shaped(t, dtype, shape, name)
+    if side is None:
         t = torch.empty(shape, dtype=dtype, device=like.device)
-        return t, t.data_ptr()
-    return t, _shaped(t, dtype, shape, name)
+    else:
+        with torch.cuda.stream(side):
+            t = torch.empty(shape, dtype=dtype, device=like.device)
+        t.record_stream(torch.cuda.current_stream(like.device))
+    return t, t.data_ptr()
 
 
 def _dtype16(dt) -> int:
@@ -380,20 +387,25 @@ def _dtype16(dt) -> int:
     return _DTYPE_OF[dt]
 
 
-def _stream_for(t: torch.Tensor, stream, *used) -> int:
-    """The stream of a call on t's device.  For a stream other than the current
-    one, torch's allocator is told of the tensors used on it, so that memory
-    freed after the call is not handed out too early."""
+def _stream_for(t: torch.Tensor, stream):
+    """(the address of a call's stream on t's device, that stream as torch's if it is
+    not the current one)."""
     current = torch._C._cuda_getCurrentRawStream(t.get_device())
     if stream is None:
-        return current
+        return current, None
     raw = _stream_ptr(stream)
-    if raw != current:
-        s = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(raw)
-        for u in used:
-            if u is not None:
-                u.record_stream(s)
-    return raw
+    if raw == current:
+        return raw, None
+    return raw, stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(raw)
+
+
+def _used_on(side, *tensors) -> None:
+    """Tells torch's allocator of the tensors used on another stream than the current
+    one, so that memory freed after the call is not handed out too early."""
+    if side is not None:
+        for t in tensors:
+            if t is not None:
+                t.record_stream(side)
 
 
 def w4a16_fp8_linear(x: torch.Tensor, x_scales: torch.Tensor, w: torch.Tensor,
@@ -412,26 +424,29 @@ def w4a16_fp8_linear(x: torch.Tensor, x_scales: torch.Tensor, w: torch.Tensor,
     xs = _shaped(x_scales, torch.float32, (M, G), "x_scales")
     ws = _shaped(w_scales, torch.float32, ((N + GROUP - 1) // GROUP, G), "w_scales")
     r = None if residual is None else _shaped(residual, dtype, (M, N), "residual")
-    y, yp = _output(y, (M, N), dtype, x, "y")
-    _check(lib.w4a16_fp8_linear(xp, xs, wp, ws, M, N, K, dt, epilogue, r, yp,
-                                _stream_for(x, stream, x, x_scales, w, w_scales, residual, y)),
+    raw, side = _stream_for(x, stream)
+    y, yp = _output(y, (M, N), dtype, x, side, "y")
+    _used_on(side, x, x_scales, w, w_scales, residual, y)
+    _check(lib.w4a16_fp8_linear(xp, xs, wp, ws, M, N, K, dt, epilogue, r, yp, raw),
            "w4a16_fp8_linear")
     return y
 
 
-def _norm_inputs(x, weight, residual, sum_out):
-    """(M, H, dtype code, addresses of x, weight, residual; sum_out and its address)."""
+def _norm_inputs(x, weight, residual, sum_out, stream):
+    """(M, H, dtype code; addresses of x, weight and residual; sum_out and its address;
+    the stream, as _stream_for gives it)."""
     M, H = _rows2d(x, "x")
     dt = x.dtype
     code = _dtype16(dt)
     xp, wp = _shaped(x, dt, (M, H), "x"), _shaped(weight, dt, (H,), "weight")
-    if residual is None:
-        if sum_out is not None:
-            raise ValueError("sum_out needs a residual")
-        return M, H, code, xp, wp, None, None, None
-    rp = _shaped(residual, dt, (M, H), "residual")
-    sum_out, sp = _output(sum_out, (M, H), dt, x, "sum_out")
-    return M, H, code, xp, wp, rp, sum_out, sp
+    raw, side = _stream_for(x, stream)
+    rp = sp = None
+    if residual is not None:
+        rp = _shaped(residual, dt, (M, H), "residual")
+        sum_out, sp = _output(sum_out, (M, H), dt, x, side, "sum_out")
+    elif sum_out is not None:
+        raise ValueError("sum_out needs a residual")
+    return M, H, code, xp, wp, rp, sum_out, sp, raw, side
 
 
 def w4a16_rmsnorm(x: torch.Tensor, weight: torch.Tensor, residual=None, eps: float = 1e-6,
@@ -439,10 +454,11 @@ def w4a16_rmsnorm(x: torch.Tensor, weight: torch.Tensor, residual=None, eps: flo
     """y [M, H] = h / sqrt(mean(h^2) + eps) * weight with h = x (+ residual).
     Returns y, or (y, sum_out) when a residual is given: sum_out is h rounded to
     the 16-bit type (sum_out=residual updates the residual in place)."""
-    M, H, code, xp, wp, rp, sum_out, sp = _norm_inputs(x, weight, residual, sum_out)
-    y, yp = _output(y, (M, H), x.dtype, x, "y")
-    _check(lib.w4a16_rmsnorm(xp, rp, wp, M, H, eps, code, sp, yp, None, None,
-                             _stream_for(x, stream, x, weight, residual, sum_out, y)),
+    M, H, code, xp, wp, rp, sum_out, sp, raw, side = _norm_inputs(x, weight, residual, sum_out,
+                                                                 stream)
+    y, yp = _output(y, (M, H), x.dtype, x, side, "y")
+    _used_on(side, x, weight, residual, sum_out, y)
+    _check(lib.w4a16_rmsnorm(xp, rp, wp, M, H, eps, code, sp, yp, None, None, raw),
            "w4a16_rmsnorm")
     return y if residual is None else (y, sum_out)
 
@@ -451,11 +467,12 @@ def w4a16_rmsnorm_fp8(x: torch.Tensor, weight: torch.Tensor, residual=None, eps:
                       sum_out=None, q=None, scales=None, stream=None):
     """w4a16_rmsnorm with its rows in 8 bits: (q [M, H], scales [M, ceil(H/128)]),
     and sum_out third when a residual is given."""
-    M, H, code, xp, wp, rp, sum_out, sp = _norm_inputs(x, weight, residual, sum_out)
-    q, qp = _output(q, (M, H), FP8, x, "q")
-    scales, cp = _output(scales, (M, (H + GROUP - 1) // GROUP), torch.float32, x, "scales")
-    _check(lib.w4a16_rmsnorm(xp, rp, wp, M, H, eps, code, sp, None, qp, cp,
-                             _stream_for(x, stream, x, weight, residual, sum_out, q, scales)),
+    M, H, code, xp, wp, rp, sum_out, sp, raw, side = _norm_inputs(x, weight, residual, sum_out,
+                                                                 stream)
+    q, qp = _output(q, (M, H), FP8, x, side, "q")
+    scales, cp = _output(scales, (M, (H + GROUP - 1) // GROUP), torch.float32, x, side, "scales")
+    _used_on(side, x, weight, residual, sum_out, q, scales)
+    _check(lib.w4a16_rmsnorm(xp, rp, wp, M, H, eps, code, sp, None, qp, cp, raw),
            "w4a16_rmsnorm_fp8")
     return (q, scales) if residual is None else (q, scales, sum_out)
 
@@ -468,10 +485,11 @@ def w4a16_fp8_quant(x: torch.Tensor, epilogue: int = EPILOGUE_NONE, q=None, scal
     dt = _dtype16(x.dtype)
     N = cols // 2 if epilogue == EPILOGUE_SILU_MUL else cols
     xp = _shaped(x, x.dtype, (M, cols), "x")
-    q, qp = _output(q, (M, N), FP8, x, "q")
-    scales, cp = _output(scales, (M, (N + GROUP - 1) // GROUP), torch.float32, x, "scales")
-    _check(lib.w4a16_fp8_quant(xp, M, cols, epilogue, dt, qp, cp,
-                               _stream_for(x, stream, x, q, scales)), "w4a16_fp8_quant")
+    raw, side = _stream_for(x, stream)
+    q, qp = _output(q, (M, N), FP8, x, side, "q")
+    scales, cp = _output(scales, (M, (N + GROUP - 1) // GROUP), torch.float32, x, side, "scales")
+    _used_on(side, x, q, scales)
+    _check(lib.w4a16_fp8_quant(xp, M, cols, epilogue, dt, qp, cp, raw), "w4a16_fp8_quant")
     return q, scales
 
 
