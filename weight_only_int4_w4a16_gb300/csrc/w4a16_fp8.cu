@@ -75,7 +75,6 @@ struct Fp8Params {
     int tiles;
     int streamk;
     int ksplit;          // CTAs of a cluster that split each tile along K (1: none)
-    int stages;
     int bf16;
 };
 
@@ -95,15 +94,12 @@ struct Cfg {
     static constexpr int kScales = kSub * T + 4;
     static constexpr uint32_t kIdesc =     // D f32, A and B e4m3 (0), N = T, M = 128
         (1u << 4) | ((uint32_t)(T >> 3) << 17) | ((uint32_t)(kTileN >> 4) << 24);
-    static int stages() {
-        const int n = kSmemBudget / (kStage + kScales * 4);
-        return n < kMaxStages ? n : kMaxStages;
-    }
+    static constexpr int kFit = kSmemBudget / (kStage + kScales * 4);
+    static constexpr int kStages = kFit < kMaxStages ? kFit : kMaxStages;
     // slack for the 1024-byte alignment, the stages, their scales, the
     // barriers, the tensor-memory address, abort and last flags
-    static int smem(int stages) {
-        return 1024 + stages * (kStage + kScales * 4) + (2 * kMaxStages + 2 * kDBufs) * 8 + 16;
-    }
+    static constexpr int kSmem =
+        1024 + kStages * (kStage + kScales * 4) + (2 * kStages + 2 * kDBufs) * 8 + 16;
 };
 
 // The CTA's work: segments (a tile and a run of its blocks), in order.
@@ -212,11 +208,11 @@ __global__ void __launch_bounds__(Cfg<T>::kThreads, 1)
     using C = Cfg<T>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
-    const int NS = p.stages;
+    constexpr int NS = C::kStages;
     float *sm_scales = reinterpret_cast<float *>(smem + (size_t)NS * C::kStage);
     uint64_t *full = reinterpret_cast<uint64_t *>(sm_scales + NS * C::kScales);
-    uint64_t *empty = full + kMaxStages;
-    uint64_t *d_full = empty + kMaxStages;
+    uint64_t *empty = full + NS;
+    uint64_t *d_full = empty + NS;
     uint64_t *d_empty = d_full + kDBufs;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(d_empty + kDBufs);
     volatile int *abort = reinterpret_cast<volatile int *>(tmem_slot + 1);
@@ -320,7 +316,7 @@ __global__ void __launch_bounds__(Cfg<T>::kThreads, 1)
                     ok = false;
                     break;
                 }
-                if (c >= kDBufs && !mbar_wait_all(bars + 8 * (2 * kMaxStages + kDBufs + d),
+                if (c >= kDBufs && !mbar_wait_all(bars + 8 * (2 * NS + kDBufs + d),
                                                   ((c / kDBufs) - 1) & 1, abort)) {
                     if (lane == 0) fail(kErrSumWait);
                     ok = false;
@@ -335,8 +331,8 @@ __global__ void __launch_bounds__(Cfg<T>::kThreads, 1)
                     if (nb > 1)
                         mma_f8_block(tm + (d * kSub + 1) * T, a + (kBlockW >> 4),
                                      b + (C::kBlockX >> 4), C::kIdesc);
-                    mma_commit(bars + 8 * (2 * kMaxStages + d));
-                    mma_commit(bars + 8 * (kMaxStages + s));
+                    mma_commit(bars + 8 * (2 * NS + d));
+                    mma_commit(bars + 8 * (NS + s));
                 }
             }
         }
@@ -361,22 +357,11 @@ __global__ void __launch_bounds__(Cfg<T>::kThreads, 1)
             for (int i = 0; i < kCols; ++i) acc[i] = 0.f;
             for (int j = j0; j < j1; j += kSub, ++c) {
                 const int s = c % NS, d = c % kDBufs;
-                // the stage's barrier shows its scales, the sums' its products
-                if (!mbar_wait_all(smem_u32(full + s), (c / NS) & 1, abort) ||
-                    !mbar_wait_all(smem_u32(d_full + d), (c / kDBufs) & 1, abort)) {
-                    if (lane == 0) fail(kErrSumWait);
-                    ok = false;
-                    break;
-                }
-                tc_fence_after();
+                const bool two = j + 1 < j1;
                 const float *sc = sm_scales + s * C::kScales;
-#pragma unroll
-                for (int b = 0; b < kSub; ++b) {
-                    if (j + b >= j1) break;
+                // the scale products of block b of the stage
+                auto factors = [&](int b, float (&f)[kCols]) {
                     const float sw = sc[kSub * T + b];
-                    uint32_t u[kCols];
-                    tmem_ld(taddr + (d * kSub + b) * T, u);
-                    float f[kCols];
 #pragma unroll
                     for (int i = 0; i < kCols; i += 4) {
                         const float4 sx = *reinterpret_cast<const float4 *>(sc + b * T + cb + i);
@@ -385,16 +370,43 @@ __global__ void __launch_bounds__(Cfg<T>::kThreads, 1)
                         f[i + 2] = sx.z * sw;
                         f[i + 3] = sx.w * sw;
                     }
-                    tmem_wait_ld(u);
+                };
+                // the stage's barrier shows its scales, the sums' its products; the first
+                // block's factors come while the tensor cores are still at work, the
+                // second's while its sums are on their way
+                float f[kCols];
+                uint32_t u[kCols], v[kCols];
+                const uint32_t from = taddr + d * kSub * T;
+                ok = mbar_wait_all(smem_u32(full + s), (c / NS) & 1, abort);
+                if (ok) {
+                    factors(0, f);
+                    ok = mbar_wait_all(smem_u32(d_full + d), (c / kDBufs) & 1, abort);
+                }
+                if (!ok) {
+                    if (lane == 0) fail(kErrSumWait);
+                    break;
+                }
+                tc_fence_after();
+                tmem_ld(from, u);
+                tmem_wait_ld(u);
+                if (two) tmem_ld(from + T, v);
 #pragma unroll
-                    for (int i = 0; i < kCols; ++i)
-                        acc[i] = fmaf(__uint_as_float(u[i]), f[i], acc[i]);
+                for (int i = 0; i < kCols; ++i)
+                    acc[i] = fmaf(__uint_as_float(u[i]), f[i], acc[i]);
+                if (two) {
+                    factors(1, f);
+                    tmem_wait_ld(v);
                 }
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) {
                     mbar_arrive(smem_u32(d_empty + d));
                     mbar_arrive(smem_u32(empty + s));
+                }
+                if (two) {
+#pragma unroll
+                    for (int i = 0; i < kCols; ++i)
+                        acc[i] = fmaf(__uint_as_float(v[i]), f[i], acc[i]);
                 }
             }
             if (!ok) break;
@@ -515,11 +527,11 @@ __global__ void __launch_bounds__(Cfg<T>::kThreads, 1)
 // ---------------------------------------------------------------------------
 template <int T>
 void config_t(cudaLaunchConfig_t &cfg, cudaLaunchAttribute (&attr)[2], int grid, int ksplit,
-              int stages, cudaStream_t stream) {
+              cudaStream_t stream) {
     cfg = {};
     cfg.gridDim = dim3(grid);
     cfg.blockDim = dim3(Cfg<T>::kThreads);
-    cfg.dynamicSmemBytes = Cfg<T>::smem(stages);
+    cfg.dynamicSmemBytes = Cfg<T>::kSmem;
     cfg.stream = stream;
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
@@ -533,20 +545,12 @@ template <int T>
 cudaError_t launch_t(const Fp8Params &p, int grid, cudaStream_t stream) {
     cudaLaunchConfig_t cfg;
     cudaLaunchAttribute attr[2];
-    config_t<T>(cfg, attr, grid, p.ksplit, p.stages, stream);
+    config_t<T>(cfg, attr, grid, p.ksplit, stream);
     return cudaLaunchKernelEx(&cfg, fp8_kernel<T>, p);
 }
 
 // clusters of k CTAs that run at the same time, found once per process
 int g_clusters[kMaxCluster + 1];
-
-int stages_of(int T) {
-    switch (T) {
-        case 16: return Cfg<16>::stages();
-        case 32: return Cfg<32>::stages();
-        default: return Cfg<64>::stages();
-    }
-}
 
 }  // namespace
 
@@ -555,7 +559,6 @@ Fp8Plan plan_fp8(int M, int N, int K, const DeviceInfo &dev, const Workspace &ws
     pl.T = M <= 16 ? 16 : M <= 32 ? 32 : 64;
     pl.G = (K + kGroup - 1) / kGroup;
     pl.tiles = (N + kTileN - 1) / kTileN;
-    pl.stages = stages_of(pl.T);
     pl.ksplit = 1;
     pl.grid = pl.tiles < dev.sm_count ? pl.tiles : dev.sm_count;
     // few tiles: the largest cluster that keeps every tile in one wave (N 5120: M 8,
@@ -608,7 +611,6 @@ cudaError_t launch_fp8(const Fp8Args &a, const Fp8Plan &plan, const Workspace &w
     p.total = (long long)plan.tiles * plan.G;
     p.streamk = plan.streamk;
     p.ksplit = plan.ksplit;
-    p.stages = plan.stages;
     p.bf16 = a.bf16;
     switch (plan.T) {
         case 16: return launch_t<16>(p, plan.grid, stream);
@@ -620,9 +622,9 @@ cudaError_t launch_fp8(const Fp8Args &a, const Fp8Plan &plan, const Workspace &w
 cudaError_t fp8_init(const DeviceInfo &) {
     if (!tensor_map_encoder()) return cudaErrorSymbolNotFound;
     const struct { const void *f; int smem; } fns[] = {
-        {(const void *)fp8_kernel<16>, Cfg<16>::smem(Cfg<16>::stages())},
-        {(const void *)fp8_kernel<32>, Cfg<32>::smem(Cfg<32>::stages())},
-        {(const void *)fp8_kernel<64>, Cfg<64>::smem(Cfg<64>::stages())}};
+        {(const void *)fp8_kernel<16>, Cfg<16>::kSmem},
+        {(const void *)fp8_kernel<32>, Cfg<32>::kSmem},
+        {(const void *)fp8_kernel<64>, Cfg<64>::kSmem}};
     for (const auto &k : fns) {
         cudaError_t e =
             cudaFuncSetAttribute(k.f, cudaFuncAttributeMaxDynamicSharedMemorySize, k.smem);
@@ -632,7 +634,7 @@ cudaError_t fp8_init(const DeviceInfo &) {
     for (int k = 2; k <= kMaxCluster; ++k) {
         cudaLaunchConfig_t cfg;
         cudaLaunchAttribute attr[2];
-        config_t<64>(cfg, attr, k, k, Cfg<64>::stages(), nullptr);
+        config_t<64>(cfg, attr, k, k, nullptr);
         attr[0] = attr[1];
         cfg.numAttrs = 1;
         const cudaError_t e = cudaOccupancyMaxActiveClusters(&g_clusters[k], fp8_kernel<64>, &cfg);

@@ -293,7 +293,6 @@ struct Fp8Plan {
     int ksplit;        // CTAs of a cluster that split each tile along K (1: none)
     bool streamk;      // CTAs take equal runs of (tile, block) work, not whole tiles
     int grid;
-    int stages;
 };
 constexpr int kFp8MaxTokens = 64;  // per launch of this kernel
 // ws: splits nothing that does not fit it
