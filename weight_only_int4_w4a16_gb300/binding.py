@@ -366,6 +366,11 @@ def _shaped(t: torch.Tensor, dtype, shape, name: str) -> int:
     return t.data_ptr()
 
 
+# A new tensor on the current device (where the kernels run) without torch.empty's way
+# through the dispatcher: 1.1 us against 1.8 beside a launch, of a small call's 10.
+_empty_cuda = torch._C._dynamo.guards._empty_strided_cuda
+
+
 def _output(t, shape, dtype, like: torch.Tensor, side, name: str):
     """(t, its address), checked, or a new tensor on like's device: of the stream
     `side`'s memory when there is one, as memory of the current stream may still be
@@ -373,7 +378,7 @@ def _output(t, shape, dtype, like: torch.Tensor, side, name: str):
     if t is not None:
         return t, _shaped(t, dtype, shape, name)
     if side is None:
-        t = torch.empty(shape, dtype=dtype, device=like.device)
+        t = _empty_cuda(shape, (shape[1], 1), dtype)
     else:
         with torch.cuda.stream(side):
             t = torch.empty(shape, dtype=dtype, device=like.device)

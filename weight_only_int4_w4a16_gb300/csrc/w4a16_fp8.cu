@@ -83,7 +83,7 @@ struct Cfg {
     // warps that add the sums: a quarter of the rows each, and from 32 tokens on
     // half of the tokens, so that a tile's outputs are written by twice the threads
     // (64 tokens, N 20480: K 2048 23.2 us against 25.2 with four warps, K 5120 43.3
-    // against 43.6, K 17408 119.4 against 116.2)
+    // against 43.6, K 17408 119.4 against 116.2; sixteen warps: no change)
     static constexpr int kSumWarps = T >= 32 ? 8 : 4;
     static constexpr int kCols = T / (kSumWarps / 4);  // tokens per thread
     static constexpr int kTmaWarp = kSumWarps, kMmaWarp = kSumWarps + 1;
