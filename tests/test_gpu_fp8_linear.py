@@ -106,6 +106,8 @@ PLANS = [
     (900, 10240, 384),
     # long tiles in equal runs: the last wave would be mostly empty
     (3, 10300, 5648), (20, 20480, 2816), (50, 21001, 2704), (300, 10240, 3328), (500, 10241, 3216),
+    # rows that TMA cannot address, split finely
+    (123, 103, 944), (300, 1021, 1024), (200, 707, 528),
 ]
 
 

@@ -739,9 +739,14 @@ Fp8WidePlan plan_fp8_wide(int M, int N, int K, const DeviceInfo &dev, const Work
     pl.ksplit = 1;
     // few tiles: the largest cluster that keeps every tile in one wave (M 256, N 5120:
     // K 5120 23.2 us, 27.3 unsplit; K 17408 37.5, 68.3), with at least eight blocks of
-    // K per pair (M 256, N 1024, K 1024: 12.9 us, 15.0 with four; K 1536 the same)
+    // K per pair (M 256, N 1024, K 1024: 12.9 us, 15.0 with four; K 1536 the same).
+    // Two are enough where rows do not go by TMA: the exchange shares out their copies
+    // too (M 300, N 1021, K 1024 with a residual 10.3 us, 13.3 with four, 19.1 with
+    // eight; without 9.8, 10.2, 11.6).  More than four pairs lose: M 512, N 1024,
+    // K 5120 19.1 us with eight, 12.8 with four.
+    const int least = N % 8 == 0 ? 8 : 2;
     for (int k = kMaxSplit; k > 1; --k)
-        if (tiles <= g_clusters[k] && pl.G >= 8 * k) {
+        if (tiles <= g_clusters[k] && pl.G >= least * k) {
             pl.ksplit = k;
             pl.pairs = (int)tiles * k;
             pl.whole = 0;
