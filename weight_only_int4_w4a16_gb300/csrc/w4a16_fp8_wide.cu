@@ -165,6 +165,10 @@ __device__ __forceinline__ float4 load4(const WideParams &p, const float *row, i
                        __ldg(row + min(j + 3, e)));
 }
 
+__device__ __forceinline__ void prefetch_l2(const void *address) {
+    asm volatile("prefetch.global.L2 [%0];" ::"l"(address));
+}
+
 template <bool kBf16>
 __device__ __forceinline__ uint32_t pack16(float lo, float hi) {  // one rounding each
     if constexpr (kBf16) {
@@ -178,7 +182,8 @@ __device__ __forceinline__ uint32_t pack16(float lo, float hi) {  // one roundin
 
 // Rows m .. m + 31, columns n .. n + 63 of the residual into a warp's staging (kIn), or
 // of y out of it, for rows that TMA cannot address: 32-bit words where N is even and
-// the address allows it, else single elements, 8 rows at a time (their loads together).
+// the address allows it, else single elements, 4 rows at a time (their loads together;
+// 8 spill more: 1240 tokens, N 33533, K 1440 113 us for 84).
 template <bool kIn>
 __device__ __forceinline__ void copy_rows(const WideParams &p, uint8_t *staging, int lane, int m,
                                           int n) {
@@ -188,7 +193,7 @@ __device__ __forceinline__ void copy_rows(const WideParams &p, uint8_t *staging,
     auto at = [&](int r, int c) {
         return staging + r * 128 + (((c >> 3) ^ (r & 7)) << 4) + (c & 7) * 2;
     };
-    constexpr int kRows = 8;
+    constexpr int kRows = 4;
     __syncwarp();
     for (int r0 = 0; r0 < rows; r0 += kRows) {
         const size_t o = (size_t)(m + r0) * p.N + n;
@@ -534,6 +539,15 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int nc = n0 + col, tt = t, end = j1;
             const bool whole = j0 == 0 && j1 == p.G;
             if (whole && staged_res) ask_residual(nc, mw);
+            if constexpr (!kTma) {
+                // the residual's rows on their way to L2 meanwhile (a row's 128 bytes
+                // are in at most two lines): 1240 tokens, N 33532, K 1440 156 us for 177
+                if (whole && p.residual && mw + lane < p.M && nc < p.N) {
+                    const uint16_t *row = p.residual + (size_t)(mw + lane) * p.N;
+                    prefetch_l2(row + nc);
+                    prefetch_l2(row + min(nc + kStoreCols, p.N) - 1);
+                }
+            }
             float acc[kCols];
 #pragma unroll
             for (int i = 0; i < kCols; ++i) acc[i] = 0.f;
