@@ -21,7 +21,10 @@
 // Layout: a lane holds 8 consecutive elements (a 16-byte load), so 16 lanes
 // hold a group and four shuffles give its largest magnitude.  Rows whose width
 // or address does not allow 16-byte accesses are read and written element by
-// element by the same code (kVec false).
+// element (kVec false), the lanes of a group on neighbours.  In the norm they then
+// change hands in shared memory (kStaged), so that a lane adds the same squares and a
+// row has the same bits; the quantisation has no sums, and its lanes keep every 16th
+// element.
 #include <float.h>
 
 #include "w4a16_internal.h"
@@ -81,38 +84,72 @@ __device__ __forceinline__ uint16_t to_16(float v) {  // nearest, ties to even
     else return __half_as_ushort(__float2half_rn(v));
 }
 
-// Elements c .. c + 7 of a row (zeros past its n elements), in pairs.
-template <bool kBf16, bool kVec>
-__device__ __forceinline__ void load8(const uint16_t *row, int c, int n, f2 (&v)[4]) {
+// Where the two groups of a warp change hands: 128 elements each, the second in other
+// banks than the first.
+constexpr int kStageGroup = kGroup + 16;
+constexpr int kStageWarp = 2 * kStageGroup;  // 16-bit words
+// The group's part of a warp's stage, and its lane's first element there and in the
+// row when the lanes take neighbours; element i of the lane is 16 i further.
+__device__ __forceinline__ uint16_t *group_stage(uint16_t *stage) {
+    return stage + (threadIdx.x & kGroupLanes ? kStageGroup : 0);
+}
+__device__ __forceinline__ int neighbour(int c) {
+    return (c & ~(kGroup - 1)) + (threadIdx.x & (kGroupLanes - 1));
+}
+
+// Elements c .. c + 7 of a row (zeros past its n elements), in pairs; with neither kVec
+// nor kStaged every 16th of its group.  All lanes of the warp call it together (and
+// store8); stage is the warp's own.
+template <bool kBf16, bool kVec, bool kStaged>
+__device__ __forceinline__ void load8(const uint16_t *row, int c, int n, f2 (&v)[4],
+                                      uint16_t *stage) {
+    uint4 u = make_uint4(0, 0, 0, 0);
     if constexpr (kVec) {  // n is a multiple of 8
-        uint4 u = make_uint4(0, 0, 0, 0);
         if (c < n) u = *reinterpret_cast<const uint4 *>(row + c);
-        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            v[i] = pack(to_float<kBf16>((uint16_t)w[i]), to_float<kBf16>((uint16_t)(w[i] >> 16)));
     } else {
+        const int e = neighbour(c);
+        uint16_t h[kLaneElems];
 #pragma unroll
-        for (int i = 0; i < 8; i += 2)
-            v[i / 2] = pack(c + i < n ? to_float<kBf16>(row[c + i]) : 0.f,
-                            c + i + 1 < n ? to_float<kBf16>(row[c + i + 1]) : 0.f);
+        for (int i = 0; i < kLaneElems; ++i)
+            h[i] = e + kGroupLanes * i < n ? row[e + kGroupLanes * i] : (uint16_t)0;
+        if constexpr (kStaged) {
+            uint16_t *own = group_stage(stage);
+#pragma unroll
+            for (int i = 0; i < kLaneElems; ++i) own[e % kGroup + kGroupLanes * i] = h[i];
+            __syncwarp();
+            u = *reinterpret_cast<const uint4 *>(own + c % kGroup);
+            __syncwarp();
+        } else {
+            u = make_uint4(h[0] | (uint32_t)h[1] << 16, h[2] | (uint32_t)h[3] << 16,
+                           h[4] | (uint32_t)h[5] << 16, h[6] | (uint32_t)h[7] << 16);
+        }
     }
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        v[i] = pack(to_float<kBf16>((uint16_t)w[i]), to_float<kBf16>((uint16_t)(w[i] >> 16)));
 }
 
 template <bool kBf16, bool kVec>
-__device__ __forceinline__ void store8(uint16_t *row, int c, int n, const f2 (&v)[4]) {
+__device__ __forceinline__ void store8(uint16_t *row, int c, int n, const f2 (&v)[4],
+                                       uint16_t *stage) {
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        w[i] = (uint32_t)to_16<kBf16>(lo(v[i])) | (uint32_t)to_16<kBf16>(hi(v[i])) << 16;
+    const uint4 u = make_uint4(w[0], w[1], w[2], w[3]);
     if constexpr (kVec) {
-        if (c < n) {
-            uint32_t w[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                w[i] = (uint32_t)to_16<kBf16>(lo(v[i])) | (uint32_t)to_16<kBf16>(hi(v[i])) << 16;
-            *reinterpret_cast<uint4 *>(row + c) = make_uint4(w[0], w[1], w[2], w[3]);
-        }
+        if (c < n) *reinterpret_cast<uint4 *>(row + c) = u;
     } else {
+        const int e = neighbour(c);
+        uint16_t *own = group_stage(stage);
+        *reinterpret_cast<uint4 *>(own + c % kGroup) = u;
+        __syncwarp();
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-            if (c + i < n) row[c + i] = to_16<kBf16>(i & 1 ? hi(v[i / 2]) : lo(v[i / 2]));
+        for (int i = 0; i < kLaneElems; ++i)
+            if (e + kGroupLanes * i < n)
+                row[e + kGroupLanes * i] = own[e % kGroup + kGroupLanes * i];
+        __syncwarp();
     }
 }
 
@@ -139,8 +176,9 @@ __device__ __forceinline__ float group_max(float a) {
 
 // A lane's 8 elements of its group -> 8 codes of row q and, from the group's
 // first lane, the group's scale.  All lanes of the warp call it together.
-template <bool kVec>
-__device__ __forceinline__ void quant8(f2 (&v)[4], uint8_t *q, float *scale, int c, int n) {
+template <bool kVec, bool kStaged>
+__device__ __forceinline__ void quant8(f2 (&v)[4], uint8_t *q, float *scale, int c, int n,
+                                       uint16_t *stage) {
     float a = 0.f;
 #pragma unroll
     for (int i = 0; i < 4; ++i) a = max_abs_nan(max_abs_nan(a, lo(v[i])), hi(v[i]));
@@ -163,16 +201,24 @@ __device__ __forceinline__ void quant8(f2 (&v)[4], uint8_t *q, float *scale, int
         const f2 q0 = mul2(v[i], r);
         v[i] = fma2(fma2(q0, ns, v[i]), r, q0);
     }
-    if (c >= n) return;
-    if (c % kGroup == 0) *scale = s;
+    if (c < n && c % kGroup == 0) *scale = s;
     const uint32_t c0 = e4m3x2(lo(v[0]), hi(v[0])) | e4m3x2(lo(v[1]), hi(v[1])) << 16;
     const uint32_t c1 = e4m3x2(lo(v[2]), hi(v[2])) | e4m3x2(lo(v[3]), hi(v[3])) << 16;
     if constexpr (kVec) {
-        *reinterpret_cast<uint2 *>(q + c) = make_uint2(c0, c1);
+        if (c < n) *reinterpret_cast<uint2 *>(q + c) = make_uint2(c0, c1);
     } else {
+        const int e = neighbour(c);
+        uint8_t *own = reinterpret_cast<uint8_t *>(group_stage(stage));
+        if constexpr (kStaged) {
+            *reinterpret_cast<uint2 *>(own + c % kGroup) = make_uint2(c0, c1);
+            __syncwarp();
+        }
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-            if (c + i < n) q[c + i] = (uint8_t)((i < 4 ? c0 : c1) >> (8 * (i & 3)));
+        for (int i = 0; i < kLaneElems; ++i)
+            if (e + kGroupLanes * i < n)
+                q[e + kGroupLanes * i] = kStaged ? own[e % kGroup + kGroupLanes * i]
+                                                 : (uint8_t)((i < 4 ? c0 : c1) >> (8 * (i & 3)));
+        if constexpr (kStaged) __syncwarp();
     }
 }
 
@@ -203,12 +249,15 @@ __device__ __forceinline__ f2 silu_mul(f2 g, f2 u) {
 // rmsnorm: a CTA per row, V steps of 8 elements per thread, the row in
 // registers between the sum of squares and the outputs (one pass over memory).
 // Bound by memory: 8192 rows of 5120 with the residual's sum, bf16 to 8 bits, take
-// 43.7 us (6.75 TB/s, 99% of the measured copy rate; 45.7 with scalar arithmetic).
+// 43.7 us (6.75 TB/s, 99% of the measured copy rate; 45.7 with scalar arithmetic);
+// rows of 5119, in 2-byte accesses, 110 us (142 with a lane's own elements in turn).
 // ---------------------------------------------------------------------------
 template <bool kBf16, bool kVec, int V>
 __global__ void __launch_bounds__(1024) rmsnorm_kernel(NormArgs a) {
     __shared__ float warp_sums[32];
+    __shared__ __align__(16) uint16_t stages[kVec ? 8 : 32 * kStageWarp];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    uint16_t *stage = stages + (kVec ? 0 : warp * kStageWarp);
     const size_t row = blockIdx.x;
     const uint16_t *x = a.x + row * a.H;
     chain_start();
@@ -216,10 +265,10 @@ __global__ void __launch_bounds__(1024) rmsnorm_kernel(NormArgs a) {
 #pragma unroll
     for (int s = 0; s < V; ++s) {
         const int c = (s * (int)blockDim.x + (int)threadIdx.x) * kLaneElems;
-        load8<kBf16, kVec>(x, c, a.H, h[s]);
+        load8<kBf16, kVec, true>(x, c, a.H, h[s], stage);
         if (a.residual) {
             f2 r[4];
-            load8<kBf16, kVec>(a.residual + row * a.H, c, a.H, r);
+            load8<kBf16, kVec, true>(a.residual + row * a.H, c, a.H, r, stage);
 #pragma unroll
             for (int i = 0; i < 4; ++i) h[s][i] = add2(h[s][i], r[i]);
         }
@@ -227,7 +276,7 @@ __global__ void __launch_bounds__(1024) rmsnorm_kernel(NormArgs a) {
 #pragma unroll
     for (int s = 0; s < V; ++s) {
         const int c = (s * (int)blockDim.x + (int)threadIdx.x) * kLaneElems;
-        if (a.sum_out) store8<kBf16, kVec>(a.sum_out + row * a.H, c, a.H, h[s]);
+        if (a.sum_out) store8<kBf16, kVec>(a.sum_out + row * a.H, c, a.H, h[s], stage);
 #pragma unroll
         for (int i = 0; i < 4; ++i) sums = fma2(h[s][i], h[s][i], sums);
     }
@@ -245,13 +294,14 @@ __global__ void __launch_bounds__(1024) rmsnorm_kernel(NormArgs a) {
     for (int s = 0; s < V; ++s) {
         const int c = (s * (int)blockDim.x + (int)threadIdx.x) * kLaneElems;
         f2 w[4];  // every row's: it comes from L1 or L2
-        load8<kBf16, kVec>(a.weight, c, a.H, w);
+        load8<kBf16, kVec, true>(a.weight, c, a.H, w, stage);
 #pragma unroll
         for (int i = 0; i < 4; ++i) h[s][i] = mul2(mul2(h[s][i], both(rstd)), w[i]);
-        if (a.y) store8<kBf16, kVec>(a.y + row * a.H, c, a.H, h[s]);
+        if (a.y) store8<kBf16, kVec>(a.y + row * a.H, c, a.H, h[s], stage);
         if (a.q)
-            quant8<kVec>(h[s], a.q + row * a.H,
-                         a.scales + row * ((a.H + kGroup - 1) / kGroup) + c / kGroup, c, a.H);
+            quant8<kVec, true>(h[s], a.q + row * a.H,
+                         a.scales + row * ((a.H + kGroup - 1) / kGroup) + c / kGroup, c, a.H,
+                         stage);
     }
 }
 
@@ -260,7 +310,8 @@ __global__ void __launch_bounds__(1024) rmsnorm_kernel(NormArgs a) {
 // computed; a CTA has 16 consecutive groups of a row.  Bound by memory: silu-and-mul
 // of 4096 x 17408 takes 57.6 us (6.23 TB/s, 92% of the measured copy rate; with scalar
 // arithmetic 60.3, then 67.1 with 256 threads and one group each, 63.9 with 256 and
-// two).
+// two); of 4096 x 17405, in 2-byte accesses, 90 us (104
+// with a lane's own elements in turn).
 // ---------------------------------------------------------------------------
 constexpr int kQuantThreads = 128;
 constexpr int kQuantU = 2;
@@ -276,8 +327,8 @@ __global__ void __launch_bounds__(kQuantThreads) quant_kernel(QuantArgs a) {
 #pragma unroll
     for (int s = 0; s < U; ++s) {  // all loads, then the arithmetic
         const int c = first + s * kQuantThreads * kLaneElems;
-        load8<kBf16, kVec>(x, c, a.N, v[s]);
-        if constexpr (kSilu) load8<kBf16, kVec>(x + a.N, c, a.N, u[s]);
+        load8<kBf16, kVec, false>(x, c, a.N, v[s], nullptr);
+        if constexpr (kSilu) load8<kBf16, kVec, false>(x + a.N, c, a.N, u[s], nullptr);
     }
 #pragma unroll
     for (int s = 0; s < U; ++s) {
@@ -286,7 +337,8 @@ __global__ void __launch_bounds__(kQuantThreads) quant_kernel(QuantArgs a) {
 #pragma unroll
             for (int i = 0; i < 4; ++i) v[s][i] = silu_mul(v[s][i], u[s][i]);
         }
-        quant8<kVec>(v[s], a.q + row * a.N, a.scales + row * a.G + c / kGroup, c, a.N);
+        quant8<kVec, false>(v[s], a.q + row * a.N, a.scales + row * a.G + c / kGroup, c, a.N,
+                            nullptr);
     }
 }
 
