@@ -35,7 +35,7 @@
 //   through the tensor-memory loads and multiply-adds of its 256 columns to the next
 //   product into the same columns is a chain of about 1500 cycles, and two buffers are
 //   all that the tensor memory holds; the operands' and the loads' shared-memory
-//   traffic takes the rest.  M 4096, N 34816, K 5120: 580 us, 2.52 PFLOP/s, 134% of
+//   traffic takes the rest.  M 4096, N 34816, K 5120: 580 to 588 us, 2.5 PFLOP/s, 133% of
 //   the measured bf16 rate (the same with eight sum warps of 128 columns each).  Not
 //   kept: four buffers of 128 columns (650 us), packed multiply-adds (730), three
 //   stages (630), five (no change).
