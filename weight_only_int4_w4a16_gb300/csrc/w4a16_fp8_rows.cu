@@ -174,11 +174,62 @@ __device__ __forceinline__ float group_max(float a) {
     return a;
 }
 
+// silu(g) * u = g / (1 + e^-g) * u for a 16-bit g.  e^-g = 2^(-g L), L = log2(e) =
+// H + R with H the leading bits of L, as many as make -g H exact in fp32 (13 beside
+// fp16's 11, 16 beside bf16's 8): the exponential's argument carries no rounding error,
+// which |g| would magnify.  2^(-g R) = 1 + y (+ y^2 / 2 in fp16), y = -g R ln 2: where the
+// exponential counts, |y| is at most 4.2e-3 in fp16 and 4.3e-4 in bf16, and the terms left
+// out 1.3e-8 and 9.2e-8 (where g is large and positive it is zero and the sum 1).
+// The quotient is corrected like quant8's.
+//
+// From about g = -86.6 down the sum comes near the end of fp32's range, where its
+// reciprocal would vanish, while u can still lift the result to any size.  kScale makes
+// e^-g y overflow there, so that the result is NaN: a warp with Inf or NaN leaves the
+// common path anyway (quant8), and takes silu_mul_deep for them.  Of 4096 x 17408: bf16
+// 59.5 us as with neither, fp16 61.5 (59.4 without its y^2 / 2); 70.7 when every warp has
+// such a gate (a test of each lane's gates instead cost every call 7 us).
+template <bool kBf16>
+__device__ __forceinline__ f2 silu_mul(f2 g, f2 u) {
+    constexpr float kH = kBf16 ? 1.44268798828125f : 1.442626953125f;
+    constexpr float kRLn2 = kBf16 ? 4.888495152e-06f : 4.719484150e-05f;
+    constexpr float kScale = kBf16 ? 16384.f : 2048.f;
+    const f2 t = mul2(g, both(-kH)), y = mul2(g, both(-kRLn2 * kScale));
+    float e0, e1, r0, r1;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e0) : "f"(lo(t)));
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e1) : "f"(hi(t)));
+    const f2 e = pack(e0, e1);
+    const f2 w = kBf16 ? both(-1.f / kScale)
+                       : fma2(y, both(-0.5f / (kScale * kScale)), both(-1.f / kScale));
+    const f2 s = fma2(e, both(-1.f), fma2(mul2(e, y), w, both(-1.f)));  // -(1 + e^-g)
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r0) : "f"(-lo(s)));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r1) : "f"(-hi(s)));
+    const f2 r = pack(r0, r1), q = mul2(g, r);
+    return mul2(fma2(fma2(s, q, g), r, q), u);
+}
+// The same where 1 + e^-g is e^-g to fp32's last bit: g p u p with p = e^(g/2), in an
+// order that neither overflows nor underflows before the result does.  -Inf gives NaN,
+// as the quotient does.
+__device__ __forceinline__ f2 silu_mul_deep(f2 g, f2 u) {
+    constexpr float kH = 1.442626953125f, kRLn2 = 4.719484150e-05f;
+    const f2 t = mul2(g, both(0.5f * kH)), y = mul2(g, both(0.5f * kRLn2));
+    float e0, e1;  // subnormal ones too
+    asm("ex2.approx.f32 %0, %1;" : "=f"(e0) : "f"(lo(t)));
+    asm("ex2.approx.f32 %0, %1;" : "=f"(e1) : "f"(hi(t)));
+    f2 p = pack(e0, e1);
+    p = fma2(mul2(p, y), fma2(y, both(0.5f), both(1.f)), p);
+    return mul2(mul2(mul2(g, p), u), p);
+}
+// v where it is a number, else d
+__device__ __forceinline__ f2 number_or(f2 v, f2 d) {
+    return pack(isnan(lo(v)) ? lo(d) : lo(v), isnan(hi(v)) ? hi(d) : hi(v));
+}
+
 // A lane's 8 elements of its group -> 8 codes of row q and, from the group's
-// first lane, the group's scale.  All lanes of the warp call it together.
-template <bool kVec, bool kStaged>
+// first lane, the group's scale.  All lanes of the warp call it together.  Where one of
+// the warp's elements is Inf or NaN, `again` may first compute them another way.
+template <bool kVec, bool kStaged, typename Again>
 __device__ __forceinline__ void quant8(f2 (&v)[4], uint8_t *q, float *scale, int c, int n,
-                                       uint16_t *stage) {
+                                       uint16_t *stage, Again again) {
     float a = 0.f;
 #pragma unroll
     for (int i = 0; i < 4; ++i) a = max_abs_nan(max_abs_nan(a, lo(v[i])), hi(v[i]));
@@ -186,6 +237,7 @@ __device__ __forceinline__ void quant8(f2 (&v)[4], uint8_t *q, float *scale, int
     if (__any_sync(0xffffffffu, !(a <= FLT_MAX))) {
         // an Inf or NaN in one of the warp's groups: make it NaN, and the largest
         // magnitude that of the others
+        again(v);
         a = 0.f;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -220,29 +272,6 @@ __device__ __forceinline__ void quant8(f2 (&v)[4], uint8_t *q, float *scale, int
                                                  : (uint8_t)((i < 4 ? c0 : c1) >> (8 * (i & 3)));
         if constexpr (kStaged) __syncwarp();
     }
-}
-
-// silu(g) * u = g / (1 + e^-g) * u for a 16-bit g.  e^-g = 2^(-g L), L = log2(e) =
-// H + R with H the 13 leading bits of L: -g H is exact in fp32 (11 + 13 bits), and
-// 2^(-g R) = 1 - g R ln 2 to first order (|g R| is at most 7e-5 |g|, and where |g| is
-// large the other factor makes the sum 1, or the result nothing).  So the
-// exponential's argument carries no rounding error, which |g| would magnify, at the
-// price of a product and an addition.  R > 0: an infinite 2^(-g H) stays infinite.
-// The quotient is corrected like quant8's; its divisor stops at 2^126, whose
-// reciprocal is still a normal number (the quotient is then below any scale).
-__device__ __forceinline__ f2 silu_mul(f2 g, f2 u) {
-    constexpr float kH = 1.442626953125f, kRLn2 = 4.719484150e-05f, kTop = 8.50705917e37f;
-    const f2 t = mul2(g, both(-kH));
-    float e0, e1, r0, r1;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e0) : "f"(lo(t)));
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e1) : "f"(hi(t)));
-    f2 s = pack(e0, e1);
-    s = add2(fma2(s, mul2(g, both(-kRLn2)), s), both(1.f));
-    s = pack(fminf(lo(s), kTop), fminf(hi(s), kTop));
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r0) : "f"(lo(s)));
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r1) : "f"(hi(s)));
-    const f2 r = pack(r0, r1), q = mul2(g, r);
-    return mul2(fma2(fma2(neg2(s), q, g), r, q), u);
 }
 
 // ---------------------------------------------------------------------------
@@ -301,7 +330,7 @@ __global__ void __launch_bounds__(1024) rmsnorm_kernel(NormArgs a) {
         if (a.q)
             quant8<kVec, true>(h[s], a.q + row * a.H,
                          a.scales + row * ((a.H + kGroup - 1) / kGroup) + c / kGroup, c, a.H,
-                         stage);
+                         stage, [](f2 (&)[4]) {});
     }
 }
 
@@ -335,10 +364,20 @@ __global__ void __launch_bounds__(kQuantThreads) quant_kernel(QuantArgs a) {
         const int c = first + s * kQuantThreads * kLaneElems;
         if constexpr (kSilu) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) v[s][i] = silu_mul(v[s][i], u[s][i]);
+            for (int i = 0; i < 4; ++i) v[s][i] = silu_mul<kBf16>(v[s][i], u[s][i]);
         }
+        // gates far below zero: their rows once more, from the cache
+        auto again = [&](f2 (&w)[4]) {
+            if constexpr (kSilu) {
+                f2 g[4], up[4];
+                load8<kBf16, kVec, false>(x, c, a.N, g, nullptr);
+                load8<kBf16, kVec, false>(x + a.N, c, a.N, up, nullptr);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) w[i] = number_or(w[i], silu_mul_deep(g[i], up[i]));
+            }
+        };
         quant8<kVec, false>(v[s], a.q + row * a.N, a.scales + row * a.G + c / kGroup, c, a.N,
-                            nullptr);
+                            nullptr, again);
     }
 }
 
