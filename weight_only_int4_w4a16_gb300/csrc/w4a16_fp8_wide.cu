@@ -282,8 +282,12 @@ __device__ __forceinline__ void exchange(const WideParams &p, const float *sums,
     for (int q = 0; q < kS; ++q)
         if (q < p.ksplit) {
             const uint32_t from = map_to_rank(smem_u32(sums), 2 * q + rank);
+            // only what is stored below (the staging takes everything): a load that
+            // nothing waits for could be on its way when the other CTA has left
 #pragma unroll
-            for (int i = 0; i < kC; ++i) v[q][i] = ld_cluster(from + i * kHalf * 4);
+            for (int i = 0; i < kC; ++i)
+                v[q][i] = !kTma || (lane < rows && (i & ~7) < cols)
+                              ? ld_cluster(from + i * kHalf * 4) : 0.f;
         }
     uint32_t out[kC / 2];
 #pragma unroll
@@ -697,7 +701,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int u = warp;; u += kSumWarps) {
                     const int qu = u & 3, c = ((u >> 2) * S + (int)(crank >> 1)) * width;
                     const int m = m0 + (int)rank * kHalf + qu * 32, n = n0 + c;
-                    if (c >= kTileN || n >= p.N) break;
+                    if (c >= kTileN || n >= p.N || m >= p.M) break;
                     const float *from = sums + c * kHalf + qu * 32 + lane;
                     if (S == 2) exchange<kBf16, kTma, 16, 2>(p, from, own, rank, lane, m, n);
                     else exchange<kBf16, kTma, 8, kMaxSplit>(p, from, own, rank, lane, m, n);
@@ -709,8 +713,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     tc_fence_before();
     __syncthreads();
-    // No CTA's shared or tensor memory goes while another uses it.  What was read of
-    // the others' has been used by now; the barrier orders execution only.
+    // No CTA's shared or tensor memory goes while another uses it.  Everything read of
+    // the others' has been stored by now, so it has arrived; the barrier orders
+    // execution only.
     cluster_arrive_relaxed();
     cluster_wait();
     if (warp == 0) {
