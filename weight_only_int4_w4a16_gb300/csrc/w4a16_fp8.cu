@@ -337,11 +337,17 @@ __global__ void __launch_bounds__(Cfg<T>::kThreads, 1)
                 }
             }
         }
-        // the products issued complete before the tensor memory is freed
-        if (lane == 0)
+        // the products issued complete before the tensor memory is freed, and the last
+        // arrivals land before the CTA exits (after an abort the sum warps' may not come)
+        if (lane == 0) {
             for (int i = c - kDBufs > 0 ? c - kDBufs : 0; i < c; ++i)
                 if (!mbar_wait_drain(smem_u32(d_full + i % kDBufs), (i / kDBufs) & 1))
                     atomicOr(p.status, kErrDrain);
+            const int e = c - 1;
+            if (ok && c > 0 && !mbar_wait(smem_u32(empty + e % NS), (e / NS) & 1, abort) &&
+                !*abort)
+                fail(kErrDrain);
+        }
     } else {
         // ------------------------------------------------ sums and outputs
         grid_dependency_wait();

@@ -427,6 +427,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                     for (int i = c - kStages > 0 ? c - kStages : 0; i < c; ++i)
                         if (!mbar_wait_drain(smem_u32(full + i % kStages), (i / kStages) & 1))
                             atomicOr(p.status, kErrDrain);
+                // and so must the leader's arrivals at this CTA's barriers (after an
+                // abort the products that were to bring them may not have been issued)
+                for (int i = c - kStages > 0 ? c - kStages : 0; ok && i < c; ++i)
+                    ok = mbar_wait(smem_u32(empty + i % kStages), (i / kStages) & 1, abort);
+                if (!ok && !*abort) fail(kErrDrain);
             }
         } else if (warp == kMmaWarp) {
             // ------------------------------------------------ products
@@ -465,6 +470,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                     for (int i = c - kDBufs > 0 ? c - kDBufs : 0; i < c; ++i)
                         if (!mbar_wait_drain(smem_u32(d_full + i % kDBufs), (i / kDBufs) & 1))
                             atomicOr(p.status, kErrDrain);
+                // as have the arrivals from the other CTA's sum warps
+                for (int i = c - kDBufs > 0 ? c - kDBufs : 0; ok && i < c; ++i)
+                    ok = mbar_wait_all(smem_u32(d_empty + i % kDBufs), (i / kDBufs) & 1, abort);
+                if (!ok && !*abort && lane == 0) fail(kErrDrain);
             }
         } else if (warp > kMmaWarp) {
             // ------------------------------------------------ scales
@@ -714,8 +723,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_before();
     __syncthreads();
     // No CTA's shared or tensor memory goes while another uses it.  Everything read of
-    // the others' has been stored by now, so it has arrived; the barrier orders
-    // execution only.
+    // the others' has been stored by now, and every arrival at a barrier of theirs has
+    // been waited for there, so all of it has landed; the barrier orders execution only.
     cluster_arrive_relaxed();
     cluster_wait();
     if (warp == 0) {
