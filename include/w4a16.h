@@ -524,7 +524,8 @@ int w4a16_device_status(void *stream, int *code);
  * waits on a completion counter that nothing increments and on an mbarrier
  * that nothing arrives at; each gives up after its limit (200 ms) and ORs a
  * bit into the device status word (4096: the counter wait, 8192: the
- * mbarrier wait), which the next w4a16_device_status returns.  When a
+ * mbarrier wait, reported by a second warp that learns of it at a barrier),
+ * which the next w4a16_device_status returns.  When a
  * w4a16_linear_noalloc call has set up the current device, a second probe
  * does the same on that scratch's status word after incrementing its first
  * block counter, as a split-K launch cut short can leave it.  Nothing faults

@@ -41,7 +41,9 @@
 //
 // Every mbarrier wait is bounded; on expiry the kernel records an error code in
 // the device status word, drains what it has in flight, frees its tensor memory
-// and exits.
+// and exits.  The barriers of split tiles have no limit of their own: every sum warp
+// comes to the first one, whether or not its waits were met, and there they agree on
+// whether to go on (barrier_all).
 #include <cstring>
 
 #include "w4a16_fp8_common.cuh"
@@ -356,13 +358,15 @@ __global__ void __launch_bounds__(Cfg<T>::kThreads, 1)
         const int cb = (warp >> 2) * kCols;     // first token within the tile
         const uint32_t taddr = tmem + ((uint32_t)((warp & 3) * 32) << 16) + cb;
         int c = 0;
+        // false once a wait has given up: then the warp computes and stores nothing more,
+        // but walks on to the next tile that is split, where all sum warps meet
         bool ok = true;
-        while (ok && walk.next(p, t, j0, j1)) {
+        while (walk.next(p, t, j0, j1)) {
             const int n = t * kTileN + r, mt = p.M - cb;  // this thread's tokens: i < mt
             float acc[kCols];
 #pragma unroll
             for (int i = 0; i < kCols; ++i) acc[i] = 0.f;
-            for (int j = j0; j < j1; j += kSub, ++c) {
+            for (int j = j0; j < j1 && ok; j += kSub, ++c) {
                 const int s = c % NS, d = c % kDBufs;
                 const bool two = j + 1 < j1;
                 const float *sc = sm_scales + s * C::kScales;
@@ -416,9 +420,8 @@ __global__ void __launch_bounds__(Cfg<T>::kThreads, 1)
                         acc[i] = fmaf(__uint_as_float(v[i]), f[i], acc[i]);
                 }
             }
-            if (!ok) break;
             if (j0 == 0 && j1 == p.G) {  // a whole tile
-                if (n < p.N) {
+                if (ok && n < p.N) {
 #pragma unroll
                     for (int i = 0; i < kCols; i += 16) store16(p, cb + i, n, acc + i);
                 }
@@ -441,7 +444,8 @@ __global__ void __launch_bounds__(Cfg<T>::kThreads, 1)
             for (int i = 0; i < kCols; ++i)
                 if (i < mt) part[(size_t)i * kTileN] = acc[i];
             __threadfence();
-            asm volatile("bar.sync 1, %0;" ::"r"(C::kSumWarps * 32) : "memory");
+            ok = barrier_all(1, C::kSumWarps * 32, ok);
+            if (!ok) break;  // all of them
             const int b0 = Walk::owner(p, tile0), b1 = Walk::owner(p, tile0 + p.G - 1);
             if (threadIdx.x == 0)
                 *s_last = atomicAdd(p.counters + t, 1u) == (unsigned)(b1 - b0) ? 1 : 0;

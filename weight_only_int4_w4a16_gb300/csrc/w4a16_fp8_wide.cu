@@ -545,13 +545,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         };
         const bool staged_res = kTma && p.residual;
         int c = 0;
+        // ok: false once a wait has given up.  Then the warp computes and stores nothing
+        // more, but walks on to the next tile that is split, where all sum warps meet
         bool ok = true, more = walk.next(p, t, j0, j1);
         while (more) {
             tile_at(p, t, m0, n0);
             const int mw = m0 + (int)rank * kHalf + quarter * 32;
             const int nc = n0 + col, tt = t, end = j1;
             const bool whole = j0 == 0 && j1 == p.G;
-            if (whole && staged_res) ask_residual(nc, mw);
+            if (ok && whole && staged_res) ask_residual(nc, mw);
             if constexpr (!kTma) {
                 // the residual's rows on their way to L2 meanwhile (a row's 128 bytes
                 // are in at most two lines): 1240 tokens, N 33532, K 1440 156 us for 177
@@ -598,7 +600,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
             }
             if (!ok && lane == 0) fail(kErrSumWait);
-            if (!ok) break;
             more = walk.next(p, t, j0, j1);
             if (p.ksplit > 1) {
                 // the cluster's tile: the sums wait in this CTA's stages, which
@@ -621,7 +622,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 };
                 unsigned *there = p.counters + 2 * (tt - p.whole) + rank;  // pieces in slots
                 if (threadIdx.x == 0) *s_last = atomicAdd(there, 0u) != 0u;
-                asm volatile("bar.sync 1, %0;" ::"r"(kSumWarps * 32) : "memory");
+                ok = barrier_all(1, kSumWarps * 32, ok);
+                if (!ok) break;  // all of them
                 if (!*s_last) {
                     float *part = slot(walk.pair);
 #pragma unroll
@@ -651,13 +653,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                 asm volatile("bar.sync 1, %0;" ::"r"(kSumWarps * 32) : "memory");
                 if (!last) continue;
             }
+            if (!ok) continue;
             // y[m][nc .. nc + 63] = sums (+ residual), one rounding each, by way of the
             // warp's staging: the residual comes there, and the outputs leave from
             // there, by TMA or (rows that TMA cannot address) by the warp's own copies
             if (staged_res) {
-                if (!mbar_wait_all(bar_res, res_taken & 1, abort)) {
+                ok = mbar_wait_all(bar_res, res_taken & 1, abort);
+                if (!ok) {
                     if (lane == 0) fail(kErrStageWait);
-                    break;
+                    continue;
                 }
                 ++res_taken;
             } else if constexpr (kTma) {
