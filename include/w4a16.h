@@ -506,18 +506,21 @@ void w4a16_probe_reset(void);
 const char *w4a16_rung_name(int rung);
 const char *w4a16_status_string(int status);
 
-/* Kernels that wait on on-chip barriers (the tensor-core rungs) bound every
- * wait by a timer; if one expires the kernel ORs a code into a device status
- * word, drains its in-flight copies, frees its tensor memory and exits, so the
- * CUDA context stays usable.  This call synchronises `stream`, returns
- * W4A16_ERR_DEVICE with the accumulated code in *code (may be NULL) if any
- * kernel reported one since the last call, and clears the word.  It also
- * reads the status word of w4a16_linear_noalloc's scratch on the current
- * device (once a call has set that device up) and ORs it in; when that word
- * is set it re-zeroes the scratch's block counters and scheduling words too,
- * since a launch cut short by an expired wait can leave them nonzero (call it
- * with no w4a16_linear_noalloc call in flight).  W4A16_ERR_NOT_INITIALIZED
- * when neither w4a16_init nor a w4a16_linear_noalloc call has run. */
+/* Kernels that wait on on-chip barriers (the tensor-core rungs, the 8-bit
+ * linear) bound every wait by a timer; if one expires the kernel ORs a code
+ * into a device status word, drains its in-flight copies, frees its tensor
+ * memory and exits, so the CUDA context stays usable.  This call synchronises
+ * `stream`, returns W4A16_ERR_DEVICE with the accumulated code in *code (may be
+ * NULL) if any kernel reported one since the last call, and clears the word.
+ * It also reads the status word of w4a16_linear_noalloc's scratch on the
+ * current device (once a call has set that device up) and ORs it in.  Where a
+ * word holds an expired wait, the block counters and scheduling words beside it
+ * (the w4a16_init workspace's, the scratch's) are zeroed too, since a launch
+ * cut short can leave them nonzero: call it with no other call of this library
+ * in flight on another stream.  A captured round or an expert MLP keeps
+ * counters of its own: after an expired wait destroy it and create it again.
+ * W4A16_ERR_NOT_INITIALIZED when neither w4a16_init nor a
+ * w4a16_linear_noalloc call has run. */
 int w4a16_device_status(void *stream, int *code);
 
 /* Exercise the expired-wait report: one thread runs the library's bounded
@@ -525,10 +528,10 @@ int w4a16_device_status(void *stream, int *code);
  * that nothing arrives at; each gives up after its limit (200 ms) and ORs a
  * bit into the device status word (4096: the counter wait, 8192: the
  * mbarrier wait, reported by a second warp that learns of it at a barrier),
- * which the next w4a16_device_status returns.  When a
+ * which the next w4a16_device_status returns.  Before that it increments the
+ * workspace's first counter, as a split launch cut short can leave it.  When a
  * w4a16_linear_noalloc call has set up the current device, a second probe
- * does the same on that scratch's status word after incrementing its first
- * block counter, as a split-K launch cut short can leave it.  Nothing faults
+ * does the same on that scratch's counter and status word.  Nothing faults
  * or hangs; the stream is busy for about 0.4 s per probe.  For tests of the
  * error path.  Needs w4a16_init. */
 int w4a16_wait_probe(void *stream);

@@ -1453,11 +1453,15 @@ int w4a16_device_status(void *stream, int *code) {
     if (e == cudaSuccess && have_na)
         e = cudaMemcpyAsync(&hn, na.status, sizeof(int), cudaMemcpyDeviceToHost, st);
     if (e == cudaSuccess) e = cudaStreamSynchronize(st);
+    // an expired wait may have left a block's or a tile's arrival counted and
+    // never reduced, or the scheduling words set: zero them with the word, in
+    // the workspace and in the allocation-free scratch, so that later calls
+    // start clean
+    if (e == cudaSuccess && (h & ~kErrMoeIds) != 0)
+        e = cudaMemsetAsync(g_state.ws.counters, 0,
+                            (size_t)g_state.ws.n_counters * sizeof(unsigned), st);
     if (e == cudaSuccess && h != 0)
         e = cudaMemsetAsync(g_state.ws.status, 0, sizeof(int), st);
-    // an expired wait in the allocation-free kernel may have left a block's
-    // arrival counted and never reduced, or the scheduling words set: zero
-    // them with the word, so that later calls start clean
     if (e == cudaSuccess && hn != 0) e = cudaMemsetAsync(na.counters, 0, na.counter_bytes, st);
     if (e == cudaSuccess && hn != 0) e = cudaMemsetAsync(na.status, 0, sizeof(int), st);
     if (e == cudaSuccess) e = cudaStreamSynchronize(st);
@@ -1469,11 +1473,14 @@ int w4a16_device_status(void *stream, int *code) {
 
 int w4a16_wait_probe(void *stream) {
     if (!g_state.initialized) return W4A16_ERR_NOT_INITIALIZED;
-    cudaError_t e = launch_wait_probe(g_state.ws.status, nullptr, (cudaStream_t)stream);
+    // the workspace's first counter is left as a cut-short split launch can
+    // leave one
+    cudaError_t e =
+        launch_wait_probe(g_state.ws.status, g_state.ws.counters, (cudaStream_t)stream);
     g_launches.fetch_add(1, std::memory_order_relaxed);
     // the allocation-free linear's scratch, when set up on this device: the
-    // same expired waits report into its word, and its first block counter is
-    // left as a cut-short split-K launch can leave one
+    // same expired waits report into its word, and its first counter is left
+    // in the same way
     NoAllocScratch na{};
     int device = 0;
     if (e == cudaSuccess && cudaGetDevice(&device) == cudaSuccess &&
