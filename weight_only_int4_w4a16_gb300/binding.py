@@ -356,33 +356,61 @@ def _rows2d(t: torch.Tensor, name: str):
     return t.shape
 
 
-def _shaped(t: torch.Tensor, dtype, shape, name: str) -> int:
-    """The address of a contiguous CUDA tensor of this type and shape (the checks
-    of a good tensor come first and are cheap: a small call's time is mostly the host's)."""
-    if not (isinstance(t, torch.Tensor) and t.is_cuda and t.dtype is dtype and
+def _shaped(t: torch.Tensor, dtype, shape, name: str, device: int) -> int:
+    """The address of a contiguous tensor of this type and shape on this CUDA device (the
+    checks of a good tensor come first and are cheap: a small call's time is mostly the
+    host's)."""
+    if not (isinstance(t, torch.Tensor) and t.get_device() == device and t.dtype is dtype and
             t.shape == shape and t.is_contiguous()):
         _dev(t, dtype, name)
+        if t.get_device() != device:
+            raise ValueError(f"{name} must live on cuda:{device} like x, not cuda:{t.get_device()}")
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
     return t.data_ptr()
 
 
-# A new tensor on the current device (where the kernels run) without torch.empty's way
-# through the dispatcher: 1.1 us against 1.8 beside a launch, of a small call's 10.
-_empty_cuda = torch._C._dynamo.guards._empty_strided_cuda
+def _home(x: torch.Tensor, dtype, shape) -> tuple[int, int]:
+    """(x's device, its address).  Kernels run on the current device, so x has to live there,
+    and everything else with it."""
+    if not (isinstance(x, torch.Tensor) and x.is_cuda):
+        _dev(x, dtype, "x")
+    device = x.get_device()
+    if device != _current_device():
+        raise ValueError(f"x lives on cuda:{device}, but the current device is "
+                         f"cuda:{_current_device()}")
+    if x.dtype is dtype and x.shape == shape and x.is_contiguous():
+        return device, x.data_ptr()
+    return device, _shaped(x, dtype, shape, "x", device)
 
 
-def _output(t, shape, dtype, like: torch.Tensor, side, name: str):
-    """(t, its address), checked, or a new tensor on like's device: of the stream
-    `side`'s memory when there is one, as memory of the current stream may still be
+# Functions of torch's that are not part of its interface, for the time that they save (a
+# new tensor on the current device without torch.empty's way through the dispatcher, 1.1 us
+# against 1.8 beside a launch; the current device and the address of its stream without
+# checks and objects made around them).  A torch that lacks one is served by the interface's
+# own.
+_empty_cuda = getattr(getattr(getattr(torch._C, "_dynamo", None), "guards", None),
+                      "_empty_strided_cuda", None)
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+if _raw_stream is None:
+    def _raw_stream(device: int) -> int:
+        return torch.cuda.current_stream(device).cuda_stream
+
+
+def _output(t, shape, dtype, device: int, side, name: str):
+    """(t, its address), checked, or a new tensor on this device, the current one: of the
+    stream `side`'s memory when there is one, as memory of the current stream may still be
     in use there, and kept for what the current stream does with it afterwards."""
     if t is not None:
-        return t, _shaped(t, dtype, shape, name)
-    if side is None:
+        return t, _shaped(t, dtype, shape, name, device)
+    if side is not None:
+        with torch.cuda.stream(side):
+            t = torch.empty(shape, dtype=dtype, device=f"cuda:{device}")
+        t.record_stream(torch.cuda.current_stream(device))
+    elif _empty_cuda is not None:
         t = _empty_cuda(shape, (shape[1], 1), dtype)
     else:
-        with torch.cuda.stream(side):
-            t = torch.empty(shape, dtype=dtype, device=like.device)
-        t.record_stream(torch.cuda.current_stream(like.device))
+        t = torch.empty(shape, dtype=dtype, device=f"cuda:{device}")
     return t, t.data_ptr()
 
 
@@ -392,16 +420,17 @@ def _dtype16(dt) -> int:
     return _DTYPE_OF[dt]
 
 
-def _stream_for(t: torch.Tensor, stream):
-    """(the address of a call's stream on t's device, that stream as torch's if it is
+def _stream_for(device: int, stream):
+    """(the address of a call's stream on this device, that stream as torch's if it is
     not the current one)."""
-    current = torch._C._cuda_getCurrentRawStream(t.get_device())
+    current = _raw_stream(device)
     if stream is None:
         return current, None
     raw = _stream_ptr(stream)
     if raw == current:
         return raw, None
-    return raw, stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(raw)
+    return raw, stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(
+        raw, device=device)
 
 
 def _used_on(side, *tensors) -> None:
@@ -425,12 +454,13 @@ def w4a16_fp8_linear(x: torch.Tensor, x_scales: torch.Tensor, w: torch.Tensor,
     if K != Kw:
         raise ValueError(f"x has {K} columns and w {Kw}")
     dt, G = _dtype16(dtype), (K + GROUP - 1) // GROUP
-    xp, wp = _shaped(x, FP8, (M, K), "x"), _shaped(w, FP8, (N, K), "w")
-    xs = _shaped(x_scales, torch.float32, (M, G), "x_scales")
-    ws = _shaped(w_scales, torch.float32, ((N + GROUP - 1) // GROUP, G), "w_scales")
-    r = None if residual is None else _shaped(residual, dtype, (M, N), "residual")
-    raw, side = _stream_for(x, stream)
-    y, yp = _output(y, (M, N), dtype, x, side, "y")
+    dev, xp = _home(x, FP8, (M, K))
+    wp = _shaped(w, FP8, (N, K), "w", dev)
+    xs = _shaped(x_scales, torch.float32, (M, G), "x_scales", dev)
+    ws = _shaped(w_scales, torch.float32, ((N + GROUP - 1) // GROUP, G), "w_scales", dev)
+    r = None if residual is None else _shaped(residual, dtype, (M, N), "residual", dev)
+    raw, side = _stream_for(dev, stream)
+    y, yp = _output(y, (M, N), dtype, dev, side, "y")
     _used_on(side, x, x_scales, w, w_scales, residual, y)
     _check(lib.w4a16_fp8_linear(xp, xs, wp, ws, M, N, K, dt, epilogue, r, yp, raw),
            "w4a16_fp8_linear")
@@ -438,20 +468,21 @@ def w4a16_fp8_linear(x: torch.Tensor, x_scales: torch.Tensor, w: torch.Tensor,
 
 
 def _norm_inputs(x, weight, residual, sum_out, stream):
-    """(M, H, dtype code; addresses of x, weight and residual; sum_out and its address;
-    the stream, as _stream_for gives it)."""
+    """(M, H, dtype code; the device; addresses of x, weight and residual; sum_out and its
+    address; the stream, as _stream_for gives it)."""
     M, H = _rows2d(x, "x")
     dt = x.dtype
     code = _dtype16(dt)
-    xp, wp = _shaped(x, dt, (M, H), "x"), _shaped(weight, dt, (H,), "weight")
-    raw, side = _stream_for(x, stream)
+    dev, xp = _home(x, dt, (M, H))
+    wp = _shaped(weight, dt, (H,), "weight", dev)
+    raw, side = _stream_for(dev, stream)
     rp = sp = None
     if residual is not None:
-        rp = _shaped(residual, dt, (M, H), "residual")
-        sum_out, sp = _output(sum_out, (M, H), dt, x, side, "sum_out")
+        rp = _shaped(residual, dt, (M, H), "residual", dev)
+        sum_out, sp = _output(sum_out, (M, H), dt, dev, side, "sum_out")
     elif sum_out is not None:
         raise ValueError("sum_out needs a residual")
-    return M, H, code, xp, wp, rp, sum_out, sp, raw, side
+    return M, H, code, dev, xp, wp, rp, sum_out, sp, raw, side
 
 
 def w4a16_rmsnorm(x: torch.Tensor, weight: torch.Tensor, residual=None, eps: float = 1e-6,
@@ -459,9 +490,9 @@ def w4a16_rmsnorm(x: torch.Tensor, weight: torch.Tensor, residual=None, eps: flo
     """y [M, H] = h / sqrt(mean(h^2) + eps) * weight with h = x (+ residual).
     Returns y, or (y, sum_out) when a residual is given: sum_out is h rounded to
     the 16-bit type (sum_out=residual updates the residual in place)."""
-    M, H, code, xp, wp, rp, sum_out, sp, raw, side = _norm_inputs(x, weight, residual, sum_out,
-                                                                 stream)
-    y, yp = _output(y, (M, H), x.dtype, x, side, "y")
+    M, H, code, dev, xp, wp, rp, sum_out, sp, raw, side = _norm_inputs(x, weight, residual,
+                                                                      sum_out, stream)
+    y, yp = _output(y, (M, H), x.dtype, dev, side, "y")
     _used_on(side, x, weight, residual, sum_out, y)
     _check(lib.w4a16_rmsnorm(xp, rp, wp, M, H, eps, code, sp, yp, None, None, raw),
            "w4a16_rmsnorm")
@@ -472,10 +503,10 @@ def w4a16_rmsnorm_fp8(x: torch.Tensor, weight: torch.Tensor, residual=None, eps:
                       sum_out=None, q=None, scales=None, stream=None):
     """w4a16_rmsnorm with its rows in 8 bits: (q [M, H], scales [M, ceil(H/128)]),
     and sum_out third when a residual is given."""
-    M, H, code, xp, wp, rp, sum_out, sp, raw, side = _norm_inputs(x, weight, residual, sum_out,
-                                                                 stream)
-    q, qp = _output(q, (M, H), FP8, x, side, "q")
-    scales, cp = _output(scales, (M, (H + GROUP - 1) // GROUP), torch.float32, x, side, "scales")
+    M, H, code, dev, xp, wp, rp, sum_out, sp, raw, side = _norm_inputs(x, weight, residual,
+                                                                      sum_out, stream)
+    q, qp = _output(q, (M, H), FP8, dev, side, "q")
+    scales, cp = _output(scales, (M, (H + GROUP - 1) // GROUP), torch.float32, dev, side, "scales")
     _used_on(side, x, weight, residual, sum_out, q, scales)
     _check(lib.w4a16_rmsnorm(xp, rp, wp, M, H, eps, code, sp, None, qp, cp, raw),
            "w4a16_rmsnorm_fp8")
@@ -489,10 +520,10 @@ def w4a16_fp8_quant(x: torch.Tensor, epilogue: int = EPILOGUE_NONE, q=None, scal
     M, cols = _rows2d(x, "x")
     dt = _dtype16(x.dtype)
     N = cols // 2 if epilogue == EPILOGUE_SILU_MUL else cols
-    xp = _shaped(x, x.dtype, (M, cols), "x")
-    raw, side = _stream_for(x, stream)
-    q, qp = _output(q, (M, N), FP8, x, side, "q")
-    scales, cp = _output(scales, (M, (N + GROUP - 1) // GROUP), torch.float32, x, side, "scales")
+    dev, xp = _home(x, x.dtype, (M, cols))
+    raw, side = _stream_for(dev, stream)
+    q, qp = _output(q, (M, N), FP8, dev, side, "q")
+    scales, cp = _output(scales, (M, (N + GROUP - 1) // GROUP), torch.float32, dev, side, "scales")
     _used_on(side, x, q, scales)
     _check(lib.w4a16_fp8_quant(xp, M, cols, epilogue, dt, qp, cp, raw), "w4a16_fp8_quant")
     return q, scales
