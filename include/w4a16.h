@@ -485,6 +485,17 @@ int w4a16_select_rung(int M, int N, int K, int group);
  * the shape. */
 int w4a16_plan_info(int M, int N, int K, int group, int epilogue, int dtype, int32_t *info);
 
+/* How w4a16_fp8_linear would cut its work for these sizes now: info[0] 0 for the
+ * kernel of up to 64 tokens (tiles of 128 weight rows, a CTA each), 1 for the one
+ * of more (tiles of 256 tokens x 256 weight rows, a pair of CTAs each); info[1]
+ * CTAs in the launch; info[2] the CTAs (or pairs) of a cluster that split each
+ * tile along K and exchange their sums, 1 for none; info[3] the tiles that are cut
+ * into equal runs of blocks, their pieces summed through the workspace, 0 for
+ * none.  Pure host query; before w4a16_init it assumes 152 SMs, clusters wherever
+ * they fit, and the default workspace.  INVALID_ARG for sizes that the call does
+ * not take (or M = 0, or a null info). */
+int w4a16_fp8_plan_info(int M, int N, int K, int32_t *info);
+
 /* Force a rung for later calls (W4A16_RUNG_AUTO restores the table).  A forced
  * rung that cannot run a shape makes that call return W4A16_ERR_UNSUPPORTED.
  * Returns the previous setting, or -2 for an invalid rung.  Host state only:

@@ -1395,6 +1395,32 @@ int w4a16_plan_info(int M, int N, int K, int group, int epilogue, int dtype, int
     return W4A16_OK;
 }
 
+int w4a16_fp8_plan_info(int M, int N, int K, int32_t *info) {
+    if (!info || M < 1 || M > kMaxM || N < 1 || K < 1 || K > kMaxK || K % 16 != 0)
+        return W4A16_ERR_INVALID_ARG;
+    DeviceInfo dev = g_state.dev;
+    Workspace ws = g_state.ws;
+    if (!g_state.initialized) {
+        dev.sm_count = 152;
+        ws.partial_bytes = kDefaultWorkspace;
+        ws.n_counters = kCounters;
+    }
+    const bool wide = fp8_takes_wide(M);
+    info[0] = wide;
+    if (wide) {
+        const Fp8WidePlan p = plan_fp8_wide(M, N, K, dev, ws);
+        info[1] = 2 * p.pairs;
+        info[2] = p.ksplit;
+        info[3] = (int32_t)(p.split / p.G);
+    } else {
+        const Fp8Plan p = plan_fp8(M, N, K, dev, ws);
+        info[1] = p.grid;
+        info[2] = p.ksplit;
+        info[3] = p.streamk ? p.tiles : 0;
+    }
+    return W4A16_OK;
+}
+
 int w4a16_set_forced_rung(int rung) {
     if (rung < W4A16_RUNG_AUTO || rung >= W4A16_NUM_RUNGS) return -2;
     std::lock_guard<std::mutex> lock(g_mutex);

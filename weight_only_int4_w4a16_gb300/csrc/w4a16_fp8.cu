@@ -560,8 +560,12 @@ cudaError_t launch_t(const Fp8Params &p, int grid, cudaStream_t stream) {
     return cudaLaunchKernelEx(&cfg, fp8_kernel<T>, p);
 }
 
-// clusters of k CTAs that run at the same time, found once per process
+// clusters of k CTAs that run at the same time, found by fp8_init (before it, as many as
+// the SMs hold)
 int g_clusters[kMaxCluster + 1];
+int clusters(int k, const DeviceInfo &dev) {
+    return g_clusters[k] ? g_clusters[k] : dev.sm_count / k;
+}
 
 }  // namespace
 
@@ -569,14 +573,14 @@ Fp8Plan plan_fp8(int M, int N, int K, const DeviceInfo &dev, const Workspace &ws
     Fp8Plan pl{};
     pl.T = M <= 16 ? 16 : M <= 32 ? 32 : 64;
     pl.G = (K + kGroup - 1) / kGroup;
-    pl.tiles = (N + kTileN - 1) / kTileN;
+    pl.tiles = (int)(((long long)N + kTileN - 1) / kTileN);  // N up to 2^31 - 1
     pl.ksplit = 1;
     pl.grid = pl.tiles < dev.sm_count ? pl.tiles : dev.sm_count;
     // few tiles: the largest cluster that keeps every tile in one wave (N 5120: M 8,
     // K 5120 15.0 us against 19.1 in equal runs; M 64, K 17408 29.3 against 33.4), with
     // at least two blocks of K per CTA (M 8, N 512, K 1024: 8.8 us, 10.9 with four)
     for (int k = kMaxCluster; k > 1; --k)
-        if (pl.tiles <= g_clusters[k] && pl.G >= 2 * k) {
+        if (pl.tiles <= clusters(k, dev) && pl.G >= 2 * k) {
             pl.ksplit = k;
             pl.grid = pl.tiles * k;
             return pl;

@@ -560,7 +560,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (whole && p.residual && mw + lane < p.M && nc < p.N) {
                     const uint16_t *row = p.residual + (size_t)(mw + lane) * p.N;
                     prefetch_l2(row + nc);
-                    prefetch_l2(row + min(nc + kStoreCols, p.N) - 1);
+                    prefetch_l2(row + nc + min(kStoreCols, p.N - nc) - 1);
                 }
             }
             float acc[kCols];
@@ -754,8 +754,12 @@ void config(cudaLaunchConfig_t &cfg, cudaLaunchAttribute (&attr)[2], int pairs, 
     cfg.numAttrs = 2;
 }
 
-// clusters of k pairs that run at the same time, found once per process
+// clusters of k pairs that run at the same time, found by fp8_wide_init (before it, as
+// many as the SMs hold)
 int g_clusters[kMaxSplit + 1];
+int clusters(int k, const DeviceInfo &dev) {
+    return g_clusters[k] ? g_clusters[k] : dev.sm_count / (2 * k);
+}
 
 }  // namespace
 
@@ -763,7 +767,7 @@ Fp8WidePlan plan_fp8_wide(int M, int N, int K, const DeviceInfo &dev, const Work
     Fp8WidePlan pl{};
     pl.G = (K + kGroup - 1) / kGroup;
     pl.tiles_m = (M + kTileM - 1) / kTileM;
-    pl.tiles_n = (N + kTileN - 1) / kTileN;
+    pl.tiles_n = (int)(((long long)N + kTileN - 1) / kTileN);  // N up to 2^31 - 1
     const long long tiles = (long long)pl.tiles_m * pl.tiles_n;
     const int pairs = dev.sm_count / 2;
     pl.pairs = (int)(tiles < pairs ? tiles : pairs);
@@ -778,7 +782,7 @@ Fp8WidePlan plan_fp8_wide(int M, int N, int K, const DeviceInfo &dev, const Work
     // K 5120 19.1 us with eight, 12.8 with four.
     const int least = N % 8 == 0 ? 8 : 2;
     for (int k = kMaxSplit; k > 1; --k)
-        if (tiles <= g_clusters[k] && pl.G >= least * k) {
+        if (tiles <= clusters(k, dev) && pl.G >= least * k) {
             pl.ksplit = k;
             pl.pairs = (int)tiles * k;
             pl.whole = 0;
@@ -827,7 +831,7 @@ cudaError_t launch_fp8_wide(const Fp8Args &a, const Fp8WidePlan &plan, const Wor
     p.M = a.M;
     p.N = a.N;
     p.G = plan.G;
-    p.NB = (a.N + kGroup - 1) / kGroup;
+    p.NB = (int)(((long long)a.N + kGroup - 1) / kGroup);
     p.tiles_m = plan.tiles_m;
     p.tiles_n = plan.tiles_n;
     p.scales16 = plan.G % 4 == 0 && ((uintptr_t)a.xs & 15) == 0 && ((uintptr_t)a.ws & 15) == 0;
