@@ -34,8 +34,8 @@ def quant(w4, x):
     return w4.w4a16_fp8_quant(x.to(DEV), epilogue=w4.EPILOGUE_SILU_MUL)
 
 
-def check(q, scales, v, what):
-    """Codes and scales of rows v (binary64) within the tolerance above."""
+def check(q, scales, v, what, E=E):
+    """Codes and scales of rows v (binary64), whose own error is E, within the tolerance above."""
     want = ref.row_scales(v)
     s = scales.cpu().double().numpy()
     off = np.abs(s - want) / want
