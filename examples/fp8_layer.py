@@ -1,6 +1,6 @@
 """The linears of a decoder layer in 8 bits, around an attention of the caller's:
 
-    q8, h   = norm(h + mlp_out)           w4a16_rmsnorm_fp8 (the residual stream in place)
+    q8      = norm(h)                     w4a16_rmsnorm_fp8
     qkv     = q8 @ Wqkv^T                 w4a16_fp8_linear
     a       = attention(qkv)              the caller's (here: a stand-in that takes columns)
     h      += quant(a) @ Wo^T             w4a16_fp8_quant, w4a16_fp8_linear with the residual
