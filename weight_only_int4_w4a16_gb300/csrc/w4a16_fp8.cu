@@ -561,11 +561,10 @@ cudaError_t launch_t(const Fp8Params &p, int grid, cudaStream_t stream) {
 }
 
 // clusters of k CTAs that run at the same time, found by fp8_init (before it, as many as
-// the SMs hold)
+// the SMs hold; there may be none of some size)
 int g_clusters[kMaxCluster + 1];
-int clusters(int k, const DeviceInfo &dev) {
-    return g_clusters[k] ? g_clusters[k] : dev.sm_count / k;
-}
+bool g_found;
+int clusters(int k, const DeviceInfo &dev) { return g_found ? g_clusters[k] : dev.sm_count / k; }
 
 }  // namespace
 
@@ -655,6 +654,7 @@ cudaError_t fp8_init(const DeviceInfo &) {
         const cudaError_t e = cudaOccupancyMaxActiveClusters(&g_clusters[k], fp8_kernel<64>, &cfg);
         if (e != cudaSuccess) return e;
     }
+    g_found = true;
     return cudaSuccess;
 }
 

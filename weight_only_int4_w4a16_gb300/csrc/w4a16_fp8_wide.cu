@@ -755,10 +755,11 @@ void config(cudaLaunchConfig_t &cfg, cudaLaunchAttribute (&attr)[2], int pairs, 
 }
 
 // clusters of k pairs that run at the same time, found by fp8_wide_init (before it, as
-// many as the SMs hold)
+// many as the SMs hold; there may be none of some size)
 int g_clusters[kMaxSplit + 1];
+bool g_found;
 int clusters(int k, const DeviceInfo &dev) {
-    return g_clusters[k] ? g_clusters[k] : dev.sm_count / (2 * k);
+    return g_found ? g_clusters[k] : dev.sm_count / (2 * k);
 }
 
 }  // namespace
@@ -862,6 +863,7 @@ cudaError_t fp8_wide_init(const DeviceInfo &) {
         cfg.numAttrs = 1;
         e = cudaOccupancyMaxActiveClusters(&g_clusters[k], fp8_wide_kernel<true, true>, &cfg);
     }
+    g_found = e == cudaSuccess;
     return e;
 }
 
