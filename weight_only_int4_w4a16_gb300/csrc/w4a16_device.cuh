@@ -1,5 +1,5 @@
 // Device helpers shared by the W4A16 kernels: the nibble unpack, the
-// activation pair order that matches it, and mbarrier / timer wrappers.
+// activation pair order that matches it, and barrier / timer wrappers.
 #pragma once
 
 #include <cuda_fp16.h>
@@ -80,6 +80,22 @@ __device__ __forceinline__ unsigned long long globaltimer() {
     unsigned long long t;
     asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
     return t;
+}
+
+// Named barrier `id` of `threads` threads (whole warps, each converged) that also tells
+// whether `ok` holds in all of them.  Warps whose waits may give up one by one agree here on whether to go on: all of
+// them have to come, so one that has given up comes too.
+__device__ __forceinline__ bool barrier_all(int id, int threads, bool ok) {
+    uint32_t all;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.u32 p, %1, 0;\n\t"
+        "barrier.cta.red.and.pred.aligned q, %2, %3, p;\n\t"
+        "selp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(all)
+        : "r"((uint32_t)ok), "r"(id), "r"(threads)
+        : "memory");
+    return all != 0;
 }
 
 }  // namespace dev

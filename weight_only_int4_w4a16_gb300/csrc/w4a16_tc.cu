@@ -58,6 +58,7 @@
 
 #include <cstring>
 
+#include "w4a16_device.cuh"
 #include "w4a16_internal.h"
 
 namespace w4a16 {
@@ -889,8 +890,10 @@ __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const __grid_constant__
         grid_dependency_wait();
         int c = 0, q = 0;
         int waited = -1;  // the last linear whose wait_for this role has waited for
+        // false once a wait has given up: then the warp computes and stores nothing more,
+        // but walks on to the next barrier of these warps, where they agree to stop
         bool ok = true;
-        while (ok && walk_next(p, lins, kRound ? n_lin : 1, wk, l, t, j0, j1)) {
+        while (walk_next(p, lins, kRound ? n_lin : 1, wk, l, t, j0, j1)) {
             const TcLinDesc &L = kRound ? p.lins[l] : p.single;
             const int dset = q % C::kDSets, duse = q / C::kDSets;
             const int n = tile_row(L, t, r);
@@ -913,22 +916,18 @@ __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const __grid_constant__
                 // and x, which the exact path reads) may belong to an earlier
                 // linear: wait until it has finished
                 waited = l;
-                bool fine = true;
-                if (threadIdx.x == 0) fine = wait_linear(p, lins, L.wait_for, abort);
-                if (!fine) fail(abort, p.status, kErrWaitLinear);
-                asm volatile("bar.sync 1, %0;" ::"r"(kEpiWarps * 32) : "memory");
-                if (*abort) {
+                if (ok && threadIdx.x == 0 && !wait_linear(p, lins, L.wait_for, abort)) {
+                    fail(abort, p.status, kErrWaitLinear);
                     ok = false;
-                    break;
                 }
+                ok = dev::barrier_all(1, kEpiWarps * 32, ok && !*abort);
+                if (!ok) break;  // all of them
             }
-            if (!__all_sync(0xffffffffu,
-                            mbar_wait(smem_u32(d_full + dset), duse & 1, abort))) {
+            if (ok && !__all_sync(0xffffffffu,
+                                  mbar_wait(smem_u32(d_full + dset), duse & 1, abort))) {
                 fail(abort, p.status, kErrWaitDFull);
                 ok = false;
-                break;
             }
-            tc_fence_after();
             const bool whole = j0 == 0 && j1 == L.spt;
             // y straight from the sums: a whole tile without SiLU-and-mul.  Else
             // the sums go to this CTA's partial-sum slot: part of a tile (the
@@ -937,6 +936,12 @@ __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const __grid_constant__
             // meet there (slot 2b + 1 for it: this CTA's last partial segment,
             // which also uses it, comes after every whole one)
             const bool direct = whole && !L.silu;
+            if (!ok) {
+                if (direct && !(kRound && p.done)) continue;  // no barrier in this segment
+                dev::barrier_all(1, kEpiWarps * 32, false);
+                break;
+            }
+            tc_fence_after();
             const long long tile0 = L.start + (long long)t * L.spt;  // its first stage
             const int slot =
                 2 * (int)blockIdx.x +
@@ -988,12 +993,14 @@ __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const __grid_constant__
             if (kRound && direct && p.done) {
                 // a round with waits: this tile's outputs are all written
                 __threadfence();
-                asm volatile("bar.sync 1, %0;" ::"r"(kEpiWarps * 32) : "memory");
+                ok = dev::barrier_all(1, kEpiWarps * 32, true);
+                if (!ok) break;
                 if (threadIdx.x == 0) atomicAdd(p.done + l, 1u);
             }
             if (!direct) {
                 __threadfence();
-                asm volatile("bar.sync 1, %0;" ::"r"(kEpiWarps * 32) : "memory");
+                ok = dev::barrier_all(1, kEpiWarps * 32, true);
+                if (!ok) break;
                 // the CTAs whose slots hold the tile's sums: this one (a whole
                 // tile), or every CTA whose range meets the tile
                 const int b0 = whole ? (int)blockIdx.x : cta_of(p, tile0);

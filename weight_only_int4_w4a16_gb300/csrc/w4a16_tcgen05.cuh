@@ -295,22 +295,6 @@ __device__ __forceinline__ void mma_commit_pair(uint32_t bar, uint16_t mask) {
         : "memory");
 }
 
-// Named barrier `id` of `threads` threads that also tells whether `ok` holds in all of
-// them.  Warps whose waits may give up one by one agree here on whether to go on: all of
-// them have to come, so one that has given up comes too.
-__device__ __forceinline__ bool barrier_all(int id, int threads, bool ok) {
-    uint32_t all;
-    asm volatile(
-        "{\n\t.reg .pred p, q;\n\t"
-        "setp.ne.u32 p, %1, 0;\n\t"
-        "barrier.cta.red.and.pred q, %2, %3, p;\n\t"
-        "selp.u32 %0, 1, 0, q;\n\t}"
-        : "=r"(all)
-        : "r"((uint32_t)ok), "r"(id), "r"(threads)
-        : "memory");
-    return all != 0;
-}
-
 // registers of the calling warpgroup (all of its warps), out of those that the
 // block was launched with
 template <int N>
