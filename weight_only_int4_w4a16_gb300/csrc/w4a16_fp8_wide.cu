@@ -65,9 +65,9 @@ constexpr int kTmaWarp = 16, kMmaWarp = 17;     // 18 and 19 load scales
 constexpr int kScaleSlots = 3;                 // batches of four blocks' scales
 constexpr int kScaleSlot = kHalf * 16 + 32;    // the tokens' four each, then the two weight blocks'
 constexpr int kThreads = 640;                  // five warpgroups
-// registers per thread: the launch's 96 x 640 split between the warpgroups
-constexpr int kSumRegs = 104, kOtherRegs = 64;
-static_assert(4 * kSumRegs + kOtherRegs <= 5 * 96, "the launch's registers");
+// registers per thread: the launch's, split between the warpgroups
+constexpr int kLaunchRegs = 96, kSumRegs = 104, kOtherRegs = 64;
+static_assert(4 * kSumRegs + kOtherRegs <= 5 * kLaunchRegs, "the launch's registers");
 constexpr int kDBufs = 2;                      // block sums in tensor memory
 constexpr int kTmemCols = 512;
 constexpr int kMaxSplit = 4;                   // pairs of a cluster
@@ -853,9 +853,15 @@ cudaError_t fp8_wide_init(const DeviceInfo &) {
         (const void *)fp8_wide_kernel<false, false>, (const void *)fp8_wide_kernel<false, true>,
         (const void *)fp8_wide_kernel<true, false>, (const void *)fp8_wide_kernel<true, true>};
     cudaError_t e = cudaSuccess;
-    for (const void *k : kernels)
+    for (const void *k : kernels) {
+        // the sum warps wait for registers that the launch has to have: a build that gives
+        // the kernel fewer than the split counts on would never get past that
+        cudaFuncAttributes attr;
+        if (e == cudaSuccess) e = cudaFuncGetAttributes(&attr, k);
+        if (e == cudaSuccess && attr.numRegs < kLaunchRegs) e = cudaErrorLaunchOutOfResources;
         if (e == cudaSuccess)
             e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+    }
     for (int k = 2; k <= kMaxSplit && e == cudaSuccess; ++k) {
         cudaLaunchConfig_t cfg;
         cudaLaunchAttribute attr[2];
