@@ -334,7 +334,7 @@ int w4a16_dense_linear(const uint16_t *x, const uint16_t *w, int M, int N, int K
  *               sum_{k in block b} x[m, k] * w[n, k]   (+ residual[m, n])
  * y and residual have the 16-bit type `dtype` (w4a16_dtype).  Sums are fp32, y is
  * rounded once (nearest even); the two scales are multiplied first, so their
- * product has to be finite in fp32.  One kernel; K may be split between CTAs, whose
+ * product has to be finite in fp32 (and below 2^-126 it keeps fewer bits).  One kernel; K may be split between CTAs, whose
  * partial sums go through the w4a16_init workspace and are added in a fixed
  * order (a workspace too small for that means no split, not an error).  K a
  * multiple of 16 (16..2^22), 1 <= N < 2^31, 0 <= M <= 65535; x and w 16-byte
@@ -347,7 +347,8 @@ int w4a16_fp8_linear(const uint8_t *x, const float *x_scales, const uint8_t *w,
 
 /* The norm before a linear, of rows of H elements in the 16-bit type `dtype`:
  *     h = x (+ residual),   v = h / sqrt(mean(h^2) + eps) * weight
- * computed in fp32 from the unrounded h.  Written where the pointer is not NULL:
+ * computed in fp32 from the unrounded h (a row whose squares add up past fp32's
+ * range counts as infinitely long).  Written where the pointer is not NULL:
  *   sum_out    [M, H] h rounded once (only with a residual; it may be the
  *              residual itself: the stream is updated in place);
  *   y          [M, H] v rounded once (the input of a w4a16_linear);
@@ -367,7 +368,8 @@ int w4a16_rmsnorm(const uint16_t *x, const uint16_t *residual, const uint16_t *w
 /* 16-bit rows x [M, cols] -> 8-bit rows, with w4a16_rmsnorm's rule for scales and
  * elements.  W4A16_EPILOGUE_NONE: of x itself, q [M, cols].
  * W4A16_EPILOGUE_SILU_MUL: of silu(x[:, :cols/2]) * x[:, cols/2:] (fp32, silu(g) =
- * g / (1 + e^-g)), q [M, cols/2]; cols even.  W4A16_EPILOGUE_RESIDUAL:
+ * g / (1 + e^-g); a product past fp32's range is Inf, a gate of -Inf NaN),
+ * q [M, cols/2]; cols even.  W4A16_EPILOGUE_RESIDUAL:
  * W4A16_ERR_UNSUPPORTED.  0 <= M <= 65535, 1 <= cols <= 2^30; x 2-byte aligned,
  * scales 4-byte; q and scales apart from x and from each other.  Needs no
  * w4a16_init. */
@@ -530,6 +532,10 @@ const char *w4a16_status_string(int status);
  * cut short can leave them nonzero: call it with no other call of this library
  * in flight on another stream.  A captured round or an expert MLP keeps
  * counters of its own: after an expired wait destroy it and create it again.
+ * Bits of the code: 1024 an invalid expert id, 4096 and 8192 the probe below,
+ * of the 8-bit linear 1 << 17 a wait for operands, 1 << 18 for a block's sums,
+ * 1 << 19 for a free stage, 1 << 20 for what was in flight at the end; the others
+ * are expired waits of the other kernels.
  * W4A16_ERR_NOT_INITIALIZED when neither w4a16_init nor a
  * w4a16_linear_noalloc call has run. */
 int w4a16_device_status(void *stream, int *code);

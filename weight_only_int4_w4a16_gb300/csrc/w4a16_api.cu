@@ -134,11 +134,12 @@ bool gemv_small(int M, int N, int K) {
 // The 8-bit linear's kernel for M tokens: up to 64 run in one pass over the weights
 // with 128 weight rows as the MMA's M and the tokens as its N, split finely over the
 // SMs (fp8_kernel); more run on pairs of CTAs, 256 tokens by 256 weight rows at a time
-// (fp8_wide_kernel).  At 64 tokens, L2 evicted (one GB300): N 8192, K 5120 19.1
-// against 25.3 us, N 5120, K 17408 29.3 against 35.5, N 34816, K 5120 47.7 against
-// 57.0; with a 128-token tile of the first kernel 128 tokens took 18.6 against 19.0 us
-// on N 8192, K 5120, but 57.2 against 52.2 on N 34816, K 5120, and 192 tokens, in two
-// such passes, 33.2 against 19.2.
+// (fp8_wide_kernel).  At 64 tokens, calls in a row on inputs larger than L2 (one GB300):
+// N 8192, K 5120 12.9 against 17.3 us, N 5120, K 6144 with a residual 11.5 against 15.4,
+// N 34816, K 5120 38.0 against 44.9, N 5120, K 17408 with a residual 23.4 against 29.2.
+// A 128-token tile of the first kernel was tried in an earlier state of both (L2
+// evicted): 128 tokens took 18.6 against 19.0 us on N 8192, K 5120, but 57.2 against 52.2
+// on N 34816, K 5120, and 192 tokens, in two such passes, 33.2 against 19.2.
 bool fp8_takes_wide(int M) { return M > kFp8MaxTokens; }
 
 Decision decide(int M, int N, int K, const DeviceInfo &dev, int forced, int epi = kEpiNone,

@@ -35,9 +35,9 @@
 //   Bound by the weights' bytes and, in short calls, by the start (about 3 us to the
 //   first weights) and the exchange of split tiles (about 2 us); from 32 tokens on the
 //   sum warps' turn per block shows too (64 tokens, multiply-adds switched off: 20.1 us
-//   for 22.3).  N 34816, K 5120 (178 MB) at 8 tokens: 28.3 us, 6.3 TB/s, 93% of the
-//   measured copy rate, at 64 tokens 35.8; N 5120, K 17408 (89 MB) at 64 tokens:
-//   22.6 us, 4.0 TB/s; N 8192, K 5120 (42 MB) at 1 token: 10.2 us, 4.1 TB/s.
+//   for 22.3).  N 34816, K 5120 (178 MB) at 8 tokens: 28.3 to 29.1 us, 6.1 to 6.3 TB/s,
+//   90 to 93% of the measured copy rate, at 64 tokens 38.0; N 5120, K 17408 (89 MB) at
+//   64 tokens: 22.6 us, 4.0 TB/s; N 8192, K 5120 (42 MB) at 1 token: 10.4 us, 4.0 TB/s.
 //
 // Every mbarrier wait is bounded; on expiry the kernel records an error code in
 // the device status word, drains what it has in flight, frees its tensor memory

@@ -339,8 +339,8 @@ __global__ void __launch_bounds__(1024) rmsnorm_kernel(NormArgs a) {
 // computed; a CTA has 16 consecutive groups of a row.  Bound by memory: silu-and-mul
 // of 4096 x 17408 takes 57.6 us (6.23 TB/s, 92% of the measured copy rate; with scalar
 // arithmetic 60.3, then 67.1 with 256 threads and one group each, 63.9 with 256 and
-// two); of 4096 x 17405, in 2-byte accesses, 90 us (104
-// with a lane's own elements in turn).
+// two); of 4096 x 17405, in 2-byte accesses, 90 us (104 with a lane's own elements in
+// turn).
 // ---------------------------------------------------------------------------
 constexpr int kQuantThreads = 128;
 constexpr int kQuantU = 2;

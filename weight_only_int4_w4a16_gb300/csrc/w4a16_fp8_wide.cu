@@ -30,19 +30,22 @@
 //   pieces, and the pair that comes last adds the other's: the order of two terms
 //   does not change their sum.
 //
-//   Bound by the turn of the two block sums: a block takes about 1000 cycles where its
+//   Bound by the turn of the two block sums: a block takes about 900 cycles where its
 //   products alone would take 512 (4.80 PFLOP/s over the GPU).  From a block's commit
 //   through the tensor-memory loads and multiply-adds of its 256 columns to the next
 //   product into the same columns is a chain of about 1500 cycles, and two buffers are
 //   all that the tensor memory holds; the operands' and the loads' shared-memory
-//   traffic takes the rest.  M 4096, N 34816, K 5120: 580 to 588 us, 2.5 PFLOP/s, 133% of
-//   the measured bf16 rate (the same with eight sum warps of 128 columns each).  Not
-//   kept: four buffers of 128 columns (650 us), packed multiply-adds (730), three
-//   stages (630), five (no change).
+//   traffic takes the rest.  M 4096, N 34816, K 5120: 563 to 574 us, 2.5 to 2.6 PFLOP/s,
+//   136 to 138% of the measured bf16 rate.  From an earlier state that took 580 to 590 us:
+//   the same with eight sum warps of 128 columns each; not kept were four buffers of 128
+//   columns (650 us), packed multiply-adds (730), three stages (630), five (no change).
+//   65 to 256 tokens take a whole tile's time (N 34816, K 5120: 45 to 46 us at 72 to 256
+//   tokens, where the weights' bytes would take 27 to 29): two rounds of 40 blocks.
 //
-// Every mbarrier wait is bounded, as in w4a16_fp8.cu.  The cluster barriers
+// Every mbarrier wait is bounded, as in w4a16_fp8.cu, and the sum warps come to the
+// barriers of split tiles whether or not their waits were met.  The cluster barriers
 // (after the setup, before the exchange, before the exit) are reached by every
-// thread: all that comes before them is bounded.
+// thread: all that comes before them ends.
 #include <cstring>
 
 #include "w4a16_fp8_common.cuh"
@@ -556,7 +559,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (ok && whole && staged_res) ask_residual(nc, mw);
             if constexpr (!kTma) {
                 // the residual's rows on their way to L2 meanwhile (a row's 128 bytes
-                // are in at most two lines): 1240 tokens, N 33532, K 1440 156 us for 177
+                // are in at most two lines): 1240 tokens, N 33532, K 1440 156 us for 177 (132
+                // in the present state of the kernel)
                 if (whole && p.residual && mw + lane < p.M && nc < p.N) {
                     const uint16_t *row = p.residual + (size_t)(mw + lane) * p.N;
                     prefetch_l2(row + nc);
