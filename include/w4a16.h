@@ -180,7 +180,8 @@ typedef enum {
  * zeros are 4-bit either way; accumulation is fp32 either way. */
 typedef enum {
     W4A16_DTYPE_F16 = 0,  /* IEEE binary16 */
-    W4A16_DTYPE_BF16 = 1  /* bfloat16 (the top half of an IEEE binary32) */
+    W4A16_DTYPE_BF16 = 1, /* bfloat16 (the top half of an IEEE binary32) */
+    W4A16_DTYPE_F32 = 2   /* IEEE binary32: a router's logits only (w4a16_moe_route) */
 } w4a16_dtype;
 
 /* One linear of a decode round.  x is [M, K] and y [M, N] ([M, N/2] with
@@ -380,7 +381,8 @@ int w4a16_fp8_quant(const uint16_t *x, int M, int cols, int epilogue, int dtype,
  * experts per token; the tokens are regrouped by expert; a W4A16 small-M GEMV
  * runs over the packed INT4 experts; each token's expert outputs are summed
  * with the router's weights).  Token t's j-th choice is slot s = t*k + j.
- * The router itself (its linear, softmax and top-k) is the caller's.
+ * The router's linear is one of the calls above (w4a16_dense_linear), its choice
+ * w4a16_moe_route.
  *
  * w4a16_moe_align: topk_ids [n_slots] int32 (device) -> the slots grouped by
  * expert, stable in slot order: offsets [E+1] (first sorted position of each
@@ -467,6 +469,55 @@ int w4a16_moe_mlp_buffers(void *mlp, uint16_t **h, uint16_t **o);
  * out of type dtype. */
 int w4a16_moe_sum(const uint16_t *y_sorted, const int32_t *pos, const float *weights, int T,
                   int k, int N, int dtype, uint16_t *out, void *stream);
+
+/* How a router's logits become weights (w4a16_moe_route). */
+typedef enum {
+    W4A16_ROUTE_SOFTMAX = 0, /* p = e^l / the row's sum of e^l */
+    W4A16_ROUTE_SIGMOID = 1  /* p = 1 / (1 + e^-l) */
+} w4a16_route_scoring;
+
+/* The experts of each token from a router's logits [T, E] (`dtype`: any w4a16_dtype,
+ * W4A16_DTYPE_F32 too): topk_ids [T, k] the k largest of a row in falling order, equal
+ * ones by index, and weights [T, k] fp32 = scale * p of the chosen, p as `scoring` names
+ * it, divided first by the sum of the chosen p where `renormalize` is not 0.  NaN counts
+ * as -Inf, whose p is 0 (a switched-off expert: it is chosen only where fewer than k
+ * others are left, and weighs 0, as does a whole row of them); equal +Inf share.
+ * 1 <= k <= E, 0 <= T <= 65535 (0: nothing is read or launched, and pointers may be
+ * NULL); E <= 1024 and k <= 32 (W4A16_ERR_UNSUPPORTED above).  logits aligned to its
+ * type, outputs 4-byte and apart from it and each other.  Needs no w4a16_init. */
+int w4a16_moe_route(const void *logits, int T, int E, int k, int dtype, int scoring,
+                    int renormalize, float scale, int32_t *topk_ids, float *weights,
+                    void *stream);
+
+/* A whole layer of experts whose weights come in 8 bits, for the few tokens of a decode
+ * step:
+ *     out[t] = sum_j weights[t, j] * down_e(silu(gate_e(x[t])) * up_e(x[t])),
+ *     e = topk_ids[t, j],  silu(g) = g / (1 + e^-g)
+ *   x              [T, K] in the 16-bit type `dtype`, out [T, N] likewise
+ *   topk_ids       [T, k] int32, weights [T, k] fp32 (w4a16_moe_route's); an id outside
+ *                  [0, E) leaves its choice out: -1 silently (padding), any other sets the
+ *                  bit of w4a16_moe_align that w4a16_device_status reports.  A row
+ *                  without choices is 0; an expert may occur twice in a row
+ *   w_gate_up      [E, 2I, K] e4m3, the gate's rows first, and gate_up_scales
+ *                  [E, ceil(2I/128), ceil(K/128)] fp32: a scale per block of 128 x 128
+ *   w_down         [E, N, I] e4m3, down_scales [E, ceil(N/128), ceil(I/128)]
+ *   scratch        w4a16_fp8_moe_scratch_bytes(T, k, I, N) bytes, 16-byte aligned, the
+ *                  call's own until its work is done (W4A16_ERR_WORKSPACE if fewer);
+ *                  calls that share none may overlap
+ * Weights and activations enter the products exactly; sums are fp32 (a block's first, then
+ * times its scale); silu(gate) * up is rounded once to `dtype` (fp16: beyond 65504 to Inf),
+ * out once.  The bits of a row do not depend on the other rows' order in a tile, but the
+ * order of the sums over K goes by the number of tokens and experts in use.
+ * T * k <= 1024 and E <= 1024 (W4A16_ERR_UNSUPPORTED above); T = 0 is an empty batch, as
+ * in the calls above; K and I multiples of 16, 1 <= N, all at most 2^22.  x and weights
+ * 16-byte aligned, out 2-byte, the others 4-byte; out and scratch overlap nothing.  Needs
+ * w4a16_init; allocates nothing and may be captured. */
+size_t w4a16_fp8_moe_scratch_bytes(int T, int k, int I, int N);
+int w4a16_fp8_moe_mlp(const uint16_t *x, const int32_t *topk_ids, const float *weights, int T,
+                      int k, int E, int K, int I, int N, int dtype, const uint8_t *w_gate_up,
+                      const float *gate_up_scales, const uint8_t *w_down,
+                      const float *down_scales, uint16_t *out, void *scratch,
+                      size_t scratch_bytes, void *stream);
 
 /* The rung the dispatch table picks for a shape (honouring a forced rung), or
  * -1 for an invalid shape.  Pure host query.  Unforced: M <= 8 takes the warp

@@ -49,6 +49,10 @@ EPILOGUE_SILU_MUL = 2
 
 DTYPE_F16 = 0
 DTYPE_BF16 = 1
+DTYPE_F32 = 2  # a router's logits only
+
+ROUTE_SOFTMAX = 0
+ROUTE_SIGMOID = 1
 
 MOE_PATH_AUTO = 0
 MOE_PATH_CHAIN = 1
@@ -101,6 +105,9 @@ _sig("w4a16_moe_mlp_buffers", [_P, ctypes.POINTER(_P), ctypes.POINTER(_P)])
 _sig("w4a16_wait_probe", [_P])
 _sig("w4a16_moe_mlp_create", [_P, _P, _I, _I, ctypes.POINTER(_P)])
 _sig("w4a16_moe_mlp_destroy", [_P])
+_sig("w4a16_moe_route", [_P, _I, _I, _I, _I, _I, _I, ctypes.c_float, _P, _P, _P])
+_sig("w4a16_fp8_moe_scratch_bytes", [_I, _I, _I, _I], _SZ)
+_sig("w4a16_fp8_moe_mlp", [_P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _P, _P, _P, _P, _P, _P, _SZ, _P])
 _sig("w4a16_moe_mlp", [_P, _P, _P, _P, _I, _P, _P])
 _sig("w4a16_decode_round", [ctypes.POINTER(LinearDesc), _I, _I, _P])
 _sig("w4a16_round_graph_create", [ctypes.POINTER(LinearDesc), _I, _I, ctypes.POINTER(_P)])
@@ -127,6 +134,7 @@ EXPORTED = ["w4a16_init", "w4a16_shutdown", "w4a16_workspace_bytes", "w4a16_pack
             "w4a16_moe_align", "w4a16_moe_create", "w4a16_moe_destroy", "w4a16_moe_linear",
             "w4a16_moe_sum", "w4a16_moe_mlp_create", "w4a16_moe_mlp_destroy", "w4a16_moe_mlp",
             "w4a16_moe_mlp_set_path", "w4a16_moe_mlp_path", "w4a16_moe_mlp_buffers",
+            "w4a16_moe_route", "w4a16_fp8_moe_scratch_bytes", "w4a16_fp8_moe_mlp",
             "w4a16_decode_round",
             "w4a16_round_graph_create", "w4a16_round_graph_launch", "w4a16_round_graph_destroy",
             "w4a16_select_rung", "w4a16_plan_info", "w4a16_fp8_plan_info",
@@ -371,18 +379,18 @@ def _shaped(t: torch.Tensor, dtype, shape, name: str, device: int) -> int:
     return t.data_ptr()
 
 
-def _home(x: torch.Tensor, dtype, shape) -> tuple[int, int]:
+def _home(x: torch.Tensor, dtype, shape, name: str = "x") -> tuple[int, int]:
     """(x's device, its address).  Kernels run on the current device, so x has to live there,
     and everything else with it."""
     if not (isinstance(x, torch.Tensor) and x.is_cuda):
-        _dev(x, dtype, "x")
+        _dev(x, dtype, name)
     device = x.get_device()
     if device != _current_device():
-        raise ValueError(f"x lives on cuda:{device}, but the current device is "
+        raise ValueError(f"{name} lives on cuda:{device}, but the current device is "
                          f"cuda:{_current_device()}")
     if x.dtype is dtype and x.shape == shape and x.is_contiguous():
         return device, x.data_ptr()
-    return device, _shaped(x, dtype, shape, "x", device)
+    return device, _shaped(x, dtype, shape, name, device)
 
 
 # Functions of torch's that are not part of its interface, for the time that they save (a
@@ -655,6 +663,65 @@ def w4a16_moe_sum(y_sorted: torch.Tensor, pos: torch.Tensor, weights: torch.Tens
                              _dev(weights, torch.float32, "weights"), T, k, N, _DTYPE_OF[dt],
                              _dev(out, dt, "out"), _stream_ptr(stream)),
            "w4a16_moe_sum")
+    return out
+
+
+def w4a16_moe_route(logits: torch.Tensor, k: int, scoring: int = ROUTE_SOFTMAX,
+                    renormalize: bool = True, scale: float = 1.0, topk_ids=None, weights=None,
+                    stream=None):
+    """(topk_ids [T, k] int32, weights [T, k] fp32) of a router's logits [T, E] (float32,
+    float16 or bfloat16): the k largest of each row in falling order, equal ones by index;
+    scale * softmax or sigmoid (ROUTE_*) of the chosen, divided by their sum first with
+    renormalize."""
+    T, E = _rows2d(logits, "logits")
+    dt = logits.dtype
+    code = DTYPE_F32 if dt is torch.float32 else _dtype16(dt)
+    dev, lp = _home(logits, dt, (T, E), "logits")
+    raw, side = _stream_for(dev, stream)
+    topk_ids, ip = _output(topk_ids, (T, k), torch.int32, dev, side, "topk_ids")
+    weights, wp = _output(weights, (T, k), torch.float32, dev, side, "weights")
+    _used_on(side, logits, topk_ids, weights)
+    _check(lib.w4a16_moe_route(lp, T, E, k, code, scoring, bool(renormalize), scale, ip, wp, raw),
+           "w4a16_moe_route")
+    return topk_ids, weights
+
+
+def _blocks(n: int) -> int:
+    return (n + GROUP - 1) // GROUP
+
+
+def w4a16_fp8_moe_mlp(x: torch.Tensor, topk_ids: torch.Tensor, weights: torch.Tensor,
+                      w_gate_up: torch.Tensor, gate_up_scales: torch.Tensor,
+                      w_down: torch.Tensor, down_scales: torch.Tensor, out=None,
+                      stream=None) -> torch.Tensor:
+    """out [T, N] = sum_j weights[t, j] * down_e(silu(gate_e(x[t])) * up_e(x[t])), e =
+    topk_ids[t, j] (outside [0, E): no expert), for few tokens (T * k <= 1024): 8-bit experts
+    w_gate_up [E, 2I, K] and w_down [E, N, I] with a scale per 128 x 128 block; x and out
+    16 bits."""
+    T, K = _rows2d(x, "x")
+    k = _rows2d(topk_ids, "topk_ids")[1]
+    for name, w in (("w_gate_up", w_gate_up), ("w_down", w_down)):
+        if not isinstance(w, torch.Tensor) or w.dim() != 3:
+            raise ValueError(f"{name} must be a 3-D torch tensor")
+    (E, I2, _), N = w_gate_up.shape, w_down.shape[1]
+    I = I2 // 2
+    dt = x.dtype
+    code = _dtype16(dt)
+    dev, xp = _home(x, dt, (T, K))
+    ip = _shaped(topk_ids, torch.int32, (T, k), "topk_ids", dev)
+    wp = _shaped(weights, torch.float32, (T, k), "weights", dev)
+    w1 = _shaped(w_gate_up, FP8, (E, 2 * I, K), "w_gate_up", dev)
+    s1 = _shaped(gate_up_scales, torch.float32, (E, _blocks(I2), _blocks(K)), "gate_up_scales",
+                 dev)
+    w2 = _shaped(w_down, FP8, (E, N, I), "w_down", dev)
+    s2 = _shaped(down_scales, torch.float32, (E, _blocks(N), _blocks(I)), "down_scales", dev)
+    raw, side = _stream_for(dev, stream)
+    out, op = _output(out, (T, N), dt, dev, side, "out")
+    need = lib.w4a16_fp8_moe_scratch_bytes(T, k, I, N)
+    scratch, sp = _output(None, (1, need), torch.uint8, dev, side, "scratch")
+    _used_on(side, x, topk_ids, weights, w_gate_up, gate_up_scales, w_down, down_scales, out)
+    _check(lib.w4a16_fp8_moe_mlp(xp, ip, wp, T, k, E, K, I, N, code, w1, s1, w2, s2, op, sp, need,
+                                 raw), "w4a16_fp8_moe_mlp")
     return out
 
 

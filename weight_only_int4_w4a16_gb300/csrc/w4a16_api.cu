@@ -630,6 +630,7 @@ int w4a16_init(int device, size_t workspace_bytes) {
     if (e == cudaSuccess) e = moe_decode_init(dev);
     if (e == cudaSuccess) e = fp8_init(dev);
     if (e == cudaSuccess) e = fp8_wide_init(dev);
+    if (e == cudaSuccess) e = fp8_moe_init();
     if (e == cudaSuccess) e = cudaDeviceSynchronize();
     if (e != cudaSuccess) {
         cudaFree(base);
@@ -1217,6 +1218,83 @@ int w4a16_moe_sum(const uint16_t *y_sorted, const int32_t *pos, const float *wei
                                    (cudaStream_t)stream);
     g_launches.fetch_add(1, std::memory_order_relaxed);
     return e == cudaSuccess ? W4A16_OK : cuda_fail(e);
+}
+
+int w4a16_moe_route(const void *logits, int T, int E, int k, int dtype, int scoring,
+                    int renormalize, float scale, int32_t *topk_ids, float *weights,
+                    void *stream) {
+    if (T < 0 || T > kMaxM || E < 1 || k < 1 || k > E) return W4A16_ERR_INVALID_ARG;
+    if (E > kMaxMoeExperts || k > kMaxRouteChoices) return W4A16_ERR_UNSUPPORTED;
+    if (dtype != W4A16_DTYPE_F16 && dtype != W4A16_DTYPE_BF16 && dtype != W4A16_DTYPE_F32)
+        return W4A16_ERR_INVALID_ARG;
+    if (scoring != W4A16_ROUTE_SOFTMAX && scoring != W4A16_ROUTE_SIGMOID)
+        return W4A16_ERR_INVALID_ARG;
+    if (T == 0) return W4A16_OK;
+    if (!logits || !topk_ids || !weights) return W4A16_ERR_INVALID_ARG;
+    const int size = dtype == W4A16_DTYPE_F32 ? 4 : 2;
+    if (!aligned(logits, size) || !aligned(topk_ids, 4) || !aligned(weights, 4))
+        return W4A16_ERR_MISALIGNED;
+    const size_t in = (size_t)T * E * size, out = (size_t)T * k * 4;
+    if (overlaps(logits, in, topk_ids, out) || overlaps(logits, in, weights, out) ||
+        overlaps(topk_ids, out, weights, out))
+        return W4A16_ERR_INVALID_ARG;
+    const RouteArgs a{logits, topk_ids, weights, T, E, k, scoring == W4A16_ROUTE_SIGMOID,
+                      renormalize != 0, scale};
+    const cudaError_t e = launch_route(a, dtype, (cudaStream_t)stream);
+    if (e != cudaSuccess) return cuda_fail(e);
+    g_launches.fetch_add(1, std::memory_order_relaxed);
+    return W4A16_OK;
+}
+
+size_t w4a16_fp8_moe_scratch_bytes(int T, int k, int I, int N) {
+    if (T < 1 || k < 1 || I < 1 || N < 1 || (long long)T * k > kFp8MoeMaxSlots) return 0;
+    return fp8_moe_scratch_bytes(T, k, I, N);
+}
+
+int w4a16_fp8_moe_mlp(const uint16_t *x, const int32_t *topk_ids, const float *weights, int T,
+                      int k, int E, int K, int I, int N, int dtype, const uint8_t *w_gate_up,
+                      const float *gate_up_scales, const uint8_t *w_down,
+                      const float *down_scales, uint16_t *out, void *scratch,
+                      size_t scratch_bytes, void *stream) {
+    if (T < 0 || k < 1 || E < 1 || K < 1 || I < 1 || N < 1) return W4A16_ERR_INVALID_ARG;
+    if (K > kMaxK || I > kMaxK || N > kMaxK || K % 16 != 0 || I % 16 != 0)
+        return W4A16_ERR_INVALID_ARG;
+    if (dtype != W4A16_DTYPE_F16 && dtype != W4A16_DTYPE_BF16) return W4A16_ERR_INVALID_ARG;
+    if (E > kMaxMoeExperts || (long long)T * k > kFp8MoeMaxSlots) return W4A16_ERR_UNSUPPORTED;
+    if (T == 0) return W4A16_OK;
+    if (!x || !topk_ids || !weights || !w_gate_up || !gate_up_scales || !w_down ||
+        !down_scales || !out || !scratch)
+        return W4A16_ERR_INVALID_ARG;
+    if (!aligned(x, 16) || !aligned(topk_ids, 4) || !aligned(weights, 4) ||
+        !aligned(w_gate_up, 16) || !aligned(gate_up_scales, 4) || !aligned(w_down, 16) ||
+        !aligned(down_scales, 4) || !aligned(out, 2) || !aligned(scratch, 16))
+        return W4A16_ERR_MISALIGNED;
+    const size_t need = fp8_moe_scratch_bytes(T, k, I, N);
+    if (scratch_bytes < need) return W4A16_ERR_WORKSPACE;
+    const auto blocks = [](size_t n) { return (n + kGroup - 1) / kGroup; };
+    const struct { const void *p; size_t bytes; } in[] = {
+        {x, (size_t)T * K * 2},
+        {topk_ids, (size_t)T * k * 4},
+        {weights, (size_t)T * k * 4},
+        {w_gate_up, (size_t)E * 2 * I * K},
+        {gate_up_scales, E * blocks(2 * (size_t)I) * blocks(K) * 4},
+        {w_down, (size_t)E * N * I},
+        {down_scales, E * blocks(N) * blocks(I) * 4}};
+    const size_t out_bytes = (size_t)T * N * 2;
+    for (const auto &i : in)
+        if (overlaps(i.p, i.bytes, out, out_bytes) || overlaps(i.p, i.bytes, scratch, need))
+            return W4A16_ERR_INVALID_ARG;
+    if (overlaps(out, out_bytes, scratch, need)) return W4A16_ERR_INVALID_ARG;
+    const State &st = g_state;
+    if (!st.initialized) return W4A16_ERR_NOT_INITIALIZED;
+    const Fp8MoeArgs a{x,      topk_ids, weights, w_gate_up, gate_up_scales, w_down, down_scales,
+                       out,    scratch,  T,       k,         E,              K,      I,
+                       N};
+    const cudaError_t e = launch_fp8_moe(a, dtype == W4A16_DTYPE_BF16, st.dev, st.ws.status,
+                                         (cudaStream_t)stream);
+    if (e != cudaSuccess) return cuda_fail(e);
+    g_launches.fetch_add(3, std::memory_order_relaxed);
+    return W4A16_OK;
 }
 
 int w4a16_linear(const uint16_t *x, const uint32_t *qweight, const uint16_t *scales,

@@ -1,0 +1,467 @@
+// A layer of experts whose weights come in 8 bits, for the few tokens of a decode step:
+//
+//   h[s] = silu(gate_e x[t]) * up_e x[t],   out[t] = sum_j weights[t, j] * down_e h[s]
+//
+// with slot s = t k + j the token's j-th choice and e = ids[t, j].  (forum.sourcefind.cn
+// thread "vLLM on Hygon Z100", section 七: tokens regrouped by expert, an expert small-M
+// product, the weighted sum; section 六: FP8 checkpoints.)  Weights are e4m3 with a scale
+// per block of 128 x 128, activations 16 bits.
+//
+// Three kernels: gate and up with silu-and-mul, down, the weighted sum.  Both products are
+// one kernel, experts_kernel.  A tile is up to 8 NT slots of one expert; a unit is a tile
+// and 16 * 8 / KS rows of the expert's weights, whose K a CTA walks in stages of KS blocks
+// of 128: a warp has 16 rows (for gate and up: 8 gate rows and their 8 up rows, so that a
+// lane holds a gate sum and its up sum) and one of the stage's KS blocks, and the KS warps
+// of the same rows add their sums at the unit's end.  So every stage brings 16 KB of
+// weights in runs of 128 KS bytes of a row, and a unit is small (KS 8) where there are few
+// tiles.  The weights are the warp MMA's M, the tokens its N: a decode step's experts see
+// one to a few tokens each, and the bytes of the weights bound the layer, not the products
+// (8 tokens need 1/16 of what the warp MMA can do while the weights arrive).
+//
+// e4m3 codes become the 16-bit type exactly (through fp16, which holds all of them); the
+// products of a block are summed in fp32, scaled once and added in fp32.  h is rounded to
+// the 16-bit type, the tensor cores' operand for down; down's sums stay fp32 up to the one
+// rounding of out.
+//
+// Every CTA groups the slots itself (a stable counting sort in shared memory), which
+// costs it no launch and no pass through memory.
+#include "w4a16_fp8_common.cuh"
+
+namespace w4a16 {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kWarps = kThreads / 32;
+constexpr int kStages = 4;
+constexpr int kStageWeights = 16 << 10;  // bytes
+constexpr int kRingBytes = 100 << 10;    // so that two CTAs share an SM
+
+__device__ __forceinline__ uint32_t smem_of(const void *p) {
+    return (uint32_t)__cvta_generic_to_shared(p);
+}
+// 16 bytes to shared memory, or zeros
+__device__ __forceinline__ void copy16(uint32_t dst, const void *src, bool valid) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
+                 "r"(valid ? 16 : 0)
+                 : "memory");
+}
+__device__ __forceinline__ void copy4(uint32_t dst, const void *src) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void commit_copies() {
+    asm volatile("cp.async.commit_group;" ::: "memory");
+}
+template <int N>
+__device__ __forceinline__ void wait_copies() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ uint4 lds128(uint32_t p) {
+    uint4 v;
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "r"(p));
+    return v;
+}
+// two e4m3 codes -> two 16-bit values, exact
+template <bool kBf16>
+__device__ __forceinline__ uint32_t widen(uint16_t codes) {
+    uint32_t d;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(d) : "h"(codes));
+    if constexpr (kBf16) {
+        const __half2 h = *reinterpret_cast<const __half2 *>(&d);
+        const __nv_bfloat162 b = __floats2bfloat162_rn(__low2float(h), __high2float(h));
+        d = *reinterpret_cast<const uint32_t *>(&b);
+    }
+    return d;
+}
+template <bool kBf16>
+__device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                    uint32_t a3, uint32_t b0, uint32_t b1) {
+    if constexpr (kBf16)
+        asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+            "{%8,%9}, {%0,%1,%2,%3};"
+            : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+            : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+    else
+        asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+            "{%8,%9}, {%0,%1,%2,%3};"
+            : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+            : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+struct Tables {
+    uint16_t slot[kFp8MoeMaxSlots];         // slots by expert, in order
+    uint16_t tile_expert[kFp8MoeMaxSlots];  // a tile: slots tile_first .. + tile_count
+    uint16_t tile_first[kFp8MoeMaxSlots];
+    uint8_t tile_count[kFp8MoeMaxSlots];
+    int warp_sums[kWarps];
+    int n_tiles;
+};
+// in the ring before its first stage is filled
+struct SortSpace {
+    uint8_t rank[kFp8MoeMaxSlots];            // among the equal ids of the slot's 32
+    uint16_t before[kMaxMoeExperts];          // slots of lower experts
+    uint16_t count[kFp8MoeMaxSlots / 32 * kMaxMoeExperts];  // [32 slots][expert]
+};
+static_assert(sizeof(SortSpace) <= kRingBytes, "the sort fits the ring");
+
+// The slots by expert (stable), in tiles of up to cap slots.  An id outside [0, E) leaves
+// its slot out; one other than -1 is reported.
+__device__ void group_slots(Tables &tb, SortSpace &sp, const int32_t *ids, int S, int E, int cap,
+                            int *status) {
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int chunks = (S + 31) / 32;
+    for (int i = tid; i < chunks * E; i += kThreads) sp.count[i] = 0;
+    __syncthreads();
+    for (int c = warp; c < chunks; c += kWarps) {
+        const int s = c * 32 + lane;
+        const int e = s < S ? ids[s] : -1;
+        const bool valid = (unsigned)e < (unsigned)E;
+        const unsigned same = __match_any_sync(0xffffffffu, valid ? e : -1);
+        const int rank = __popc(same & ((1u << lane) - 1));
+        sp.rank[s] = (uint8_t)rank;
+        if (valid && rank == 0) sp.count[c * E + e] = (uint16_t)__popc(same);
+        if (!valid && e != -1 && status && blockIdx.x == 0) atomicOr(status, kErrMoeIds);
+    }
+    __syncthreads();
+    // experts 4 tid .. 4 tid + 3: their chunks' counts become what lies before each chunk,
+    // and the slots and tiles of lower experts come from a scan over the threads
+    static_assert(kMaxMoeExperts <= 4 * kThreads, "four experts per thread");
+    int n[4], own = 0;  // slots, tiles << 16
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int e = 4 * tid + i;
+        n[i] = 0;
+        if (e < E)
+            for (int c = 0; c < chunks; ++c) {
+                const int v = sp.count[c * E + e];
+                sp.count[c * E + e] = (uint16_t)n[i];
+                n[i] += v;
+            }
+        own += n[i] + ((n[i] + cap - 1) / cap << 16);
+    }
+    int incl = own;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += v;
+    }
+    if (lane == 31) tb.warp_sums[warp] = incl;
+    __syncthreads();
+    int at = incl - own;
+    for (int w = 0; w < warp; ++w) at += tb.warp_sums[w];
+    if (tid == kThreads - 1) tb.n_tiles = (at + own) >> 16;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int e = 4 * tid + i, first = at & 0xffff;
+        if (e < E) sp.before[e] = (uint16_t)first;
+        for (int p = 0, tile = at >> 16; p < n[i]; p += cap, ++tile) {
+            tb.tile_expert[tile] = (uint16_t)e;
+            tb.tile_first[tile] = (uint16_t)(first + p);
+            tb.tile_count[tile] = (uint8_t)min(cap, n[i] - p);
+        }
+        at += n[i] + ((n[i] + cap - 1) / cap << 16);
+    }
+    __syncthreads();
+    for (int s = tid; s < S; s += kThreads) {
+        const int e = ids[s];
+        if ((unsigned)e < (unsigned)E)
+            tb.slot[sp.before[e] + sp.count[s / 32 * E + e] + sp.rank[s]] = (uint16_t)s;
+    }
+    __syncthreads();
+}
+
+// kSilu: gate and up, x by token, h by slot; else down, h by slot, o (fp32) by slot
+template <bool kBf16, int NT, bool kSilu>
+__global__ void __launch_bounds__(kThreads, 2) experts_kernel(Fp8ExpertsArgs a) {
+    extern __shared__ __align__(128) uint8_t ring[];
+    __shared__ Tables tb;
+    __shared__ float red[kWarps * 32 * NT * 4];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int g = lane >> 2, c = lane & 3;
+    const int S = a.T * a.k, cap = a.cap;
+
+    if constexpr (kSilu) {
+        asm volatile("griddepcontrol.wait;" ::: "memory");
+        asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    } else {
+        asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    }
+    group_slots(tb, *reinterpret_cast<SortSpace *>(ring), a.ids, S, a.E, cap,
+                kSilu ? a.status : nullptr);
+    const int n_tiles = tb.n_tiles;
+
+    // the split of a stage's blocks among the warps: the fewest bytes on the busiest CTA,
+    // 8 KB being what a unit costs beside its own
+    int ks_log = 0, units = 0;
+    {
+        long long best = 0;
+        for (int l = 0; l <= 3; ++l) {
+            if (kStages * (kStageWeights + cap * (256 << l) + 64) > kRingBytes) break;
+            const int per = (kSilu ? 64 : 128) >> l;
+            const int n = n_tiles * ((a.rows + per - 1) / per);
+            const long long cost = (long long)((n + (int)gridDim.x - 1) / (int)gridDim.x) *
+                                   ((long long)(128 >> l) * a.K + 2ll * min(cap, 4) * a.K + 8192);
+            if (l == 0 || cost < best) best = cost, ks_log = l, units = n;
+        }
+    }
+    const int KS = 1 << ks_log, per = (kSilu ? 64 : 128) >> ks_log;
+    const int blocks = (a.rows + per - 1) / per;
+    const int ksteps = (a.K + 128 * KS - 1) / (128 * KS);
+    const int mine = blockIdx.x < units ? (units - 1 - (int)blockIdx.x) / (int)gridDim.x + 1 : 0;
+    const int steps = mine * ksteps;
+    const int x_bytes = cap * 256 * KS, stage_bytes = kStageWeights + x_bytes + 64;
+    const uint32_t ring0 = smem_of(ring);
+    const int Gk = (a.K + kGroup - 1) / kGroup;
+
+    // what a stage brings: parts & 1 the weights and scales, & 2 the activations
+    auto issue = [&](int step, int parts) {
+        const int u = blockIdx.x + step / ksteps * gridDim.x, kb0 = step % ksteps * KS;
+        const int tile = u / blocks, row0 = (u - tile * blocks) * per;
+        const int e = tb.tile_expert[tile];
+        const uint32_t st = ring0 + step % kStages * stage_bytes;
+        if (parts & 1) {
+            const uint8_t *w = a.w + (size_t)e * a.w_rows * a.K;
+#pragma unroll
+            for (int i = 0; i < kStageWeights / 16 / kThreads; ++i) {
+                const int q = tid + i * kThreads, r = q >> (3 + ks_log), c16 = q & (8 * KS - 1);
+                const int k = kb0 * kGroup + c16 * 16;
+                int row;
+                bool valid = k < a.K;
+                if constexpr (kSilu) {
+                    const int j = row0 + (r >> 4) * 8 + (r & 7);
+                    valid = valid && j < a.rows;
+                    row = j + (r & 8 ? a.rows : 0);
+                } else {
+                    row = row0 + r;
+                    valid = valid && row < a.rows;
+                }
+                copy16(st + (r << (7 + ks_log)) + ((c16 ^ ((r & 1) << 2)) << 4),
+                       valid ? w + (size_t)row * a.K + k : a.w, valid);
+            }
+            if (tid < 2 * kWarps) {
+                const int w_rg = (tid >> 1) >> ks_log, kb = min(kb0 + ((tid >> 1) & (KS - 1)), Gk - 1);
+                int row;
+                if constexpr (kSilu)
+                    row = min(row0 + w_rg * 8, a.rows - 1) + (tid & 1 ? a.rows : 0);
+                else
+                    row = min(row0 + w_rg * 16 + (tid & 1 ? 8 : 0), a.rows - 1);
+                copy4(st + kStageWeights + x_bytes + tid * 4,
+                      a.s + ((size_t)e * ((a.w_rows + kGroup - 1) / kGroup) + row / kGroup) * Gk + kb);
+            }
+        }
+        if (parts & 2) {
+            const int first = tb.tile_first[tile], n = tb.tile_count[tile];
+            for (int q = tid; q < n << (4 + ks_log); q += kThreads) {
+                const int r = q >> (4 + ks_log), c16 = q & (16 * KS - 1);
+                const int k = kb0 * kGroup + c16 * 8;
+                const int s = tb.slot[first + r], row = kSilu ? s / a.k : s;
+                copy16(st + kStageWeights + (r << (8 + ks_log)) + ((c16 ^ (r & 1)) << 4),
+                       k < a.K ? a.x + (size_t)row * a.K + k : a.x, k < a.K);
+            }
+        }
+    };
+
+    if constexpr (kSilu) {
+#pragma unroll
+        for (int i = 0; i < kStages - 1; ++i) {
+            if (i < steps) issue(i, 3);
+            commit_copies();
+        }
+    } else {
+        // the weights do not depend on the kernel before
+        for (int i = 0; i < kStages - 1 && i < steps; ++i) issue(i, 1);
+        asm volatile("griddepcontrol.wait;" ::: "memory");
+#pragma unroll
+        for (int i = 0; i < kStages - 1; ++i) {
+            if (i < steps) issue(i, 2);
+            commit_copies();  // the first group holds all stages' weights
+        }
+    }
+
+    const int rg = warp >> ks_log, ks = warp & (KS - 1);
+    float tot[NT][4] = {};
+    for (int step = 0; step < steps; ++step) {
+        wait_copies<kStages - 2>();
+        __syncthreads();  // the stage is there, and the one before it is free
+        if (step + kStages - 1 < steps) issue(step + kStages - 1, 3);
+        commit_copies();
+        const uint32_t st = ring0 + step % kStages * stage_bytes;
+        float acc[NT][4] = {};
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const uint32_t wp = st + ((rg * 16 + g) << (7 + ks_log)) +
+                                (((ks * 8 + h * 4 + c) ^ ((g & 1) << 2)) << 4);
+            const uint4 lo = lds128(wp), hi = lds128(wp + (8 << (7 + ks_log)));
+            const uint32_t wl[4] = {lo.x, lo.y, lo.z, lo.w}, wh[4] = {hi.x, hi.y, hi.z, hi.w};
+            uint32_t b[NT][8];
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+                const int tok = min(n * 8 + g, cap - 1);
+                const uint32_t xp = st + kStageWeights + (tok << (8 + ks_log));
+                const int c16 = ks * 16 + h * 8 + c * 2;
+                const uint4 b0 = lds128(xp + ((c16 ^ (tok & 1)) << 4)),
+                            b1 = lds128(xp + (((c16 + 1) ^ (tok & 1)) << 4));
+                b[n][0] = b0.x, b[n][1] = b0.y, b[n][2] = b0.z, b[n][3] = b0.w;
+                b[n][4] = b1.x, b[n][5] = b1.y, b[n][6] = b1.z, b[n][7] = b1.w;
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const uint32_t a0 = widen<kBf16>((uint16_t)wl[j]),
+                               a2 = widen<kBf16>((uint16_t)(wl[j] >> 16)),
+                               a1 = widen<kBf16>((uint16_t)wh[j]),
+                               a3 = widen<kBf16>((uint16_t)(wh[j] >> 16));
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+                    mma<kBf16>(acc[n], a0, a1, a2, a3, b[n][2 * j], b[n][2 * j + 1]);
+            }
+        }
+        const float *sc = reinterpret_cast<const float *>(ring + step % kStages * stage_bytes +
+                                                          kStageWeights + x_bytes) + warp * 2;
+        const float s0 = sc[0], s1 = sc[1];
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+            tot[n][0] = fmaf(s0, acc[n][0], tot[n][0]);
+            tot[n][1] = fmaf(s0, acc[n][1], tot[n][1]);
+            tot[n][2] = fmaf(s1, acc[n][2], tot[n][2]);
+            tot[n][3] = fmaf(s1, acc[n][3], tot[n][3]);
+        }
+        if ((step + 1) % ksteps != 0) continue;
+
+        // the unit's end: the warps of the same rows add up, in the order of their blocks
+        if (ks != 0) {
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) red[((warp * NT + n) * 4 + i) * 32 + lane] = tot[n][i];
+        }
+        __syncthreads();
+        if (ks == 0) {
+            for (int w = 1; w < KS; ++w)
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        tot[n][i] += red[(((warp + w) * NT + n) * 4 + i) * 32 + lane];
+            const int u = blockIdx.x + step / ksteps * gridDim.x;
+            const int tile = u / blocks, row0 = (u - tile * blocks) * per;
+            const int first = tb.tile_first[tile], count = tb.tile_count[tile];
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const int tok = n * 8 + c * 2 + i;
+                    if (tok >= count) continue;
+                    const size_t s = tb.slot[first + tok];
+                    if constexpr (kSilu) {
+                        const int j = row0 + rg * 8 + g;
+                        const float gate = tot[n][i], up = tot[n][2 + i];
+                        if (j < a.rows)
+                            a.h[s * a.rows + j] =
+                                float_to_half_bits(gate / (1.f + expf(-gate)) * up, kBf16);
+                    } else {
+                        const int j = row0 + rg * 16 + g;
+                        if (j < a.rows) a.o[s * a.rows + j] = tot[n][i];
+                        if (j + 8 < a.rows) a.o[s * a.rows + j + 8] = tot[n][2 + i];
+                    }
+                }
+        }
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) tot[n][i] = 0.f;
+    }
+}
+
+// out[t] = sum_j weights[t, j] * o[t k + j], j in order, without the choices that are none
+template <bool kBf16>
+__global__ void __launch_bounds__(256) combine_kernel(const float *o, const int32_t *ids,
+                                                      const float *weights, int T, int k, int E,
+                                                      int N, uint16_t *out) {
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int t = blockIdx.y, n = blockIdx.x * 256 + threadIdx.x;
+    if (n >= N) return;
+    float v = 0.f;
+    for (int j = 0; j < k; ++j) {
+        const int s = t * k + j;
+        if ((unsigned)ids[s] < (unsigned)E) v = fmaf(weights[s], o[(size_t)s * N + n], v);
+    }
+    out[(size_t)t * N + n] = float_to_half_bits(v, kBf16);
+}
+
+template <typename... Params, typename... Args>
+cudaError_t launch_chained(void (*kernel)(Params...), dim3 grid, int smem, cudaStream_t stream,
+                           Args... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+template <bool kBf16, int NT>
+cudaError_t launch_nt(const Fp8MoeArgs &a, const DeviceInfo &dev, int *status,
+                      cudaStream_t stream) {
+    const int grid = 2 * dev.sm_count, cap = a.T < 8 * NT ? a.T : 8 * NT;
+    uint16_t *h = static_cast<uint16_t *>(a.scratch);
+    float *o = reinterpret_cast<float *>(static_cast<char *>(a.scratch) +
+                                         fp8_moe_h_bytes(a.T, a.k, a.I));
+    Fp8ExpertsArgs p{a.x, a.w1, a.s1, a.ids, h, nullptr, status, a.T, a.k, a.E, a.K, a.I, 2 * a.I,
+                     cap};
+    cudaError_t e =
+        launch_chained(experts_kernel<kBf16, NT, true>, dim3(grid), kRingBytes, stream, p);
+    if (e != cudaSuccess) return e;
+    p = {h, a.w2, a.s2, a.ids, nullptr, o, status, a.T, a.k, a.E, a.I, a.N, a.N, cap};
+    e = launch_chained(experts_kernel<kBf16, NT, false>, dim3(grid), kRingBytes, stream, p);
+    if (e != cudaSuccess) return e;
+    return launch_chained(combine_kernel<kBf16>, dim3((a.N + 255) / 256, a.T), 0, stream,
+                          (const float *)o, a.ids, a.weights, a.T, a.k, a.E, a.N, a.out);
+}
+
+template <bool kBf16, int NT>
+cudaError_t init_nt() {
+    const void *kernels[] = {(const void *)experts_kernel<kBf16, NT, true>,
+                             (const void *)experts_kernel<kBf16, NT, false>};
+    for (const void *k : kernels) {
+        cudaError_t e =
+            cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kRingBytes);
+        if (e != cudaSuccess) return e;
+    }
+    return cudaSuccess;
+}
+
+}  // namespace
+
+cudaError_t launch_fp8_moe(const Fp8MoeArgs &a, bool bf16, const DeviceInfo &dev, int *status,
+                           cudaStream_t stream) {
+    // the tiles' width: so that an expert's slots fit one tile where they are as many as
+    // the average and somewhat more
+    const int slots = a.T * a.k;
+    if (slots <= 5 * a.E || a.T <= 8)
+        return bf16 ? launch_nt<true, 1>(a, dev, status, stream)
+                    : launch_nt<false, 1>(a, dev, status, stream);
+    if (slots <= 10 * a.E || a.T <= 16)
+        return bf16 ? launch_nt<true, 2>(a, dev, status, stream)
+                    : launch_nt<false, 2>(a, dev, status, stream);
+    return bf16 ? launch_nt<true, 4>(a, dev, status, stream)
+                : launch_nt<false, 4>(a, dev, status, stream);
+}
+
+cudaError_t fp8_moe_init() {
+    cudaError_t e = init_nt<true, 1>();
+    if (e == cudaSuccess) e = init_nt<true, 2>();
+    if (e == cudaSuccess) e = init_nt<true, 4>();
+    if (e == cudaSuccess) e = init_nt<false, 1>();
+    if (e == cudaSuccess) e = init_nt<false, 2>();
+    if (e == cudaSuccess) e = init_nt<false, 4>();
+    return e;
+}
+
+}  // namespace w4a16

@@ -361,6 +361,59 @@ cudaError_t launch_moe_prepare(const MmaLinDesc *tmpl, const MmaLinDesc *tmpl2,
 cudaError_t launch_moe_sum(const __half *y, const int32_t *pos, const float *w, int T, int k,
                            int N, bool bf16, __half *out, cudaStream_t stream);
 
+// ---- the choice of experts (w4a16_moe_route.cu) -----------------------------
+constexpr int kLogitsF32 = 2;  // the type of logits, beside kDtypeF16 and kDtypeBf16
+constexpr int kMaxRouteChoices = 32;
+// logits [T, E] -> the k largest of each row, ids [T, k] and weights [T, k]
+struct RouteArgs {
+    const void *logits;
+    int32_t *ids;
+    float *weights;
+    int T, E, k;
+    bool sigmoid, renormalize;
+    float scale;
+};
+cudaError_t launch_route(const RouteArgs &a, int type, cudaStream_t stream);
+
+// ---- layers of 8-bit experts for few tokens (w4a16_fp8_moe.cu) ----------------
+constexpr int kFp8MoeMaxSlots = 1024;  // T * k
+// w1 [E, 2I, K], s1 [E, ceil(2I/128), ceil(K/128)], w2 [E, N, I], s2 [E, ceil(N/128),
+// ceil(I/128)]; scratch: h [T k, I] in 16 bits, then o [T k, N] in fp32
+struct Fp8MoeArgs {
+    const uint16_t *x;
+    const int32_t *ids;
+    const float *weights;
+    const uint8_t *w1;
+    const float *s1;
+    const uint8_t *w2;
+    const float *s2;
+    uint16_t *out;
+    void *scratch;
+    int T, k, E, K, I, N;
+};
+inline size_t fp8_moe_h_bytes(int T, int k, int I) {
+    return ((size_t)T * k * I * 2 + 255) & ~(size_t)255;
+}
+inline size_t fp8_moe_scratch_bytes(int T, int k, int I, int N) {
+    return fp8_moe_h_bytes(T, k, I) + (size_t)T * k * N * 4;
+}
+// one of the layer's two products as its kernel reads it: rows [., K] of x (by token, or
+// by slot), weights w [E, w_rows, K], `rows` results per slot into h or o
+struct Fp8ExpertsArgs {
+    const uint16_t *x;
+    const uint8_t *w;
+    const float *s;
+    const int32_t *ids;
+    uint16_t *h;
+    float *o;
+    int *status;
+    int T, k, E, K, rows, w_rows;
+    int cap;  // slots per tile
+};
+cudaError_t launch_fp8_moe(const Fp8MoeArgs &a, bool bf16, const DeviceInfo &dev, int *status,
+                           cudaStream_t stream);
+cudaError_t fp8_moe_init();
+
 // ---- expert MLP decode kernel (w4a16_moe_decode.cu) ------------------------
 constexpr int kMoeDecodeMaxSlots = 128;  // T * k per launch
 constexpr int kMoeDecodeMaxTokens = 8;
