@@ -519,6 +519,36 @@ int w4a16_fp8_moe_mlp(const uint16_t *x, const int32_t *topk_ids, const float *w
                       const float *down_scales, uint16_t *out, void *scratch,
                       size_t scratch_bytes, void *stream);
 
+/* The low-rank adapters of many requests beside a shared projection (any of the linears
+ * above), each row with its own:
+ *     y[m] = residual[m] + scales[l] * B_l (A_l x[m]),   l = adapter_ids[m]
+ *   x            [M, K] in the 16-bit type `dtype`, as a, b, residual and y
+ *   a            [L, n_parts * R, K]: the projection's columns come in n_parts parts (q, k
+ *                and v; gate and up), parts[p] columns each (a HOST array, together N),
+ *                and part p uses rows p * R .. p * R + R - 1 of A
+ *   b            [L, N, R]
+ *   scales       [L] fp32; ranks [L] int32 or NULL: adapter l uses the first ranks[l] of R
+ *                in each part (clamped to 0..R), and what lies beyond is not read
+ *   adapter_ids  [M] int32; a row whose id is not in [0, L), or whose rank is 0, has no
+ *                adapter: y[m] = residual[m], bit by bit
+ *   residual     [M, N]: what the adapters add to, mostly the projection's output; y itself
+ *                (y += ...) or apart from it, or NULL for 0
+ *   scratch      w4a16_lora_scratch_bytes(M, L, R, n_parts) bytes, 16-byte aligned, the
+ *                call's own until its work is done (W4A16_ERR_WORKSPACE if fewer); calls
+ *                that share none may overlap
+ * Sums are fp32; A x enters the second product as two values of the 16-bit type (16 bits of
+ * it in bf16, 22 in fp16, of the row's largest); y is rounded once.  Three kernels.  A row's
+ * bits do not depend on its place in the batch, but the order of the sums over K goes by
+ * how many rows the adapters have.  K and R multiples of 8, K and N at most 2^22, 0 <= M
+ * <= 65535 (0: an empty batch); L <= 1024, R <= 128, n_parts <= 4 (W4A16_ERR_UNSUPPORTED
+ * above).  x, a and b 16-byte aligned, y and residual 2-byte, the others 4-byte; y and
+ * scratch overlap nothing else.  Needs w4a16_init; allocates nothing and may be captured. */
+size_t w4a16_lora_scratch_bytes(int M, int L, int R, int n_parts);
+int w4a16_lora(const uint16_t *x, const uint16_t *a, const uint16_t *b, const float *scales,
+               const int32_t *ranks, const int32_t *adapter_ids, int M, int K, int N, int L, int R,
+               const int32_t *parts, int n_parts, int dtype, const uint16_t *residual, uint16_t *y,
+               void *scratch, size_t scratch_bytes, void *stream);
+
 /* The rung the dispatch table picks for a shape (honouring a forced rung), or
  * -1 for an invalid shape.  Pure host query.  Unforced: M <= 8 takes the warp
  * MMA rungs, except small fp16 linears without an epilogue, which take the

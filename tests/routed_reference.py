@@ -89,3 +89,60 @@ def make_experts(seed, T, k, E, K, I, N, dtype):
     ids = torch.rand((T, E), generator=g).topk(k, 1).indices.to(torch.int32)
     weights = torch.softmax(2 * torch.randn((T, k), generator=g), 1)
     return (x, ids, weights, *codes(2 * I, K), *codes(N, I))
+
+
+def adapters(x, a, b, scales, ids, parts, ranks, residual, dtype):
+    """(y, bound), both [M, N], of the low-rank adapters.
+
+    With c = 2^-22 (16 + K / 16): t's K products (exact in fp32) are added 16 at a time, each
+    addition off by a unit of the largest term (2^-23, doubled for a truncating adder), its
+    slices and warps at most 16 + 16 times more.  t enters the second product with an error
+    of 2^-16 (bf16: two roundings of 2^-8; fp16: 2^-22) of itself, and at least 2^-24 of the
+    row's largest (fp16's subnormal spacing, as the row is scaled to at most 2).  Its sums
+    over R carry 2^-22 (16 + R / 16) of their magnitudes, the factor and the sum with the
+    residual three roundings, y one of its type.
+    """
+    X, S, ids = f64(x), f64(scales), ids.cpu().numpy()
+    (M, K), (L, N, R), u = X.shape, b.shape, UNIT[dtype]
+    y, off = np.zeros((M, N)), np.zeros((M, N))
+    res = np.zeros((M, N)) if residual is None else f64(residual)
+    adapted = np.zeros(M, dtype=bool)
+    with np.errstate(all="ignore"):
+        for l in range(L):
+            rows = np.nonzero(ids == l)[0]
+            r = R if ranks is None else min(max(int(ranks[l]), 0), R)
+            if rows.size == 0 or r == 0:
+                continue
+            adapted[rows] = True
+            first = 0
+            for p, n in enumerate(parts):
+                A, B = f64(a[l, p * R:p * R + r]), f64(b[l, first:first + n, :r])
+                t, mag = X[rows] @ A.T, np.abs(X[rows]) @ np.abs(A).T
+                dt = (2.0 ** -22 * (16 + K / 16) * mag + u * u * np.abs(t)
+                      + 2.0 ** -24 * np.abs(t).max(1, keepdims=True))
+                v, size = t @ B.T, (np.abs(t) + dt) @ np.abs(B).T
+                dv = dt @ np.abs(B).T + (2.0 ** -22 * (16 + R / 16) + 3 * 2.0 ** -23) * size
+                at = np.ix_(rows, np.arange(first, first + n))
+                y[at], off[at] = S[l] * v, abs(S[l]) * dv
+                first += n
+        y = y + res
+        bound = np.where(adapted[:, None],
+                         off + 2.0 ** -23 * np.abs(res) + u * (np.abs(y) + off) + 2.0 ** -24, 0.0)
+    return y, bound
+
+
+def make_adapters(seed, M, K, parts, L, R, dtype, ids=None, ranks=False, residual=True):
+    """Seeded operands (CPU) of the low-rank adapters, in the order of the call's arguments up
+    to the ids, then a dict of the others."""
+    g = torch.Generator().manual_seed(seed)
+    N = sum(parts)
+    x = torch.randn((M, K), generator=g).to(dtype)
+    a = (torch.randn((L, len(parts) * R, K), generator=g) * K ** -0.5).to(dtype)
+    b = (torch.randn((L, N, R), generator=g) * 0.5).to(dtype)
+    scales = 0.5 + torch.rand(L, generator=g)
+    if ids is None:
+        ids = torch.randint(-1, L, (M,), generator=g, dtype=torch.int32)
+    kw = dict(parts=list(parts),
+              ranks=torch.randint(0, R + 1, (L,), generator=g, dtype=torch.int32) if ranks else None,
+              residual=(torch.randn((M, N), generator=g) * 2).to(dtype) if residual else None)
+    return (x, a, b, scales, ids), kw

@@ -108,6 +108,9 @@ _sig("w4a16_moe_mlp_destroy", [_P])
 _sig("w4a16_moe_route", [_P, _I, _I, _I, _I, _I, _I, ctypes.c_float, _P, _P, _P])
 _sig("w4a16_fp8_moe_scratch_bytes", [_I, _I, _I, _I], _SZ)
 _sig("w4a16_fp8_moe_mlp", [_P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _P, _P, _P, _P, _P, _P, _SZ, _P])
+_sig("w4a16_lora_scratch_bytes", [_I, _I, _I, _I], _SZ)
+_sig("w4a16_lora", [_P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, ctypes.POINTER(ctypes.c_int32), _I,
+                    _I, _P, _P, _P, _SZ, _P])
 _sig("w4a16_moe_mlp", [_P, _P, _P, _P, _I, _P, _P])
 _sig("w4a16_decode_round", [ctypes.POINTER(LinearDesc), _I, _I, _P])
 _sig("w4a16_round_graph_create", [ctypes.POINTER(LinearDesc), _I, _I, ctypes.POINTER(_P)])
@@ -135,6 +138,7 @@ EXPORTED = ["w4a16_init", "w4a16_shutdown", "w4a16_workspace_bytes", "w4a16_pack
             "w4a16_moe_sum", "w4a16_moe_mlp_create", "w4a16_moe_mlp_destroy", "w4a16_moe_mlp",
             "w4a16_moe_mlp_set_path", "w4a16_moe_mlp_path", "w4a16_moe_mlp_buffers",
             "w4a16_moe_route", "w4a16_fp8_moe_scratch_bytes", "w4a16_fp8_moe_mlp",
+            "w4a16_lora_scratch_bytes", "w4a16_lora",
             "w4a16_decode_round",
             "w4a16_round_graph_create", "w4a16_round_graph_launch", "w4a16_round_graph_destroy",
             "w4a16_select_rung", "w4a16_plan_info", "w4a16_fp8_plan_info",
@@ -723,6 +727,40 @@ def w4a16_fp8_moe_mlp(x: torch.Tensor, topk_ids: torch.Tensor, weights: torch.Te
     _check(lib.w4a16_fp8_moe_mlp(xp, ip, wp, T, k, E, K, I, N, code, w1, s1, w2, s2, op, sp, need,
                                  raw), "w4a16_fp8_moe_mlp")
     return out
+
+
+def w4a16_lora(x: torch.Tensor, a: torch.Tensor, b: torch.Tensor, scales: torch.Tensor,
+               adapter_ids: torch.Tensor, parts=None, ranks=None, residual=None, y=None,
+               stream=None) -> torch.Tensor:
+    """y [M, N] = residual + scales[l] * B_l (A_l x), l = adapter_ids[m] of each row (outside
+    [0, L): no adapter): x [M, K], a [L, len(parts) * R, K], b [L, N, R] and residual [M, N]
+    (None for 0; it may be y itself) of one 16-bit type; parts: the columns of each part of
+    the projection that has R rows of A of its own (default: one part of N); ranks [L]
+    int32: how many of R each adapter uses."""
+    M, K = _rows2d(x, "x")
+    for name, w in (("a", a), ("b", b)):
+        if not isinstance(w, torch.Tensor) or w.dim() != 3:
+            raise ValueError(f"{name} must be a 3-D torch tensor")
+    L, N, R = b.shape
+    parts = (N,) if parts is None else tuple(parts)
+    n = len(parts)
+    dt = x.dtype
+    code = _dtype16(dt)
+    dev, xp = _home(x, dt, (M, K))
+    ap = _shaped(a, dt, (L, n * R, K), "a", dev)
+    bp = _shaped(b, dt, (L, N, R), "b", dev)
+    cp = _shaped(scales, torch.float32, (L,), "scales", dev)
+    kp = None if ranks is None else _shaped(ranks, torch.int32, (L,), "ranks", dev)
+    ip = _shaped(adapter_ids, torch.int32, (M,), "adapter_ids", dev)
+    rp = None if residual is None else _shaped(residual, dt, (M, N), "residual", dev)
+    raw, side = _stream_for(dev, stream)
+    y, yp = _output(y, (M, N), dt, dev, side, "y")
+    need = lib.w4a16_lora_scratch_bytes(M, L, R, n)
+    scratch, sp = _output(None, (1, need), torch.uint8, dev, side, "scratch")
+    _used_on(side, x, a, b, scales, ranks, adapter_ids, residual, y)
+    _check(lib.w4a16_lora(xp, ap, bp, cp, kp, ip, M, K, N, L, R, (ctypes.c_int32 * n)(*parts), n,
+                          code, rp, yp, sp, need, raw), "w4a16_lora")
+    return y
 
 
 def make_descs(layers) -> ctypes.Array:

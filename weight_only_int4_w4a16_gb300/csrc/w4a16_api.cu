@@ -631,6 +631,7 @@ int w4a16_init(int device, size_t workspace_bytes) {
     if (e == cudaSuccess) e = fp8_init(dev);
     if (e == cudaSuccess) e = fp8_wide_init(dev);
     if (e == cudaSuccess) e = fp8_moe_init();
+    if (e == cudaSuccess) e = lora_init();
     if (e == cudaSuccess) e = cudaDeviceSynchronize();
     if (e != cudaSuccess) {
         cudaFree(base);
@@ -1292,6 +1293,64 @@ int w4a16_fp8_moe_mlp(const uint16_t *x, const int32_t *topk_ids, const float *w
                        N};
     const cudaError_t e = launch_fp8_moe(a, dtype == W4A16_DTYPE_BF16, st.dev, st.ws.status,
                                          (cudaStream_t)stream);
+    if (e != cudaSuccess) return cuda_fail(e);
+    g_launches.fetch_add(3, std::memory_order_relaxed);
+    return W4A16_OK;
+}
+
+size_t w4a16_lora_scratch_bytes(int M, int L, int R, int n_parts) {
+    if (M < 1 || M > kMaxM || L < 1 || L > kMaxAdapters || R < 1 || R > kMaxRank || n_parts < 1 ||
+        n_parts > kMaxParts)
+        return 0;
+    return lora_scratch_bytes(M, L, R, n_parts);
+}
+
+int w4a16_lora(const uint16_t *x, const uint16_t *a, const uint16_t *b, const float *scales,
+               const int32_t *ranks, const int32_t *adapter_ids, int M, int K, int N, int L, int R,
+               const int32_t *parts, int n_parts, int dtype, const uint16_t *residual, uint16_t *y,
+               void *scratch, size_t scratch_bytes, void *stream) {
+    if (M < 0 || M > kMaxM || K < 1 || K > kMaxK || N < 1 || N > kMaxK || L < 1 || R < 1 ||
+        K % 8 != 0 || R % 8 != 0)
+        return W4A16_ERR_INVALID_ARG;
+    if (!parts || n_parts < 1) return W4A16_ERR_INVALID_ARG;
+    if (L > kMaxAdapters || R > kMaxRank || n_parts > kMaxParts) return W4A16_ERR_UNSUPPORTED;
+    LoraArgs p{};
+    long long columns = 0;
+    for (int i = 0; i < n_parts; ++i) {
+        if (parts[i] < 1) return W4A16_ERR_INVALID_ARG;
+        columns += p.part[i] = parts[i];
+    }
+    if (columns != N) return W4A16_ERR_INVALID_ARG;
+    if (dtype != W4A16_DTYPE_F16 && dtype != W4A16_DTYPE_BF16) return W4A16_ERR_INVALID_ARG;
+    if (M == 0) return W4A16_OK;
+    if (!x || !a || !b || !scales || !adapter_ids || !y || !scratch) return W4A16_ERR_INVALID_ARG;
+    if (!aligned(x, 16) || !aligned(a, 16) || !aligned(b, 16) || !aligned(scales, 4) ||
+        !aligned(ranks, 4) || !aligned(adapter_ids, 4) || !aligned(residual, 2) ||
+        !aligned(y, 2) || !aligned(scratch, 16))
+        return W4A16_ERR_MISALIGNED;
+    const size_t need = lora_scratch_bytes(M, L, R, n_parts);
+    if (scratch_bytes < need) return W4A16_ERR_WORKSPACE;
+    const size_t ybytes = (size_t)M * N * 2;
+    const struct { const void *p; size_t bytes; } in[] = {
+        {x, (size_t)M * K * 2},      {a, (size_t)L * n_parts * R * K * 2},
+        {b, (size_t)L * N * R * 2},  {scales, (size_t)L * 4},
+        {ranks, (size_t)L * 4},      {adapter_ids, (size_t)M * 4},
+        {residual, ybytes}};
+    for (const auto &i : in) {
+        if (!i.p) continue;
+        // the residual is y itself (y += ...) or lies apart from it
+        if (!(i.p == residual && residual == y) && overlaps(i.p, i.bytes, y, ybytes))
+            return W4A16_ERR_INVALID_ARG;
+        if (overlaps(i.p, i.bytes, scratch, need)) return W4A16_ERR_INVALID_ARG;
+    }
+    if (overlaps(y, ybytes, scratch, need)) return W4A16_ERR_INVALID_ARG;
+    const State &st = g_state;
+    if (!st.initialized) return W4A16_ERR_NOT_INITIALIZED;
+    p.x = x, p.a = a, p.b = b, p.scales = scales, p.ranks = ranks, p.ids = adapter_ids;
+    p.residual = residual, p.y = y, p.scratch = scratch;
+    p.M = M, p.K = K, p.N = N, p.L = L, p.R = R, p.parts = n_parts;
+    const cudaError_t e =
+        launch_lora(p, dtype == W4A16_DTYPE_BF16, st.dev, (cudaStream_t)stream);
     if (e != cudaSuccess) return cuda_fail(e);
     g_launches.fetch_add(3, std::memory_order_relaxed);
     return W4A16_OK;

@@ -414,6 +414,38 @@ cudaError_t launch_fp8_moe(const Fp8MoeArgs &a, bool bf16, const DeviceInfo &dev
                            cudaStream_t stream);
 cudaError_t fp8_moe_init();
 
+// ---- low-rank adapters (w4a16_lora.cu) ----------------------------------------
+constexpr int kMaxAdapters = 1024;
+constexpr int kMaxRank = 128;
+constexpr int kMaxParts = 4;
+// x [M, K], a [L, parts R, K], b [L, N, R], scales [L], ranks [L] or null, ids [M]; part:
+// the columns of each part, together N; residual and y [M, N]
+struct LoraArgs {
+    const uint16_t *x, *a, *b;
+    const float *scales;
+    const int32_t *ranks, *ids;
+    const uint16_t *residual;
+    uint16_t *y;
+    void *scratch;
+    int M, K, N, L, R, parts;
+    int part[kMaxParts];
+    int ctas, max_slices;  // filled in by launch_lora
+};
+// the scratch: the plan (16-byte header, tiles of 16 bytes, the rows' order), then t in
+// max_slices parts.  Slices make few rows' K parallel; many rows need none
+__host__ __device__ inline int lora_max_tiles(int M, int L) {
+    return (M < L ? M : L) + M / 128 + 2;
+}
+__host__ __device__ inline size_t lora_plan_bytes(int M, int L) {
+    return (16 + 16 * (size_t)lora_max_tiles(M, L) + 4 * (size_t)M + 255) & ~(size_t)255;
+}
+inline int lora_max_slices(int M) { return M >= 32768 ? 1 : M <= 2048 ? 16 : 32768 / M; }
+inline size_t lora_scratch_bytes(int M, int L, int R, int parts) {
+    return lora_plan_bytes(M, L) + (size_t)lora_max_slices(M) * M * parts * R * 4;
+}
+cudaError_t launch_lora(LoraArgs a, bool bf16, const DeviceInfo &dev, cudaStream_t stream);
+cudaError_t lora_init();
+
 // ---- expert MLP decode kernel (w4a16_moe_decode.cu) ------------------------
 constexpr int kMoeDecodeMaxSlots = 128;  // T * k per launch
 constexpr int kMoeDecodeMaxTokens = 8;
