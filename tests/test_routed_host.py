@@ -118,10 +118,10 @@ def test_lora_codes(w4):
 
 
 def test_lora_scratch_holds_the_plan(w4):
-    # 16 bytes, 16 per tile, 4 per row, then t: at least one part of M x parts x R floats
+    # 16 bytes, 8 per tile, 2 per row, then t: M x parts x R floats
     for M, L in ((1, 1), (1, 1024), (17, 3), (4096, 1024), (65535, 1)):
         tiles = min(M, L) + M // 128 + 1  # full ones and a rest per adapter, those without
-        need = 16 + 16 * tiles + 4 * M + M * 2 * 16 * 4
+        need = 16 + 8 * tiles + 2 * M + M * 2 * 16 * 4
         assert w4.lib.w4a16_lora_scratch_bytes(M, L, 16, 2) >= need
 
 

@@ -1352,7 +1352,7 @@ int w4a16_lora(const uint16_t *x, const uint16_t *a, const uint16_t *b, const fl
     const cudaError_t e =
         launch_lora(p, dtype == W4A16_DTYPE_BF16, st.dev, (cudaStream_t)stream);
     if (e != cudaSuccess) return cuda_fail(e);
-    g_launches.fetch_add(3, std::memory_order_relaxed);
+    g_launches.fetch_add(lora_kernels(M), std::memory_order_relaxed);
     return W4A16_OK;
 }
 

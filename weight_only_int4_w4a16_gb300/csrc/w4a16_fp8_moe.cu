@@ -25,43 +25,17 @@
 //
 // Every CTA groups the slots itself (a stable counting sort in shared memory), which
 // costs it no launch and no pass through memory.
-#include "w4a16_fp8_common.cuh"
+#include "w4a16_routed.cuh"
 
 namespace w4a16 {
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kWarps = kThreads / 32;
+using namespace routed;
+
 constexpr int kStages = 4;
 constexpr int kStageWeights = 16 << 10;  // bytes
 constexpr int kRingBytes = 100 << 10;    // so that two CTAs share an SM
 
-__device__ __forceinline__ uint32_t smem_of(const void *p) {
-    return (uint32_t)__cvta_generic_to_shared(p);
-}
-// 16 bytes to shared memory, or zeros
-__device__ __forceinline__ void copy16(uint32_t dst, const void *src, bool valid) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
-                 "r"(valid ? 16 : 0)
-                 : "memory");
-}
-__device__ __forceinline__ void copy4(uint32_t dst, const void *src) {
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
-}
-__device__ __forceinline__ void commit_copies() {
-    asm volatile("cp.async.commit_group;" ::: "memory");
-}
-template <int N>
-__device__ __forceinline__ void wait_copies() {
-    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
-__device__ __forceinline__ uint4 lds128(uint32_t p) {
-    uint4 v;
-    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-                 : "r"(p));
-    return v;
-}
 // two e4m3 codes -> two 16-bit values, exact
 template <bool kBf16>
 __device__ __forceinline__ uint32_t widen(uint16_t codes) {
@@ -74,101 +48,39 @@ __device__ __forceinline__ uint32_t widen(uint16_t codes) {
     }
     return d;
 }
-template <bool kBf16>
-__device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
-                                    uint32_t a3, uint32_t b0, uint32_t b1) {
-    if constexpr (kBf16)
-        asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
-            "{%8,%9}, {%0,%1,%2,%3};"
-            : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-            : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-    else
-        asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
-            "{%8,%9}, {%0,%1,%2,%3};"
-            : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-            : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
-
 struct Tables {
     uint16_t slot[kFp8MoeMaxSlots];         // slots by expert, in order
     uint16_t tile_expert[kFp8MoeMaxSlots];  // a tile: slots tile_first .. + tile_count
     uint16_t tile_first[kFp8MoeMaxSlots];
     uint8_t tile_count[kFp8MoeMaxSlots];
-    int warp_sums[kWarps];
-    int n_tiles;
 };
-// in the ring before its first stage is filled
-struct SortSpace {
-    uint8_t rank[kFp8MoeMaxSlots];            // among the equal ids of the slot's 32
-    uint16_t before[kMaxMoeExperts];          // slots of lower experts
-    uint16_t count[kFp8MoeMaxSlots / 32 * kMaxMoeExperts];  // [32 slots][expert]
-};
-static_assert(sizeof(SortSpace) <= kRingBytes, "the sort fits the ring");
+static_assert(kFp8MoeMaxSlots <= kMaxRows && kMaxMoeExperts <= kMaxBins, "the sort holds them");
+static_assert(sizeof(RowSort) <= kRingBytes, "the sort fits the ring");
+static_assert(kStages * (kStageWeights + 32 * 256 + 128) <= kRingBytes, "cap * KS <= 32 fits");
 
-// The slots by expert (stable), in tiles of up to cap slots.  An id outside [0, E) leaves
-// its slot out; one other than -1 is reported.
-__device__ void group_slots(Tables &tb, SortSpace &sp, const int32_t *ids, int S, int E, int cap,
-                            int *status) {
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int chunks = (S + 31) / 32;
-    for (int i = tid; i < chunks * E; i += kThreads) sp.count[i] = 0;
-    __syncthreads();
-    for (int c = warp; c < chunks; c += kWarps) {
-        const int s = c * 32 + lane;
-        const int e = s < S ? ids[s] : -1;
-        const bool valid = (unsigned)e < (unsigned)E;
-        const unsigned same = __match_any_sync(0xffffffffu, valid ? e : -1);
-        const int rank = __popc(same & ((1u << lane) - 1));
-        sp.rank[s] = (uint8_t)rank;
-        if (valid && rank == 0) sp.count[c * E + e] = (uint16_t)__popc(same);
-        if (!valid && e != -1 && status && blockIdx.x == 0) atomicOr(status, kErrMoeIds);
-    }
-    __syncthreads();
-    // experts 4 tid .. 4 tid + 3: their chunks' counts become what lies before each chunk,
-    // and the slots and tiles of lower experts come from a scan over the threads
-    static_assert(kMaxMoeExperts <= 4 * kThreads, "four experts per thread");
-    int n[4], own = 0;  // slots, tiles << 16
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int e = 4 * tid + i;
-        n[i] = 0;
-        if (e < E)
-            for (int c = 0; c < chunks; ++c) {
-                const int v = sp.count[c * E + e];
-                sp.count[c * E + e] = (uint16_t)n[i];
-                n[i] += v;
-            }
-        own += n[i] + ((n[i] + cap - 1) / cap << 16);
-    }
-    int incl = own;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const int v = __shfl_up_sync(0xffffffffu, incl, o);
-        if (lane >= o) incl += v;
-    }
-    if (lane == 31) tb.warp_sums[warp] = incl;
-    __syncthreads();
-    int at = incl - own;
-    for (int w = 0; w < warp; ++w) at += tb.warp_sums[w];
-    if (tid == kThreads - 1) tb.n_tiles = (at + own) >> 16;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int e = 4 * tid + i, first = at & 0xffff;
-        if (e < E) sp.before[e] = (uint16_t)first;
-        for (int p = 0, tile = at >> 16; p < n[i]; p += cap, ++tile) {
-            tb.tile_expert[tile] = (uint16_t)e;
-            tb.tile_first[tile] = (uint16_t)(first + p);
-            tb.tile_count[tile] = (uint8_t)min(cap, n[i] - p);
-        }
-        at += n[i] + ((n[i] + cap - 1) / cap << 16);
-    }
-    __syncthreads();
-    for (int s = tid; s < S; s += kThreads) {
-        const int e = ids[s];
-        if ((unsigned)e < (unsigned)E)
-            tb.slot[sp.before[e] + sp.count[s / 32 * E + e] + sp.rank[s]] = (uint16_t)s;
-    }
-    __syncthreads();
+// The slots by expert, in tiles of up to cap slots; how many tiles.  An id outside [0, E)
+// leaves its slot out; one other than -1 is reported.
+__device__ int make_tiles(Tables &tb, RowSort &sp, const int32_t *ids, int S, int E, int cap,
+                          int *status) {
+    const auto pack = [&](int, int n) { return (unsigned)n | (unsigned)(n + cap - 1) / cap << 11; };
+    return group_rows(
+               sp, tb.slot, S, E,
+               [&](int s) {
+                   const int e = ids[s];
+                   if ((unsigned)e >= (unsigned)E && e != -1 && status && blockIdx.x == 0)
+                       atomicOr(status, kErrMoeIds);
+                   return e;
+               },
+               pack,
+               [&](int e, int n, unsigned at, unsigned) {
+                   int tile = at >> 11, first = at & 2047;
+                   for (; n > 0; n -= cap, first += cap, ++tile) {
+                       tb.tile_expert[tile] = (uint16_t)e;
+                       tb.tile_first[tile] = (uint16_t)first;
+                       tb.tile_count[tile] = (uint8_t)min(cap, n);
+                   }
+               }) >>
+           11;
 }
 
 // kSilu: gate and up, x by token, h by slot; else down, h by slot, o (fp32) by slot
@@ -181,15 +93,10 @@ __global__ void __launch_bounds__(kThreads, 2) experts_kernel(Fp8ExpertsArgs a) 
     const int g = lane >> 2, c = lane & 3;
     const int S = a.T * a.k, cap = a.cap;
 
-    if constexpr (kSilu) {
-        asm volatile("griddepcontrol.wait;" ::: "memory");
-        asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    } else {
-        asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    }
-    group_slots(tb, *reinterpret_cast<SortSpace *>(ring), a.ids, S, a.E, cap,
-                kSilu ? a.status : nullptr);
-    const int n_tiles = tb.n_tiles;
+    if constexpr (kSilu) wait_for_last();
+    launch_next();
+    const int n_tiles = make_tiles(tb, *reinterpret_cast<RowSort *>(ring), a.ids, S, a.E, cap,
+                                   kSilu ? a.status : nullptr);
 
     // the split of a stage's blocks among the warps: the fewest bytes on the busiest CTA,
     // 8 KB being what a unit costs beside its own
@@ -197,7 +104,7 @@ __global__ void __launch_bounds__(kThreads, 2) experts_kernel(Fp8ExpertsArgs a) 
     {
         long long best = 0;
         for (int l = 0; l <= 3; ++l) {
-            if (kStages * (kStageWeights + cap * (256 << l) + 64) > kRingBytes) break;
+            if (cap << l > 32) break;  // what the ring's stages hold
             const int per = (kSilu ? 64 : 128) >> l;
             const int n = n_tiles * ((a.rows + per - 1) / per);
             const long long cost = (long long)((n + (int)gridDim.x - 1) / (int)gridDim.x) *
@@ -210,83 +117,132 @@ __global__ void __launch_bounds__(kThreads, 2) experts_kernel(Fp8ExpertsArgs a) 
     const int ksteps = (a.K + 128 * KS - 1) / (128 * KS);
     const int mine = blockIdx.x < units ? (units - 1 - (int)blockIdx.x) / (int)gridDim.x + 1 : 0;
     const int steps = mine * ksteps;
-    const int x_bytes = cap * 256 * KS, stage_bytes = kStageWeights + x_bytes + 64;
+    const int x_bytes = cap * 256 * KS, stage_bytes = kStageWeights + x_bytes + 128;
     const uint32_t ring0 = smem_of(ring);
     const int Gk = (a.K + kGroup - 1) / kGroup;
 
-    // what a stage brings: parts & 1 the weights and scales, & 2 the activations
-    auto issue = [&](int step, int parts) {
-        const int u = blockIdx.x + step / ksteps * gridDim.x, kb0 = step % ksteps * KS;
-        const int tile = u / blocks, row0 = (u - tile * blocks) * per;
-        const int e = tb.tile_expert[tile];
-        const uint32_t st = ring0 + step % kStages * stage_bytes;
-        if (parts & 1) {
-            const uint8_t *w = a.w + (size_t)e * a.w_rows * a.K;
+    // Copies walk the units' stages in order.  Per unit each thread keeps where its 16-byte
+    // pieces of weights (four), activations (at most two) and its scale come from.
+    constexpr int kW = kStageWeights / 16 / kThreads, kX = 2;
+    const int wc = tid & (8 * KS - 1), wr = tid >> (3 + ks_log);     // piece of a row, row
+    const int xc = tid & (16 * KS - 1), xr = tid >> (4 + ks_log);
+    struct Cursor {
+        int unit, kstep, stage;
+    };
+    const uint8_t *wp[kW];
+    const uint16_t *xp[kX];
+    const float *sp = a.s;
+    unsigned w_rows = 0;  // bit i: piece i is of a row that exists
+    auto enter_weights = [&](int unit) {
+        const int tile = unit / blocks, row0 = (unit - tile * blocks) * per;
+        const size_t e = tb.tile_expert[tile];
+        const uint8_t *w = a.w + e * a.w_rows * a.K + wc * 16;
+        w_rows = 0;
 #pragma unroll
-            for (int i = 0; i < kStageWeights / 16 / kThreads; ++i) {
-                const int q = tid + i * kThreads, r = q >> (3 + ks_log), c16 = q & (8 * KS - 1);
-                const int k = kb0 * kGroup + c16 * 16;
-                int row;
-                bool valid = k < a.K;
-                if constexpr (kSilu) {
-                    const int j = row0 + (r >> 4) * 8 + (r & 7);
-                    valid = valid && j < a.rows;
-                    row = j + (r & 8 ? a.rows : 0);
-                } else {
-                    row = row0 + r;
-                    valid = valid && row < a.rows;
-                }
-                copy16(st + (r << (7 + ks_log)) + ((c16 ^ ((r & 1) << 2)) << 4),
-                       valid ? w + (size_t)row * a.K + k : a.w, valid);
+        for (int i = 0; i < kW; ++i) {
+            const int r = wr + i * (32 >> ks_log);
+            int row = row0 + r, j = row;
+            if constexpr (kSilu) {
+                j = row0 + (r >> 4) * 8 + (r & 7);
+                row = j + (r & 8 ? a.rows : 0);
             }
-            if (tid < 2 * kWarps) {
-                const int w_rg = (tid >> 1) >> ks_log, kb = min(kb0 + ((tid >> 1) & (KS - 1)), Gk - 1);
-                int row;
-                if constexpr (kSilu)
-                    row = min(row0 + w_rg * 8, a.rows - 1) + (tid & 1 ? a.rows : 0);
-                else
-                    row = min(row0 + w_rg * 16 + (tid & 1 ? 8 : 0), a.rows - 1);
-                copy4(st + kStageWeights + x_bytes + tid * 4,
-                      a.s + ((size_t)e * ((a.w_rows + kGroup - 1) / kGroup) + row / kGroup) * Gk + kb);
-            }
+            wp[i] = w + (size_t)row * a.K;
+            if (j < a.rows) w_rows |= 1u << i;
         }
-        if (parts & 2) {
-            const int first = tb.tile_first[tile], n = tb.tile_count[tile];
-            for (int q = tid; q < n << (4 + ks_log); q += kThreads) {
-                const int r = q >> (4 + ks_log), c16 = q & (16 * KS - 1);
-                const int k = kb0 * kGroup + c16 * 8;
-                const int s = tb.slot[first + r], row = kSilu ? s / a.k : s;
-                copy16(st + kStageWeights + (r << (8 + ks_log)) + ((c16 ^ (r & 1)) << 4),
-                       k < a.K ? a.x + (size_t)row * a.K + k : a.x, k < a.K);
+        if (tid < 2 * kWarps) {
+            const int rg = (tid >> 1) >> ks_log;
+            int row;
+            if constexpr (kSilu)
+                row = min(row0 + rg * 8, a.rows - 1) + (tid & 1 ? a.rows : 0);
+            else
+                row = min(row0 + rg * 16 + (tid & 1 ? 8 : 0), a.rows - 1);
+            sp = a.s + (e * ((a.w_rows + kGroup - 1) / kGroup) + row / kGroup) * Gk;
+        }
+    };
+    auto enter_x = [&](int unit) {
+        const int tile = unit / blocks, first = tb.tile_first[tile], n = tb.tile_count[tile];
+#pragma unroll
+        for (int i = 0; i < kX; ++i) {
+            const int r = xr + i * (16 >> ks_log);
+            xp[i] = nullptr;
+            if (r < n) {
+                const int s = tb.slot[first + r];
+                xp[i] = a.x + (size_t)(kSilu ? s / a.k : s) * a.K + xc * 8;
             }
         }
     };
+    auto copy_weights = [&](const Cursor &cu) {
+        const uint32_t st = ring0 + cu.stage * stage_bytes + tid * 16;
+        const int k = cu.kstep * KS * kGroup;
+        const int in = k + wc * 16 < a.K ? 16 : 0;
+#pragma unroll
+        for (int i = 0; i < kW; ++i) {
+            const int n = w_rows >> i & 1 ? in : 0;
+            // piece c of row r is at c ^ 4 in odd rows: so that lanes of neighbouring rows
+            // read other banks
+            const int r = wr + i * (32 >> ks_log);
+            copy16((st + i * kThreads * 16) ^ ((r & 1) << 6), n ? wp[i] + k : a.w, n);
+        }
+        if (tid < 2 * kWarps)
+            copy4(ring0 + cu.stage * stage_bytes + kStageWeights + x_bytes + tid * 4,
+                  sp + min(cu.kstep * KS + ((tid >> 1) & (KS - 1)), Gk - 1));
+    };
+    auto copy_x = [&](const Cursor &cu) {
+        const uint32_t st = ring0 + cu.stage * stage_bytes + kStageWeights;
+        const int k = cu.kstep * KS * kGroup;
+        const int in = k + xc * 8 < a.K ? 16 : 0;
+#pragma unroll
+        for (int i = 0; i < kX; ++i) {
+            const int r = xr + i * (16 >> ks_log);
+            if (xp[i])
+                copy16(st + (r << (8 + ks_log)) + ((xc ^ (r & 1)) << 4), in ? xp[i] + k : a.x, in);
+        }
+    };
+    auto advance = [&](Cursor &cu) {
+        cu.stage = cu.stage == kStages - 1 ? 0 : cu.stage + 1;
+        if (++cu.kstep == ksteps) {
+            cu.kstep = 0;
+            cu.unit += gridDim.x;
+        }
+    };
 
-    if constexpr (kSilu) {
-#pragma unroll
-        for (int i = 0; i < kStages - 1; ++i) {
-            if (i < steps) issue(i, 3);
-            commit_copies();
-        }
-    } else {
+    Cursor in = {(int)blockIdx.x, 0, 0};
+    if constexpr (!kSilu) {
         // the weights do not depend on the kernel before
-        for (int i = 0; i < kStages - 1 && i < steps; ++i) issue(i, 1);
-        asm volatile("griddepcontrol.wait;" ::: "memory");
-#pragma unroll
-        for (int i = 0; i < kStages - 1; ++i) {
-            if (i < steps) issue(i, 2);
-            commit_copies();  // the first group holds all stages' weights
+        for (int i = 0; i < kStages - 1 && i < steps; ++i) {
+            if (in.kstep == 0) enter_weights(in.unit);
+            copy_weights(in);
+            advance(in);
         }
+        in = {(int)blockIdx.x, 0, 0};
+        wait_for_last();
+    }
+#pragma unroll
+    for (int i = 0; i < kStages - 1; ++i) {
+        if (i < steps) {
+            if (kSilu && in.kstep == 0) enter_weights(in.unit);
+            if (in.kstep == 0) enter_x(in.unit);
+            if (kSilu) copy_weights(in);
+            copy_x(in);
+            advance(in);
+        }
+        commit_copies();  // (down: the first group holds the weights of all)
     }
 
     const int rg = warp >> ks_log, ks = warp & (KS - 1);
     float tot[NT][4] = {};
-    for (int step = 0; step < steps; ++step) {
+    Cursor at = {(int)blockIdx.x, 0, 0};
+    for (int step = 0; step < steps; ++step, advance(at)) {
         wait_copies<kStages - 2>();
         __syncthreads();  // the stage is there, and the one before it is free
-        if (step + kStages - 1 < steps) issue(step + kStages - 1, 3);
+        if (step + kStages - 1 < steps) {
+            if (in.kstep == 0) enter_weights(in.unit), enter_x(in.unit);
+            copy_weights(in);
+            copy_x(in);
+            advance(in);
+        }
         commit_copies();
-        const uint32_t st = ring0 + step % kStages * stage_bytes;
+        const uint32_t st = ring0 + at.stage * stage_bytes;
         float acc[NT][4] = {};
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
@@ -316,7 +272,7 @@ __global__ void __launch_bounds__(kThreads, 2) experts_kernel(Fp8ExpertsArgs a) 
                     mma<kBf16>(acc[n], a0, a1, a2, a3, b[n][2 * j], b[n][2 * j + 1]);
             }
         }
-        const float *sc = reinterpret_cast<const float *>(ring + step % kStages * stage_bytes +
+        const float *sc = reinterpret_cast<const float *>(ring + at.stage * stage_bytes +
                                                           kStageWeights + x_bytes) + warp * 2;
         const float s0 = sc[0], s1 = sc[1];
 #pragma unroll
@@ -326,7 +282,7 @@ __global__ void __launch_bounds__(kThreads, 2) experts_kernel(Fp8ExpertsArgs a) 
             tot[n][2] = fmaf(s1, acc[n][2], tot[n][2]);
             tot[n][3] = fmaf(s1, acc[n][3], tot[n][3]);
         }
-        if ((step + 1) % ksteps != 0) continue;
+        if (at.kstep != ksteps - 1) continue;
 
         // the unit's end: the warps of the same rows add up, in the order of their blocks
         if (ks != 0) {
@@ -343,8 +299,7 @@ __global__ void __launch_bounds__(kThreads, 2) experts_kernel(Fp8ExpertsArgs a) 
 #pragma unroll
                     for (int i = 0; i < 4; ++i)
                         tot[n][i] += red[(((warp + w) * NT + n) * 4 + i) * 32 + lane];
-            const int u = blockIdx.x + step / ksteps * gridDim.x;
-            const int tile = u / blocks, row0 = (u - tile * blocks) * per;
+            const int tile = at.unit / blocks, row0 = (at.unit - tile * blocks) * per;
             const int first = tb.tile_first[tile], count = tb.tile_count[tile];
 #pragma unroll
             for (int n = 0; n < NT; ++n)
@@ -378,8 +333,8 @@ template <bool kBf16>
 __global__ void __launch_bounds__(256) combine_kernel(const float *o, const int32_t *ids,
                                                       const float *weights, int T, int k, int E,
                                                       int N, uint16_t *out) {
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    launch_next();
+    wait_for_last();
     const int t = blockIdx.y, n = blockIdx.x * 256 + threadIdx.x;
     if (n >= N) return;
     float v = 0.f;
@@ -388,22 +343,6 @@ __global__ void __launch_bounds__(256) combine_kernel(const float *o, const int3
         if ((unsigned)ids[s] < (unsigned)E) v = fmaf(weights[s], o[(size_t)s * N + n], v);
     }
     out[(size_t)t * N + n] = float_to_half_bits(v, kBf16);
-}
-
-template <typename... Params, typename... Args>
-cudaError_t launch_chained(void (*kernel)(Params...), dim3 grid, int smem, cudaStream_t stream,
-                           Args... args) {
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = grid;
-    cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
 template <bool kBf16, int NT>
@@ -416,13 +355,12 @@ cudaError_t launch_nt(const Fp8MoeArgs &a, const DeviceInfo &dev, int *status,
     Fp8ExpertsArgs p{a.x, a.w1, a.s1, a.ids, h, nullptr, status, a.T, a.k, a.E, a.K, a.I, 2 * a.I,
                      cap};
     cudaError_t e =
-        launch_chained(experts_kernel<kBf16, NT, true>, dim3(grid), kRingBytes, stream, p);
+        launch_chained(experts_kernel<kBf16, NT, true>, dim3(grid), kThreads, kRingBytes, 1, stream, p);
     if (e != cudaSuccess) return e;
     p = {h, a.w2, a.s2, a.ids, nullptr, o, status, a.T, a.k, a.E, a.I, a.N, a.N, cap};
-    e = launch_chained(experts_kernel<kBf16, NT, false>, dim3(grid), kRingBytes, stream, p);
+    e = launch_chained(experts_kernel<kBf16, NT, false>, dim3(grid), kThreads, kRingBytes, 1, stream, p);
     if (e != cudaSuccess) return e;
-    return launch_chained(combine_kernel<kBf16>, dim3((a.N + 255) / 256, a.T), 0, stream,
-                          (const float *)o, a.ids, a.weights, a.T, a.k, a.E, a.N, a.out);
+    return launch_chained(combine_kernel<kBf16>, dim3((a.N + 255) / 256, a.T), 256, 0, 1, stream, (const float *)o, a.ids, a.weights, a.T, a.k, a.E, a.N, a.out);
 }
 
 template <bool kBf16, int NT>

@@ -429,21 +429,22 @@ struct LoraArgs {
     void *scratch;
     int M, K, N, L, R, parts;
     int part[kMaxParts];
-    int ctas, max_slices;  // filled in by launch_lora
 };
-// the scratch: the plan (16-byte header, tiles of 16 bytes, the rows' order), then t in
-// max_slices parts.  Slices make few rows' K parallel; many rows need none
+// the scratch: the plan (a 16-byte header, tiles of 8 bytes, the rows' order in 2 bytes
+// each), then t [M, parts R] in fp32
 __host__ __device__ inline int lora_max_tiles(int M, int L) {
     return (M < L ? M : L) + M / 128 + 2;
 }
 __host__ __device__ inline size_t lora_plan_bytes(int M, int L) {
-    return (16 + 16 * (size_t)lora_max_tiles(M, L) + 4 * (size_t)M + 255) & ~(size_t)255;
+    return (16 + 8 * (size_t)lora_max_tiles(M, L) + 2 * (size_t)M + 255) & ~(size_t)255;
 }
-inline int lora_max_slices(int M) { return M >= 32768 ? 1 : M <= 2048 ? 16 : 32768 / M; }
 inline size_t lora_scratch_bytes(int M, int L, int R, int parts) {
-    return lora_plan_bytes(M, L) + (size_t)lora_max_slices(M) * M * parts * R * 4;
+    return lora_plan_bytes(M, L) + (size_t)M * parts * R * 4;
 }
-cudaError_t launch_lora(LoraArgs a, bool bf16, const DeviceInfo &dev, cudaStream_t stream);
+// kernels of a call: the grouping of more rows than a CTA does for itself is one of its own
+constexpr int kLoraLocalRows = 1024;
+inline int lora_kernels(int M) { return M > kLoraLocalRows ? 3 : 2; }
+cudaError_t launch_lora(const LoraArgs &a, bool bf16, const DeviceInfo &dev, cudaStream_t stream);
 cudaError_t lora_init();
 
 // ---- expert MLP decode kernel (w4a16_moe_decode.cu) ------------------------
