@@ -615,8 +615,8 @@ const char *w4a16_status_string(int status);
  * counters of its own: after an expired wait destroy it and create it again.
  * Bits of the code: 1024 an invalid expert id, 4096 and 8192 the probe below,
  * of the 8-bit linear 1 << 17 a wait for operands, 1 << 18 for a block's sums,
- * 1 << 19 for a free stage, 1 << 20 for what was in flight at the end; the others
- * are expired waits of the other kernels.
+ * 1 << 19 for a free stage, 1 << 20 for what was in flight at the end; 1 << 21
+ * a wait for products of w4a16_lora; the others are expired waits of the other kernels.
  * W4A16_ERR_NOT_INITIALIZED when neither w4a16_init nor a
  * w4a16_linear_noalloc call has run. */
 int w4a16_device_status(void *stream, int *code);

@@ -1347,7 +1347,7 @@ int w4a16_lora(const uint16_t *x, const uint16_t *a, const uint16_t *b, const fl
     const State &st = g_state;
     if (!st.initialized) return W4A16_ERR_NOT_INITIALIZED;
     p.x = x, p.a = a, p.b = b, p.scales = scales, p.ranks = ranks, p.ids = adapter_ids;
-    p.residual = residual, p.y = y, p.scratch = scratch;
+    p.residual = residual, p.y = y, p.scratch = scratch, p.status = st.ws.status;
     p.M = M, p.K = K, p.N = N, p.L = L, p.R = R, p.parts = n_parts;
     const cudaError_t e =
         launch_lora(p, dtype == W4A16_DTYPE_BF16, st.dev, (cudaStream_t)stream);

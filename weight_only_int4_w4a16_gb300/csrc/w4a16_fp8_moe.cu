@@ -25,6 +25,7 @@
 //
 // Every CTA groups the slots itself (a stable counting sort in shared memory), which
 // costs it no launch and no pass through memory.
+#include <cstdlib>
 #include "w4a16_routed.cuh"
 
 namespace w4a16 {
@@ -32,6 +33,8 @@ namespace {
 
 using namespace routed;
 
+constexpr int kThreads = 256;
+constexpr int kWarps = kThreads / 32;
 constexpr int kStages = 4;
 constexpr int kStageWeights = 16 << 10;  // bytes
 constexpr int kRingBytes = 100 << 10;    // so that two CTAs share an SM
@@ -53,34 +56,35 @@ struct Tables {
     uint16_t tile_expert[kFp8MoeMaxSlots];  // a tile: slots tile_first .. + tile_count
     uint16_t tile_first[kFp8MoeMaxSlots];
     uint8_t tile_count[kFp8MoeMaxSlots];
+    int tiles;
 };
-static_assert(kFp8MoeMaxSlots <= kMaxRows && kMaxMoeExperts <= kMaxBins, "the sort holds them");
-static_assert(sizeof(RowSort) <= kRingBytes, "the sort fits the ring");
+using Sort = RowSort<kFp8MoeMaxSlots>;
+static_assert(kMaxMoeExperts <= kMaxBins && sizeof(Sort) <= kRingBytes, "the sort fits the ring");
 static_assert(kStages * (kStageWeights + 32 * 256 + 128) <= kRingBytes, "cap * KS <= 32 fits");
 
 // The slots by expert, in tiles of up to cap slots; how many tiles.  An id outside [0, E)
 // leaves its slot out; one other than -1 is reported.
-__device__ int make_tiles(Tables &tb, RowSort &sp, const int32_t *ids, int S, int E, int cap,
+__device__ int make_tiles(Tables &tb, Sort &sp, const int32_t *ids, int S, int E, int cap,
                           int *status) {
-    const auto pack = [&](int, int n) { return (unsigned)n | (unsigned)(n + cap - 1) / cap << 11; };
-    return group_rows(
-               sp, tb.slot, S, E,
-               [&](int s) {
-                   const int e = ids[s];
-                   if ((unsigned)e >= (unsigned)E && e != -1 && status && blockIdx.x == 0)
-                       atomicOr(status, kErrMoeIds);
-                   return e;
-               },
-               pack,
-               [&](int e, int n, unsigned at, unsigned) {
-                   int tile = at >> 11, first = at & 2047;
-                   for (; n > 0; n -= cap, first += cap, ++tile) {
-                       tb.tile_expert[tile] = (uint16_t)e;
-                       tb.tile_first[tile] = (uint16_t)first;
-                       tb.tile_count[tile] = (uint8_t)min(cap, n);
-                   }
-               }) >>
-           11;
+    group_rows<kThreads>(
+        sp, tb.slot, S, E,
+        [&](int s) {
+            const int e = ids[s];
+            if ((unsigned)e >= (unsigned)E && e != -1 && status && blockIdx.x == 0)
+                atomicOr(status, kErrMoeIds);
+            return e;
+        },
+        [&](int, int n) { return (unsigned)n | (unsigned)(n + cap - 1) / cap << 11; },
+        [&](int e, int n, unsigned at) {
+            int tile = at >> 11, first = at & 2047;
+            for (; n > 0; n -= cap, first += cap, ++tile) {
+                tb.tile_expert[tile] = (uint16_t)e;
+                tb.tile_first[tile] = (uint16_t)first;
+                tb.tile_count[tile] = (uint8_t)min(cap, n);
+            }
+        },
+        [&](unsigned total) { tb.tiles = total >> 11; });
+    return tb.tiles;
 }
 
 // kSilu: gate and up, x by token, h by slot; else down, h by slot, o (fp32) by slot
@@ -95,22 +99,22 @@ __global__ void __launch_bounds__(kThreads, 2) experts_kernel(Fp8ExpertsArgs a) 
 
     if constexpr (kSilu) wait_for_last();
     launch_next();
-    const int n_tiles = make_tiles(tb, *reinterpret_cast<RowSort *>(ring), a.ids, S, a.E, cap,
+    const int n_tiles = make_tiles(tb, *reinterpret_cast<Sort *>(ring), a.ids, S, a.E, cap,
                                    kSilu ? a.status : nullptr);
 
     // the split of a stage's blocks among the warps: the fewest bytes on the busiest CTA,
     // 8 KB being what a unit costs beside its own
-    int ks_log = 0, units = 0;
+    int ks_log, units;
     {
-        long long best = 0;
-        for (int l = 0; l <= 3; ++l) {
-            if (cap << l > 32) break;  // what the ring's stages hold
-            const int per = (kSilu ? 64 : 128) >> l;
-            const int n = n_tiles * ((a.rows + per - 1) / per);
-            const long long cost = (long long)((n + (int)gridDim.x - 1) / (int)gridDim.x) *
-                                   ((long long)(128 >> l) * a.K + 2ll * min(cap, 4) * a.K + 8192);
-            if (l == 0 || cost < best) best = cost, ks_log = l, units = n;
-        }
+        const int l = lane & 3, per = (kSilu ? 64 : 128) >> l;  // a lane for each
+        const int n = n_tiles * ((a.rows + per - 1) / per);
+        float cost = (float)((n + gridDim.x - 1) / gridDim.x) *
+                     ((float)(128 >> l) * a.K + 2.f * min(cap, 4) * a.K + 8192.f);
+        if (cap << l > 32) cost = INFINITY;  // more than the ring's stages hold
+        float best = fminf(cost, __shfl_xor_sync(0xffffffffu, cost, 1));
+        best = fminf(best, __shfl_xor_sync(0xffffffffu, best, 2));
+        ks_log = __ffs(__ballot_sync(0xffffffffu, cost == best)) - 1;
+        units = __shfl_sync(0xffffffffu, n, ks_log);
     }
     const int KS = 1 << ks_log, per = (kSilu ? 64 : 128) >> ks_log;
     const int blocks = (a.rows + per - 1) / per;
@@ -348,7 +352,7 @@ __global__ void __launch_bounds__(256) combine_kernel(const float *o, const int3
 template <bool kBf16, int NT>
 cudaError_t launch_nt(const Fp8MoeArgs &a, const DeviceInfo &dev, int *status,
                       cudaStream_t stream) {
-    const int grid = 2 * dev.sm_count, cap = a.T < 8 * NT ? a.T : 8 * NT;
+    const int grid = (getenv("W4_G") ? atoi(getenv("W4_G")) : 2) * dev.sm_count, cap = a.T < 8 * NT ? a.T : 8 * NT;
     uint16_t *h = static_cast<uint16_t *>(a.scratch);
     float *o = reinterpret_cast<float *>(static_cast<char *>(a.scratch) +
                                          fp8_moe_h_bytes(a.T, a.k, a.I));

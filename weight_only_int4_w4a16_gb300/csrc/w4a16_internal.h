@@ -427,13 +427,14 @@ struct LoraArgs {
     const uint16_t *residual;
     uint16_t *y;
     void *scratch;
+    int *status;
     int M, K, N, L, R, parts;
     int part[kMaxParts];
 };
 // the scratch: the plan (a 16-byte header, tiles of 8 bytes, the rows' order in 2 bytes
 // each), then t [M, parts R] in fp32
 __host__ __device__ inline int lora_max_tiles(int M, int L) {
-    return (M < L ? M : L) + M / 128 + 2;
+    return (M < L ? M : L) + M / 128;
 }
 __host__ __device__ inline size_t lora_plan_bytes(int M, int L) {
     return (16 + 8 * (size_t)lora_max_tiles(M, L) + 2 * (size_t)M + 255) & ~(size_t)255;

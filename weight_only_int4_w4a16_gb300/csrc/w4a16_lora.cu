@@ -21,15 +21,20 @@
 //   * expand: y.  All steps (64 columns of a tall tile, 32 of a low one for each warp) are
 //     one sequence of which every CTA takes an equal run; B and the residual come through
 //     rings of asynchronous copies, which start before shrink has ended.
-// Both are bound by the bytes of x, y and the adapters (R products per byte of y read and
-// written), so they run on the warp MMA, whose fragments hold 16 contiguous bytes of a row
-// of y once the columns of four 8-column tiles are interleaved.
+// Both are bound by the bytes of x, y and the adapters.  Tall tiles run on tcgen05 (M = 128
+// rows of the tile; the warp MMA, at an eighth of its rate, paced them: 4096 rows, rank 64
+// beside gate+up took 34 and 191 us where they take XX and YY), low ones on the warp MMA with
+// the rows as its M = 16, straight from what the asynchronous copies bring.
 //
 // t is fp32; as expand's operand it is split into two values of the 16-bit type, the value
 // rounded and the rest rounded, of a row first scaled by a power of two to at most 2: 16
 // bits (bf16) or 22 (fp16) of it enter the product, at twice the MMAs, which are not the
-// bound up to rank 64.
+// bound.
+//
+// Every wait for a product is bounded; one that expires sets a status bit, and the kernel
+// goes on to its end without waiting any more.
 #include "w4a16_routed.cuh"
+#include "w4a16_tcgen05.cuh"
 
 namespace w4a16 {
 namespace {
@@ -38,36 +43,54 @@ using namespace routed;
 
 constexpr int kTall = 128;   // rows of a tall tile
 constexpr int kLow = 16;     // and of a low one, at most
+constexpr int kFewRows = 128;    // calls of up to so many rows have low tiles only
+constexpr int kLocalRows = kLoraLocalRows;  // and up to so many every CTA groups for itself
 constexpr int kPlanThreads = 1024;
+constexpr int kShrinkThreads = 256;
 constexpr int kCluster = 8;      // CTAs that share a shrink unit's K
 constexpr int kTallRanks = 128;  // rows of A of a shrink unit of a tall tile
 constexpr int kLowRanks = 32;    // and of a low one
 constexpr int kShrinkStages = 3;
 constexpr int kShrinkStage = (kTall + kTallRanks) * 128;  // bytes: 64 k of x and A
-constexpr int kShrinkSmem = kShrinkStages * kShrinkStage;
-constexpr int kTallCols = 64;  // columns of a step of expand, tall tiles
-constexpr int kLowCols = 32;   // low ones
+constexpr int kTallCols = 128;  // columns of a step of expand, tall tiles
+constexpr int kLowCols = 32;    // low ones
+constexpr int kLowPitch = kLowRanks + 8;  // of a low unit's sums in shared memory
+constexpr int max_of(int a, int b) { return a > b ? a : b; }
+constexpr int kShrinkTmem = 128, kExpandTmem = 256;  // columns: a tile's sums; two steps'
+constexpr int kErrProducts = 1 << 21;  // device status bit: a wait for products expired
 
 struct Tile {
     uint16_t adapter, first, count, pad;
 };
-// tall tiles, then low ones, then those of rows without an adapter (as high as tall ones)
 struct Counts {
-    int tall, low, none, pad;
+    int tall, low;      // tiles
+    int rows, none;     // with an adapter, and without (those come last)
+};
+// a CTA's own, of up to kRows rows; tall tiles from the front, low ones from the back, as
+// adapter << 17 | first << 7 | count - 1
+template <int kRows>
+struct LocalPlan {
+    static constexpr int kTiles = kRows + kRows / kLow;
+    Counts n;
+    uint32_t tiles[kTiles];
+    uint16_t order[kRows];
 };
 struct Plan {
     Counts n;
-    const Tile *tiles;
-    const uint16_t *order;  // the rows by adapter
-};
-// a CTA's own, of up to kMaxRows rows
-struct LocalPlan {
-    Counts n;
-    Tile tiles[kMaxRows + kMaxRows / kTall + 2];
-    uint16_t order[kMaxRows];
+    const Tile *shared;      // tall tiles, then low ones; null: the CTA's own
+    const uint32_t *own;
+    int own_tiles;
+    const uint16_t *order;   // the rows by adapter
+
+    static __device__ __forceinline__ Tile unpack(uint32_t t) {
+        return {(uint16_t)(t >> 17), (uint16_t)(t >> 7 & 1023), (uint16_t)((t & 127) + 1), 0};
+    }
+    __device__ __forceinline__ Tile tall(int i) const { return shared ? shared[i] : unpack(own[i]); }
+    __device__ __forceinline__ Tile low(int i) const {
+        return shared ? shared[n.tall + i] : unpack(own[own_tiles - 1 - i]);
+    }
 };
 static_assert(sizeof(Counts) == 16 && sizeof(Tile) == 8, "as lora_plan_bytes counts them");
-static_assert(kMaxRows == kLoraLocalRows, "as lora_kernels counts them");
 static_assert(kMaxAdapters + 1 <= kMaxBins, "the sort holds every adapter and none");
 
 __device__ __forceinline__ int rank_of(const LoraArgs &a, int l) {
@@ -79,54 +102,147 @@ __device__ __forceinline__ int bin_of(const LoraArgs &a, int m) {
     const int l = a.ids[m];
     return (unsigned)l < (unsigned)a.L && rank_of(a, l) > 0 ? l : a.L;
 }
-__device__ __forceinline__ int tall_tiles(int n) {
-    return n > kLow ? (n + kTall - 1) / kTall : 0;
+// the tiles of an adapter with n rows: tall ones, low ones
+__device__ __forceinline__ int tall_tiles(int n, bool few) {
+    return !few && n > kLow ? (n + kTall - 1) / kTall : 0;
 }
-__device__ __forceinline__ void put_tiles(Tile *tiles, int l, int first, int n) {
-    for (int i = 0; i < n; i += kTall)
-        tiles[i / kTall] = {(uint16_t)l, (uint16_t)(first + i), (uint16_t)min(kTall, n - i), 0};
+__device__ __forceinline__ int low_tiles(int n, bool few) {
+    return few || n <= kLow ? (n + kLow - 1) / kLow : 0;
 }
-
 __device__ Counts *shared_counts(const LoraArgs &a) { return static_cast<Counts *>(a.scratch); }
 __device__ __forceinline__ float *sums_of(const LoraArgs &a) {
     return reinterpret_cast<float *>(static_cast<char *>(a.scratch) + lora_plan_bytes(a.M, a.L));
 }
 __device__ __forceinline__ Plan shared_plan(const LoraArgs &a) {
-    Plan p;
-    p.tiles = reinterpret_cast<const Tile *>(shared_counts(a) + 1);
-    p.order = reinterpret_cast<const uint16_t *>(p.tiles + lora_max_tiles(a.M, a.L));
+    Plan p{};
+    p.shared = reinterpret_cast<const Tile *>(shared_counts(a) + 1);
+    p.order = reinterpret_cast<const uint16_t *>(p.shared + lora_max_tiles(a.M, a.L));
     return p;
 }
 
-// The plan of the call; `space` is free again afterwards.
-__device__ Plan make_plan(const LoraArgs &a, LocalPlan &own, void *space) {
+// The plan of the call; `space` is free again afterwards.  kRows: of calls that the CTA
+// groups for itself.
+template <int kCta, int kRows>
+__device__ Plan make_plan(const LoraArgs &a, LocalPlan<kRows> &own, void *space) {
+    constexpr bool few = kRows == kFewRows;
     Plan p = shared_plan(a);
-    if (a.M > kMaxRows) {
+    if (a.M > kRows) {
         p.n = *shared_counts(a);
         return p;
     }
-    group_rows(
-        *static_cast<RowSort *>(space), own.order, a.M, a.L + 1,
+    // a pack: rows, tall tiles << 11, low tiles << 21; bin L (no adapter), the last, has none
+    group_rows<kCta>(
+        *static_cast<RowSort<kRows> *>(space), own.order, a.M, a.L + 1,
         [&](int m) { return bin_of(a, m); },
-        [&](int l, int n) {  // rows, tall tiles << 11, low tiles << 21
-            if (l == a.L) return (unsigned)n;
-            return (unsigned)n | (unsigned)tall_tiles(n) << 11 |
-                   (unsigned)(n > 0 && n <= kLow) << 21;
+        [&](int l, int n) {
+            return l == a.L ? 0u
+                            : (unsigned)n | (unsigned)tall_tiles(n, few) << 11 |
+                                  (unsigned)low_tiles(n, few) << 21;
         },
-        [&](int l, int n, unsigned at, unsigned total) {
-            const int tall = total >> 11 & 1023, low = total >> 21, first = at & 2047;
-            if (l == a.L) {
-                own.n = {tall, low, (n + kTall - 1) / kTall, 0};
-                put_tiles(own.tiles + tall + low, l, first, n);
-            } else if (n > 0) {
-                put_tiles(own.tiles + (n <= kLow ? tall + (at >> 21) : at >> 11 & 1023), l, first,
-                          n);
-            }
+        [&](int l, int n, unsigned at) {
+            if (l == a.L) return;
+            const bool tall = tall_tiles(n, few) > 0;
+            const int height = tall ? kTall : kLow;
+            int i = tall ? (int)(at >> 11 & 1023)
+                         : LocalPlan<kRows>::kTiles - 1 - (int)(at >> 21);
+            for (int r = 0; r < n; r += height, i += tall ? 1 : -1)
+                own.tiles[i] = (uint32_t)l << 17 | ((at & 2047) + r) << 7 |
+                               (min(height, n - r) - 1);
+        },
+        [&](unsigned total) {
+            const int rows = total & 2047;
+            own.n = {(int)(total >> 11 & 1023), (int)(total >> 21), rows, a.M - rows};
         });
     p.n = own.n;
-    p.tiles = own.tiles;
+    p.shared = nullptr;
+    p.own = own.tiles;
+    p.own_tiles = LocalPlan<kRows>::kTiles;
     p.order = own.order;
     return p;
+}
+
+__device__ __forceinline__ uint8_t *align1024(uint8_t *p) {
+    return reinterpret_cast<uint8_t *>(((uintptr_t)p + 1023) & ~(uintptr_t)1023);
+}
+
+// ---------------------------------------------------------------------------
+// products of tall tiles: tensor memory, the barriers that tell of their ends
+// ---------------------------------------------------------------------------
+struct ProductSpace {
+    uint64_t done[kShrinkStages];
+    uint32_t tmem;
+    int abort;
+};
+struct Products {
+    ProductSpace *sp;
+    int *status;
+    uint32_t tmem;
+    unsigned count;  // committed so far, by barrier in turn
+
+    // all threads, before the next kernel may start: its CTAs take tensor memory too
+    template <int kCols>
+    __device__ __forceinline__ void begin(ProductSpace *space, int *status_word) {
+        sp = space, status = status_word, count = 0;
+        if (threadIdx.x == 0) {
+            for (int i = 0; i < kShrinkStages; ++i) dev::mbar_init(smem_of(&sp->done[i]), 1);
+            dev::mbar_init_fence();
+            sp->abort = 0;
+        }
+        __syncwarp();
+        if (threadIdx.x < 32) {
+            asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                             smem_of(&sp->tmem)),
+                         "r"(kCols)
+                         : "memory");
+            asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+        }
+        dev::tc_fence_before();
+        __syncthreads();
+        dev::tc_fence_after();
+        tmem = sp->tmem;
+    }
+    template <int kCols>
+    __device__ __forceinline__ void end() {
+        dev::tc_fence_before();
+        __syncthreads();
+        if (threadIdx.x < 32) {
+            dev::tc_fence_after();
+            asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem),
+                         "r"(kCols)
+                         : "memory");
+        }
+    }
+    __device__ __forceinline__ void commit(unsigned n, int bars) {  // by the issuing thread
+        dev::mma_commit(smem_of(&sp->done[n % bars]));
+    }
+    // products n (counted from 0) and all before are done
+    __device__ __forceinline__ void wait(unsigned n, int bars) {
+        volatile int *abort = &sp->abort;
+        if (!dev::mbar_wait(smem_of(&sp->done[n % bars]), n / bars & 1, abort) && !*abort) {
+            *abort = 1;
+            atomicOr(status, kErrProducts);
+        }
+    }
+};
+// D[tensor memory] (+)= A B^T over 16 k, both 128-byte swizzled in shared memory
+__device__ __forceinline__ void product16(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
+                                          bool add) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)add)
+        : "memory");
+}
+// M = 128, N = n (a multiple of 16), fp32 sums
+template <bool kBf16>
+__device__ __forceinline__ uint32_t product_desc(int n) {
+    return (1u << 4) | (kBf16 ? (1u << 7) | (1u << 10) : 0u) | ((uint32_t)(n >> 3) << 17) |
+           ((uint32_t)(kTall >> 4) << 24);
+}
+// where 16-byte piece c of a 128-byte row r lies in the swizzled layout
+__device__ __forceinline__ uint32_t swizzled(int r, int c) {
+    return (uint32_t)(r << 7) + (uint32_t)((c ^ (r & 7)) << 4);
 }
 
 // ---------------------------------------------------------------------------
@@ -139,7 +255,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(LoraArgs a) {
     wait_for_last();
     launch_next();
     const Plan plan = shared_plan(a);
-    Tile *tiles = const_cast<Tile *>(plan.tiles);
+    Tile *tiles = const_cast<Tile *>(plan.shared);
     uint16_t *order = const_cast<uint16_t *>(plan.order);
     for (int l = tid; l <= a.L; l += kPlanThreads) count[l] = 0;
     __syncthreads();
@@ -154,7 +270,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(LoraArgs a) {
     __syncthreads();
     // scans over the adapters (one per thread) of rows, tall and low tiles
     const int n = tid < a.L ? count[tid] : 0;
-    int v[3] = {n, tall_tiles(n), n > 0 && n <= kLow};
+    int v[3] = {n, tall_tiles(n, false), low_tiles(n, false)};
     const int own[3] = {v[0], v[1], v[2]};
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1)
@@ -174,14 +290,15 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(LoraArgs a) {
             if (w < warp) v[i] += sums[i][w];
             all[i] += sums[i][w];
         }
-    const int none = a.M - all[0], first = v[0] - own[0];
+    const int first = v[0] - own[0];
     if (tid == 0) {
-        *shared_counts(a) = {all[1], all[2], (none + kTall - 1) / kTall, 0};
+        *shared_counts(a) = {all[1], all[2], all[0], a.M - all[0]};
         count[a.L] = all[0];
     }
-    put_tiles(tiles + (own[2] ? all[1] + v[2] - own[2] : v[1] - own[1]), tid, first, n);
-    for (int i = tid * kTall; i < none; i += kPlanThreads * kTall)
-        put_tiles(tiles + all[1] + all[2] + i / kTall, a.L, all[0] + i, min(kTall, none - i));
+    for (int i = 0; i < own[1]; ++i)
+        tiles[v[1] - own[1] + i] = {(uint16_t)tid, (uint16_t)(first + i * kTall),
+                                    (uint16_t)min(kTall, n - i * kTall), 0};
+    if (own[2]) tiles[all[1] + v[2] - 1] = {(uint16_t)tid, (uint16_t)first, (uint16_t)n, 0};
     if (tid < a.L) count[tid] = first;
     __syncthreads();
     for (int i = 0; i < rounds; ++i) {
@@ -230,7 +347,7 @@ __device__ void join_sums(const LoraArgs &a, const uint16_t *order, int rows, in
     cluster_sync();
     const int share = (rows + kCluster - 1) / kCluster, first = (int)cluster_rank() * share;
     const int n = max(0, min(share, rows - first)) * quads;
-    for (int i = threadIdx.x; i < n; i += kThreads) {
+    for (int i = threadIdx.x; i < n; i += kShrinkThreads) {
         const int r = first + i / quads, q = i % quads * 4;
         float4 v[kCluster];
 #pragma unroll
@@ -243,15 +360,14 @@ __device__ void join_sums(const LoraArgs &a, const uint16_t *order, int rows, in
     cluster_sync();  // the others have read this CTA's
 }
 
-// A tile of up to 128 rows, rows q0 .. q0 + 127 of A, k0 <= k < k1.  Warps 4 x 2: 32 rows,
-// every other 8 rows of A.
+// A tile of up to 128 rows, rows q0 .. q0 + 127 of A, k0 <= k < k1: the products of a stage
+// of 64 k are issued once it is there, and its slot is filled again once they are done.
 template <bool kBf16>
 __device__ void shrink_tall(const LoraArgs &a, const uint16_t *order, const Tile &t, int q0, int k0,
-                            int k1, uint8_t *smem) {
+                            int k1, uint8_t *smem, Products &pr) {
     constexpr int kPitch = kTallRanks + 4;
-    static_assert(kTall * kPitch * 4 <= kShrinkSmem, "the sums fit the stages");
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, c = lane & 3;
-    const int wm = warp >> 1, wn = warp & 1;
+    static_assert(kTall * kPitch * 4 <= kShrinkStages * kShrinkStage, "the sums fit the stages");
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int Q = a.parts * a.R, rank = rank_of(a, t.adapter);
     const uint32_t base = smem_of(smem);
     // this thread's 16 bytes of four rows of x and of A, per stage
@@ -265,22 +381,19 @@ __device__ void shrink_tall(const LoraArgs &a, const uint16_t *order, const Tile
     }
     const int ranks = min(kTallRanks, Q - q0);
     auto issue = [&](int s) {
-        const uint32_t st = base + s % kShrinkStages * kShrinkStage;
+        const uint32_t st = base + (pr.count + s) % kShrinkStages * kShrinkStage;
         const int k = k0 + s * 64 + col * 8, in = k < k1 ? 16 : 0;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const int r = r0 + 32 * i;
-            // piece c of row r is at c ^ 4 in odd rows: lanes of neighbouring rows read
-            // other banks
-            const uint32_t at = (r << 7) + ((col ^ ((r & 1) << 2)) << 4);
+            const uint32_t at = swizzled(r, col);
             if (xp[i]) copy16(st + at, in ? xp[i] + k : a.x, in);
             if (r < ranks)
                 copy16(st + kTall * 128 + at, ap[i] && in ? ap[i] + k : a.a, ap[i] ? in : 0);
         }
     };
     const int steps = k1 > k0 ? (k1 - k0 + 63) / 64 : 0;
-    const int tiles_n = ranks / 8;
-    float acc[2][8][4] = {};
+    const uint32_t idesc = product_desc<kBf16>((ranks + 15) / 16 * 16);
 #pragma unroll
     for (int s = 0; s < kShrinkStages - 1; ++s) {
         if (s < steps) issue(s);
@@ -288,44 +401,43 @@ __device__ void shrink_tall(const LoraArgs &a, const uint16_t *order, const Tile
     }
     for (int s = 0; s < steps; ++s) {
         wait_copies<kShrinkStages - 2>();
+        dev::fence_async_shared();
         __syncthreads();
-        if (s + kShrinkStages - 1 < steps) issue(s + kShrinkStages - 1);
+        if (tid == 0) {
+            dev::tc_fence_after();
+            const uint32_t st = base + (pr.count + s) % kShrinkStages * kShrinkStage;
+            const uint64_t x = dev::smem_desc_sw128(st), w = dev::smem_desc_sw128(st + kTall * 128);
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                product16(pr.tmem, x + 2 * k, w + 2 * k, idesc, s + k > 0);
+            pr.commit(pr.count + s, kShrinkStages);
+        }
+        if (s + kShrinkStages - 1 < steps) {
+            if (s > 0) pr.wait(pr.count + s - 1, kShrinkStages);
+            issue(s + kShrinkStages - 1);
+        }
         commit_copies();
-        const uint32_t st = base + s % kShrinkStages * kShrinkStage;
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const uint32_t at = (((h * 4 + c) ^ ((g & 1) << 2)) << 4);
-            uint4 x[2][2];
-#pragma unroll
-            for (int i = 0; i < 2; ++i)
-#pragma unroll
-                for (int u = 0; u < 2; ++u)
-                    x[i][u] = lds128(st + ((wm * 32 + i * 16 + u * 8 + g) << 7) + at);
-#pragma unroll
-            for (int n = 0; n < 8; ++n) {
-                if (2 * n + wn >= tiles_n) break;
-                const uint4 w = lds128(st + kTall * 128 + (((2 * n + wn) * 8 + g) << 7) + at);
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    mma<kBf16>(acc[i][n], x[i][0].x, x[i][1].x, x[i][0].y, x[i][1].y, w.x, w.y);
-                    mma<kBf16>(acc[i][n], x[i][0].z, x[i][1].z, x[i][0].w, x[i][1].w, w.z, w.w);
-                }
-            }
-        }
     }
-    wait_copies<0>();
+    if (steps > 0) pr.wait(pr.count + steps - 1, kShrinkStages);
+    pr.count += steps;
+    dev::tc_fence_after();
     __syncthreads();  // the sums go where the stages were
-    float *red = reinterpret_cast<float *>(smem);
+    // a warp's 32 rows (its quarter of the tensor memory's lanes), half of A's rows
+    const int r = (warp & 3) * 32 + lane, q = (warp >> 2) * 64;
+    float *row = reinterpret_cast<float *>(smem) + r * kPitch + q;
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
-#pragma unroll
-        for (int u = 0; u < 2; ++u) {
-            float *row = red + (wm * 32 + i * 16 + u * 8 + g) * kPitch + c * 2;
-#pragma unroll
-            for (int n = 0; n < 8; ++n)
-                *reinterpret_cast<float2 *>(row + (2 * n + wn) * 8) =
-                    make_float2(acc[i][n][2 * u], acc[i][n][2 * u + 1]);
+    for (int h = 0; h < 2; ++h) {
+        uint32_t v[32] = {};
+        if (steps > 0) {
+            dev::tmem_ld(pr.tmem + ((uint32_t)(warp & 3) << 21) + q + h * 32, v);
+            dev::tmem_wait_ld(v);
         }
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            *reinterpret_cast<uint4 *>(row + h * 32 + i * 4) =
+                make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+    }
+    dev::tc_fence_before();
     join_sums(a, order, t.count, q0, ranks, kPitch, base);
 }
 
@@ -333,7 +445,7 @@ __device__ void shrink_tall(const LoraArgs &a, const uint16_t *order, const Tile
 template <bool kBf16>
 __device__ void shrink_low(const LoraArgs &a, const uint16_t *order, const Tile &t, int q0, int k0,
                            int k1, uint8_t *smem) {
-    constexpr int NT = kLowRanks / 8, kPitch = kLowRanks + 8;
+    constexpr int NT = kLowRanks / 8, kPitch = kLowPitch, kWarps = kShrinkThreads / 32;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, c = lane & 3;
     const int Q = a.parts * a.R, rank = rank_of(a, t.adapter);
     const uint16_t *x0 = a.x + (size_t)order[min(g, t.count - 1)] * a.K,
@@ -372,7 +484,7 @@ __device__ void shrink_low(const LoraArgs &a, const uint16_t *order, const Tile 
         for (int i = 0; i < 4; ++i)
             red[(warp * kLow + g + (i >> 1) * 8) * kPitch + n * 8 + c * 2 + (i & 1)] = acc[n][i];
     __syncthreads();
-    for (int i = tid; i < kLow * kLowRanks; i += kThreads) {
+    for (int i = tid; i < kLow * kLowRanks; i += kShrinkThreads) {
         const int r = i / kLowRanks, q = i % kLowRanks;
         float v = 0.f;
 #pragma unroll
@@ -382,48 +494,103 @@ __device__ void shrink_low(const LoraArgs &a, const uint16_t *order, const Tile 
     join_sums(a, order, t.count, q0, min(kLowRanks, Q - q0), kPitch, smem_of(smem));
 }
 
-template <bool kBf16>
-__global__ void __launch_bounds__(kThreads, 2) shrink_kernel(LoraArgs a) {
-    extern __shared__ __align__(128) uint8_t smem[];
-    __shared__ LocalPlan own;
+// kFew: calls of up to kFewRows rows, with low tiles only; the others' shared memory holds
+// the stages
+template <bool kFew>
+constexpr int shrink_smem() {
+    return kFew ? max_of((kShrinkThreads / 32 + 1) * kLow * kLowPitch * 4,
+                         (int)sizeof(RowSort<kFewRows>))
+                : kShrinkStages * kShrinkStage + 1024;  // (to align them)
+}
+
+template <bool kBf16, bool kFew>
+__global__ void __launch_bounds__(kShrinkThreads, 2) shrink_kernel(LoraArgs a) {
+    constexpr int kRows = kFew ? kFewRows : kLocalRows;
+    extern __shared__ __align__(128) uint8_t smem_raw[];
+    uint8_t *smem = kFew ? smem_raw : align1024(smem_raw);
+    __shared__ LocalPlan<kRows> own;
+    __shared__ ProductSpace space;
+    Products pr;
+    if constexpr (!kFew) pr.begin<kShrinkTmem>(&space, a.status);
     wait_for_last();
     launch_next();
-    const Plan p = make_plan(a, own, smem);
+    const Plan p = make_plan<kShrinkThreads, kRows>(a, own, smem);
     const int Q = a.parts * a.R;
     const int tq = (Q + kTallRanks - 1) / kTallRanks, lq = (Q + kLowRanks - 1) / kLowRanks;
     const int tall = p.n.tall * tq, units = tall + p.n.low * lq;
     const int slice = (a.K + kCluster * 8 - 1) / (kCluster * 8) * 8;
     const int k0 = (int)cluster_rank() * slice, k1 = min(a.K, k0 + slice);
     for (int u = blockIdx.x / kCluster; u < units; u += gridDim.x / kCluster) {
-        const bool is_tall = u < tall;
-        const int v = is_tall ? u : u - tall, per = is_tall ? tq : lq;
-        const Tile t = p.tiles[(is_tall ? 0 : p.n.tall) + v / per];
-        const uint16_t *order = p.order + t.first;
-        if (is_tall)
-            shrink_tall<kBf16>(a, order, t, v % per * kTallRanks, k0, k1, smem);
-        else
-            shrink_low<kBf16>(a, order, t, v % per * kLowRanks, k0, k1, smem);
+        if (!kFew && u < tall) {
+            const Tile t = p.tall(u / tq);
+            if constexpr (!kFew)
+                shrink_tall<kBf16>(a, p.order + t.first, t, u % tq * kTallRanks, k0, k1, smem, pr);
+        } else {
+            const int v = u - tall;
+            const Tile t = p.low(v / lq);
+            shrink_low<kBf16>(a, p.order + t.first, t, v % lq * kLowRanks, k0, k1, smem);
+        }
     }
+    if constexpr (!kFew) pr.end<kShrinkTmem>();
 }
 
 // ---------------------------------------------------------------------------
 // expand.  RK: 16s of rank that the kernel holds.
 // ---------------------------------------------------------------------------
-// bytes of a row of B in shared memory: an odd number of 32 bytes, so that rows next to each
-// other lie in other banks
+// bytes of a row of B in shared memory (low tiles): an odd number of 32 bytes, so that rows
+// next to each other lie in other banks
 constexpr int row_pitch(int RK) { return (RK | 1) * 32; }
-constexpr int tall_stages(int RK) { return RK == 1 ? 5 : RK == 2 ? 4 : RK == 4 ? 3 : 2; }
-constexpr int low_stages(int RK) { return 8 / RK; }
-constexpr int tall_stage(int RK) { return kTall * kTallCols * 2 + kTallCols * row_pitch(RK); }
-constexpr int low_stage(int RK) { return kLowCols * row_pitch(RK); }
-constexpr int max_of(int a, int b) { return a > b ? a : b; }
-constexpr int expand_smem(int RK) {
-    return max_of(max_of(tall_stages(RK) * tall_stage(RK), kWarps * low_stages(RK) * low_stage(RK)),
-                  (int)sizeof(RowSort));
+// Calls of few rows: two CTAs of 8 warps per SM, so small that shrink's CTAs fit beside them
+// and they start while it runs.  Others: one of 16 warps with all of the SM.
+constexpr int expand_threads(bool few) { return few ? 256 : 512; }
+constexpr int kResidualStage = kTall * kTallCols * 2;
+constexpr int blocks64(int RK) { return RK > 4 ? 2 : 1; }  // of 64 of the rank
+constexpr int b_stage(int RK) { return blocks64(RK) * kTallCols * 128; }
+constexpr int t_half(int RK) { return blocks64(RK) * kTall * 128; }
+constexpr int residual_stages(int RK) { return RK > 4 ? 2 : 4; }
+constexpr int b_stages(int RK) { return RK > 4 ? 2 : 3; }
+constexpr int low_residual = kLow * kLowCols * 2;
+constexpr int low_stage(int RK) { return kLowCols * row_pitch(RK) + low_residual; }
+constexpr int low_stages(int RK, bool few) {
+    return few ? (RK == 1 ? 4 : RK == 2 ? 2 : 1) : (RK == 1 ? 6 : RK == 2 ? 3 : RK == 4 ? 2 : 1);
+}
+constexpr int expand_smem(int RK, bool few) {
+    const int low = expand_threads(few) / 32 * low_stages(RK, few) * low_stage(RK);
+    return few ? max_of(low, (int)sizeof(RowSort<kFewRows>))
+               : 1024 + max_of(max_of(2 * t_half(RK) + residual_stages(RK) * kResidualStage +
+                                          b_stages(RK) * b_stage(RK),
+                                      low),
+                               (int)sizeof(RowSort<kLocalRows>));
 }
 
-__device__ __forceinline__ uint32_t pack16(float lo, float hi, bool bf16) {
-    return (uint32_t)float_to_half_bits(lo, bf16) | (uint32_t)float_to_half_bits(hi, bf16) << 16;
+// two values rounded to the 16-bit type (nearest even), and back
+template <bool kBf16>
+__device__ __forceinline__ uint32_t pack16(float lo, float hi) {
+    uint32_t d;
+    if constexpr (kBf16) asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
+    else asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
+    return d;
+}
+template <bool kBf16>
+__device__ __forceinline__ float2 unpack16(uint32_t v) {
+    if constexpr (kBf16)
+        return make_float2(__uint_as_float(v << 16), __uint_as_float(v & 0xffff0000u));
+    return __half22float2(*reinterpret_cast<const __half2 *>(&v));
+}
+// the power of two (its exponent field) that scales a row whose largest value is `most` to at
+// most 2; a row of zeros, or with an Inf, stays as it is
+__device__ __forceinline__ int row_exponent(float most) {
+    const int top = __float_as_uint(most) >> 23;
+    return top >= 255 || top == 0 ? 127 : min(max(top, 2), 252);
+}
+__device__ __forceinline__ float scale_down(int e) { return __uint_as_float((uint32_t)(254 - e) << 23); }
+__device__ __forceinline__ float scale_up(int e) { return __uint_as_float((uint32_t)e << 23); }
+// two values as the sum of two pairs of the 16-bit type
+template <bool kBf16>
+__device__ __forceinline__ void split(float x, float y, uint32_t &hi, uint32_t &lo) {
+    hi = pack16<kBf16>(x, y);
+    const float2 h = unpack16<kBf16>(hi);
+    lo = pack16<kBf16>(isfinite(h.x) ? x - h.x : 0.f, isfinite(h.y) ? y - h.y : 0.f);
 }
 
 // where column j of 32 lies among the rows of four 8-column MMA tiles so that a lane's
@@ -466,23 +633,13 @@ struct Rows {
                              fmaxf(fabsf(v[u][k].z), fabsf(v[u][k].w)));
             most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 1));
             most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 2));
-            // a row of zeros, or with an Inf, stays as it is
-            const int top = __float_as_uint(most) >> 23;
-            const int e = top >= 255 || top == 0 ? 127 : min(max(top, 2), 252);
-            const float down = __uint_as_float((uint32_t)(254 - e) << 23);  // 2^(127 - e)
-            factor[u] = __uint_as_float((uint32_t)e << 23) * scale;
+            const int e = row_exponent(most);
+            const float down = scale_down(e);
+            factor[u] = scale_up(e) * scale;
 #pragma unroll
             for (int k = 0; k < RK; ++k) {
-                const float w[4] = {v[u][k].x * down, v[u][k].y * down, v[u][k].z * down,
-                                    v[u][k].w * down};
-                float h[4], l[4];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    h[i] = half_bits_to_float(float_to_half_bits(w[i], kBf16), kBf16);
-                    l[i] = isfinite(h[i]) ? w[i] - h[i] : 0.f;
-                }
-                hi[k][u] = pack16(h[0], h[1], kBf16), hi[k][2 + u] = pack16(h[2], h[3], kBf16);
-                lo[k][u] = pack16(l[0], l[1], kBf16), lo[k][2 + u] = pack16(l[2], l[3], kBf16);
+                split<kBf16>(v[u][k].x * down, v[u][k].y * down, hi[k][u], lo[k][u]);
+                split<kBf16>(v[u][k].z * down, v[u][k].w * down, hi[k][2 + u], lo[k][2 + u]);
             }
         }
     }
@@ -536,144 +693,271 @@ template <bool kBf16>
 __device__ __forceinline__ uint4 add_cells(uint4 r, const float (&v)[8]) {
     uint32_t w[4] = {r.x, r.y, r.z, r.w};
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-        w[i] = pack16(half_bits_to_float((uint16_t)w[i], kBf16) + v[2 * i],
-                      half_bits_to_float((uint16_t)(w[i] >> 16), kBf16) + v[2 * i + 1], kBf16);
+    for (int i = 0; i < 4; ++i) {
+        const float2 f = unpack16<kBf16>(w[i]);
+        w[i] = pack16<kBf16>(f.x + v[2 * i], f.y + v[2 * i + 1]);
+    }
     return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// Rows without an adapter: columns n0 <= n < n1 of the residual, or zeros.
-template <bool kVec>
-__device__ void copy_rows(const LoraArgs &a, const uint16_t *order, const Tile &t, int n0, int n1) {
+// Rows without an adapter: those of `rows` from this CTA's share on, all columns of the
+// residual, or zeros.
+template <int kCta, bool kVec>
+__device__ void copy_rows(const LoraArgs &a, const uint16_t *rows, int n) {
     if (a.residual == a.y) return;
-    const int cells = (n1 - n0 + 7) / 8;
-    for (int i = threadIdx.x; i < t.count * cells; i += kThreads) {
-        const int r = i / cells, n = n0 + i % cells * 8;
-        const size_t at = (size_t)order[r] * a.N + n;
-        store_cells<kVec>(a.y + at, n1 - n,
-                          a.residual ? load_cells<kVec>(a.residual + at, n1 - n)
+    const int cells = (a.N + 7) / 8;
+    const long long all = (long long)n * cells;
+    for (long long i = (long long)blockIdx.x * kCta + threadIdx.x; i < all;
+         i += (long long)gridDim.x * kCta) {
+        const int r = (int)(i / cells), c = (int)(i - (long long)r * cells) * 8;
+        const size_t at = (size_t)rows[r] * a.N + c;
+        store_cells<kVec>(a.y + at, a.N - c,
+                          a.residual ? load_cells<kVec>(a.residual + at, a.N - c)
                                      : make_uint4(0, 0, 0, 0));
     }
 }
 
-// A tall tile, columns n0 <= n < n1 of a part: every warp 16 rows.  A stage is 64 columns of
-// B and (kVec) of the tile's residual.
+// A tall tile, columns n0 <= n < n1 of a part, 128 at a time: the products of a step are
+// issued a step ahead of its outputs.  The residual lies in the stage where the outputs
+// take its place, row by row, and leave in whole sectors.  (256 bytes of a row at a time:
+// with steps of 64 columns the same kernel ran at 2.8 TB/s, XX.)
 template <bool kBf16, int RK, bool kVec>
 __device__ void expand_tall(const LoraArgs &a, const uint16_t *order, const Tile &t, int part,
-                            int n0, int n1, uint8_t *smem) {
-    constexpr int kStages = tall_stages(RK), kBytes = tall_stage(RK), kRes = kTall * kTallCols * 2;
-    constexpr int kPieces = 2 * RK;  // of 16 bytes in a row of B
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, c = lane & 3;
+                            int n0, int n1, uint8_t *smem, Products &pr) {
+    constexpr int kCta = expand_threads(false), kRs = residual_stages(RK), kBs = b_stages(RK);
+    constexpr int kBlocks = blocks64(RK), kPieces = kBlocks * 8;  // of 16 bytes in a row of B
+    // a step's copies are two groups, residual and B: at a step's start B of the next and the
+    // residual of this one have to be there, and all younger groups may still be under way
+    constexpr int kPending = kBs > 2 ? 2 : 0;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int rank = rank_of(a, t.adapter), ksteps = (rank + 15) / 16;
-    const uint32_t base = smem_of(smem);
+    const uint32_t t_hi = smem_of(smem), t_lo = t_hi + t_half(RK), res0 = t_hi + 2 * t_half(RK),
+                   b0 = res0 + kRs * kResidualStage;
+    __shared__ float factor[kTall];
     const bool staged = kVec && a.residual;
     // this thread's 16 bytes of four rows of the residual, per stage
-    const int col = tid & 7, r0 = tid >> 3;
+    const int col = tid & 15, r0 = tid >> 4;
     const uint16_t *rp[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const int r = r0 + 32 * i;
-        rp[i] = staged && r < t.count ? a.residual + (size_t)order[r] * a.N + col * 8 : nullptr;
+        rp[i] = staged && r < t.count ? a.residual + (size_t)order[r] * a.N + n0 + col * 8 : nullptr;
     }
-    const uint16_t *b = a.b + (size_t)t.adapter * a.N * a.R;
-    auto issue = [&](int n, int stage) {
-        const uint32_t st = base + stage * kBytes;
+    const uint16_t *b = a.b + ((size_t)t.adapter * a.N + n0) * a.R;
+    const int steps = (n1 - n0 + kTallCols - 1) / kTallCols;
+    // where 8 columns c of a row of a residual stage lie: two halves of 64 columns
+    const auto cell = [](int r, int c) { return (uint32_t)(c >> 3) * (kTall * 128) + swizzled(r, c & 7); };
+    auto issue_b = [&](int s) {
+        const uint32_t st = b0 + s % kBs * b_stage(RK);
+        const int n = s * kTallCols;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int r = r0 + 32 * i, in = n + col * 8 < n1 ? 16 : 0;
-            if (rp[i])
-                copy16(st + (r << 7) + ((col ^ ((r & 1) << 2)) << 4), in ? rp[i] + n : a.residual,
-                       in);
-        }
-#pragma unroll
-        for (int i = 0; i < (kTallCols * kPieces + kThreads - 1) / kThreads; ++i) {
-            const int q = tid + i * kThreads, j = q / kPieces, r = q % kPieces * 8;
-            if (j >= kTallCols) break;
-            const int in = n + j < n1 ? max(0, min(2 * (rank - r), 16)) : 0;
-            copy16(st + kRes + ((j & ~31) + interleaved(j & 31)) * row_pitch(RK) + r * 2,
-                   in ? b + (size_t)(n + j) * a.R + r : a.b, in);
+        for (int i = 0; i < kTallCols * kPieces / kCta; ++i) {
+            const int q = tid + i * kCta, j = q / kPieces, c = q % kPieces;
+            if (c >= 2 * ksteps) continue;
+            const int in = n0 + n + j < n1 ? max(0, min(2 * (rank - c * 8), 16)) : 0;
+            copy16(st + (c >> 3) * kTallCols * 128 + swizzled(j, c & 7),
+                   in ? b + (size_t)(n + j) * a.R + c * 8 : a.b, in);
         }
     };
-    int next = n0;
+    auto issue_residual = [&](int s) {
+        const uint32_t st = res0 + s % kRs * kResidualStage;
+        const int n = s * kTallCols, in = n0 + n + col * 8 < n1 ? 16 : 0;
 #pragma unroll
-    for (int s = 0; s < kStages - 1; ++s, next += kTallCols) {
-        if (next < n1) issue(next, s);
+        for (int i = 0; i < 4; ++i)
+            if (rp[i]) copy16(st + cell(r0 + 32 * i, col), in ? rp[i] + n : a.residual, in);
+    };
+#pragma unroll
+    for (int s = 0; s < kBs; ++s) {
+        if (s < steps) issue_b(s);
         commit_copies();
     }
-    const int r[2] = {warp * 16 + g, warp * 16 + g + 8};
-    const int m[2] = {r[0] < t.count ? order[r[0]] : -1, r[1] < t.count ? order[r[1]] : -1};
-    const size_t at[2] = {(size_t)max(m[0], 0) * a.N, (size_t)max(m[1], 0) * a.N};
-    const float scale = a.scales[t.adapter];
-    Rows<kBf16, RK> rows;
-    wait_for_last();  // t
-    rows.load(a, m, part, rank, scale);
-    int stage = 0, free = kStages - 1;
-    for (int n = n0; n < n1; n += kTallCols, next += kTallCols) {
-        wait_copies<kStages - 2>();
-        __syncthreads();  // this stage is there, the one before is free
-        if (next < n1) issue(next, free);
+#pragma unroll
+    for (int s = 0; s < kRs - 1; ++s) {
+        if (s < steps) issue_residual(s);
         commit_copies();
-        const uint32_t st = base + stage * kBytes;
+    }
+    const float scale = a.scales[t.adapter];
+    wait_for_last();  // t
+    {
+        // four threads per row of t, a quarter of its part each
+        constexpr int kQuads = kBlocks * 4;
+        const int r = tid >> 2, quarter = tid & 3;
+        const bool mine = r < t.count;
+        const float *row = sums_of(a) + (mine ? (size_t)order[r] * a.parts * a.R + part * a.R : 0);
+        float4 v[kQuads];
+        float most = 0.f;  // (a NaN does not count)
 #pragma unroll
-        for (int s = 0; s < kTallCols / 32; ++s) {
-            float v[2][8];
-            rows.product(v, st + kRes + s * 32 * row_pitch(RK), ksteps);
-            const int cc = n + s * 32 + c * 8;
+        for (int i = 0; i < kQuads; ++i) {
+            const int k = (quarter * kQuads + i) * 4, left = mine ? rank - k : 0;
+            v[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (left > 0) v[i] = __ldcg(reinterpret_cast<const float4 *>(row + k));
+            if (left < 4) v[i].w = 0.f;
+            if (left < 3) v[i].z = 0.f;
+            if (left < 2) v[i].y = 0.f;
+        }
 #pragma unroll
-            for (int u = 0; u < 2; ++u) {
-                const int cells = m[u] >= 0 ? n1 - cc : 0;
-                uint4 res = make_uint4(0, 0, 0, 0);
-                if (staged)
-                    res = lds128(st + (r[u] << 7) + (((s * 4 + c) ^ ((r[u] & 1) << 2)) << 4));
-                else if (a.residual)
-                    res = load_cells<kVec>(a.residual + at[u] + cc, cells);
-                store_cells<kVec>(a.y + at[u] + cc, cells, add_cells<kBf16>(res, v[u]));
+        for (int i = 0; i < kQuads; ++i)
+            most = fmaxf(fmaxf(most, fmaxf(fabsf(v[i].x), fabsf(v[i].y))),
+                         fmaxf(fabsf(v[i].z), fabsf(v[i].w)));
+        most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 1));
+        most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 2));
+        const int e = row_exponent(most);
+        const float down = scale_down(e);
+        if (quarter == 0) factor[r] = scale_up(e) * scale;
+#pragma unroll
+        for (int i = 0; i < kQuads; i += 2) {
+            uint32_t h[4], l[4];
+            split<kBf16>(v[i].x * down, v[i].y * down, h[0], l[0]);
+            split<kBf16>(v[i].z * down, v[i].w * down, h[1], l[1]);
+            split<kBf16>(v[i + 1].x * down, v[i + 1].y * down, h[2], l[2]);
+            split<kBf16>(v[i + 1].z * down, v[i + 1].w * down, h[3], l[3]);
+            const int c = (quarter * kQuads + i) / 2;  // piece of 8
+            const uint32_t at = (c >> 3) * kTall * 128 + swizzled(r, c & 7);
+            sts128(t_hi + at, make_uint4(h[0], h[1], h[2], h[3]));
+            sts128(t_lo + at, make_uint4(l[0], l[1], l[2], l[3]));
+        }
+    }
+    const uint32_t idesc = product_desc<kBf16>(kTallCols);
+    auto products = [&](int s) {  // thread 0
+        dev::tc_fence_after();
+        const uint32_t st = b0 + s % kBs * b_stage(RK);
+        const uint32_t d = pr.tmem + ((pr.count + s) & 1) * kTallCols;
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+            for (int k = 0; k < ksteps; ++k)
+                product16(d,
+                          dev::smem_desc_sw128((h ? t_lo : t_hi) + (k >> 2) * kTall * 128) +
+                              2 * (k & 3),
+                          dev::smem_desc_sw128(st + (k >> 2) * kTallCols * 128) + 2 * (k & 3), idesc,
+                          h + k > 0);
+        pr.commit(pr.count + s, 2);
+    };
+    // outputs: a warp's 32 rows (its quarter of the tensor memory's lanes) and 32 columns;
+    // out[i]: where row i * 8 + lane / 4 of them lies in y
+    const int quarter = (warp & 3) * 32, side = (warp >> 2) * 32;
+    const int mine = quarter + lane;
+    size_t out[4];
+    bool there[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int r = quarter + i * 8 + (lane >> 2);
+        there[i] = r < t.count;
+        out[i] = (there[i] ? (size_t)order[r] * a.N : 0) + n0;
+    }
+    wait_copies<kBs - 1 + kRs - 1>();  // the first step's B
+    dev::fence_async_shared();
+    __syncthreads();
+    const float f = factor[mine];
+    if (tid == 0) products(0);
+    for (int s = 0; s < steps; ++s) {
+        wait_copies<kPending>();
+        dev::fence_async_shared();
+        __syncthreads();
+        if (tid == 0 && s + 1 < steps) products(s + 1);
+        if (s + kRs - 1 < steps) issue_residual(s + kRs - 1);
+        commit_copies();
+        const uint32_t st = res0 + s % kRs * kResidualStage;
+        const int n = s * kTallCols + side, left = n1 - n0 - n;
+        if constexpr (!kVec) {
+            if (a.residual)
+#pragma unroll 8
+                for (int i = 0; i < 32; ++i) {
+                    const int r = quarter + i;
+                    uint16_t v = 0;
+                    if (r < t.count && lane < left)
+                        v = a.residual[(size_t)order[r] * a.N + n0 + n + lane];
+                    sts16(st + cell(r, (side + lane) >> 3) + (lane & 7) * 2, v);
+                }
+            __syncwarp();
+        }
+        pr.wait(pr.count + s, 2);
+        dev::tc_fence_after();
+        // this step's products are done: its B makes room
+        if (s + kBs < steps) issue_b(s + kBs);
+        commit_copies();
+        uint32_t v[32];
+        dev::tmem_ld(pr.tmem + ((pr.count + s) & 1) * kTallCols + ((uint32_t)quarter << 16) + side,
+                     v);
+        dev::tmem_wait_ld(v);
+        dev::tc_fence_before();
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const uint32_t at = st + cell(mine, (side >> 3) + i);
+            const uint4 r = a.residual ? lds128(at) : make_uint4(0, 0, 0, 0);
+            float w[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) w[j] = __uint_as_float(v[8 * i + j]) * f;
+            sts128(at, add_cells<kBf16>(r, w));
+        }
+        __syncwarp();
+        if constexpr (kVec) {
+            const int c = lane & 3;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const uint4 w = lds128(st + cell(quarter + i * 8 + (lane >> 2), (side >> 3) + c));
+                if (there[i] && c * 8 < left)
+                    *reinterpret_cast<uint4 *>(a.y + out[i] + n + c * 8) = w;
+            }
+        } else {
+#pragma unroll 8
+            for (int i = 0; i < 32; ++i) {
+                const int r = quarter + i;
+                const uint16_t w = lds16(st + cell(r, (side + lane) >> 3) + (lane & 7) * 2);
+                if (r < t.count && lane < left)
+                    a.y[(size_t)order[r] * a.N + n0 + n + lane] = w;
             }
         }
-        free = stage;
-        stage = stage == kStages - 1 ? 0 : stage + 1;
     }
+    pr.count += steps;
     wait_copies<0>();
     __syncthreads();  // what comes next fills the same memory
 }
 
 // A low tile, columns n0 <= n < n1 of a part: every warp 32 of them in turn, with a ring of
-// its own for B.
-template <bool kBf16, int RK, bool kVec>
+// its own for B and (kVec) the residual.
+template <bool kBf16, int RK, bool kVec, bool kFew>
 __device__ void expand_low(const LoraArgs &a, const uint16_t *order, const Tile &t, int part,
                            int n0, int n1, uint8_t *smem) {
-    constexpr int kStages = low_stages(RK), kBytes = low_stage(RK), kPieces = 2 * RK;
+    constexpr int kStages = low_stages(RK, kFew), kBytes = low_stage(RK), kPieces = 2 * RK;
+    constexpr int kStride = expand_threads(kFew) / 32 * kLowCols;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, c = lane & 3;
     const int rank = rank_of(a, t.adapter), ksteps = (rank + 15) / 16;
     const uint32_t base = smem_of(smem) + warp * kStages * kBytes;
     const uint16_t *b = a.b + (size_t)t.adapter * a.N * a.R;
+    const bool staged = kVec && a.residual;
+    const int m[2] = {g < t.count ? order[g] : -1, g + 8 < t.count ? order[g + 8] : -1};
+    const size_t at[2] = {(size_t)max(m[0], 0) * a.N + c * 8, (size_t)max(m[1], 0) * a.N + c * 8};
     auto issue = [&](int n, int stage) {
+        const uint32_t st = base + stage * kBytes;
 #pragma unroll
         for (int i = 0; i < kPieces; ++i) {
             const int q = lane + i * 32, j = q / kPieces, r = q % kPieces * 8;
             const int in = n + j < n1 ? max(0, min(2 * (rank - r), 16)) : 0;
-            copy16(base + stage * kBytes + interleaved(j) * row_pitch(RK) + r * 2,
+            copy16(st + interleaved(j) * row_pitch(RK) + r * 2,
                    in ? b + (size_t)(n + j) * a.R + r : a.b, in);
         }
+        if (staged)
+#pragma unroll
+            for (int u = 0; u < 2; ++u)
+                if (m[u] >= 0 && n + c * 8 < n1)
+                    copy16(st + kLowCols * row_pitch(RK) + (u * 8 + g) * (kLowCols * 2) + c * 16,
+                           a.residual + at[u] + n, 16);
     };
-    constexpr int kStride = kWarps * kLowCols;
     int n = n0 + warp * kLowCols, next = n;
 #pragma unroll
     for (int s = 0; s < kStages; ++s, next += kStride) {
         if (next < n1) issue(next, s);
         commit_copies();
     }
-    const int m[2] = {g < t.count ? order[g] : -1, g + 8 < t.count ? order[g + 8] : -1};
-    const size_t at[2] = {(size_t)max(m[0], 0) * a.N + c * 8, (size_t)max(m[1], 0) * a.N + c * 8};
     uint4 res[2];
-    auto fetch = [&](int n) {
+    auto fetch = [&](int n) {  // the residual from memory, a step ahead
 #pragma unroll
         for (int u = 0; u < 2; ++u)
             res[u] = a.residual && n < n1 && m[u] >= 0
                          ? load_cells<kVec>(a.residual + at[u] + n, n1 - n - c * 8)
                          : make_uint4(0, 0, 0, 0);
     };
-    fetch(n);
+    if constexpr (!kVec) fetch(n);
     const float scale = a.scales[t.adapter];
     Rows<kBf16, RK> rows;
     wait_for_last();  // t
@@ -681,16 +965,23 @@ __device__ void expand_low(const LoraArgs &a, const uint16_t *order, const Tile 
     for (int stage = 0; n < n1; n += kStride, next += kStride) {
         wait_copies<kStages - 1>();
         __syncwarp();
+        const uint32_t st = base + stage * kBytes;
         float v[2][8];
-        rows.product(v, base + stage * kBytes, ksteps);
+        rows.product(v, st, ksteps);
         uint4 out[2];
 #pragma unroll
-        for (int u = 0; u < 2; ++u) out[u] = add_cells<kBf16>(res[u], v[u]);
+        for (int u = 0; u < 2; ++u) {
+            if constexpr (kVec)
+                res[u] = staged ? lds128(st + kLowCols * row_pitch(RK) +
+                                         (u * 8 + g) * (kLowCols * 2) + c * 16)
+                                : make_uint4(0, 0, 0, 0);
+            out[u] = add_cells<kBf16>(res[u], v[u]);
+        }
         __syncwarp();  // all lanes have read the stage
         if (next < n1) issue(next, stage);
         commit_copies();
         stage = stage == kStages - 1 ? 0 : stage + 1;
-        fetch(n + kStride);
+        if constexpr (!kVec) fetch(n + kStride);
 #pragma unroll
         for (int u = 0; u < 2; ++u)
             store_cells<kVec>(a.y + at[u] + n, m[u] >= 0 ? n1 - n - c * 8 : 0, out[u]);
@@ -699,75 +990,74 @@ __device__ void expand_low(const LoraArgs &a, const uint16_t *order, const Tile 
     __syncthreads();  // what comes next fills the same memory
 }
 
-// The steps from, .. , to - 1 of (tile, part, step of `cols` columns), in runs of one tile and part
+// This CTA's share of `tiles` tiles' steps of `cols` columns, the parts' steps in turn: equal
+// runs of the sequence, each piece of one tile and part to `run`
 template <typename Run>
-__device__ __forceinline__ void walk(const LoraArgs &a, int cols, long long from, long long to,
-                                     Run run) {
+__device__ __forceinline__ void walk(const LoraArgs &a, int cols, int tiles, Run run) {
     int per = 0;
     for (int i = 0; i < a.parts; ++i) per += (a.part[i] + cols - 1) / cols;
+    const int G = gridDim.x, i = blockIdx.x, all = tiles * per;
+    int from = all / G * i + min(i, all % G);
+    const int to = from + all / G + (i < all % G);
+    int tile = from / per, s = from - tile * per;
     while (from < to) {
-        const int tile = (int)(from / per);
-        int s = (int)(from - (long long)tile * per), part = 0, first = 0, steps;
+        int part = 0, first = 0, steps, at = s;
         for (;; ++part) {
             steps = (a.part[part] + cols - 1) / cols;
-            if (s < steps) break;
-            s -= steps;
+            if (at < steps) break;
+            at -= steps;
             first += a.part[part];
         }
-        const int n = (int)min((long long)(steps - s), to - from);
-        run(tile, part, first + s * cols, min(first + (s + n) * cols, first + a.part[part]));
-        from += n;
+        const int n = min(steps - at, to - from);
+        run(tile, part, first + at * cols, min(first + (at + n) * cols, first + a.part[part]));
+        from += n, s += n;
+        if (s == per) ++tile, s = 0;
     }
 }
 
-template <bool kBf16, int RK, bool kVec>
-__global__ void __launch_bounds__(kThreads, RK == 8 ? 1 : 2) expand_kernel(LoraArgs a) {
-    extern __shared__ __align__(128) uint8_t smem[];
-    __shared__ LocalPlan own;
+template <bool kBf16, int RK, bool kVec, bool kFew>
+__global__ void __launch_bounds__(expand_threads(kFew), kFew ? 2 : 1) expand_kernel(LoraArgs a) {
+    constexpr int kCta = expand_threads(kFew), kRows = kFew ? kFewRows : kLocalRows;
+    extern __shared__ __align__(128) uint8_t smem_raw[];
+    uint8_t *smem = kFew ? smem_raw : align1024(smem_raw);
+    __shared__ LocalPlan<kRows> own;
+    __shared__ ProductSpace space;
+    Products pr;
+    if constexpr (!kFew) pr.begin<kExpandTmem>(&space, a.status);
     launch_next();
     // shrink has let this kernel start after all that came before shrink had ended: the plan,
     // B and the residual may be read before shrink's own results
-    const Plan p = make_plan(a, own, smem);
-    int tall_steps = 0, low_steps = 0;
-    for (int i = 0; i < a.parts; ++i) {
-        tall_steps += (a.part[i] + kTallCols - 1) / kTallCols;
-        low_steps += (a.part[i] + kLowCols - 1) / kLowCols;
-    }
-    const auto share = [&](long long steps, int i) { return steps * i / (int)gridDim.x; };
-    const long long tall = (long long)(p.n.tall + p.n.none) * tall_steps,
-                    low = (long long)p.n.low * low_steps;
-    walk(a, kTallCols, share(tall, blockIdx.x), share(tall, blockIdx.x + 1),
-         [&](int tile, int part, int n0, int n1) {
-             const Tile t = p.tiles[tile < p.n.tall ? tile : tile + p.n.low];
-             if (t.adapter == a.L)
-                 copy_rows<kVec>(a, p.order + t.first, t, n0, n1);
-             else
-                 expand_tall<kBf16, RK, kVec>(a, p.order + t.first, t, part, n0, n1, smem);
-         });
-    walk(a, kLowCols, share(low, blockIdx.x), share(low, blockIdx.x + 1),
-         [&](int tile, int part, int n0, int n1) {
-             const Tile t = p.tiles[p.n.tall + tile];
-             expand_low<kBf16, RK, kVec>(a, p.order + t.first, t, part, n0, n1, smem);
-         });
+    const Plan p = make_plan<kCta, kRows>(a, own, smem);
+    if constexpr (!kFew)
+        walk(a, kTallCols, p.n.tall, [&](int tile, int part, int n0, int n1) {
+            const Tile t = p.tall(tile);
+            expand_tall<kBf16, RK, kVec>(a, p.order + t.first, t, part, n0, n1, smem, pr);
+        });
+    walk(a, kLowCols, p.n.low, [&](int tile, int part, int n0, int n1) {
+        const Tile t = p.low(tile);
+        expand_low<kBf16, RK, kVec, kFew>(a, p.order + t.first, t, part, n0, n1, smem);
+    });
+    copy_rows<kCta, kVec>(a, p.order + p.n.rows, p.n.none);
     wait_for_last();  // (for those without a step: what follows this kernel waits for it alone)
+    if constexpr (!kFew) pr.end<kExpandTmem>();
 }
 
-template <bool kBf16, int RK, bool kVec>
+template <bool kBf16, int RK, bool kVec, bool kFew>
 cudaError_t launch_expand(const LoraArgs &a, const DeviceInfo &dev, cudaStream_t stream) {
-    return launch_chained(expand_kernel<kBf16, RK, kVec>, dim3((RK == 8 ? 1 : 2) * dev.sm_count),
-                          kThreads, expand_smem(RK), 1, stream, a);
+    return launch_chained(expand_kernel<kBf16, RK, kVec, kFew>, dim3((kFew ? 2 : 1) * dev.sm_count),
+                          expand_threads(kFew), expand_smem(RK, kFew), 1, stream, a);
 }
-template <bool kBf16, bool kVec>
+template <bool kBf16, bool kVec, bool kFew>
 cudaError_t launch_expand_rank(const LoraArgs &a, const DeviceInfo &dev, cudaStream_t stream) {
-    if (a.R <= 16) return launch_expand<kBf16, 1, kVec>(a, dev, stream);
-    if (a.R <= 32) return launch_expand<kBf16, 2, kVec>(a, dev, stream);
-    if (a.R <= 64) return launch_expand<kBf16, 4, kVec>(a, dev, stream);
-    return launch_expand<kBf16, 8, kVec>(a, dev, stream);
+    if (a.R <= 16) return launch_expand<kBf16, 1, kVec, kFew>(a, dev, stream);
+    if (a.R <= 32) return launch_expand<kBf16, 2, kVec, kFew>(a, dev, stream);
+    if (a.R <= 64) return launch_expand<kBf16, 4, kVec, kFew>(a, dev, stream);
+    return launch_expand<kBf16, 8, kVec, kFew>(a, dev, stream);
 }
 
-template <bool kBf16>
-cudaError_t launch_type(const LoraArgs &a, bool vec, const DeviceInfo &dev, cudaStream_t stream) {
-    if (a.M > kMaxRows) {
+template <bool kBf16, bool kFew>
+cudaError_t launch_calls(const LoraArgs &a, bool vec, const DeviceInfo &dev, cudaStream_t stream) {
+    if (a.M > kLocalRows) {
         const cudaError_t e = launch_chained(plan_kernel, dim3(1), kPlanThreads, 0, 1, stream, a);
         if (e != cudaSuccess) return e;
     }
@@ -776,33 +1066,32 @@ cudaError_t launch_type(const LoraArgs &a, bool vec, const DeviceInfo &dev, cuda
                             ((a.parts * a.R + kLowRanks - 1) / kLowRanks);
     const int most = 2 * dev.sm_count / kCluster;
     const int clusters = units < most ? (int)units : most;
-    const cudaError_t e = launch_chained(shrink_kernel<kBf16>, dim3(clusters * kCluster), kThreads,
-                                         kShrinkSmem, kCluster, stream, a);
+    const cudaError_t e =
+        launch_chained(shrink_kernel<kBf16, kFew>, dim3(clusters * kCluster), kShrinkThreads,
+                       shrink_smem<kFew>(), kCluster, stream, a);
     if (e != cudaSuccess) return e;
-    return vec ? launch_expand_rank<kBf16, true>(a, dev, stream)
-               : launch_expand_rank<kBf16, false>(a, dev, stream);
+    return vec ? launch_expand_rank<kBf16, true, kFew>(a, dev, stream)
+               : launch_expand_rank<kBf16, false, kFew>(a, dev, stream);
 }
 
-template <bool kBf16, int RK>
+cudaError_t set_smem(const void *kernel, int bytes) {
+    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+}
+template <bool kBf16, bool kFew, int RK>
 cudaError_t init_expand() {
-    const void *kernels[] = {(const void *)expand_kernel<kBf16, RK, true>,
-                             (const void *)expand_kernel<kBf16, RK, false>};
-    for (const void *k : kernels) {
-        cudaError_t e =
-            cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, expand_smem(RK));
-        if (e != cudaSuccess) return e;
-    }
-    return cudaSuccess;
+    const cudaError_t e =
+        set_smem((const void *)expand_kernel<kBf16, RK, true, kFew>, expand_smem(RK, kFew));
+    return e != cudaSuccess ? e
+                            : set_smem((const void *)expand_kernel<kBf16, RK, false, kFew>,
+                                       expand_smem(RK, kFew));
 }
-
-template <bool kBf16>
-cudaError_t init_type() {
-    cudaError_t e = cudaFuncSetAttribute((const void *)shrink_kernel<kBf16>,
-                                         cudaFuncAttributeMaxDynamicSharedMemorySize, kShrinkSmem);
-    if (e == cudaSuccess) e = init_expand<kBf16, 1>();
-    if (e == cudaSuccess) e = init_expand<kBf16, 2>();
-    if (e == cudaSuccess) e = init_expand<kBf16, 4>();
-    if (e == cudaSuccess) e = init_expand<kBf16, 8>();
+template <bool kBf16, bool kFew>
+cudaError_t init_calls() {
+    cudaError_t e = set_smem((const void *)shrink_kernel<kBf16, kFew>, shrink_smem<kFew>());
+    if (e == cudaSuccess) e = init_expand<kBf16, kFew, 1>();
+    if (e == cudaSuccess) e = init_expand<kBf16, kFew, 2>();
+    if (e == cudaSuccess) e = init_expand<kBf16, kFew, 4>();
+    if (e == cudaSuccess) e = init_expand<kBf16, kFew, 8>();
     return e;
 }
 
@@ -812,12 +1101,19 @@ cudaError_t launch_lora(const LoraArgs &a, bool bf16, const DeviceInfo &dev, cud
     // 16-byte accesses of y and the residual
     bool vec = a.N % 8 == 0 && ((uintptr_t)a.y & 15) == 0 && ((uintptr_t)a.residual & 15) == 0;
     for (int i = 0; i < a.parts; ++i) vec = vec && a.part[i] % 8 == 0;
-    return bf16 ? launch_type<true>(a, vec, dev, stream) : launch_type<false>(a, vec, dev, stream);
+    if (a.M <= kFewRows)
+        return bf16 ? launch_calls<true, true>(a, vec, dev, stream)
+                    : launch_calls<false, true>(a, vec, dev, stream);
+    return bf16 ? launch_calls<true, false>(a, vec, dev, stream)
+                : launch_calls<false, false>(a, vec, dev, stream);
 }
 
 cudaError_t lora_init() {
-    const cudaError_t e = init_type<true>();
-    return e == cudaSuccess ? init_type<false>() : e;
+    cudaError_t e = init_calls<true, true>();
+    if (e == cudaSuccess) e = init_calls<true, false>();
+    if (e == cudaSuccess) e = init_calls<false, true>();
+    if (e == cudaSuccess) e = init_calls<false, false>();
+    return e;
 }
 
 }  // namespace w4a16

@@ -7,9 +7,6 @@
 namespace w4a16 {
 namespace routed {
 
-constexpr int kThreads = 256;
-constexpr int kWarps = kThreads / 32;
-
 __device__ __forceinline__ uint32_t smem_of(const void *p) {
     return (uint32_t)__cvta_generic_to_shared(p);
 }
@@ -32,12 +29,26 @@ __device__ __forceinline__ uint4 lds128(uint32_t p) {
     uint4 v;
     asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
                  : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-                 : "r"(p));
+                 : "r"(p)
+                 : "memory");
     return v;
+}
+__device__ __forceinline__ void sts128(uint32_t p, uint4 v) {
+    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(p), "r"(v.x), "r"(v.y), "r"(v.z),
+                 "r"(v.w)
+                 : "memory");
+}
+__device__ __forceinline__ uint16_t lds16(uint32_t p) {
+    uint16_t v;
+    asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(p) : "memory");
+    return v;
+}
+__device__ __forceinline__ void sts16(uint32_t p, uint16_t v) {
+    asm volatile("st.shared.u16 [%0], %1;" ::"r"(p), "h"(v) : "memory");
 }
 __device__ __forceinline__ uint2 lds64(uint32_t p) {
     uint2 v;
-    asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(p));
+    asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(p) : "memory");
     return v;
 }
 template <bool kBf16>
@@ -62,31 +73,61 @@ __device__ __forceinline__ void wait_for_last() {
     asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
-// ---- up to 1024 rows by bin, in one CTA of kThreads ---------------------------
-constexpr int kMaxRows = 1024;
+// ---- rows by bin, in one CTA ------------------------------------------------------
 constexpr int kMaxBins = 1025;
-constexpr int kBinsPerThread = (kMaxBins + kThreads - 1) / kThreads;
+template <int kRows>
 struct RowSort {  // space that is free again afterwards
-    uint16_t bin[kMaxRows];
-    uint8_t rank[kMaxRows];                       // among the equal bins of the row's 32
-    uint16_t before[kMaxBins];                    // rows of lower bins
-    unsigned sums[kWarps];
-    uint16_t count[kMaxRows / 32 * kMaxBins];     // [32 rows][bin]
+    uint16_t bin[kRows];
+    uint8_t rank[kRows];                    // among the equal bins of the row's 32
+    uint16_t before[kMaxBins + 1];          // rows of lower bins
+    unsigned sums[32];
+    uint16_t count[kRows / 32 * kMaxBins + 1];  // [32 rows][bin]
 };
 
-// order: the rows s < n by bin_of(s) in [0, bins), stable, those outside left out.
-// pack(bin, n) is a bin's n rows in its low 11 bits and counts of what the caller cuts
-// them into above; emit(bin, n, at, total) gets the sums of the packs of the lower bins and of
-// all.  Returns the latter.
-template <typename BinOf, typename Pack, typename Emit>
-__device__ unsigned group_rows(RowSort &sp, uint16_t *order, int n, int bins, BinOf bin_of,
-                               Pack pack, Emit emit) {
+// order: the rows s < n (n <= kRows) by bin_of(s) in [0, bins), stable, those outside left
+// out.  pack(bin, n) is a bin's n rows in its low 11 bits and counts of what the caller cuts
+// them into above; emit(bin, n, at) gets each bin that has rows and the sum of the packs of
+// the lower ones, done(total) the sum of all, before the last emit or after.  Up to 32 rows
+// are one warp's work.  (1.5 us from the ids' arrival for 512 rows and 128 bins.)
+template <int kCta, int kRows, typename BinOf, typename Pack, typename Emit, typename Done>
+__device__ void group_rows(RowSort<kRows> &sp, uint16_t *order, int n, int bins, BinOf bin_of,
+                           Pack pack, Emit emit, Done done) {
+    constexpr int kCtaWarps = kCta / 32;
+    constexpr int kBinsPerThread = (kMaxBins + kCta - 1) / kCta;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    if (n <= 32) {
+        if (warp == 0) {
+            int b = lane < n ? bin_of(lane) : -1;
+            if ((unsigned)b >= (unsigned)bins) b = bins;  // sorts behind all
+            int place = 0, rows = 0;
+            bool first = true;
+            for (int j = 0; j < n; ++j) {
+                const int o = __shfl_sync(0xffffffffu, b, j);
+                place += o < b || (o == b && j < lane);
+                rows += o == b;
+                first = first && !(o == b && j < lane);
+            }
+            const bool lead = first && b < bins && lane < n;
+            const unsigned own = lead ? pack(b, rows) : 0u;
+            unsigned at = 0, total = 0;
+            for (int j = 0; j < n; ++j) {
+                const int o = __shfl_sync(0xffffffffu, b, j);
+                const unsigned v = __shfl_sync(0xffffffffu, own, j);
+                at += o < b ? v : 0u;
+                total += v;
+            }
+            if (b < bins) order[place] = (uint16_t)lane;
+            if (lead) emit(b, rows, at);
+            if (lane == 0) done(total);
+        }
+        __syncthreads();
+        return;
+    }
     const int chunks = (n + 31) / 32;
-    for (int i = tid; i < (chunks * bins + 1) / 2; i += kThreads)
+    for (int i = tid; i < (chunks * bins + 1) / 2; i += kCta)
         reinterpret_cast<uint32_t *>(sp.count)[i] = 0;
     __syncthreads();
-    for (int c = warp; c < chunks; c += kWarps) {
+    for (int c = warp; c < chunks; c += kCtaWarps) {
         const int s = c * 32 + lane;
         int b = s < n ? bin_of(s) : -1;
         if ((unsigned)b >= (unsigned)bins) b = -1;
@@ -101,7 +142,7 @@ __device__ unsigned group_rows(RowSort &sp, uint16_t *order, int n, int bins, Bi
     // them, and the bins' packs are added up over the threads
     int rows[kBinsPerThread];
     unsigned own = 0;
-    const int per = (bins + kThreads - 1) / kThreads;
+    const int per = (bins + kCta - 1) / kCta;
 #pragma unroll
     for (int i = 0; i < kBinsPerThread; ++i) {
         const int b = per * tid + i;
@@ -125,27 +166,28 @@ __device__ unsigned group_rows(RowSort &sp, uint16_t *order, int n, int bins, Bi
     __syncthreads();
     unsigned at = incl - own, total = 0;
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
+    for (int w = 0; w < kCtaWarps; ++w) {
         const unsigned v = sp.sums[w];
         if (w < warp) at += v;
         total += v;
     }
+    if (tid == 0) done(total);
 #pragma unroll
     for (int i = 0; i < kBinsPerThread; ++i) {
         const int b = per * tid + i;
         if (i < per && b < bins) {
             sp.before[b] = (uint16_t)(at & 2047);
-            emit(b, rows[i], at, total);
+            if (rows[i] > 0) emit(b, rows[i], at);
             at += pack(b, rows[i]);
         }
     }
     __syncthreads();
-    for (int s = tid; s < n; s += kThreads) {
+    for (int s = tid; s < n; s += kCta) {
         const int b = sp.bin[s];
-        if (b != 0xffff) order[sp.before[b] + sp.count[s / 32 * bins + b] + sp.rank[s]] = (uint16_t)s;
+        if (b != 0xffff)
+            order[sp.before[b] + sp.count[s / 32 * bins + b] + sp.rank[s]] = (uint16_t)s;
     }
     __syncthreads();
-    return total;
 }
 
 template <typename... Params, typename... Args>
