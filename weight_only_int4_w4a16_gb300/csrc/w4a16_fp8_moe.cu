@@ -25,7 +25,8 @@
 //
 // Every CTA groups the slots itself (a stable counting sort in shared memory), which
 // costs it no launch and no pass through memory.
-#include <cstdlib>
+#include <math.h>
+
 #include "w4a16_routed.cuh"
 
 namespace w4a16 {
@@ -59,8 +60,10 @@ struct Tables {
     int tiles;
 };
 using Sort = RowSort<kFp8MoeMaxSlots>;
+// slots of a tile: 8 NT, fewer where a stage of KS blocks leaves no room for them
+template <int NT, int KS>
+constexpr int kCap = 8 * NT * KS <= 32 ? 8 * NT : 32 / KS;
 static_assert(kMaxMoeExperts <= kMaxBins && sizeof(Sort) <= kRingBytes, "the sort fits the ring");
-static_assert(kStages * (kStageWeights + 32 * 256 + 128) <= kRingBytes, "cap * KS <= 32 fits");
 
 // The slots by expert, in tiles of up to cap slots; how many tiles.  An id outside [0, E)
 // leaves its slot out; one other than -1 is reported.
@@ -88,7 +91,7 @@ __device__ int make_tiles(Tables &tb, Sort &sp, const int32_t *ids, int S, int E
 }
 
 // kSilu: gate and up, x by token, h by slot; else down, h by slot, o (fp32) by slot
-template <bool kBf16, int NT, bool kSilu>
+template <bool kBf16, int NT, int KS, bool kSilu>
 __global__ void __launch_bounds__(kThreads, 2) experts_kernel(Fp8ExpertsArgs a) {
     extern __shared__ __align__(128) uint8_t ring[];
     __shared__ Tables tb;
@@ -102,32 +105,21 @@ __global__ void __launch_bounds__(kThreads, 2) experts_kernel(Fp8ExpertsArgs a) 
     const int n_tiles = make_tiles(tb, *reinterpret_cast<Sort *>(ring), a.ids, S, a.E, cap,
                                    kSilu ? a.status : nullptr);
 
-    // the split of a stage's blocks among the warps: the fewest bytes on the busiest CTA,
-    // 8 KB being what a unit costs beside its own
-    int ks_log, units;
-    {
-        const int l = lane & 3, per = (kSilu ? 64 : 128) >> l;  // a lane for each
-        const int n = n_tiles * ((a.rows + per - 1) / per);
-        float cost = (float)((n + gridDim.x - 1) / gridDim.x) *
-                     ((float)(128 >> l) * a.K + 2.f * min(cap, 4) * a.K + 8192.f);
-        if (cap << l > 32) cost = INFINITY;  // more than the ring's stages hold
-        float best = fminf(cost, __shfl_xor_sync(0xffffffffu, cost, 1));
-        best = fminf(best, __shfl_xor_sync(0xffffffffu, best, 2));
-        ks_log = __ffs(__ballot_sync(0xffffffffu, cost == best)) - 1;
-        units = __shfl_sync(0xffffffffu, n, ks_log);
-    }
-    const int KS = 1 << ks_log, per = (kSilu ? 64 : 128) >> ks_log;
-    const int blocks = (a.rows + per - 1) / per;
+    constexpr int ks_log = KS == 8 ? 3 : KS == 4 ? 2 : KS == 2 ? 1 : 0;
+    constexpr int per = (kSilu ? 64 : 128) / KS;  // rows of results of a unit
+    constexpr int x_bytes = kCap<NT, KS> * 256 * KS, stage_bytes = kStageWeights + x_bytes + 128;
+    static_assert(kStages * stage_bytes <= kRingBytes, "the stages fit the ring");
+    const int blocks = (a.rows + per - 1) / per, units = n_tiles * blocks;
     const int ksteps = (a.K + 128 * KS - 1) / (128 * KS);
     const int mine = blockIdx.x < units ? (units - 1 - (int)blockIdx.x) / (int)gridDim.x + 1 : 0;
     const int steps = mine * ksteps;
-    const int x_bytes = cap * 256 * KS, stage_bytes = kStageWeights + x_bytes + 128;
     const uint32_t ring0 = smem_of(ring);
     const int Gk = (a.K + kGroup - 1) / kGroup;
 
     // Copies walk the units' stages in order.  Per unit each thread keeps where its 16-byte
-    // pieces of weights (four), activations (at most two) and its scale come from.
-    constexpr int kW = kStageWeights / 16 / kThreads, kX = 2;
+    // pieces of weights (four), activations (kX) and its scale come from.
+    constexpr int kW = kStageWeights / 16 / kThreads;
+    constexpr int kX = (kCap<NT, KS> * 16 * KS + kThreads - 1) / kThreads;
     const int wc = tid & (8 * KS - 1), wr = tid >> (3 + ks_log);     // piece of a row, row
     const int xc = tid & (16 * KS - 1), xr = tid >> (4 + ks_log);
     struct Cursor {
@@ -136,12 +128,11 @@ __global__ void __launch_bounds__(kThreads, 2) experts_kernel(Fp8ExpertsArgs a) 
     const uint8_t *wp[kW];
     const uint16_t *xp[kX];
     const float *sp = a.s;
-    unsigned w_rows = 0;  // bit i: piece i is of a row that exists
+    int w_size[kW] = {};  // 16, or 0 for a piece of a row that does not exist
     auto enter_weights = [&](int unit) {
         const int tile = unit / blocks, row0 = (unit - tile * blocks) * per;
         const size_t e = tb.tile_expert[tile];
         const uint8_t *w = a.w + e * a.w_rows * a.K + wc * 16;
-        w_rows = 0;
 #pragma unroll
         for (int i = 0; i < kW; ++i) {
             const int r = wr + i * (32 >> ks_log);
@@ -151,7 +142,7 @@ __global__ void __launch_bounds__(kThreads, 2) experts_kernel(Fp8ExpertsArgs a) 
                 row = j + (r & 8 ? a.rows : 0);
             }
             wp[i] = w + (size_t)row * a.K;
-            if (j < a.rows) w_rows |= 1u << i;
+            w_size[i] = j < a.rows ? 16 : 0;
         }
         if (tid < 2 * kWarps) {
             const int rg = (tid >> 1) >> ks_log;
@@ -176,17 +167,14 @@ __global__ void __launch_bounds__(kThreads, 2) experts_kernel(Fp8ExpertsArgs a) 
         }
     };
     auto copy_weights = [&](const Cursor &cu) {
-        const uint32_t st = ring0 + cu.stage * stage_bytes + tid * 16;
+        // piece c of row r is at c ^ 4 in odd rows, so that lanes of neighbouring rows read
+        // other banks (this thread's rows are all odd or all even)
+        const uint32_t st = (ring0 + cu.stage * stage_bytes + tid * 16) ^ ((wr & 1) << 6);
         const int k = cu.kstep * KS * kGroup;
         const int in = k + wc * 16 < a.K ? 16 : 0;
 #pragma unroll
-        for (int i = 0; i < kW; ++i) {
-            const int n = w_rows >> i & 1 ? in : 0;
-            // piece c of row r is at c ^ 4 in odd rows: so that lanes of neighbouring rows
-            // read other banks
-            const int r = wr + i * (32 >> ks_log);
-            copy16((st + i * kThreads * 16) ^ ((r & 1) << 6), n ? wp[i] + k : a.w, n);
-        }
+        for (int i = 0; i < kW; ++i)  // (no bytes are read where the size is 0)
+            copy16(st + i * kThreads * 16, wp[i] + k, min(in, w_size[i]));
         if (tid < 2 * kWarps)
             copy4(ring0 + cu.stage * stage_bytes + kStageWeights + x_bytes + tid * 4,
                   sp + min(cu.kstep * KS + ((tid >> 1) & (KS - 1)), Gk - 1));
@@ -199,7 +187,7 @@ __global__ void __launch_bounds__(kThreads, 2) experts_kernel(Fp8ExpertsArgs a) 
         for (int i = 0; i < kX; ++i) {
             const int r = xr + i * (16 >> ks_log);
             if (xp[i])
-                copy16(st + (r << (8 + ks_log)) + ((xc ^ (r & 1)) << 4), in ? xp[i] + k : a.x, in);
+                copy16(st + (r << (8 + ks_log)) + ((xc ^ (r & 1)) << 4), xp[i] + k, in);
         }
     };
     auto advance = [&](Cursor &cu) {
@@ -257,7 +245,7 @@ __global__ void __launch_bounds__(kThreads, 2) experts_kernel(Fp8ExpertsArgs a) 
             uint32_t b[NT][8];
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
-                const int tok = min(n * 8 + g, cap - 1);
+                const int tok = min(n * 8 + g, kCap<NT, KS> - 1);
                 const uint32_t xp = st + kStageWeights + (tok << (8 + ks_log));
                 const int c16 = ks * 16 + h * 8 + c * 2;
                 const uint4 b0 = lds128(xp + ((c16 ^ (tok & 1)) << 4)),
@@ -349,28 +337,78 @@ __global__ void __launch_bounds__(256) combine_kernel(const float *o, const int3
     out[(size_t)t * N + n] = float_to_half_bits(v, kBf16);
 }
 
-template <bool kBf16, int NT>
-cudaError_t launch_nt(const Fp8MoeArgs &a, const DeviceInfo &dev, int *status,
-                      cudaStream_t stream) {
-    const int grid = (getenv("W4_G") ? atoi(getenv("W4_G")) : 2) * dev.sm_count, cap = a.T < 8 * NT ? a.T : 8 * NT;
+// How a product is cut: NT by which slots of an expert share a tile, KS by which a stage's
+// blocks are split among the warps.
+struct Cut {
+    int nt, ks;
+};
+// The cut of the smallest cost: the units of the busiest CTA, each its weights' bytes, its
+// activations' and 8 KB for its start and end, a tenth more for each further 8 slots of a
+// tile.  The choices are on the device, so the tiles are those of even choices: `used`
+// experts with `each` slots.  (T 37, 10 experts, 3 each, 1040 -> 2 x 336: 2 and 2, XX us;
+// 4 and 1, by the slots alone, 19.0.)
+Cut cut_of(double used, double each, int T, int rows_per_unit, int rows, int K, int grid) {
+    Cut best{1, 1};
+    double least = INFINITY;
+    for (int nt = 1; nt <= 4; nt *= 2) {
+        const int cap = T < 8 * nt ? T : 8 * nt;
+        const double tiles = used * (cap == T || each <= 0.6 * cap ? 1.0 : each / cap + 0.5);
+        for (int ks = 1; ks <= 8 / nt && ks * cap <= 32 && ks * nt <= (nt == 1 ? 8 : 4); ks *= 2) {
+            const int per = rows_per_unit / ks;
+            const double units = tiles * ((rows + per - 1) / per);
+            const double cost = ceil(units / grid) * (0.9 + 0.1 * nt) *
+                                (128.0 / ks * K + 2.0 * fmin(cap, each) * K + 8192);
+            if (cost < least) least = cost, best = {nt, ks};
+        }
+        if (T <= 8 * nt) break;
+    }
+    return best;
+}
+
+template <bool kBf16, bool kSilu, int NT, int KS>
+cudaError_t launch_cut(Fp8ExpertsArgs &p, int grid, cudaStream_t stream) {
+    p.cap = p.T < 8 * NT ? p.T : 8 * NT;
+    return launch_chained(experts_kernel<kBf16, NT, KS, kSilu>, dim3(grid), kThreads, kRingBytes, 1,
+                          stream, p);
+}
+template <bool kBf16, bool kSilu>
+cudaError_t launch_product(Fp8ExpertsArgs p, Cut cut, int grid, cudaStream_t stream) {
+    switch (cut.nt * 16 + cut.ks) {
+        case 1 * 16 + 1: return launch_cut<kBf16, kSilu, 1, 1>(p, grid, stream);
+        case 1 * 16 + 2: return launch_cut<kBf16, kSilu, 1, 2>(p, grid, stream);
+        case 1 * 16 + 4: return launch_cut<kBf16, kSilu, 1, 4>(p, grid, stream);
+        case 1 * 16 + 8: return launch_cut<kBf16, kSilu, 1, 8>(p, grid, stream);
+        case 2 * 16 + 1: return launch_cut<kBf16, kSilu, 2, 1>(p, grid, stream);
+        case 2 * 16 + 2: return launch_cut<kBf16, kSilu, 2, 2>(p, grid, stream);
+        default: return launch_cut<kBf16, kSilu, 4, 1>(p, grid, stream);
+    }
+}
+
+template <bool kBf16>
+cudaError_t launch_type(const Fp8MoeArgs &a, const DeviceInfo &dev, int *status,
+                        cudaStream_t stream) {
+    const int grid = 2 * dev.sm_count;
+    const double used = a.E * (1.0 - pow(1.0 - fmin(1.0, (double)a.k / a.E), a.T)),
+                 each = a.T * a.k / used;
     uint16_t *h = static_cast<uint16_t *>(a.scratch);
     float *o = reinterpret_cast<float *>(static_cast<char *>(a.scratch) +
                                          fp8_moe_h_bytes(a.T, a.k, a.I));
-    Fp8ExpertsArgs p{a.x, a.w1, a.s1, a.ids, h, nullptr, status, a.T, a.k, a.E, a.K, a.I, 2 * a.I,
-                     cap};
-    cudaError_t e =
-        launch_chained(experts_kernel<kBf16, NT, true>, dim3(grid), kThreads, kRingBytes, 1, stream, p);
+    cudaError_t e = launch_product<kBf16, true>(
+        {a.x, a.w1, a.s1, a.ids, h, nullptr, status, a.T, a.k, a.E, a.K, a.I, 2 * a.I, 0},
+        cut_of(used, each, a.T, 64, a.I, a.K, grid), grid, stream);
     if (e != cudaSuccess) return e;
-    p = {h, a.w2, a.s2, a.ids, nullptr, o, status, a.T, a.k, a.E, a.I, a.N, a.N, cap};
-    e = launch_chained(experts_kernel<kBf16, NT, false>, dim3(grid), kThreads, kRingBytes, 1, stream, p);
+    e = launch_product<kBf16, false>(
+        {h, a.w2, a.s2, a.ids, nullptr, o, status, a.T, a.k, a.E, a.I, a.N, a.N, 0},
+        cut_of(used, each, a.T, 128, a.N, a.I, grid), grid, stream);
     if (e != cudaSuccess) return e;
-    return launch_chained(combine_kernel<kBf16>, dim3((a.N + 255) / 256, a.T), 256, 0, 1, stream, (const float *)o, a.ids, a.weights, a.T, a.k, a.E, a.N, a.out);
+    return launch_chained(combine_kernel<kBf16>, dim3((a.N + 255) / 256, a.T), 256, 0, 1, stream,
+                          (const float *)o, a.ids, a.weights, a.T, a.k, a.E, a.N, a.out);
 }
 
-template <bool kBf16, int NT>
-cudaError_t init_nt() {
-    const void *kernels[] = {(const void *)experts_kernel<kBf16, NT, true>,
-                             (const void *)experts_kernel<kBf16, NT, false>};
+template <bool kBf16, int NT, int KS>
+cudaError_t init_split() {
+    const void *kernels[] = {(const void *)experts_kernel<kBf16, NT, KS, true>,
+                             (const void *)experts_kernel<kBf16, NT, KS, false>};
     for (const void *k : kernels) {
         cudaError_t e =
             cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kRingBytes);
@@ -378,32 +416,29 @@ cudaError_t init_nt() {
     }
     return cudaSuccess;
 }
+template <bool kBf16>
+cudaError_t init_type() {
+    cudaError_t e = init_split<kBf16, 1, 1>();
+    if (e == cudaSuccess) e = init_split<kBf16, 1, 2>();
+    if (e == cudaSuccess) e = init_split<kBf16, 1, 4>();
+    if (e == cudaSuccess) e = init_split<kBf16, 1, 8>();
+    if (e == cudaSuccess) e = init_split<kBf16, 2, 1>();
+    if (e == cudaSuccess) e = init_split<kBf16, 2, 2>();
+    if (e == cudaSuccess) e = init_split<kBf16, 4, 1>();
+    return e;
+}
 
 }  // namespace
 
 cudaError_t launch_fp8_moe(const Fp8MoeArgs &a, bool bf16, const DeviceInfo &dev, int *status,
                            cudaStream_t stream) {
-    // the tiles' width: so that an expert's slots fit one tile where they are as many as
-    // the average and somewhat more
-    const int slots = a.T * a.k;
-    if (slots <= 5 * a.E || a.T <= 8)
-        return bf16 ? launch_nt<true, 1>(a, dev, status, stream)
-                    : launch_nt<false, 1>(a, dev, status, stream);
-    if (slots <= 10 * a.E || a.T <= 16)
-        return bf16 ? launch_nt<true, 2>(a, dev, status, stream)
-                    : launch_nt<false, 2>(a, dev, status, stream);
-    return bf16 ? launch_nt<true, 4>(a, dev, status, stream)
-                : launch_nt<false, 4>(a, dev, status, stream);
+    return bf16 ? launch_type<true>(a, dev, status, stream)
+                : launch_type<false>(a, dev, status, stream);
 }
 
 cudaError_t fp8_moe_init() {
-    cudaError_t e = init_nt<true, 1>();
-    if (e == cudaSuccess) e = init_nt<true, 2>();
-    if (e == cudaSuccess) e = init_nt<true, 4>();
-    if (e == cudaSuccess) e = init_nt<false, 1>();
-    if (e == cudaSuccess) e = init_nt<false, 2>();
-    if (e == cudaSuccess) e = init_nt<false, 4>();
-    return e;
+    const cudaError_t e = init_type<true>();
+    return e == cudaSuccess ? init_type<false>() : e;
 }
 
 }  // namespace w4a16
