@@ -212,26 +212,30 @@ struct Products {
                          : "memory");
         }
     }
-    __device__ __forceinline__ void commit(unsigned n, int bars) {  // by the issuing thread
-        dev::mma_commit(smem_of(&sp->done[n % bars]));
+    // the barrier of products n, of `bars` in turn
+    __device__ __forceinline__ uint32_t bar(unsigned n, int bars) const {
+        return smem_of(&sp->done[n % bars]);
     }
-    // products n (counted from 0) and all before are done
+    // products n (counted from 0) and all before are done; whole warps wait, and go on together
     __device__ __forceinline__ void wait(unsigned n, int bars) {
         volatile int *abort = &sp->abort;
-        if (!dev::mbar_wait(smem_of(&sp->done[n % bars]), n / bars & 1, abort) && !*abort) {
+        if (!dev::mbar_wait_all(bar(n, bars), n / bars & 1, abort) && !*abort) {
             *abort = 1;
             atomicOr(status, kErrProducts);
         }
+        __syncwarp();
     }
 };
-// D[tensor memory] (+)= A B^T over 16 k, both 128-byte swizzled in shared memory
+// D[tensor memory] (+)= A B^T over 16 k, both 128-byte swizzled in shared memory.  Issued by
+// the elected lane of a warp whose control flow and operands are uniform: by one thread of a
+// diverged warp each took about 220 cycles.
 __device__ __forceinline__ void product16(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
-                                          bool add) {
+                                          uint32_t add) {
     asm volatile(
         "{\n\t.reg .pred p;\n\t"
         "setp.ne.b32 p, %4, 0;\n\t"
         "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-        "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)add)
+        "l"(a), "l"(b), "r"(idesc), "r"(add)
         : "memory");
 }
 // M = 128, N = n (a multiple of 16), fp32 sums
@@ -319,6 +323,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(LoraArgs a) {
 // All threads of the cluster's CTAs come to each of these, whatever their share of the work:
 // these waits have no limit of their own, but nothing before them waits.
 __device__ __forceinline__ void cluster_sync() {
+    __syncwarp();
     asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
     asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
@@ -367,7 +372,7 @@ __device__ void shrink_tall(const LoraArgs &a, const uint16_t *order, const Tile
                             int k1, uint8_t *smem, Products &pr) {
     constexpr int kPitch = kTallRanks + 4;
     static_assert(kTall * kPitch * 4 <= kShrinkStages * kShrinkStage, "the sums fit the stages");
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int tid = threadIdx.x, lane = tid & 31, warp = (int)dev::uniform(tid >> 5);
     const int Q = a.parts * a.R, rank = rank_of(a, t.adapter);
     const uint32_t base = smem_of(smem);
     // this thread's 16 bytes of four rows of x and of A, per stage
@@ -393,7 +398,8 @@ __device__ void shrink_tall(const LoraArgs &a, const uint16_t *order, const Tile
         }
     };
     const int steps = k1 > k0 ? (k1 - k0 + 63) / 64 : 0;
-    const uint32_t idesc = product_desc<kBf16>((ranks + 15) / 16 * 16);
+    const uint32_t idesc = dev::uniform(product_desc<kBf16>((ranks + 15) / 16 * 16)),
+                   tmem = dev::uniform(pr.tmem);
 #pragma unroll
     for (int s = 0; s < kShrinkStages - 1; ++s) {
         if (s < steps) issue(s);
@@ -403,14 +409,19 @@ __device__ void shrink_tall(const LoraArgs &a, const uint16_t *order, const Tile
         wait_copies<kShrinkStages - 2>();
         dev::fence_async_shared();
         __syncthreads();
-        if (tid == 0) {
+        if (warp == 0) {
             dev::tc_fence_after();
-            const uint32_t st = base + (pr.count + s) % kShrinkStages * kShrinkStage;
+            const uint32_t st =
+                dev::uniform(base + (pr.count + s) % kShrinkStages * kShrinkStage);
             const uint64_t x = dev::smem_desc_sw128(st), w = dev::smem_desc_sw128(st + kTall * 128);
+            const uint32_t bar = dev::uniform(pr.bar(pr.count + s, kShrinkStages));
+            if (dev::elect_one()) {
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
-                product16(pr.tmem, x + 2 * k, w + 2 * k, idesc, s + k > 0);
-            pr.commit(pr.count + s, kShrinkStages);
+                for (int k = 0; k < 4; ++k)
+                    product16(tmem, x + 2 * k, w + 2 * k, idesc, s + k > 0);
+                dev::mma_commit(bar);
+            }
+            __syncwarp();
         }
         if (s + kShrinkStages - 1 < steps) {
             if (s > 0) pr.wait(pr.count + s - 1, kShrinkStages);
@@ -729,8 +740,8 @@ __device__ void expand_tall(const LoraArgs &a, const uint16_t *order, const Tile
     // a step's copies are two groups, residual and B: at a step's start B of the next and the
     // residual of this one have to be there, and all younger groups may still be under way
     constexpr int kPending = kBs > 2 ? 2 : 0;
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int rank = rank_of(a, t.adapter), ksteps = (rank + 15) / 16;
+    const int tid = threadIdx.x, lane = tid & 31, warp = (int)dev::uniform(tid >> 5);
+    const int rank = rank_of(a, t.adapter), ksteps = (int)dev::uniform((rank + 15) / 16);
     const uint32_t t_hi = smem_of(smem), t_lo = t_hi + t_half(RK), res0 = t_hi + 2 * t_half(RK),
                    b0 = res0 + kRs * kResidualStage;
     __shared__ float factor[kTall];
@@ -747,24 +758,28 @@ __device__ void expand_tall(const LoraArgs &a, const uint16_t *order, const Tile
     const int steps = (n1 - n0 + kTallCols - 1) / kTallCols;
     // where 8 columns c of a row of a residual stage lie: two halves of 64 columns
     const auto cell = [](int r, int c) { return (uint32_t)(c >> 3) * (kTall * 128) + swizzled(r, c & 7); };
+    // (a thread's rows are multiples of 8 apart, so their swizzle is the same)
+    const int bj = tid / kPieces, bc = tid % kPieces;
+    constexpr int kBRows = kCta / kPieces;  // rows of B between a thread's pieces
+    static_assert(kBRows % 8 == 0, "the same swizzle");
+    const uint32_t b_at = (bc >> 3) * kTallCols * 128 + swizzled(bj, bc & 7), r_at = cell(r0, col);
+    const int b_size = bc < 2 * ksteps ? max(0, min(2 * (rank - bc * 8), 16)) : -1;
+    const uint16_t *bp = b + (size_t)bj * a.R + bc * 8;
     auto issue_b = [&](int s) {
-        const uint32_t st = b0 + s % kBs * b_stage(RK);
-        const int n = s * kTallCols;
+        if (b_size < 0) return;
+        const uint32_t st = b0 + s % kBs * b_stage(RK) + b_at;
+        const int n = s * kTallCols + bj;
 #pragma unroll
-        for (int i = 0; i < kTallCols * kPieces / kCta; ++i) {
-            const int q = tid + i * kCta, j = q / kPieces, c = q % kPieces;
-            if (c >= 2 * ksteps) continue;
-            const int in = n0 + n + j < n1 ? max(0, min(2 * (rank - c * 8), 16)) : 0;
-            copy16(st + (c >> 3) * kTallCols * 128 + swizzled(j, c & 7),
-                   in ? b + (size_t)(n + j) * a.R + c * 8 : a.b, in);
-        }
+        for (int i = 0; i < kTallCols / kBRows; ++i)
+            copy16(st + i * kBRows * 128, bp + (size_t)(s * kTallCols + i * kBRows) * a.R,
+                   n0 + n + i * kBRows < n1 ? b_size : 0);
     };
     auto issue_residual = [&](int s) {
-        const uint32_t st = res0 + s % kRs * kResidualStage;
+        const uint32_t st = res0 + s % kRs * kResidualStage + r_at;
         const int n = s * kTallCols, in = n0 + n + col * 8 < n1 ? 16 : 0;
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-            if (rp[i]) copy16(st + cell(r0 + 32 * i, col), in ? rp[i] + n : a.residual, in);
+            if (rp[i]) copy16(st + i * 32 * 128, rp[i] + n, in);
     };
 #pragma unroll
     for (int s = 0; s < kBs; ++s) {
@@ -817,20 +832,27 @@ __device__ void expand_tall(const LoraArgs &a, const uint16_t *order, const Tile
             sts128(t_lo + at, make_uint4(l[0], l[1], l[2], l[3]));
         }
     }
-    const uint32_t idesc = product_desc<kBf16>(kTallCols);
-    auto products = [&](int s) {  // thread 0
+    const uint32_t idesc = product_desc<kBf16>(kTallCols), tmem = dev::uniform(pr.tmem);
+    const uint32_t u_hi = dev::uniform(t_hi), u_lo = dev::uniform(t_lo), u_b = dev::uniform(b0);
+    auto products = [&](int s) {  // warp 0
         dev::tc_fence_after();
-        const uint32_t st = b0 + s % kBs * b_stage(RK);
-        const uint32_t d = pr.tmem + ((pr.count + s) & 1) * kTallCols;
+        const unsigned n = dev::uniform(pr.count + s);
+        const uint32_t st = u_b + s % kBs * b_stage(RK), d = tmem + (n & 1) * kTallCols;
+        const uint32_t bar = dev::uniform(pr.bar(n, 2));
+        if (dev::elect_one()) {
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
-            for (int k = 0; k < ksteps; ++k)
-                product16(d,
-                          dev::smem_desc_sw128((h ? t_lo : t_hi) + (k >> 2) * kTall * 128) +
-                              2 * (k & 3),
-                          dev::smem_desc_sw128(st + (k >> 2) * kTallCols * 128) + 2 * (k & 3), idesc,
-                          h + k > 0);
-        pr.commit(pr.count + s, 2);
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int k = 0; k < kBlocks * 4; ++k)
+                    if (k < ksteps)
+                        product16(d,
+                                  dev::smem_desc_sw128((h ? u_lo : u_hi) + (k >> 2) * kTall * 128) +
+                                      2 * (k & 3),
+                                  dev::smem_desc_sw128(st + (k >> 2) * kTallCols * 128) + 2 * (k & 3),
+                                  idesc, h + k > 0);
+            dev::mma_commit(bar);
+        }
+        __syncwarp();
     };
     // outputs: a warp's 32 rows (its quarter of the tensor memory's lanes) and 32 columns;
     // out[i]: where row i * 8 + lane / 4 of them lies in y
@@ -848,12 +870,12 @@ __device__ void expand_tall(const LoraArgs &a, const uint16_t *order, const Tile
     dev::fence_async_shared();
     __syncthreads();
     const float f = factor[mine];
-    if (tid == 0) products(0);
+    if (warp == 0) products(0);
     for (int s = 0; s < steps; ++s) {
         wait_copies<kPending>();
         dev::fence_async_shared();
         __syncthreads();
-        if (tid == 0 && s + 1 < steps) products(s + 1);
+        if (warp == 0 && s + 1 < steps) products(s + 1);
         if (s + kRs - 1 < steps) issue_residual(s + kRs - 1);
         commit_copies();
         const uint32_t st = res0 + s % kRs * kResidualStage;
@@ -880,24 +902,29 @@ __device__ void expand_tall(const LoraArgs &a, const uint16_t *order, const Tile
                      v);
         dev::tmem_wait_ld(v);
         dev::tc_fence_before();
+        uint4 r[4];  // (all loads, then the arithmetic: their latency shows)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            r[i] = a.residual ? lds128(st + cell(mine, (side >> 3) + i)) : make_uint4(0, 0, 0, 0);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const uint32_t at = st + cell(mine, (side >> 3) + i);
-            const uint4 r = a.residual ? lds128(at) : make_uint4(0, 0, 0, 0);
             float w[8];
 #pragma unroll
             for (int j = 0; j < 8; ++j) w[j] = __uint_as_float(v[8 * i + j]) * f;
-            sts128(at, add_cells<kBf16>(r, w));
+            r[i] = add_cells<kBf16>(r[i], w);
         }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) sts128(st + cell(mine, (side >> 3) + i), r[i]);
         __syncwarp();
         if constexpr (kVec) {
             const int c = lane & 3;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const uint4 w = lds128(st + cell(quarter + i * 8 + (lane >> 2), (side >> 3) + c));
+            for (int i = 0; i < 4; ++i)
+                r[i] = lds128(st + cell(quarter + i * 8 + (lane >> 2), (side >> 3) + c));
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
                 if (there[i] && c * 8 < left)
-                    *reinterpret_cast<uint4 *>(a.y + out[i] + n + c * 8) = w;
-            }
+                    *reinterpret_cast<uint4 *>(a.y + out[i] + n + c * 8) = r[i];
         } else {
 #pragma unroll 8
             for (int i = 0; i < 32; ++i) {
