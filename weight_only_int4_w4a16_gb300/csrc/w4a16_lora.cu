@@ -50,8 +50,14 @@ constexpr int kShrinkThreads = 256;
 constexpr int kCluster = 8;      // CTAs that share a shrink unit's K
 constexpr int kTallRanks = 128;  // rows of A of a shrink unit of a tall tile
 constexpr int kLowRanks = 32;    // and of a low one
-constexpr int kShrinkStages = 3;
 constexpr int kShrinkStage = (kTall + kTallRanks) * 128;  // bytes: 64 k of x and A
+// Its kernel's kind: calls of few rows, with low tiles only, in small shared memory; calls
+// whose tall units are no more than the clusters of one CTA per SM that run at once, with six
+// stages each (1000 rows beside o: 29.5 us for 31.3 with three); others, two CTAs per SM
+// (4096 rows beside gate+up: 152 us for 160 with the one of six stages)
+enum Kind { kFew, kDeep, kMany };
+constexpr int shrink_stages(Kind kind) { return kind == kDeep ? 6 : 3; }
+constexpr int kMaxShrinkStages = 6;
 constexpr int kTallCols = 128;  // columns of a step of expand, tall tiles
 constexpr int kLowCols = 32;    // low ones
 constexpr int kLowPitch = kLowRanks + 8;  // of a low unit's sums in shared memory
@@ -169,7 +175,7 @@ __device__ __forceinline__ uint8_t *align1024(uint8_t *p) {
 // products of tall tiles: tensor memory, the barriers that tell of their ends
 // ---------------------------------------------------------------------------
 struct ProductSpace {
-    uint64_t done[kShrinkStages];
+    uint64_t done[kMaxShrinkStages];
     uint32_t tmem;
     int abort;
 };
@@ -184,7 +190,7 @@ struct Products {
     __device__ __forceinline__ void begin(ProductSpace *space, int *status_word) {
         sp = space, status = status_word, count = 0;
         if (threadIdx.x == 0) {
-            for (int i = 0; i < kShrinkStages; ++i) dev::mbar_init(smem_of(&sp->done[i]), 1);
+            for (int i = 0; i < kMaxShrinkStages; ++i) dev::mbar_init(smem_of(&sp->done[i]), 1);
             dev::mbar_init_fence();
             sp->abort = 0;
         }
@@ -247,6 +253,17 @@ __device__ __forceinline__ uint32_t product_desc(int n) {
 // where 16-byte piece c of a 128-byte row r lies in the swizzled layout
 __device__ __forceinline__ uint32_t swizzled(int r, int c) {
     return (uint32_t)(r << 7) + (uint32_t)((c ^ (r & 7)) << 4);
+}
+
+// The plan to where the expanding kernel reads it.
+__device__ void share_plan(const LoraArgs &a, const Plan &p) {
+    const Plan to = shared_plan(a);
+    Tile *tiles = const_cast<Tile *>(to.shared);
+    uint16_t *order = const_cast<uint16_t *>(to.order);
+    for (int i = threadIdx.x; i < p.n.tall + p.n.low; i += kShrinkThreads)
+        tiles[i] = i < p.n.tall ? p.tall(i) : p.low(i - p.n.tall);
+    for (int i = threadIdx.x; i < a.M; i += kShrinkThreads) order[i] = p.order[i];
+    if (threadIdx.x == 0) *shared_counts(a) = p.n;
 }
 
 // ---------------------------------------------------------------------------
@@ -367,7 +384,7 @@ __device__ void join_sums(const LoraArgs &a, const uint16_t *order, int rows, in
 
 // A tile of up to 128 rows, rows q0 .. q0 + 127 of A, k0 <= k < k1: the products of a stage
 // of 64 k are issued once it is there, and its slot is filled again once they are done.
-template <bool kBf16>
+template <bool kBf16, int kShrinkStages>
 __device__ void shrink_tall(const LoraArgs &a, const uint16_t *order, const Tile &t, int q0, int k0,
                             int k1, uint8_t *smem, Products &pr) {
     constexpr int kPitch = kTallRanks + 4;
@@ -505,44 +522,43 @@ __device__ void shrink_low(const LoraArgs &a, const uint16_t *order, const Tile 
     join_sums(a, order, t.count, q0, min(kLowRanks, Q - q0), kPitch, smem_of(smem));
 }
 
-// kFew: calls of up to kFewRows rows, with low tiles only; the others' shared memory holds
-// the stages
-template <bool kFew>
-constexpr int shrink_smem() {
-    return kFew ? max_of((kShrinkThreads / 32 + 1) * kLow * kLowPitch * 4,
+constexpr int shrink_smem(Kind kind) {
+    return kind == kFew ? max_of((kShrinkThreads / 32 + 1) * kLow * kLowPitch * 4,
                          (int)sizeof(RowSort<kFewRows>))
-                : kShrinkStages * kShrinkStage + 1024;  // (to align them)
+                : shrink_stages(kind) * kShrinkStage + 1024;  // (to align them)
 }
 
-template <bool kBf16, bool kFew>
-__global__ void __launch_bounds__(kShrinkThreads, 2) shrink_kernel(LoraArgs a) {
-    constexpr int kRows = kFew ? kFewRows : kLocalRows;
+template <bool kBf16, Kind kKind>
+__global__ void __launch_bounds__(kShrinkThreads, kKind == kDeep ? 1 : 2) shrink_kernel(LoraArgs a) {
+    constexpr bool few = kKind == kFew;
+    constexpr int kRows = few ? kFewRows : kLocalRows;
     extern __shared__ __align__(128) uint8_t smem_raw[];
-    uint8_t *smem = kFew ? smem_raw : align1024(smem_raw);
+    uint8_t *smem = few ? smem_raw : align1024(smem_raw);
     __shared__ LocalPlan<kRows> own;
     __shared__ ProductSpace space;
     Products pr;
-    if constexpr (!kFew) pr.begin<kShrinkTmem>(&space, a.status);
+    if constexpr (!few) pr.begin<kShrinkTmem>(&space, a.status);
     wait_for_last();
     launch_next();
     const Plan p = make_plan<kShrinkThreads, kRows>(a, own, smem);
+    if (!few && a.M <= kRows && blockIdx.x == 0) share_plan(a, p);
     const int Q = a.parts * a.R;
     const int tq = (Q + kTallRanks - 1) / kTallRanks, lq = (Q + kLowRanks - 1) / kLowRanks;
     const int tall = p.n.tall * tq, units = tall + p.n.low * lq;
     const int slice = (a.K + kCluster * 8 - 1) / (kCluster * 8) * 8;
     const int k0 = (int)cluster_rank() * slice, k1 = min(a.K, k0 + slice);
     for (int u = blockIdx.x / kCluster; u < units; u += gridDim.x / kCluster) {
-        if (!kFew && u < tall) {
+        if (!few && u < tall) {
             const Tile t = p.tall(u / tq);
-            if constexpr (!kFew)
-                shrink_tall<kBf16>(a, p.order + t.first, t, u % tq * kTallRanks, k0, k1, smem, pr);
+            if constexpr (!few)
+                shrink_tall<kBf16, shrink_stages(kKind)>(a, p.order + t.first, t, u % tq * kTallRanks, k0, k1, smem, pr);
         } else {
             const int v = u - tall;
             const Tile t = p.low(v / lq);
             shrink_low<kBf16>(a, p.order + t.first, t, v % lq * kLowRanks, k0, k1, smem);
         }
     }
-    if constexpr (!kFew) pr.end<kShrinkTmem>();
+    if constexpr (!few) pr.end<kShrinkTmem>();
 }
 
 // ---------------------------------------------------------------------------
@@ -568,10 +584,9 @@ constexpr int low_stages(int RK, bool few) {
 constexpr int expand_smem(int RK, bool few) {
     const int low = expand_threads(few) / 32 * low_stages(RK, few) * low_stage(RK);
     return few ? max_of(low, (int)sizeof(RowSort<kFewRows>))
-               : 1024 + max_of(max_of(2 * t_half(RK) + residual_stages(RK) * kResidualStage +
-                                          b_stages(RK) * b_stage(RK),
-                                      low),
-                               (int)sizeof(RowSort<kLocalRows>));
+               : 1024 + max_of(2 * t_half(RK) + residual_stages(RK) * kResidualStage +
+                                   b_stages(RK) * b_stage(RK),
+                               low);
 }
 
 // two values rounded to the 16-bit type (nearest even), and back
@@ -942,11 +957,11 @@ __device__ void expand_tall(const LoraArgs &a, const uint16_t *order, const Tile
 
 // A low tile, columns n0 <= n < n1 of a part: every warp 32 of them in turn, with a ring of
 // its own for B and (kVec) the residual.
-template <bool kBf16, int RK, bool kVec, bool kFew>
+template <bool kBf16, int RK, bool kVec, bool few>
 __device__ void expand_low(const LoraArgs &a, const uint16_t *order, const Tile &t, int part,
                            int n0, int n1, uint8_t *smem) {
-    constexpr int kStages = low_stages(RK, kFew), kBytes = low_stage(RK), kPieces = 2 * RK;
-    constexpr int kStride = expand_threads(kFew) / 32 * kLowCols;
+    constexpr int kStages = low_stages(RK, few), kBytes = low_stage(RK), kPieces = 2 * RK;
+    constexpr int kStride = expand_threads(few) / 32 * kLowCols;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, c = lane & 3;
     const int rank = rank_of(a, t.adapter), ksteps = (rank + 15) / 16;
     const uint32_t base = smem_of(smem) + warp * kStages * kBytes;
@@ -1042,83 +1057,122 @@ __device__ __forceinline__ void walk(const LoraArgs &a, int cols, int tiles, Run
     }
 }
 
-template <bool kBf16, int RK, bool kVec, bool kFew>
-__global__ void __launch_bounds__(expand_threads(kFew), kFew ? 2 : 1) expand_kernel(LoraArgs a) {
-    constexpr int kCta = expand_threads(kFew), kRows = kFew ? kFewRows : kLocalRows;
+template <bool kBf16, int RK, bool kVec, bool few>
+__global__ void __launch_bounds__(expand_threads(few), few ? 2 : 1) expand_kernel(LoraArgs a) {
+    constexpr int kCta = expand_threads(few);
     extern __shared__ __align__(128) uint8_t smem_raw[];
-    uint8_t *smem = kFew ? smem_raw : align1024(smem_raw);
-    __shared__ LocalPlan<kRows> own;
+    uint8_t *smem = few ? smem_raw : align1024(smem_raw);
+    __shared__ LocalPlan<kFewRows> own;
     __shared__ ProductSpace space;
     Products pr;
-    if constexpr (!kFew) pr.begin<kExpandTmem>(&space, a.status);
+    if constexpr (!few) pr.begin<kExpandTmem>(&space, a.status);
     launch_next();
-    // shrink has let this kernel start after all that came before shrink had ended: the plan,
-    // B and the residual may be read before shrink's own results
-    const Plan p = make_plan<kCta, kRows>(a, own, smem);
-    if constexpr (!kFew)
+    Plan p;
+    if constexpr (few) {
+        // shrink has let this kernel start after all that came before shrink had ended: the
+        // ids, B and the residual may be read before shrink's own results
+        p = make_plan<kCta, kFewRows>(a, own, smem);
+    } else {
+        wait_for_last();  // (its shared memory lets it start only beside the last of shrink)
+        p = shared_plan(a);
+        p.n = *shared_counts(a);
+    }
+    if constexpr (!few)
         walk(a, kTallCols, p.n.tall, [&](int tile, int part, int n0, int n1) {
             const Tile t = p.tall(tile);
             expand_tall<kBf16, RK, kVec>(a, p.order + t.first, t, part, n0, n1, smem, pr);
         });
     walk(a, kLowCols, p.n.low, [&](int tile, int part, int n0, int n1) {
         const Tile t = p.low(tile);
-        expand_low<kBf16, RK, kVec, kFew>(a, p.order + t.first, t, part, n0, n1, smem);
+        expand_low<kBf16, RK, kVec, few>(a, p.order + t.first, t, part, n0, n1, smem);
     });
     copy_rows<kCta, kVec>(a, p.order + p.n.rows, p.n.none);
     wait_for_last();  // (for those without a step: what follows this kernel waits for it alone)
-    if constexpr (!kFew) pr.end<kExpandTmem>();
+    if constexpr (!few) pr.end<kExpandTmem>();
 }
 
-template <bool kBf16, int RK, bool kVec, bool kFew>
+template <bool kBf16, int RK, bool kVec, bool few>
 cudaError_t launch_expand(const LoraArgs &a, const DeviceInfo &dev, cudaStream_t stream) {
-    return launch_chained(expand_kernel<kBf16, RK, kVec, kFew>, dim3((kFew ? 2 : 1) * dev.sm_count),
-                          expand_threads(kFew), expand_smem(RK, kFew), 1, stream, a);
+    return launch_chained(expand_kernel<kBf16, RK, kVec, few>, dim3((few ? 2 : 1) * dev.sm_count),
+                          expand_threads(few), expand_smem(RK, few), 1, stream, a);
 }
-template <bool kBf16, bool kVec, bool kFew>
+template <bool kBf16, bool kVec, bool few>
 cudaError_t launch_expand_rank(const LoraArgs &a, const DeviceInfo &dev, cudaStream_t stream) {
-    if (a.R <= 16) return launch_expand<kBf16, 1, kVec, kFew>(a, dev, stream);
-    if (a.R <= 32) return launch_expand<kBf16, 2, kVec, kFew>(a, dev, stream);
-    if (a.R <= 64) return launch_expand<kBf16, 4, kVec, kFew>(a, dev, stream);
-    return launch_expand<kBf16, 8, kVec, kFew>(a, dev, stream);
+    if (a.R <= 16) return launch_expand<kBf16, 1, kVec, few>(a, dev, stream);
+    if (a.R <= 32) return launch_expand<kBf16, 2, kVec, few>(a, dev, stream);
+    if (a.R <= 64) return launch_expand<kBf16, 4, kVec, few>(a, dev, stream);
+    return launch_expand<kBf16, 8, kVec, few>(a, dev, stream);
 }
 
-template <bool kBf16, bool kFew>
+constexpr int kRounds = 4;
+int resident_clusters[3];  // of shrink_kernel's kinds, that run at once (set by lora_init)
+
+template <bool kBf16, Kind kKind>
 cudaError_t launch_calls(const LoraArgs &a, bool vec, const DeviceInfo &dev, cudaStream_t stream) {
+    constexpr bool few = kKind == kFew;
     if (a.M > kLocalRows) {
         const cudaError_t e = launch_chained(plan_kernel, dim3(1), kPlanThreads, 0, 1, stream, a);
         if (e != cudaSuccess) return e;
     }
-    // as many clusters as there can be units, or as run at once
+    // a cluster for each unit that there can be, up to some rounds of those that run at once
+    // (just those, each with all its units, 166 us for 152 at 4096 rows beside gate+up)
     const long long units = (long long)lora_max_tiles(a.M, a.L) *
                             ((a.parts * a.R + kLowRanks - 1) / kLowRanks);
-    const int most = 2 * dev.sm_count / kCluster;
+    const int most = kRounds * resident_clusters[kKind];
     const int clusters = units < most ? (int)units : most;
     const cudaError_t e =
-        launch_chained(shrink_kernel<kBf16, kFew>, dim3(clusters * kCluster), kShrinkThreads,
-                       shrink_smem<kFew>(), kCluster, stream, a);
+        launch_chained(shrink_kernel<kBf16, kKind>, dim3(clusters * kCluster), kShrinkThreads,
+                       shrink_smem(kKind), kCluster, stream, a);
     if (e != cudaSuccess) return e;
-    return vec ? launch_expand_rank<kBf16, true, kFew>(a, dev, stream)
-               : launch_expand_rank<kBf16, false, kFew>(a, dev, stream);
+    return vec ? launch_expand_rank<kBf16, true, few>(a, dev, stream)
+               : launch_expand_rank<kBf16, false, few>(a, dev, stream);
 }
 
 cudaError_t set_smem(const void *kernel, int bytes) {
     return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
 }
-template <bool kBf16, bool kFew, int RK>
+template <bool kBf16, bool few, int RK>
 cudaError_t init_expand() {
     const cudaError_t e =
-        set_smem((const void *)expand_kernel<kBf16, RK, true, kFew>, expand_smem(RK, kFew));
+        set_smem((const void *)expand_kernel<kBf16, RK, true, few>, expand_smem(RK, few));
     return e != cudaSuccess ? e
-                            : set_smem((const void *)expand_kernel<kBf16, RK, false, kFew>,
-                                       expand_smem(RK, kFew));
+                            : set_smem((const void *)expand_kernel<kBf16, RK, false, few>,
+                                       expand_smem(RK, few));
 }
-template <bool kBf16, bool kFew>
+template <bool kBf16, Kind kKind>
+cudaError_t init_shrink() {
+    cudaError_t e = set_smem((const void *)shrink_kernel<kBf16, kKind>, shrink_smem(kKind));
+    if (e == cudaSuccess) {
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(kCluster);
+        cfg.blockDim = dim3(kShrinkThreads);
+        cfg.dynamicSmemBytes = shrink_smem(kKind);
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = kCluster;
+        attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        int n = 0;
+        e = cudaOccupancyMaxActiveClusters(&n, shrink_kernel<kBf16, kKind>, &cfg);
+        if (e == cudaSuccess && n < 1) e = cudaErrorInvalidConfiguration;
+        resident_clusters[kKind] = n;
+    }
+    return e;
+}
+template <bool kBf16>
 cudaError_t init_calls() {
-    cudaError_t e = set_smem((const void *)shrink_kernel<kBf16, kFew>, shrink_smem<kFew>());
-    if (e == cudaSuccess) e = init_expand<kBf16, kFew, 1>();
-    if (e == cudaSuccess) e = init_expand<kBf16, kFew, 2>();
-    if (e == cudaSuccess) e = init_expand<kBf16, kFew, 4>();
-    if (e == cudaSuccess) e = init_expand<kBf16, kFew, 8>();
+    cudaError_t e = init_shrink<kBf16, kFew>();
+    if (e == cudaSuccess) e = init_shrink<kBf16, kDeep>();
+    if (e == cudaSuccess) e = init_shrink<kBf16, kMany>();
+    if (e == cudaSuccess) e = init_expand<kBf16, true, 1>();
+    if (e == cudaSuccess) e = init_expand<kBf16, false, 1>();
+    if (e == cudaSuccess) e = init_expand<kBf16, true, 2>();
+    if (e == cudaSuccess) e = init_expand<kBf16, false, 2>();
+    if (e == cudaSuccess) e = init_expand<kBf16, true, 4>();
+    if (e == cudaSuccess) e = init_expand<kBf16, false, 4>();
+    if (e == cudaSuccess) e = init_expand<kBf16, true, 8>();
+    if (e == cudaSuccess) e = init_expand<kBf16, false, 8>();
     return e;
 }
 
@@ -1129,18 +1183,19 @@ cudaError_t launch_lora(const LoraArgs &a, bool bf16, const DeviceInfo &dev, cud
     bool vec = a.N % 8 == 0 && ((uintptr_t)a.y & 15) == 0 && ((uintptr_t)a.residual & 15) == 0;
     for (int i = 0; i < a.parts; ++i) vec = vec && a.part[i] % 8 == 0;
     if (a.M <= kFewRows)
-        return bf16 ? launch_calls<true, true>(a, vec, dev, stream)
-                    : launch_calls<false, true>(a, vec, dev, stream);
-    return bf16 ? launch_calls<true, false>(a, vec, dev, stream)
-                : launch_calls<false, false>(a, vec, dev, stream);
+        return bf16 ? launch_calls<true, kFew>(a, vec, dev, stream)
+                    : launch_calls<false, kFew>(a, vec, dev, stream);
+    const int units = (a.M + kTall - 1) / kTall * ((a.parts * a.R + kTallRanks - 1) / kTallRanks);
+    if (units <= resident_clusters[kDeep])
+        return bf16 ? launch_calls<true, kDeep>(a, vec, dev, stream)
+                    : launch_calls<false, kDeep>(a, vec, dev, stream);
+    return bf16 ? launch_calls<true, kMany>(a, vec, dev, stream)
+                : launch_calls<false, kMany>(a, vec, dev, stream);
 }
 
 cudaError_t lora_init() {
-    cudaError_t e = init_calls<true, true>();
-    if (e == cudaSuccess) e = init_calls<true, false>();
-    if (e == cudaSuccess) e = init_calls<false, true>();
-    if (e == cudaSuccess) e = init_calls<false, false>();
-    return e;
+    const cudaError_t e = init_calls<true>();
+    return e == cudaSuccess ? init_calls<false>() : e;
 }
 
 }  // namespace w4a16
