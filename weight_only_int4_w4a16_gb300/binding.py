@@ -9,6 +9,7 @@ built: there is no fallback implementation.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 import torch
@@ -721,12 +722,23 @@ def w4a16_fp8_moe_mlp(x: torch.Tensor, topk_ids: torch.Tensor, weights: torch.Te
     s2 = _shaped(down_scales, torch.float32, (E, _blocks(N), _blocks(I)), "down_scales", dev)
     raw, side = _stream_for(dev, stream)
     out, op = _output(out, (T, N), dt, dev, side, "out")
-    need = lib.w4a16_fp8_moe_scratch_bytes(T, k, I, N)
+    need = _fp8_moe_scratch(T, k, I, N)
     scratch, sp = _output(None, (1, need), torch.uint8, dev, side, "scratch")
     _used_on(side, x, topk_ids, weights, w_gate_up, gate_up_scales, w_down, down_scales, out)
     _check(lib.w4a16_fp8_moe_mlp(xp, ip, wp, T, k, E, K, I, N, code, w1, s1, w2, s2, op, sp, need,
                                  raw), "w4a16_fp8_moe_mlp")
     return out
+
+
+@functools.lru_cache(maxsize=256)
+def _host_ints(values: tuple):
+    """(a host array of them, their number), which the library only reads."""
+    return (ctypes.c_int32 * len(values))(*values), len(values)
+
+
+# the scratch of a call's sizes
+_fp8_moe_scratch = functools.lru_cache(maxsize=1024)(lib.w4a16_fp8_moe_scratch_bytes)
+_lora_scratch = functools.lru_cache(maxsize=1024)(lib.w4a16_lora_scratch_bytes)
 
 
 def w4a16_lora(x: torch.Tensor, a: torch.Tensor, b: torch.Tensor, scales: torch.Tensor,
@@ -742,8 +754,7 @@ def w4a16_lora(x: torch.Tensor, a: torch.Tensor, b: torch.Tensor, scales: torch.
         if not isinstance(w, torch.Tensor) or w.dim() != 3:
             raise ValueError(f"{name} must be a 3-D torch tensor")
     L, N, R = b.shape
-    parts = (N,) if parts is None else tuple(parts)
-    n = len(parts)
+    host, n = _host_ints((N,) if parts is None else tuple(parts))
     dt = x.dtype
     code = _dtype16(dt)
     dev, xp = _home(x, dt, (M, K))
@@ -755,11 +766,11 @@ def w4a16_lora(x: torch.Tensor, a: torch.Tensor, b: torch.Tensor, scales: torch.
     rp = None if residual is None else _shaped(residual, dt, (M, N), "residual", dev)
     raw, side = _stream_for(dev, stream)
     y, yp = _output(y, (M, N), dt, dev, side, "y")
-    need = lib.w4a16_lora_scratch_bytes(M, L, R, n)
+    need = _lora_scratch(M, L, R, n)
     scratch, sp = _output(None, (1, need), torch.uint8, dev, side, "scratch")
     _used_on(side, x, a, b, scales, ranks, adapter_ids, residual, y)
-    _check(lib.w4a16_lora(xp, ap, bp, cp, kp, ip, M, K, N, L, R, (ctypes.c_int32 * n)(*parts), n,
-                          code, rp, yp, sp, need, raw), "w4a16_lora")
+    _check(lib.w4a16_lora(xp, ap, bp, cp, kp, ip, M, K, N, L, R, host, n, code, rp, yp, sp, need,
+                          raw), "w4a16_lora")
     return y
 
 
