@@ -9,22 +9,31 @@
 // rows, read beside them.)
 //
 // The rows are grouped by adapter, those of an adapter in tall tiles of 128 rows, or in one
-// low tile if they are at most 16.  All tiles of an adapter are of one kind, and a row's
-// sums do not depend on its place in a tile, so the order within an adapter changes no
-// result.  Up to 1024 rows each CTA groups for itself in shared memory; more are grouped by
-// a kernel of one CTA before (plan_kernel).
+// low tile if they are at most 16; in calls of up to 128 rows, decode steps mostly, in low
+// tiles whatever their number.  All tiles of an adapter are of one kind, and a row's sums do
+// not depend on its place in a tile, so the order within an adapter changes no result.  Up to
+// 1024 rows each CTA groups for itself in shared memory; more are grouped by a kernel of one
+// CTA before (plan_kernel).
 //   * shrink: t, a cluster of 8 CTAs per tile and block of A's rows, each with an eighth of
-//     K, whose sums meet through distributed shared memory (one CTA per SM walking all of
-//     K would leave most SMs idle: a tall tile's x is 1.3 MB at K 5120, and there are few).
-//     A tall tile and 128 rows of A go through shared memory; a low one and 32 rows of A
-//     come straight from memory, since each of their weights is used once.
-//   * expand: y.  All steps (64 columns of a tall tile, 32 of a low one for each warp) are
+//     K, whose sums meet through distributed shared memory (a tall tile's x is 1.3 MB at
+//     K 5120, and there are few tiles: without the split most SMs would idle).  A tall tile
+//     and 128 rows of A go through shared memory; a low one and 32 rows of A come straight
+//     from memory, since each of their weights is used once.
+//   * expand: y.  All steps (128 columns of a tall tile, 32 of a low one for each warp) are
 //     one sequence of which every CTA takes an equal run; B and the residual come through
-//     rings of asynchronous copies, which start before shrink has ended.
-// Both are bound by the bytes of x, y and the adapters.  Tall tiles run on tcgen05 (M = 128
-// rows of the tile; the warp MMA, at an eighth of its rate, paced them: 4096 rows, rank 64
-// beside gate+up took 34 and 191 us where they take XX and YY), low ones on the warp MMA with
-// the rows as its M = 16, straight from what the asynchronous copies bring.
+//     rings of asynchronous copies.  In calls of few rows its CTAs fit beside shrink's, so
+//     that their grouping and first copies are done when shrink ends.
+// Tall tiles run on tcgen05 (M = 128 rows of the tile), low ones on the warp MMA with the rows
+// as its M = 16, straight from what the asynchronous copies bring.
+//
+// What bounds it (one GB300, calls in a row in a graph).  Few rows: the chain of two kernels
+// and their dependent loads, 7.1 us for one row, rank 16, beside qkv (0.8 MB), of which the
+// grouping is 1, the loads of A 1.5, the sums' meeting 1.5, t and the outputs 1.5; 64 rows of
+// 32 adapters beside gate+up 21.8 us, of which the adapters' 46 MB are 7 to 8.  Many rows:
+// the bytes of y, 152 to 158 us for 4096 rows, rank 64, beside gate+up (643 MB, 4.1 to 4.2
+// TB/s): shrink 20, then expand, where copies alone would take about 105 and products and
+// outputs alone about 90, which one CTA per SM, in step at a barrier per 128 columns, overlaps
+// in part.  With the tall tiles on the warp MMA the same call took 189 to 221 us.
 //
 // t is fp32; as expand's operand it is split into two values of the 16-bit type, the value
 // rounded and the rest rounded, of a row first scaled by a power of two to at most 2: 16
@@ -745,8 +754,8 @@ __device__ void copy_rows(const LoraArgs &a, const uint16_t *rows, int n) {
 
 // A tall tile, columns n0 <= n < n1 of a part, 128 at a time: the products of a step are
 // issued a step ahead of its outputs.  The residual lies in the stage where the outputs
-// take its place, row by row, and leave in whole sectors.  (256 bytes of a row at a time:
-// with steps of 64 columns the same kernel ran at 2.8 TB/s, XX.)
+// take its place, row by row, and leave in whole sectors.  (Steps of 64 columns, 128 bytes of
+// a row at a time, in two CTAs of 8 warps per SM: 189 us for 160, 4096 rows beside gate+up.)
 template <bool kBf16, int RK, bool kVec>
 __device__ void expand_tall(const LoraArgs &a, const uint16_t *order, const Tile &t, int part,
                             int n0, int n1, uint8_t *smem, Products &pr) {
