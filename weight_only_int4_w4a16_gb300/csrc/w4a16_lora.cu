@@ -735,20 +735,26 @@ __device__ __forceinline__ uint4 add_cells(uint4 r, const float (&v)[8]) {
     return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// Rows without an adapter: those of `rows` from this CTA's share on, all columns of the
-// residual, or zeros.
+// Rows without an adapter: all columns of the residual, or zeros, 1024 at a time for each warp
+// of the grid in turn.
 template <int kCta, bool kVec>
 __device__ void copy_rows(const LoraArgs &a, const uint16_t *rows, int n) {
     if (a.residual == a.y) return;
-    const int cells = (a.N + 7) / 8;
-    const long long all = (long long)n * cells;
-    for (long long i = (long long)blockIdx.x * kCta + threadIdx.x; i < all;
-         i += (long long)gridDim.x * kCta) {
-        const int r = (int)(i / cells), c = (int)(i - (long long)r * cells) * 8;
+    constexpr int kCols = 1024;
+    const int lane = threadIdx.x & 31, pieces = (a.N + kCols - 1) / kCols;
+    const long long all = (long long)n * pieces;
+    for (long long i = (long long)blockIdx.x * (kCta / 32) + (threadIdx.x >> 5); i < all;
+         i += (long long)gridDim.x * (kCta / 32)) {
+        const int r = (int)(i / pieces), c = (int)(i - (long long)r * pieces) * kCols + lane * 8;
         const size_t at = (size_t)rows[r] * a.N + c;
-        store_cells<kVec>(a.y + at, a.N - c,
-                          a.residual ? load_cells<kVec>(a.residual + at, a.N - c)
-                                     : make_uint4(0, 0, 0, 0));
+        uint4 v[kCols / 256];
+#pragma unroll
+        for (int j = 0; j < kCols / 256; ++j)
+            v[j] = a.residual ? load_cells<kVec>(a.residual + at + j * 256, a.N - c - j * 256)
+                              : make_uint4(0, 0, 0, 0);
+#pragma unroll
+        for (int j = 0; j < kCols / 256; ++j)
+            store_cells<kVec>(a.y + at + j * 256, a.N - c - j * 256, v[j]);
     }
 }
 
@@ -882,14 +888,18 @@ __device__ void expand_tall(const LoraArgs &a, const uint16_t *order, const Tile
     // out[i]: where row i * 8 + lane / 4 of them lies in y
     const int quarter = (warp & 3) * 32, side = (warp >> 2) * 32;
     const int mine = quarter + lane;
-    size_t out[4];
+    uint16_t *out[4];
     bool there[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const int r = quarter + i * 8 + (lane >> 2);
         there[i] = r < t.count;
-        out[i] = (there[i] ? (size_t)order[r] * a.N : 0) + n0;
+        out[i] = a.y + (there[i] ? (size_t)order[r] * a.N : 0) + n0 + side + (lane & 3) * 8;
     }
+    // in a residual stage (whose address is a multiple of 1024): piece i of the lane's row is at
+    // own ^ i * 16, its piece of row i * 8 + lane / 4 at shared + i * 1024
+    const uint32_t own = cell(mine, side >> 3),
+                   shared = cell(quarter + (lane >> 2), (side >> 3) + (lane & 3));
     wait_copies<kBs - 1 + kRs - 1>();  // the first step's B
     dev::fence_async_shared();
     __syncthreads();
@@ -929,7 +939,7 @@ __device__ void expand_tall(const LoraArgs &a, const uint16_t *order, const Tile
         uint4 r[4];  // (all loads, then the arithmetic: their latency shows)
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-            r[i] = a.residual ? lds128(st + cell(mine, (side >> 3) + i)) : make_uint4(0, 0, 0, 0);
+            r[i] = a.residual ? lds128((st + own) ^ (i << 4)) : make_uint4(0, 0, 0, 0);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             float w[8];
@@ -938,17 +948,15 @@ __device__ void expand_tall(const LoraArgs &a, const uint16_t *order, const Tile
             r[i] = add_cells<kBf16>(r[i], w);
         }
 #pragma unroll
-        for (int i = 0; i < 4; ++i) sts128(st + cell(mine, (side >> 3) + i), r[i]);
+        for (int i = 0; i < 4; ++i) sts128((st + own) ^ (i << 4), r[i]);
         __syncwarp();
         if constexpr (kVec) {
-            const int c = lane & 3;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) r[i] = lds128(st + shared + i * 1024);
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-                r[i] = lds128(st + cell(quarter + i * 8 + (lane >> 2), (side >> 3) + c));
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                if (there[i] && c * 8 < left)
-                    *reinterpret_cast<uint4 *>(a.y + out[i] + n + c * 8) = r[i];
+                if (there[i] && (lane & 3) * 8 < left)
+                    *reinterpret_cast<uint4 *>(out[i] + s * kTallCols) = r[i];
         } else {
 #pragma unroll 8
             for (int i = 0; i < 32; ++i) {
