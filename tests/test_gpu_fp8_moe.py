@@ -184,3 +184,31 @@ def test_routed_layer_beside_the_4_bit_experts_calls(w4):
     srt, pos, off = w4.w4a16_moe_align(ids, E)
     assert int(off[-1]) == T * k
     assert w4.w4a16_device_status() == 0
+
+
+def test_weights_beyond_32_bits(w4):
+    # 8.6 GB of gate and up: the last expert's offset does not fit 32 bits
+    T, E, K, I, N = 3, 1024, 4096, 1024, 40
+    used = [0, 700, E - 1]
+    x, ids, weights, w1, s1, w2, s2 = ref.make_experts(11, T, 1, 3, K, I, N, BF16)
+
+    def spread(t):
+        out = torch.zeros((E, *t.shape[1:]), dtype=t.dtype, device=DEV)
+        for i, e in enumerate(used):
+            out.view(torch.uint8 if t.element_size() == 1 else t.dtype)[e] = (
+                t[i].view(torch.uint8) if t.element_size() == 1 else t[i]).to(DEV)
+        return out
+
+    ids[:, 0] = torch.tensor([0, 1, 2], dtype=torch.int32)
+    far = torch.tensor(used, dtype=torch.int32)[ids.long()]
+    out = w4.w4a16_fp8_moe_mlp(x.to(DEV), far.to(DEV), weights.to(DEV), *map(spread, (w1, s1, w2, s2)))
+    check(out, *ref.experts(x, ids, weights, w1, s1, w2, s2, BF16))
+
+
+@pytest.mark.parametrize("T", [1, 8])
+def test_one_expert_for_everything(w4, T):
+    # all choices on one expert: more slots than a tile of that many tokens holds
+    k, E, K, I, N = 8, 16, 256, 128, 64
+    ops = list(ref.make_experts(12, T, k, E, K, I, N, F16))
+    ops[1][:] = 9
+    check(w4.w4a16_fp8_moe_mlp(*dev(ops)), *ref.experts(*ops, F16))

@@ -50,7 +50,7 @@ SHAPES = [  # M, K, parts, L, R
     (16, 256, (384, 384), 2, 32), (17, 264, (96, 40, 8, 16), 1, 40), (33, 1024, (520,), 40, 16),
     (37, 1040, (1021,), 5, 56), (64, 2048, (768, 768), 32, 16), (100, 384, (257,), 1, 128),
     (129, 136, (200,), 1, 72), (145, 520, (136, 264), 2, 8), (256, 1000, (512,), 3, 64),
-    (300, 640, (640, 128, 128), 4, 48), (1000, 256, (320,), 6, 64), (1025, 64, (72,), 1024, 8),
+    (200, 256, (136,), 2, 128), (300, 640, (640, 128, 128), 4, 48), (1000, 256, (320,), 6, 64), (1025, 64, (72,), 1024, 8),
     (4100, 128, (136,), 3, 16),
 ]
 
@@ -241,4 +241,21 @@ def test_beside_the_projections(w4, M):
         check(out, ops, dict(parts=parts, ranks=None, residual=res.cpu()), BF16)
     want = fp8_reference.linear(q.cpu(), qs.cpu(), f8.cpu(), ws.cpu())[0]
     assert np.all(np.abs(ref.f64(y8) - want) <= 2.0 ** -7 * np.abs(want).max())
+    assert w4.w4a16_device_status() == 0
+
+
+def test_outputs_beyond_32_bits(w4):
+    # 65535 rows of 34816: 4.6 GB of y, elements past 2^31; rows of all parts, compared where
+    # they lie at both ends and around the limit
+    M, K, parts, L, R = 65535, 64, (17408, 17408), 2, 8
+    rows = [0, 1, 61679, 61680, 65533, 65534]  # 2^31 / 34816 = 61680.9
+    ops, kw = ref.make_adapters(10, len(rows), K, parts, L, R, BF16,
+                                ids=torch.tensor([0, 1, 0, 1, -1, 1], dtype=torch.int32))
+    x = torch.randn((M, K), device=DEV).to(BF16)
+    ids = torch.arange(M, dtype=torch.int32, device=DEV) % 3 - 1
+    y = torch.zeros((M, 2 * 17408), dtype=BF16, device=DEV)
+    x[rows], ids[rows], y[rows] = ops[0].to(DEV), ops[4].to(DEV), kw["residual"].to(DEV)
+    w4.w4a16_lora(x, ops[1].to(DEV), ops[2].to(DEV), ops[3].to(DEV), ids, parts=parts, residual=y,
+                  y=y)
+    check(y[rows], ops, kw, BF16)
     assert w4.w4a16_device_status() == 0
