@@ -506,8 +506,8 @@ int w4a16_moe_route(const void *logits, int T, int E, int k, int dtype, int scor
  *                  calls that share none may overlap
  * Weights and activations enter the products exactly; sums are fp32 (a block's first, then
  * times its scale); silu(gate) * up is rounded once to `dtype` (fp16: beyond 65504 to Inf),
- * out once.  The bits of a row do not depend on the other rows' order in a tile, but the
- * order of the sums over K goes by the number of tokens and experts in use.
+ * out once.  The bits of a row do not depend on the other rows, but the order of the sums
+ * over K goes by the call's sizes.
  * T * k <= 1024 and E <= 1024 (W4A16_ERR_UNSUPPORTED above); T = 0 is an empty batch, as
  * in the calls above; K and I multiples of 16, 1 <= N, all at most 2^22.  x and weights
  * 16-byte aligned, out 2-byte, the others 4-byte; out and scratch overlap nothing.  Needs
@@ -538,8 +538,8 @@ int w4a16_fp8_moe_mlp(const uint16_t *x, const int32_t *topk_ids, const float *w
  *                that share none may overlap
  * Sums are fp32; A x enters the second product as two values of the 16-bit type (16 bits of
  * it in bf16, 22 in fp16, of the row's largest); y is rounded once.  Two kernels, three above 1024 rows.  A row's
- * bits do not depend on its place in the batch, but the order of the sums over K goes by
- * how many rows the adapters have.  K and R multiples of 8, K and N at most 2^22, 0 <= M
+ * bits do not depend on its place in the batch, but the order of its sums goes by how many
+ * rows the call and its adapter have.  K and R multiples of 8, K and N at most 2^22, 0 <= M
  * <= 65535 (0: an empty batch); L <= 1024, R <= 128, n_parts <= 4 (W4A16_ERR_UNSUPPORTED
  * above).  x, a and b 16-byte aligned, y and residual 2-byte, the others 4-byte; y and
  * scratch overlap nothing else.  Needs w4a16_init; allocates nothing and may be captured. */

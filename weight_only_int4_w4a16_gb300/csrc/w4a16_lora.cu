@@ -30,8 +30,8 @@
 // and their dependent loads, 7.1 us for one row, rank 16, beside qkv (0.8 MB), of which the
 // grouping is 1, the loads of A 1.5, the sums' meeting 1.5, t and the outputs 1.5; 64 rows of
 // 32 adapters beside gate+up 21.8 us, of which the adapters' 46 MB are 7 to 8.  Many rows:
-// the bytes of y, 152 to 158 us for 4096 rows, rank 64, beside gate+up (643 MB, 4.1 to 4.2
-// TB/s): shrink 20, then expand, where copies alone would take about 105 and products and
+// the bytes of y, 149 us for 4096 rows, rank 64, beside gate+up (643 MB, 4.3 TB/s): the
+// grouping, shrink 20, then expand 122, where copies alone would take about 105 and products and
 // outputs alone about 90, which one CTA per SM, in step at a barrier per 128 columns, overlaps
 // in part.  With the tall tiles on the warp MMA the same call took 189 to 221 us.
 //
@@ -761,7 +761,9 @@ __device__ void copy_rows(const LoraArgs &a, const uint16_t *rows, int n) {
 // A tall tile, columns n0 <= n < n1 of a part, 128 at a time: the products of a step are
 // issued a step ahead of its outputs.  The residual lies in the stage where the outputs
 // take its place, row by row, and leave in whole sectors.  (Steps of 64 columns, 128 bytes of
-// a row at a time, in two CTAs of 8 warps per SM: 189 us for 160, 4096 rows beside gate+up.)
+// a row at a time, in two CTAs of 8 warps per SM: 189 us for 160, 4096 rows beside gate+up.
+// Without the barrier per step, each warp with its own cells of the residual, 64 bytes of a
+// row, and a further warp for B and the products: 160 for 149.)
 template <bool kBf16, int RK, bool kVec>
 __device__ void expand_tall(const LoraArgs &a, const uint16_t *order, const Tile &t, int part,
                             int n0, int n1, uint8_t *smem, Products &pr) {
