@@ -212,3 +212,11 @@ def test_one_expert_for_everything(w4, T):
     ops = list(ref.make_experts(12, T, k, E, K, I, N, F16))
     ops[1][:] = 9
     check(w4.w4a16_fp8_moe_mlp(*dev(ops)), *ref.experts(*ops, F16))
+
+
+@pytest.mark.parametrize("T,k", [(3, 2), (64, 8)])
+def test_no_choice_at_all(w4, T, k):
+    ops = list(ref.make_experts(13, T, k, 8, 128, 64, 48, BF16))
+    ops[1][:] = -1
+    out = w4.w4a16_fp8_moe_mlp(*dev(ops), out=torch.full((T, 48), 7.0, dtype=BF16, device=DEV))
+    assert bool((out == 0).all())
