@@ -579,6 +579,14 @@ int w4a16_plan_info(int M, int N, int K, int group, int epilogue, int dtype, int
  * not take (or M = 0, or a null info). */
 int w4a16_fp8_plan_info(int M, int N, int K, int32_t *info);
 
+/* How w4a16_fp8_moe_mlp would cut its products for these sizes now: info[0] 8-column tiles
+ * side by side (1, 2 or 4) and info[1] blocks of 128 of K per stage (1, 2, 4 or 8, the warps
+ * that share a row's sum) of gate and up, info[2] and info[3] of down, info[4] CTAs in each
+ * launch, info[5] CTAs of these two kernels that an SM holds at once, the smaller number (0
+ * before w4a16_init).  Pure host query; before w4a16_init it assumes 152 SMs.  INVALID_ARG
+ * or UNSUPPORTED as the call itself (and for T = 0 or a null info). */
+int w4a16_fp8_moe_plan_info(int T, int k, int E, int K, int I, int N, int32_t *info);
+
 /* Force a rung for later calls (W4A16_RUNG_AUTO restores the table).  A forced
  * rung that cannot run a shape makes that call return W4A16_ERR_UNSUPPORTED.
  * Returns the previous setting, or -2 for an invalid rung.  Host state only:

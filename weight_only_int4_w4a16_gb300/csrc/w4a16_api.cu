@@ -1559,6 +1559,17 @@ int w4a16_fp8_plan_info(int M, int N, int K, int32_t *info) {
     return W4A16_OK;
 }
 
+int w4a16_fp8_moe_plan_info(int T, int k, int E, int K, int I, int N, int32_t *info) {
+    if (!info || T < 1 || k < 1 || E < 1 || K < 1 || I < 1 || N < 1 || K > kMaxK || I > kMaxK ||
+        N > kMaxK || K % 16 != 0 || I % 16 != 0)
+        return W4A16_ERR_INVALID_ARG;
+    if (E > kMaxMoeExperts || (long long)T * k > kFp8MoeMaxSlots) return W4A16_ERR_UNSUPPORTED;
+    DeviceInfo dev = g_state.dev;
+    if (!g_state.initialized) dev.sm_count = 152;
+    fp8_moe_plan(T, k, E, K, I, N, dev, info);
+    return W4A16_OK;
+}
+
 int w4a16_set_forced_rung(int rung) {
     if (rung < W4A16_RUNG_AUTO || rung >= W4A16_NUM_RUNGS) return -2;
     std::lock_guard<std::mutex> lock(g_mutex);

@@ -49,7 +49,6 @@ constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kStages = 4;
 constexpr int kStageWeights = 16 << 10;  // bytes
-constexpr int kRingBytes = 100 << 10;    // so that two CTAs share an SM
 
 // two e4m3 codes -> two 16-bit values, exact
 template <bool kBf16>
@@ -74,7 +73,17 @@ using Sort = RowSort<kFp8MoeMaxSlots>;
 // slots of a tile: 8 NT, fewer where a stage of KS blocks leaves no room for them
 template <int NT, int KS>
 constexpr int kCap = 8 * NT * KS <= 32 ? 8 * NT : 32 / KS;
-static_assert(kMaxMoeExperts <= kMaxBins && sizeof(Sort) <= kRingBytes, "the sort fits the ring");
+// bytes of a stage: the weights, the columns' activations, the scales
+template <int NT, int KS>
+constexpr int kStageBytes = kStageWeights + kCap<NT, KS> * 256 * KS + 128;
+// The kernel's dynamic shared memory: the stages, where the slots are sorted before.  No more
+// than that, so that two CTAs share an SM: NT 2, KS 2 with its 15 KB of tables and sums, too
+// (40 tokens, 2 of 8 experts, 2048 -> 2 x 1024 -> 2048: 20.4 us, with 100 KB for every cut 27.6).
+template <int NT, int KS>
+constexpr int kRingBytes = kStages * kStageBytes<NT, KS> > (int)sizeof(Sort)
+                               ? kStages * kStageBytes<NT, KS>
+                               : (int)sizeof(Sort);
+static_assert(kMaxMoeExperts <= kMaxBins, "the sort holds every expert");
 
 // The slots by expert, in tiles of up to cap slots; how many tiles.  An id outside [0, E)
 // leaves its slot out; one other than -1 is reported.
@@ -118,8 +127,7 @@ __global__ void __launch_bounds__(kThreads, 2) experts_kernel(Fp8ExpertsArgs a) 
 
     constexpr int ks_log = KS == 8 ? 3 : KS == 4 ? 2 : KS == 2 ? 1 : 0;
     constexpr int per = (kSilu ? 64 : 128) / KS;  // rows of results of a unit
-    constexpr int x_bytes = kCap<NT, KS> * 256 * KS, stage_bytes = kStageWeights + x_bytes + 128;
-    static_assert(kStages * stage_bytes <= kRingBytes, "the stages fit the ring");
+    constexpr int x_bytes = kCap<NT, KS> * 256 * KS, stage_bytes = kStageBytes<NT, KS>;
     const int blocks = (a.rows + per - 1) / per, units = n_tiles * blocks;
     const int ksteps = (a.K + 128 * KS - 1) / (128 * KS);
     const int mine = blockIdx.x < units ? (units - 1 - (int)blockIdx.x) / (int)gridDim.x + 1 : 0;
@@ -379,8 +387,8 @@ Cut cut_of(double used, double each, int T, int rows_per_unit, int rows, int K, 
 template <bool kBf16, bool kSilu, int NT, int KS>
 cudaError_t launch_cut(Fp8ExpertsArgs &p, int grid, cudaStream_t stream) {
     p.cap = p.T < 8 * NT ? p.T : 8 * NT;
-    return launch_chained(experts_kernel<kBf16, NT, KS, kSilu>, dim3(grid), kThreads, kRingBytes, 1,
-                          stream, p);
+    return launch_chained(experts_kernel<kBf16, NT, KS, kSilu>, dim3(grid), kThreads,
+                          kRingBytes<NT, KS>, 1, stream, p);
 }
 template <bool kBf16, bool kSilu>
 cudaError_t launch_product(Fp8ExpertsArgs p, Cut cut, int grid, cudaStream_t stream) {
@@ -395,47 +403,61 @@ cudaError_t launch_product(Fp8ExpertsArgs p, Cut cut, int grid, cudaStream_t str
     }
 }
 
+struct Plan {
+    Cut gate_up, down;
+    int grid;
+};
+Plan plan_of(int T, int k, int E, int K, int I, int N, const DeviceInfo &dev) {
+    const int grid = 2 * dev.sm_count;
+    const double used = E * (1.0 - pow(1.0 - fmin(1.0, (double)k / E), T)), each = T * k / used;
+    return {cut_of(used, each, T, 64, I, K, grid), cut_of(used, each, T, 128, N, I, grid), grid};
+}
+
 template <bool kBf16>
 cudaError_t launch_type(const Fp8MoeArgs &a, const DeviceInfo &dev, int *status,
                         cudaStream_t stream) {
-    const int grid = 2 * dev.sm_count;
-    const double used = a.E * (1.0 - pow(1.0 - fmin(1.0, (double)a.k / a.E), a.T)),
-                 each = a.T * a.k / used;
+    const Plan plan = plan_of(a.T, a.k, a.E, a.K, a.I, a.N, dev);
     uint16_t *h = static_cast<uint16_t *>(a.scratch);
     float *o = reinterpret_cast<float *>(static_cast<char *>(a.scratch) +
                                          fp8_moe_h_bytes(a.T, a.k, a.I));
     cudaError_t e = launch_product<kBf16, true>(
         {a.x, a.w1, a.s1, a.ids, h, nullptr, status, a.T, a.k, a.E, a.K, a.I, 2 * a.I, 0},
-        cut_of(used, each, a.T, 64, a.I, a.K, grid), grid, stream);
+        plan.gate_up, plan.grid, stream);
     if (e != cudaSuccess) return e;
     e = launch_product<kBf16, false>(
         {h, a.w2, a.s2, a.ids, nullptr, o, status, a.T, a.k, a.E, a.I, a.N, a.N, 0},
-        cut_of(used, each, a.T, 128, a.N, a.I, grid), grid, stream);
+        plan.down, plan.grid, stream);
     if (e != cudaSuccess) return e;
     return launch_chained(combine_kernel<kBf16>, dim3((a.N + 255) / 256, a.T), 256, 0, 1, stream,
                           (const float *)o, a.ids, a.weights, a.T, a.k, a.E, a.N, a.out);
 }
 
-template <bool kBf16, int NT, int KS>
-cudaError_t init_split() {
-    const void *kernels[] = {(const void *)experts_kernel<kBf16, NT, KS, true>,
-                             (const void *)experts_kernel<kBf16, NT, KS, false>};
-    for (const void *k : kernels) {
-        cudaError_t e =
-            cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kRingBytes);
-        if (e != cudaSuccess) return e;
-    }
-    return cudaSuccess;
+// CTAs of each cut's kernels that an SM holds at once, the fewest of both types (set by
+// fp8_moe_init)
+int resident[2][5][9];  // [gate and up][NT][KS]
+
+template <bool kBf16, bool kSilu, int NT, int KS>
+cudaError_t init_cut() {
+    const auto kernel = experts_kernel<kBf16, NT, KS, kSilu>;
+    cudaError_t e = cudaFuncSetAttribute((const void *)kernel,
+                                         cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         kRingBytes<NT, KS>);
+    int n = 0;
+    if (e == cudaSuccess)
+        e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kernel, kThreads, kRingBytes<NT, KS>);
+    int &r = resident[kSilu][NT][KS];
+    if (e == cudaSuccess && (r == 0 || n < r)) r = n;
+    return e;
 }
-template <bool kBf16>
-cudaError_t init_type() {
-    cudaError_t e = init_split<kBf16, 1, 1>();
-    if (e == cudaSuccess) e = init_split<kBf16, 1, 2>();
-    if (e == cudaSuccess) e = init_split<kBf16, 1, 4>();
-    if (e == cudaSuccess) e = init_split<kBf16, 1, 8>();
-    if (e == cudaSuccess) e = init_split<kBf16, 2, 1>();
-    if (e == cudaSuccess) e = init_split<kBf16, 2, 2>();
-    if (e == cudaSuccess) e = init_split<kBf16, 4, 1>();
+template <bool kBf16, bool kSilu>
+cudaError_t init_product() {
+    cudaError_t e = init_cut<kBf16, kSilu, 1, 1>();
+    if (e == cudaSuccess) e = init_cut<kBf16, kSilu, 1, 2>();
+    if (e == cudaSuccess) e = init_cut<kBf16, kSilu, 1, 4>();
+    if (e == cudaSuccess) e = init_cut<kBf16, kSilu, 1, 8>();
+    if (e == cudaSuccess) e = init_cut<kBf16, kSilu, 2, 1>();
+    if (e == cudaSuccess) e = init_cut<kBf16, kSilu, 2, 2>();
+    if (e == cudaSuccess) e = init_cut<kBf16, kSilu, 4, 1>();
     return e;
 }
 
@@ -448,8 +470,20 @@ cudaError_t launch_fp8_moe(const Fp8MoeArgs &a, bool bf16, const DeviceInfo &dev
 }
 
 cudaError_t fp8_moe_init() {
-    const cudaError_t e = init_type<true>();
-    return e == cudaSuccess ? init_type<false>() : e;
+    cudaError_t e = init_product<true, true>();
+    if (e == cudaSuccess) e = init_product<true, false>();
+    if (e == cudaSuccess) e = init_product<false, true>();
+    if (e == cudaSuccess) e = init_product<false, false>();
+    return e;
+}
+
+void fp8_moe_plan(int T, int k, int E, int K, int I, int N, const DeviceInfo &dev, int32_t *info) {
+    const Plan p = plan_of(T, k, E, K, I, N, dev);
+    info[0] = p.gate_up.nt, info[1] = p.gate_up.ks;
+    info[2] = p.down.nt, info[3] = p.down.ks;
+    info[4] = p.grid;
+    const int a = resident[1][p.gate_up.nt][p.gate_up.ks], b = resident[0][p.down.nt][p.down.ks];
+    info[5] = a < b ? a : b;
 }
 
 }  // namespace w4a16

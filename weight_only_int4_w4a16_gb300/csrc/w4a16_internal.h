@@ -413,6 +413,8 @@ struct Fp8ExpertsArgs {
 cudaError_t launch_fp8_moe(const Fp8MoeArgs &a, bool bf16, const DeviceInfo &dev, int *status,
                            cudaStream_t stream);
 cudaError_t fp8_moe_init();
+// as w4a16_fp8_moe_plan_info gives it
+void fp8_moe_plan(int T, int k, int E, int K, int I, int N, const DeviceInfo &dev, int32_t *info);
 
 // ---- low-rank adapters (w4a16_lora.cu) ----------------------------------------
 constexpr int kMaxAdapters = 1024;
