@@ -505,8 +505,8 @@ int w4a16_moe_route(const void *logits, int T, int E, int k, int dtype, int scor
  *                  call's own until its work is done (W4A16_ERR_WORKSPACE if fewer);
  *                  calls that share none may overlap
  * Weights and activations enter the products exactly; sums are fp32 (a block's first, then
- * times its scale); silu(gate) * up is rounded once to `dtype` (fp16: beyond 65504 to Inf),
- * out once.  The bits of a row do not depend on the other rows, but the order of the sums
+ * times its scale); silu(gate) * up enters down as two bf16 values, 16 bits of it at fp32's
+ * range, whatever `dtype` is; out is rounded once.  The bits of a row do not depend on the other rows, but the order of the sums
  * over K goes by the call's sizes.
  * T * k <= 1024 and E <= 1024 (W4A16_ERR_UNSUPPORTED above); T = 0 is an empty batch, as
  * in the calls above; K and I multiples of 16, 1 <= N, all at most 2^22.  x and weights

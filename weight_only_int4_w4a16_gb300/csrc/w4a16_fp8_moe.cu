@@ -8,31 +8,36 @@
 // per block of 128 x 128, activations 16 bits.
 //
 // Three kernels: gate and up with silu-and-mul, down, the weighted sum.  Both products are
-// one kernel, experts_kernel.  A tile is up to 8 NT slots of one expert; a unit is a tile
-// and 16 * 8 / KS rows of the expert's weights, whose K a CTA walks in stages of KS blocks
-// of 128: a warp has 16 rows (for gate and up: 8 gate rows and their 8 up rows, so that a
-// lane holds a gate sum and its up sum) and one of the stage's KS blocks, and the KS warps
-// of the same rows add their sums at the unit's end.  So every stage brings 16 KB of
+// one kernel, experts_kernel.  A tile is up to 8 NT columns of one expert, a slot each (of
+// down two, see below); a unit is a tile and 16 * 8 / KS rows of the expert's weights, whose K
+// a CTA walks in stages of KS blocks of 128: a warp has 16 rows (for gate and up: 8 gate rows
+// and their 8 up rows, so that a lane holds a gate sum and its up sum) and one of the stage's
+// KS blocks, and the KS warps of the same rows add their sums at the unit's end.  So every stage brings 16 KB of
 // weights in runs of 128 KS bytes of a row, and a unit is small (KS 8) where there are few
 // tiles.  The weights are the warp MMA's M, the tokens its N: a decode step's experts see
 // one to a few tokens each, and the bytes of the weights bound the layer, not the products
 // (8 tokens need 1/16 of what the warp MMA can do while the weights arrive).
 //
 // e4m3 codes become the 16-bit type exactly (through fp16, which holds all of them); the
-// products of a block are summed in fp32, scaled once and added in fp32.  h is rounded to
-// the 16-bit type, the tensor cores' operand for down; down's sums stay fp32 up to the one
-// rounding of out.
+// products of a block are summed in fp32, scaled once and added in fp32.  h enters down as two
+// bf16 values, the value rounded and the rest rounded, whatever the layer's type: 16 bits of
+// it at fp32's range (fp16 would end at 65504).  They are two neighbouring columns of down's
+// tile, whose sums one lane holds; so a tile of few slots costs no further products.  down's
+// sums stay fp32 up to the one rounding of out.
 //
 // Every CTA groups the slots itself (a stable counting sort in shared memory, or one warp's
 // work up to 32 slots), which costs it no launch and no pass through memory.
 //
 // What bounds it (one GB300, calls in a row in a graph; 128 experts, 8 each, 2048 -> 2 x 768
-// -> 2048).  64 tokens, bf16: 109 us, 595 MB at 5.5 TB/s, 80% of the measured copy rate; the
+// -> 2048).  64 tokens, bf16: 113 us, 595 MB at 5.3 TB/s, 78% of the measured copy rate; the
 // issue slots (the codes' way to bf16 is four instructions a pair, for fp16 one) and the
-// barrier per stage (with the products switched off 99 us).  8 tokens, fp16: 46.9 us, 5.2
-// TB/s.  One token: 13.9 us for 38 MB, of which the weights' stream is 6; the rest are the
-// ids' load, the grouping and the first weights' latency, twice, and the sum.
-// Tried and not kept: bf16 activations scaled to fp16 in the stage (30% fewer instructions,
+// barrier per stage (with the products switched off, h in one value, 99 us).  8 tokens, fp16:
+// 48.9 us, 5.0 TB/s.  One token: 14.2 us for 38 MB, of which the weights' stream is 6; the rest
+// are the ids' load, the grouping and the first weights' latency, twice, and the sum.
+// With h rounded once to the 16-bit type these took 109, 46.9 and 13.9 us, and out's error was
+// 1.4 to 1.5 times that of h in fp32 (now the same to four digits); with the two values in
+// tiles of their own 114, 50.5 and 14.4.
+// Tried and not kept, with h in one value: bf16 activations scaled to fp16 in the stage (30% fewer instructions,
 // but on every stage's critical path: 124 us at 64 tokens for 115), five or six stages (no
 // change: the bytes in flight are enough), one CTA per SM (205), the sum by the last of down's
 // units (one token 15.1 for 13.9).
@@ -70,7 +75,7 @@ struct Tables {
     int tiles;
 };
 using Sort = RowSort<kFp8MoeMaxSlots>;
-// slots of a tile: 8 NT, fewer where a stage of KS blocks leaves no room for them
+// columns of a tile: 8 NT, fewer where a stage of KS blocks leaves no room for them
 template <int NT, int KS>
 constexpr int kCap = 8 * NT * KS <= 32 ? 8 * NT : 32 / KS;
 // bytes of a stage: the weights, the columns' activations, the scales
@@ -110,7 +115,20 @@ __device__ int make_tiles(Tables &tb, Sort &sp, const int32_t *ids, int S, int E
     return tb.tiles;
 }
 
-// kSilu: gate and up, x by token, h by slot; else down, h by slot, o (fp32) by slot
+// v as two bf16 values; the largest finite ones, whose nearest bf16 is Inf, stay finite
+__device__ __forceinline__ void halves(float v, uint16_t &hi, uint16_t &lo) {
+    __nv_bfloat16 h = __float2bfloat16_rn(v);
+    float rest = v - __bfloat162float(h);
+    if (__hisinf(h)) {
+        h = __float2bfloat16_rz(v);  // (of Inf Inf)
+        rest = isinf(v) ? 0.f : __bfloat162float(__float2bfloat16_rz(v - __bfloat162float(h)));
+    }
+    hi = __bfloat16_as_ushort(h);
+    lo = __bfloat16_as_ushort(__float2bfloat16_rn(rest));
+}
+
+// kSilu: gate and up, x by token, h by slot; else down, h by slot, o (fp32) by slot.  h is
+// two rows of bf16 per slot, the values and the rests.
 template <bool kBf16, int NT, int KS, bool kSilu>
 __global__ void __launch_bounds__(kThreads, 2) experts_kernel(Fp8ExpertsArgs a) {
     extern __shared__ __align__(128) uint8_t ring[];
@@ -177,11 +195,11 @@ __global__ void __launch_bounds__(kThreads, 2) experts_kernel(Fp8ExpertsArgs a) 
         const int tile = unit / blocks, first = tb.tile_first[tile], n = tb.tile_count[tile];
 #pragma unroll
         for (int i = 0; i < kX; ++i) {
-            const int r = xr + i * (16 >> ks_log);
+            const int r = xr + i * (16 >> ks_log), tok = kSilu ? r : r >> 1;
             xp[i] = nullptr;
-            if (r < n) {
-                const int s = tb.slot[first + r];
-                xp[i] = a.x + (size_t)(kSilu ? s / a.k : s) * a.K + xc * 8;
+            if (tok < n) {
+                const int s = tb.slot[first + tok];
+                xp[i] = a.x + (size_t)(kSilu ? s / a.k : 2 * s + (r & 1)) * a.K + xc * 8;
             }
         }
     };
@@ -264,11 +282,11 @@ __global__ void __launch_bounds__(kThreads, 2) experts_kernel(Fp8ExpertsArgs a) 
             uint32_t b[NT][8];
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
-                const int tok = min(n * 8 + g, kCap<NT, KS> - 1);
-                const uint32_t xp = st + kStageWeights + (tok << (8 + ks_log));
+                const int col = min(n * 8 + g, kCap<NT, KS> - 1);
+                const uint32_t xp = st + kStageWeights + (col << (8 + ks_log));
                 const int c16 = ks * 16 + h * 8 + c * 2;
-                const uint4 b0 = lds128(xp + ((c16 ^ (tok & 1)) << 4)),
-                            b1 = lds128(xp + (((c16 + 1) ^ (tok & 1)) << 4));
+                const uint4 b0 = lds128(xp + ((c16 ^ (col & 1)) << 4)),
+                            b1 = lds128(xp + (((c16 + 1) ^ (col & 1)) << 4));
                 b[n][0] = b0.x, b[n][1] = b0.y, b[n][2] = b0.z, b[n][3] = b0.w;
                 b[n][4] = b1.x, b[n][5] = b1.y, b[n][6] = b1.z, b[n][7] = b1.w;
             }
@@ -313,24 +331,25 @@ __global__ void __launch_bounds__(kThreads, 2) experts_kernel(Fp8ExpertsArgs a) 
             const int tile = at.unit / blocks, row0 = (at.unit - tile * blocks) * per;
             const int first = tb.tile_first[tile], count = tb.tile_count[tile];
 #pragma unroll
-            for (int n = 0; n < NT; ++n)
+            for (int n = 0; n < NT; ++n) {
+                if constexpr (kSilu) {
+                    const int j = row0 + rg * 8 + g;
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const int tok = n * 8 + c * 2 + i;
-                    if (tok >= count) continue;
-                    const size_t s = tb.slot[first + tok];
-                    if constexpr (kSilu) {
-                        const int j = row0 + rg * 8 + g;
+                    for (int i = 0; i < 2; ++i) {
+                        const int tok = n * 8 + c * 2 + i;
+                        if (tok >= count || j >= a.rows) continue;
                         const float gate = tot[n][i], up = tot[n][2 + i];
-                        if (j < a.rows)
-                            a.h[s * a.rows + j] =
-                                float_to_half_bits(gate / (1.f + expf(-gate)) * up, kBf16);
-                    } else {
-                        const int j = row0 + rg * 16 + g;
-                        if (j < a.rows) a.o[s * a.rows + j] = tot[n][i];
-                        if (j + 8 < a.rows) a.o[s * a.rows + j + 8] = tot[n][2 + i];
+                        uint16_t *h = a.h + 2 * (size_t)tb.slot[first + tok] * a.rows + j;
+                        halves(gate / (1.f + expf(-gate)) * up, h[0], h[a.rows]);
                     }
+                } else {
+                    const int tok = n * 4 + c, j = row0 + rg * 16 + g;
+                    if (tok >= count) continue;
+                    float *o = a.o + (size_t)tb.slot[first + tok] * a.rows + j;
+                    if (j < a.rows) o[0] = tot[n][0] + tot[n][1];
+                    if (j + 8 < a.rows) o[8] = tot[n][2] + tot[n][3];
                 }
+            }
         }
 #pragma unroll
         for (int n = 0; n < NT; ++n)
@@ -356,37 +375,41 @@ __global__ void __launch_bounds__(256) combine_kernel(const float *o, const int3
     out[(size_t)t * N + n] = float_to_half_bits(v, kBf16);
 }
 
-// How a product is cut: NT by which slots of an expert share a tile, KS by which a stage's
+// How a product is cut: NT by which columns of an expert share a tile, KS by which a stage's
 // blocks are split among the warps.
 struct Cut {
     int nt, ks;
 };
 // The cut of the smallest cost: the units of the busiest CTA, each its weights' bytes, its
-// activations' and 8 KB for its start and end, a tenth more for each further 8 slots of a
+// activations' and 8 KB for its start and end, a tenth more for each further 8 columns of a
 // tile.  The choices are on the device, so the tiles are those of even choices: `used`
-// experts with `each` slots.  (T 37, 10 experts, 3 each, 1040 -> 2 x 336: 2 and 2, 13.7 us;
-// 4 and 1, by the slots alone, 19.0.)
-Cut cut_of(double used, double each, int T, int rows_per_unit, int rows, int K, int grid) {
+// experts with `each` slots, each so many columns.  (64 tokens, 4 of 16 experts, 2048 -> 2 x
+// 768 -> 2048, bf16: gate and up by NT 2, KS 1 36.9 us, by 1, 1 46.3, by 4, 1 42.2; down by
+// 4, 1 36.9, by 2, 1 38.4, by 1, 1 42.5.  Of twelve such sizes, 1 to 64 tokens and 8 to 128
+// experts, the choice is at most 7% behind the best: 64 tokens, 4 of 8, 34.0 for 31.8.)
+Cut cut_of(double used, double each, int T, int columns, int rows_per_unit, int rows, int K,
+           int grid) {
     Cut best{1, 1};
     double least = INFINITY;
     for (int nt = 1; nt <= 4; nt *= 2) {
-        const int cap = T < 8 * nt ? T : 8 * nt;
+        const int most = 8 / columns * nt, cap = T < most ? T : most;  // slots
         const double tiles = used * (cap == T || each <= 0.6 * cap ? 1.0 : each / cap + 0.5);
-        for (int ks = 1; ks <= 8 / nt && ks * cap <= 32 && ks * nt <= (nt == 1 ? 8 : 4); ks *= 2) {
+        for (int ks = 1; ks * columns * cap <= 32 && ks * nt <= (nt == 1 ? 8 : 4); ks *= 2) {
             const int per = rows_per_unit / ks;
             const double units = tiles * ((rows + per - 1) / per);
             const double cost = ceil(units / grid) * (0.9 + 0.1 * nt) *
-                                (128.0 / ks * K + 2.0 * fmin(cap, each) * K + 8192);
+                                (128.0 / ks * K + 2.0 * columns * fmin(cap, each) * K + 8192);
             if (cost < least) least = cost, best = {nt, ks};
         }
-        if (T <= 8 * nt) break;
+        if (T <= most) break;
     }
     return best;
 }
 
 template <bool kBf16, bool kSilu, int NT, int KS>
 cudaError_t launch_cut(Fp8ExpertsArgs &p, int grid, cudaStream_t stream) {
-    p.cap = p.T < 8 * NT ? p.T : 8 * NT;
+    constexpr int most = (kSilu ? 8 : 4) * NT;
+    p.cap = p.T < most ? p.T : most;
     return launch_chained(experts_kernel<kBf16, NT, KS, kSilu>, dim3(grid), kThreads,
                           kRingBytes<NT, KS>, 1, stream, p);
 }
@@ -410,7 +433,8 @@ struct Plan {
 Plan plan_of(int T, int k, int E, int K, int I, int N, const DeviceInfo &dev) {
     const int grid = 2 * dev.sm_count;
     const double used = E * (1.0 - pow(1.0 - fmin(1.0, (double)k / E), T)), each = T * k / used;
-    return {cut_of(used, each, T, 64, I, K, grid), cut_of(used, each, T, 128, N, I, grid), grid};
+    return {cut_of(used, each, T, 1, 64, I, K, grid), cut_of(used, each, T, 2, 128, N, I, grid),
+            grid};
 }
 
 template <bool kBf16>
@@ -424,7 +448,7 @@ cudaError_t launch_type(const Fp8MoeArgs &a, const DeviceInfo &dev, int *status,
         {a.x, a.w1, a.s1, a.ids, h, nullptr, status, a.T, a.k, a.E, a.K, a.I, 2 * a.I, 0},
         plan.gate_up, plan.grid, stream);
     if (e != cudaSuccess) return e;
-    e = launch_product<kBf16, false>(
+    e = launch_product<true, false>(
         {h, a.w2, a.s2, a.ids, nullptr, o, status, a.T, a.k, a.E, a.I, a.N, a.N, 0},
         plan.down, plan.grid, stream);
     if (e != cudaSuccess) return e;
@@ -471,9 +495,8 @@ cudaError_t launch_fp8_moe(const Fp8MoeArgs &a, bool bf16, const DeviceInfo &dev
 
 cudaError_t fp8_moe_init() {
     cudaError_t e = init_product<true, true>();
-    if (e == cudaSuccess) e = init_product<true, false>();
     if (e == cudaSuccess) e = init_product<false, true>();
-    if (e == cudaSuccess) e = init_product<false, false>();
+    if (e == cudaSuccess) e = init_product<true, false>();
     return e;
 }
 

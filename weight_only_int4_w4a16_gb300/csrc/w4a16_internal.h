@@ -378,7 +378,7 @@ cudaError_t launch_route(const RouteArgs &a, int type, cudaStream_t stream);
 // ---- layers of 8-bit experts for few tokens (w4a16_fp8_moe.cu) ----------------
 constexpr int kFp8MoeMaxSlots = 1024;  // T * k
 // w1 [E, 2I, K], s1 [E, ceil(2I/128), ceil(K/128)], w2 [E, N, I], s2 [E, ceil(N/128),
-// ceil(I/128)]; scratch: h [T k, I] in 16 bits, then o [T k, N] in fp32
+// ceil(I/128)]; scratch: h [T k, 2, I] in bf16 (values, rests), then o [T k, N] in fp32
 struct Fp8MoeArgs {
     const uint16_t *x;
     const int32_t *ids;
@@ -392,13 +392,13 @@ struct Fp8MoeArgs {
     int T, k, E, K, I, N;
 };
 inline size_t fp8_moe_h_bytes(int T, int k, int I) {
-    return ((size_t)T * k * I * 2 + 255) & ~(size_t)255;
+    return ((size_t)T * k * I * 4 + 255) & ~(size_t)255;
 }
 inline size_t fp8_moe_scratch_bytes(int T, int k, int I, int N) {
     return fp8_moe_h_bytes(T, k, I) + (size_t)T * k * N * 4;
 }
 // one of the layer's two products as its kernel reads it: rows [., K] of x (by token, or
-// by slot), weights w [E, w_rows, K], `rows` results per slot into h or o
+// two by slot), weights w [E, w_rows, K], `rows` results per slot into h or o
 struct Fp8ExpertsArgs {
     const uint16_t *x;
     const uint8_t *w;
