@@ -1,6 +1,6 @@
 """What the layer of 8-bit experts (w4a16_fp8_moe_mlp) keeps of h = silu(gate) up between
-its two products: more bits than the 16-bit type has, and a range that is not the 16-bit
-type's.
+its two products: more bits than the 16-bit type has, a range that is not the 16-bit
+type's, and silu's values far below zero.
 
 The operands make gate and up exact: x and the codes are small whole numbers and the scales
 powers of two, so that every sum is a whole number below 2^24 times one, and h's own error
@@ -132,3 +132,38 @@ def test_the_largest_finite_h(w4, dtype):
     out = ref.f64(w4.w4a16_fp8_moe_mlp(*[o.to(DEV) for o in ops]))
     want = np.array(codes) * 64.0 * float(s1[0, 1, 0]) * 2.0 ** -120
     assert np.all(np.abs(out - want) <= (ref.UNIT[dtype] + 2.0 ** -15) * np.abs(want))
+
+
+@pytest.mark.parametrize("dtype", [F16, BF16])
+def test_gates_far_below_zero(w4, dtype):
+    """silu(g) = g e^g / (1 + e^g) does not vanish where 1 + e^-g leaves fp32's range: up is
+    large there, and exact, as every sum has one product."""
+    gates = [-30.0, -60.0, -80.0, -88.0, -96.0, -104.0, -112.0, -128.0, -144.0, -160.0]
+    T, K, I, N = len(gates), 256, 128, 4
+    x = torch.zeros((T, K))
+    x[:, 0] = torch.tensor(gates) / -2.0  # (exact in both types)
+    x[:, 200] = 1.0
+    w1 = torch.zeros((1, 2 * I, K))
+    w1[0, :I, 0] = -2.0
+    w1[0, I:, 200] = 1.0
+    s1 = torch.ones((1, 2, 2))
+    w2 = torch.zeros((1, N, I))
+    w2[0, 0, 5], w2[0, 1, 100], w2[0, 2, :2] = 1.0, -2.0, 0.5
+    ops = [x.to(dtype), torch.zeros((T, 1), dtype=torch.int32), torch.ones((T, 1)),
+           w1.to(torch.float8_e4m3fn), s1, w2.to(torch.float8_e4m3fn), torch.ones((1, 1, 1))]
+    for t, g in enumerate(gates):
+        # up so that h is near 1 (or as large as up can be)
+        up = 2.0 ** min(126, int(-g / np.log(2)) - 4)
+        s1[0, 1, 1] = up
+        out = ref.f64(w4.w4a16_fp8_moe_mlp(*[o.to(DEV) for o in ops]))[t]
+        h = g * np.exp(g) / (1 + np.exp(g)) * up
+        want = h * np.array([1.0, -2.0, 1.0, 0.0])
+        bound = (ref.UNIT[dtype] + 2.0 ** -15) * np.abs(want) + 2.0 ** -24
+        assert np.all(np.abs(out - want) <= bound), (g, out, want)
+    # -Inf is NaN, as in the quotient, and the other rows keep their bits (those of gates near
+    # zero times this up are beyond fp16's range)
+    before = w4.w4a16_fp8_moe_mlp(*[o.to(DEV) for o in ops]).cpu()
+    ops[0][3, 0] = float("inf")
+    out = w4.w4a16_fp8_moe_mlp(*[o.to(DEV) for o in ops]).cpu()
+    rows = [t for t in range(T) if t != 3]
+    assert out[3, :3].isnan().all() and torch.equal(out[rows], before[rows])

@@ -115,6 +115,17 @@ __device__ int make_tiles(Tables &tb, Sort &sp, const int32_t *ids, int S, int E
     return tb.tiles;
 }
 
+// silu(g) u = g u / (1 + e^-g).  Far below zero, where 1 + e^-g is e^-g to fp32's last bit and
+// leaves its range soon, it is g p u p with p = e^(g/2), in an order that neither overflows nor
+// underflows before the result does.  -Inf gives NaN, as the quotient does.
+__device__ __forceinline__ float silu_mul(float g, float u) {
+    if (g < -80.f) {
+        const float p = expf(0.5f * g);
+        return g * p * u * p;
+    }
+    return g / (1.f + expf(-g)) * u;
+}
+
 // v as two bf16 values; the largest finite ones, whose nearest bf16 is Inf, stay finite
 __device__ __forceinline__ void halves(float v, uint16_t &hi, uint16_t &lo) {
     __nv_bfloat16 h = __float2bfloat16_rn(v);
@@ -338,9 +349,8 @@ __global__ void __launch_bounds__(kThreads, 2) experts_kernel(Fp8ExpertsArgs a) 
                     for (int i = 0; i < 2; ++i) {
                         const int tok = n * 8 + c * 2 + i;
                         if (tok >= count || j >= a.rows) continue;
-                        const float gate = tot[n][i], up = tot[n][2 + i];
                         uint16_t *h = a.h + 2 * (size_t)tb.slot[first + tok] * a.rows + j;
-                        halves(gate / (1.f + expf(-gate)) * up, h[0], h[a.rows]);
+                        halves(silu_mul(tot[n][i], tot[n][2 + i]), h[0], h[a.rows]);
                     }
                 } else {
                     const int tok = n * 4 + c, j = row0 + rg * 16 + g;
