@@ -481,7 +481,8 @@ typedef enum {
  * ones by index, and weights [T, k] fp32 = scale * p of the chosen, p as `scoring` names
  * it, divided first by the sum of the chosen p where `renormalize` is not 0.  NaN counts
  * as -Inf, whose p is 0 (a switched-off expert: it is chosen only where fewer than k
- * others are left, and weighs 0, as does a whole row of them); equal +Inf share.
+ * others are left, and weighs 0, as does a whole row of them); equal +Inf share.  The
+ * sigmoid of a logit below -745 counts as 0 too.
  * 1 <= k <= E, 0 <= T <= 65535 (0: nothing is read or launched, and pointers may be
  * NULL); E <= 1024 and k <= 32 (W4A16_ERR_UNSUPPORTED above).  logits aligned to its
  * type, outputs 4-byte and apart from it and each other.  Needs no w4a16_init. */

@@ -9,7 +9,9 @@
 // A NaN counts as -Inf; the p of -Inf is 0, so a switched-off expert that has to be
 // chosen all the same weighs nothing; the p of equal +Inf are equal shares (softmax) or
 // 1.  Everything is fp32: the exponentials' arguments are differences to the row's
-// largest, and the sums are over p of at most 1.
+// largest, and the sums are over p of at most 1.  Sigmoids that are renormalised count in
+// units of e^top where the row's largest is negative, so that their shares outlive their p;
+// below l = -745, where binary64 has no e^l either, p is 0.
 //
 // A warp has a row, each lane every 32nd logit in registers as an integer key that
 // orders as the number does.  A step finds the largest key and the lowest index that
@@ -55,6 +57,13 @@ __device__ __forceinline__ float share(uint32_t key, uint32_t top) {
     return key == top ? 1.f : expf(value_of(key) - value_of(top));
 }
 
+// 1 / (1 + e^-v) in units of e^unit (unit <= 0, and v <= unit where v is negative): e^(v - unit)
+// / (1 + e^v) there
+__device__ __forceinline__ float sigmoid(float v, float unit) {
+    if (v >= 0.f) return 1.f / (1.f + expf(-v));
+    return v > -745.f ? expf(v - unit) / (1.f + expf(v)) : 0.f;
+}
+
 template <int kType, int V>
 __global__ void __launch_bounds__(kRouteWarps * 32) route_kernel(RouteArgs a) {
     const int lane = threadIdx.x & 31;
@@ -98,7 +107,8 @@ __global__ void __launch_bounds__(kRouteWarps * 32) route_kernel(RouteArgs a) {
     }
     float p = 0.f;
     if (lane < a.k && mine > kKeyMinusInf)
-        p = a.sigmoid ? 1.f / (1.f + expf(-value_of(mine))) : share(mine, top) / total;
+        p = a.sigmoid ? sigmoid(value_of(mine), a.renormalize ? fminf(value_of(top), 0.f) : 0.f)
+                      : share(mine, top) / total;
     if (a.renormalize) {
         const float sum = warp_sum(p);
         p = sum > 0.f ? p / sum : 0.f;
