@@ -538,7 +538,8 @@ int w4a16_fp8_moe_mlp(const uint16_t *x, const int32_t *topk_ids, const float *w
  *                call's own until its work is done (W4A16_ERR_WORKSPACE if fewer); calls
  *                that share none may overlap
  * Sums are fp32; A x enters the second product as two values of the 16-bit type (16 bits of
- * it in bf16, 22 in fp16, of the row's largest); y is rounded once.  Two kernels, three above 1024 rows.  A row's
+ * it in bf16, 22 in fp16, of the row's largest); y is rounded once.  Infinite weights and A x
+ * give the infinities and NaN of the formula.  Two kernels, three above 1024 rows.  A row's
  * bits do not depend on its place in the batch, but the order of its sums goes by how many
  * rows the call and its adapter have.  K and R multiples of 8, K and N at most 2^22, 0 <= M
  * <= 65535 (0: an empty batch); L <= 1024, R <= 128, n_parts <= 4 (W4A16_ERR_UNSUPPORTED

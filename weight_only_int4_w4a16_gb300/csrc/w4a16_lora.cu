@@ -35,10 +35,11 @@
 // outputs alone about 90, which one CTA per SM, in step at a barrier per 128 columns, overlaps
 // in part.  With the tall tiles on the warp MMA the same call took 189 to 221 us.
 //
-// t is fp32; as expand's operand it is split into two values of the 16-bit type, the value
-// rounded and the rest rounded, of a row first scaled by a power of two to at most 2: 16
-// bits (bf16) or 22 (fp16) of it enter the product, at twice the MMAs, which are not the
-// bound.
+// t is fp32; as expand's operand it is split into two values of the 16-bit type, of a row first
+// scaled by a power of two: the value cut to the type and the rest rounded.  16 bits (bf16) or
+// 22 (fp16) of it enter the product, at twice the MMAs, which are not the bound.  Both halves
+// have t's sign and neither is zero unless t is, so that an infinite weight times them is what
+// it is times t (a rest of zero, or of the other sign, would make it NaN).
 //
 // Every wait for a product is bounded; one that expires sets a status bit, and the kernel
 // goes on to its end without waiting any more.
@@ -598,7 +599,7 @@ constexpr int expand_smem(int RK, bool few) {
                                low);
 }
 
-// two values rounded to the 16-bit type (nearest even), and back
+// two values rounded to the 16-bit type (nearest even), or cut to it; and back
 template <bool kBf16>
 __device__ __forceinline__ uint32_t pack16(float lo, float hi) {
     uint32_t d;
@@ -607,25 +608,49 @@ __device__ __forceinline__ uint32_t pack16(float lo, float hi) {
     return d;
 }
 template <bool kBf16>
+__device__ __forceinline__ uint32_t cut16(float lo, float hi) {
+    uint32_t d;
+    if constexpr (kBf16) asm("cvt.rz.bf16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
+    else asm("cvt.rz.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
+    return d;
+}
+template <bool kBf16>
 __device__ __forceinline__ float2 unpack16(uint32_t v) {
     if constexpr (kBf16)
         return make_float2(__uint_as_float(v << 16), __uint_as_float(v & 0xffff0000u));
     return __half22float2(*reinterpret_cast<const __half2 *>(&v));
 }
-// the power of two (its exponent field) that scales a row whose largest value is `most` to at
-// most 2; a row of zeros, or with an Inf, stays as it is
+// the power of two (its exponent field) that scales a row whose largest finite value is `most`
+// to at most 4 (bf16), 2^16 (fp16, whose smallest value is then 2^-38 of the largest)
+template <bool kBf16>
 __device__ __forceinline__ int row_exponent(float most) {
-    const int top = __float_as_uint(most) >> 23;
-    return top >= 255 || top == 0 ? 127 : min(max(top, 2), 252);
+    return min(max((int)(__float_as_uint(most) >> 23) - (kBf16 ? 0 : 14), 2), 252);
 }
 __device__ __forceinline__ float scale_down(int e) { return __uint_as_float((uint32_t)(254 - e) << 23); }
 __device__ __forceinline__ float scale_up(int e) { return __uint_as_float((uint32_t)e << 23); }
-// two values as the sum of two pairs of the 16-bit type
+// the larger of a row's largest finite value so far and |v|
+__device__ __forceinline__ float larger(float most, float v) {
+    return isfinite(v) ? fmaxf(most, fabsf(v)) : most;
+}
+// the larger magnitude (NaN stays) with x's sign
+__device__ __forceinline__ float at_least(float v, float least, float x) {
+    float d;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(fabsf(v)), "f"(least));
+    return copysignf(d, x);
+}
+// x * down and y * down as the sum of two pairs of the 16-bit type, hi cut and lo rounded.
+// Where one would be zero though the value is not, it is the least number of its sign: in the
+// scaled row 2^-38 (fp16) or less of the largest.
 template <bool kBf16>
-__device__ __forceinline__ void split(float x, float y, uint32_t &hi, uint32_t &lo) {
-    hi = pack16<kBf16>(x, y);
+__device__ __forceinline__ void split(float x, float y, float down, uint32_t &hi, uint32_t &lo) {
+    constexpr float kLeast = kBf16 ? 0x1p-126f : 0x1p-24f;  // (bf16: the smallest normal one)
+    const float lx = x != 0.f ? kLeast : 0.f, ly = y != 0.f ? kLeast : 0.f;
+    const float u = at_least(x * down, lx, x), v = at_least(y * down, ly, y);
+    hi = cut16<kBf16>(u, v);
     const float2 h = unpack16<kBf16>(hi);
-    lo = pack16<kBf16>(isfinite(h.x) ? x - h.x : 0.f, isfinite(h.y) ? y - h.y : 0.f);
+    // (fmaxf takes the number: the rest of an Inf is the least one, that of a NaN does not matter)
+    lo = pack16<kBf16>(copysignf(fmaxf(fabsf(u - h.x), lx), x),
+                       copysignf(fmaxf(fabsf(v - h.y), ly), y));
 }
 
 // where column j of 32 lies among the rows of four 8-column MMA tiles so that a lane's
@@ -661,20 +686,20 @@ struct Rows {
         }
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
-            float most = 0.f;  // (a NaN does not count)
+            float most = 0.f;
 #pragma unroll
             for (int k = 0; k < RK; ++k)
-                most = fmaxf(fmaxf(most, fmaxf(fabsf(v[u][k].x), fabsf(v[u][k].y))),
-                             fmaxf(fabsf(v[u][k].z), fabsf(v[u][k].w)));
+                most = larger(larger(larger(larger(most, v[u][k].x), v[u][k].y), v[u][k].z),
+                              v[u][k].w);
             most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 1));
             most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 2));
-            const int e = row_exponent(most);
+            const int e = row_exponent<kBf16>(most);
             const float down = scale_down(e);
             factor[u] = scale_up(e) * scale;
 #pragma unroll
             for (int k = 0; k < RK; ++k) {
-                split<kBf16>(v[u][k].x * down, v[u][k].y * down, hi[k][u], lo[k][u]);
-                split<kBf16>(v[u][k].z * down, v[u][k].w * down, hi[k][2 + u], lo[k][2 + u]);
+                split<kBf16>(v[u][k].x, v[u][k].y, down, hi[k][u], lo[k][u]);
+                split<kBf16>(v[u][k].z, v[u][k].w, down, hi[k][2 + u], lo[k][2 + u]);
             }
         }
     }
@@ -832,7 +857,7 @@ __device__ void expand_tall(const LoraArgs &a, const uint16_t *order, const Tile
         const bool mine = r < t.count;
         const float *row = sums_of(a) + (mine ? (size_t)order[r] * a.parts * a.R + part * a.R : 0);
         float4 v[kQuads];
-        float most = 0.f;  // (a NaN does not count)
+        float most = 0.f;
 #pragma unroll
         for (int i = 0; i < kQuads; ++i) {
             const int k = (quarter * kQuads + i) * 4, left = mine ? rank - k : 0;
@@ -844,20 +869,19 @@ __device__ void expand_tall(const LoraArgs &a, const uint16_t *order, const Tile
         }
 #pragma unroll
         for (int i = 0; i < kQuads; ++i)
-            most = fmaxf(fmaxf(most, fmaxf(fabsf(v[i].x), fabsf(v[i].y))),
-                         fmaxf(fabsf(v[i].z), fabsf(v[i].w)));
+            most = larger(larger(larger(larger(most, v[i].x), v[i].y), v[i].z), v[i].w);
         most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 1));
         most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 2));
-        const int e = row_exponent(most);
+        const int e = row_exponent<kBf16>(most);
         const float down = scale_down(e);
         if (quarter == 0) factor[r] = scale_up(e) * scale;
 #pragma unroll
         for (int i = 0; i < kQuads; i += 2) {
             uint32_t h[4], l[4];
-            split<kBf16>(v[i].x * down, v[i].y * down, h[0], l[0]);
-            split<kBf16>(v[i].z * down, v[i].w * down, h[1], l[1]);
-            split<kBf16>(v[i + 1].x * down, v[i + 1].y * down, h[2], l[2]);
-            split<kBf16>(v[i + 1].z * down, v[i + 1].w * down, h[3], l[3]);
+            split<kBf16>(v[i].x, v[i].y, down, h[0], l[0]);
+            split<kBf16>(v[i].z, v[i].w, down, h[1], l[1]);
+            split<kBf16>(v[i + 1].x, v[i + 1].y, down, h[2], l[2]);
+            split<kBf16>(v[i + 1].z, v[i + 1].w, down, h[3], l[3]);
             const int c = (quarter * kQuads + i) / 2;  // piece of 8
             const uint32_t at = (c >> 3) * kTall * 128 + swizzled(r, c & 7);
             sts128(t_hi + at, make_uint4(h[0], h[1], h[2], h[3]));
