@@ -589,6 +589,13 @@ int w4a16_fp8_plan_info(int M, int N, int K, int32_t *info);
  * or UNSUPPORTED as the call itself (and for T = 0 or a null info). */
 int w4a16_fp8_moe_plan_info(int T, int k, int E, int K, int I, int N, int32_t *info);
 
+/* How w4a16_lora would run a call of these sizes: info[0] its first product's kind (0: up to
+ * 128 rows; 1: so few tiles that each cluster gets a whole SM per CTA; 2: others), info[1] the
+ * clusters of 8 CTAs in its launch, info[2] the call's kernels.  Pure host query, after
+ * w4a16_init (the clusters that run at once are asked of the device there; NOT_INITIALIZED
+ * before).  INVALID_ARG or UNSUPPORTED as the call itself (and for M = 0 or a null info). */
+int w4a16_lora_plan_info(int M, int L, int R, int n_parts, int32_t *info);
+
 /* Force a rung for later calls (W4A16_RUNG_AUTO restores the table).  A forced
  * rung that cannot run a shape makes that call return W4A16_ERR_UNSUPPORTED.
  * Returns the previous setting, or -2 for an invalid rung.  Host state only:

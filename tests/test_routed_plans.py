@@ -39,3 +39,16 @@ def test_fp8_moe_plan(w4):
         for nt, ks in (p["gate_up"], p["down"]):
             assert nt in (1, 2, 4) and ks in (1, 2, 4, 8)
         assert p["grid"] >= 2 and p["ctas_per_sm"] in (0, 2)
+
+
+def test_lora_plan_refusals(w4):
+    L, info = w4.lib.w4a16_lora_plan_info, (ctypes.c_int32 * 3)()
+    bad, un = w4.W4A16_ERR_INVALID_ARG, w4.W4A16_ERR_UNSUPPORTED
+    for sizes in ((0, 1, 8, 1), (65536, 1, 8, 1), (1, 0, 8, 1), (1, 1, 0, 1), (1, 1, 12, 1),
+                  (1, 1, 8, 0), (-1, 1, 8, 1)):
+        assert L(*sizes, info) == bad
+    assert L(1, 1, 8, 1, None) == bad
+    for sizes in ((1, 1025, 8, 1), (1, 1, 136, 1), (1, 1, 8, 5)):
+        assert L(*sizes, info) == un
+    if w4.lib.w4a16_device_sm_count() == 0:
+        assert L(1, 1, 8, 1, info) == w4.W4A16_ERR_NOT_INITIALIZED

@@ -120,6 +120,7 @@ _sig("w4a16_round_graph_destroy", [_P])
 _sig("w4a16_select_rung", [_I, _I, _I, _I])
 _sig("w4a16_fp8_plan_info", [_I, _I, _I, ctypes.POINTER(ctypes.c_int32)])
 _sig("w4a16_fp8_moe_plan_info", [_I, _I, _I, _I, _I, _I, ctypes.POINTER(ctypes.c_int32)])
+_sig("w4a16_lora_plan_info", [_I, _I, _I, _I, ctypes.POINTER(ctypes.c_int32)])
 _sig("w4a16_plan_info", [_I, _I, _I, _I, _I, _I, ctypes.POINTER(ctypes.c_int32)])
 _sig("w4a16_set_forced_rung", [_I])
 _sig("w4a16_probe_counts", [ctypes.POINTER(ctypes.c_uint64), _I])
@@ -144,7 +145,7 @@ EXPORTED = ["w4a16_init", "w4a16_shutdown", "w4a16_workspace_bytes", "w4a16_pack
             "w4a16_decode_round",
             "w4a16_round_graph_create", "w4a16_round_graph_launch", "w4a16_round_graph_destroy",
             "w4a16_select_rung", "w4a16_plan_info", "w4a16_fp8_plan_info",
-            "w4a16_fp8_moe_plan_info",
+            "w4a16_fp8_moe_plan_info", "w4a16_lora_plan_info",
             "w4a16_set_forced_rung", "w4a16_probe_counts",
             "w4a16_probe_reset", "w4a16_kernel_launches", "w4a16_rung_name", "w4a16_status_string",
             "w4a16_device_status", "w4a16_wait_probe", "w4a16_last_cuda_error",
@@ -849,6 +850,14 @@ def w4a16_fp8_moe_plan_info(T: int, k: int, E: int, K: int, I: int, N: int) -> d
     _check(lib.w4a16_fp8_moe_plan_info(T, k, E, K, I, N, info), "w4a16_fp8_moe_plan_info")
     return {"gate_up": (info[0], info[1]), "down": (info[2], info[3]), "grid": info[4],
             "ctas_per_sm": info[5]}
+
+
+def w4a16_lora_plan_info(M: int, L: int, R: int, n_parts: int = 1) -> dict:
+    """How w4a16_lora runs a call of these sizes: its first product's kind (0 few rows, 1 few
+    tiles, 2 others), the clusters in its launch, the call's kernels."""
+    info = (ctypes.c_int32 * 3)()
+    _check(lib.w4a16_lora_plan_info(M, L, R, n_parts, info), "w4a16_lora_plan_info")
+    return {"kind": info[0], "clusters": info[1], "kernels": info[2]}
 
 
 def w4a16_set_forced_rung(rung: int) -> int:

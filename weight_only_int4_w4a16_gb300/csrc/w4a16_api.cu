@@ -1570,6 +1570,15 @@ int w4a16_fp8_moe_plan_info(int T, int k, int E, int K, int I, int N, int32_t *i
     return W4A16_OK;
 }
 
+int w4a16_lora_plan_info(int M, int L, int R, int n_parts, int32_t *info) {
+    if (!info || M < 1 || M > kMaxM || L < 1 || R < 1 || R % 8 != 0 || n_parts < 1)
+        return W4A16_ERR_INVALID_ARG;
+    if (L > kMaxAdapters || R > kMaxRank || n_parts > kMaxParts) return W4A16_ERR_UNSUPPORTED;
+    if (!g_state.initialized) return W4A16_ERR_NOT_INITIALIZED;
+    lora_plan(M, L, R, n_parts, info);
+    return W4A16_OK;
+}
+
 int w4a16_set_forced_rung(int rung) {
     if (rung < W4A16_RUNG_AUTO || rung >= W4A16_NUM_RUNGS) return -2;
     std::lock_guard<std::mutex> lock(g_mutex);

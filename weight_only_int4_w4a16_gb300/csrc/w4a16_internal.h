@@ -449,6 +449,7 @@ constexpr int kLoraLocalRows = 1024;
 inline int lora_kernels(int M) { return M > kLoraLocalRows ? 3 : 2; }
 cudaError_t launch_lora(const LoraArgs &a, bool bf16, const DeviceInfo &dev, cudaStream_t stream);
 cudaError_t lora_init();
+void lora_plan(int M, int L, int R, int parts, int32_t *info);  // as w4a16_lora_plan_info gives it
 
 // ---- expert MLP decode kernel (w4a16_moe_decode.cu) ------------------------
 constexpr int kMoeDecodeMaxSlots = 128;  // T * k per launch

@@ -1150,6 +1150,26 @@ cudaError_t launch_expand_rank(const LoraArgs &a, const DeviceInfo &dev, cudaStr
 constexpr int kRounds = 4;
 int resident_clusters[3];  // of shrink_kernel's kinds, that run at once (set by lora_init)
 
+Kind kind_of(int M, int R, int parts) {
+    if (M <= kFewRows) return kFew;
+    const int units = (M + kTall - 1) / kTall * ((parts * R + kTallRanks - 1) / kTallRanks);
+    return units <= resident_clusters[kDeep] ? kDeep : kMany;
+}
+// Shrink's clusters: one for each unit that there can be, up to some rounds of those that run
+// at once (just those, each with all its units, 166 us for 152 at 4096 rows beside gate+up).
+// Calls of few rows cut every adapter into low tiles, so they have up to M / 16 more of them
+// than adapters (128 rows of one adapter beside qkv, K 5120, rank 16: 13.1 us, 22.6 with the
+// bound of the others; 100 rows beside o 11.4 for 27.5).
+int clusters_of(int M, int L, int R, int parts, Kind kind) {
+    const int adapters = M < L ? M : L;
+    const long long tiles = kind != kFew              ? lora_max_tiles(M, L)
+                            : adapters + M / kLow < M ? adapters + M / kLow
+                                                      : M;
+    const long long units = tiles * ((parts * R + kLowRanks - 1) / kLowRanks);
+    const int most = kRounds * resident_clusters[kind];
+    return units < most ? (int)units : most;
+}
+
 template <bool kBf16, Kind kKind>
 cudaError_t launch_calls(const LoraArgs &a, bool vec, const DeviceInfo &dev, cudaStream_t stream) {
     constexpr bool few = kKind == kFew;
@@ -1157,12 +1177,7 @@ cudaError_t launch_calls(const LoraArgs &a, bool vec, const DeviceInfo &dev, cud
         const cudaError_t e = launch_chained(plan_kernel, dim3(1), kPlanThreads, 0, 1, stream, a);
         if (e != cudaSuccess) return e;
     }
-    // a cluster for each unit that there can be, up to some rounds of those that run at once
-    // (just those, each with all its units, 166 us for 152 at 4096 rows beside gate+up)
-    const long long units = (long long)lora_max_tiles(a.M, a.L) *
-                            ((a.parts * a.R + kLowRanks - 1) / kLowRanks);
-    const int most = kRounds * resident_clusters[kKind];
-    const int clusters = units < most ? (int)units : most;
+    const int clusters = clusters_of(a.M, a.L, a.R, a.parts, kKind);
     const cudaError_t e =
         launch_chained(shrink_kernel<kBf16, kKind>, dim3(clusters * kCluster), kShrinkThreads,
                        shrink_smem(kKind), kCluster, stream, a);
@@ -1225,15 +1240,24 @@ cudaError_t launch_lora(const LoraArgs &a, bool bf16, const DeviceInfo &dev, cud
     // 16-byte accesses of y and the residual
     bool vec = a.N % 8 == 0 && ((uintptr_t)a.y & 15) == 0 && ((uintptr_t)a.residual & 15) == 0;
     for (int i = 0; i < a.parts; ++i) vec = vec && a.part[i] % 8 == 0;
-    if (a.M <= kFewRows)
-        return bf16 ? launch_calls<true, kFew>(a, vec, dev, stream)
-                    : launch_calls<false, kFew>(a, vec, dev, stream);
-    const int units = (a.M + kTall - 1) / kTall * ((a.parts * a.R + kTallRanks - 1) / kTallRanks);
-    if (units <= resident_clusters[kDeep])
-        return bf16 ? launch_calls<true, kDeep>(a, vec, dev, stream)
-                    : launch_calls<false, kDeep>(a, vec, dev, stream);
-    return bf16 ? launch_calls<true, kMany>(a, vec, dev, stream)
-                : launch_calls<false, kMany>(a, vec, dev, stream);
+    switch (kind_of(a.M, a.R, a.parts)) {
+        case kFew:
+            return bf16 ? launch_calls<true, kFew>(a, vec, dev, stream)
+                        : launch_calls<false, kFew>(a, vec, dev, stream);
+        case kDeep:
+            return bf16 ? launch_calls<true, kDeep>(a, vec, dev, stream)
+                        : launch_calls<false, kDeep>(a, vec, dev, stream);
+        default:
+            return bf16 ? launch_calls<true, kMany>(a, vec, dev, stream)
+                        : launch_calls<false, kMany>(a, vec, dev, stream);
+    }
+}
+
+void lora_plan(int M, int L, int R, int parts, int32_t *info) {
+    const Kind kind = kind_of(M, R, parts);
+    info[0] = kind;
+    info[1] = clusters_of(M, L, R, parts, kind);
+    info[2] = lora_kernels(M);
 }
 
 cudaError_t lora_init() {
