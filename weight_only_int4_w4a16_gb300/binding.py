@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import ctypes
 import functools
+import operator
 import os
 
 import torch
@@ -736,6 +737,8 @@ def w4a16_fp8_moe_mlp(x: torch.Tensor, topk_ids: torch.Tensor, weights: torch.Te
 @functools.lru_cache(maxsize=256)
 def _host_ints(values: tuple):
     """(a host array of them, their number), which the library only reads."""
+    if any(v != ctypes.c_int32(v).value for v in values):
+        raise ValueError(f"{values} do not all fit 32 bits")
     return (ctypes.c_int32 * len(values))(*values), len(values)
 
 
@@ -757,7 +760,7 @@ def w4a16_lora(x: torch.Tensor, a: torch.Tensor, b: torch.Tensor, scales: torch.
         if not isinstance(w, torch.Tensor) or w.dim() != 3:
             raise ValueError(f"{name} must be a 3-D torch tensor")
     L, N, R = b.shape
-    host, n = _host_ints((N,) if parts is None else tuple(parts))
+    host, n = _host_ints((N,) if parts is None else tuple(map(operator.index, parts)))
     dt = x.dtype
     code = _dtype16(dt)
     dev, xp = _home(x, dt, (M, K))
