@@ -85,3 +85,40 @@ def test_few_rows_of_every_rank(w4, M, R, dtype):
         y = run(w4, ops, kw)
         check(y, ops, kw, dtype)
         assert w4.w4a16_device_status() == 0
+
+
+@pytest.mark.parametrize("M", [150, 1200])
+def test_between_kernels_that_take_all_tensor_memory(w4, M):
+    """Tall tiles right after and before the 8-bit linear, whose kernels take all of an SM's
+    tensor memory, and with kernels between them that let the next one start at once."""
+    K, N, L, R = 256, 512, 3, 64
+    ops, kw = ref.make_adapters(M, M, K, (256, 256), L, R, BF16, ids=grouped(M, L, 3))
+    x, a, b, scales, ids = [t.cuda() for t in ops]
+    g = torch.Generator().manual_seed(1)
+    w = (torch.randn((N, K), generator=g) * 4).to(torch.float8_e4m3fn).cuda()
+    ws = torch.full((N // 128, K // 128), 2.0 ** -6, device="cuda")
+    q, qs = w4.w4a16_fp8_quant(x)
+    logits = torch.randn((M, 64), generator=g).cuda()
+
+    def layer():
+        outs = []
+        for _ in range(3):
+            y = w4.w4a16_fp8_linear(q, qs, w, ws)
+            outs.append(w4.w4a16_lora(x, a, b, scales, ids, parts=[256, 256], residual=y))
+            z = w4.w4a16_fp8_linear(q, qs, w, ws)
+            outs.extend(w4.w4a16_moe_route(logits, 4))
+            outs.append(w4.w4a16_lora(x, a, b, scales, ids, parts=[256, 256], residual=z))
+        return y, outs
+
+    y, eager = layer()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        _, captured = layer()
+    for _ in range(5):
+        graph.replay()
+    torch.cuda.synchronize()
+    for i, (e, c) in enumerate(zip(eager, captured)):
+        assert torch.equal(e, c) and torch.equal(e, eager[i % 4])
+    check(eager[0], ops, dict(parts=[256, 256], ranks=None, residual=y.cpu()), BF16)
+    assert torch.equal(eager[0], eager[3])
+    assert w4.w4a16_device_status() == 0

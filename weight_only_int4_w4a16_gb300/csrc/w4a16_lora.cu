@@ -547,8 +547,11 @@ __global__ void __launch_bounds__(kShrinkThreads, kKind == kDeep ? 1 : 2) shrink
     __shared__ LocalPlan<kRows> own;
     __shared__ ProductSpace space;
     Products pr;
-    if constexpr (!few) pr.begin<kShrinkTmem>(&space, a.status);
+    // tensor memory is taken once the kernels before have ended: others of the library let this
+    // one start before they have taken theirs, all 512 columns, and would wait for these
+    // without end if their shared memory left room beside it
     wait_for_last();
+    if constexpr (!few) pr.begin<kShrinkTmem>(&space, a.status);
     launch_next();
     const Plan p = make_plan<kShrinkThreads, kRows>(a, own, smem);
     if (!few && a.M <= kRows && blockIdx.x == 0) share_plan(a, p);
