@@ -42,7 +42,8 @@
 // it is times t (a rest of zero, or of the other sign, would make it NaN).
 //
 // Every wait for a product is bounded; one that expires sets a status bit, and the kernel
-// goes on to its end without waiting any more.
+// goes on to its end without further products or waits, but for one at the end, bounded too,
+// for those in flight, before the tensor memory is freed.
 #include "w4a16_routed.cuh"
 #include "w4a16_tcgen05.cuh"
 
@@ -73,6 +74,7 @@ constexpr int kLowCols = 32;    // low ones
 constexpr int kLowPitch = kLowRanks + 8;  // of a low unit's sums in shared memory
 constexpr int max_of(int a, int b) { return a > b ? a : b; }
 constexpr int kShrinkTmem = 128, kExpandTmem = 256;  // columns: a tile's sums; two steps'
+constexpr int kExpandBars = 2;
 constexpr int kErrProducts = 1 << 21;  // device status bit: a wait for products expired
 
 struct Tile {
@@ -193,12 +195,14 @@ struct Products {
     ProductSpace *sp;
     int *status;
     uint32_t tmem;
-    unsigned count;  // committed so far, by barrier in turn
+    unsigned count;   // committed so far, by barrier in turn
+    unsigned issued;  // warp 0, which issues them: the same, but for those left out
+    bool ok;          // none of this warp's waits has given up; warp 0 issues none after one
 
     // all threads, before the next kernel may start: its CTAs take tensor memory too
     template <int kCols>
     __device__ __forceinline__ void begin(ProductSpace *space, int *status_word) {
-        sp = space, status = status_word, count = 0;
+        sp = space, status = status_word, count = issued = 0, ok = true;
         if (threadIdx.x == 0) {
             for (int i = 0; i < kMaxShrinkStages; ++i) dev::mbar_init(smem_of(&sp->done[i]), 1);
             dev::mbar_init_fence();
@@ -217,11 +221,17 @@ struct Products {
         dev::tc_fence_after();
         tmem = sp->tmem;
     }
-    template <int kCols>
+    // kBars: as wait's
+    template <int kCols, int kBars>
     __device__ __forceinline__ void end() {
         dev::tc_fence_before();
         __syncthreads();
         if (threadIdx.x < 32) {
+            if (!ok)
+                for (unsigned n = issued > kBars ? issued - kBars : 0; n < issued; ++n) {
+                    dev::mbar_wait_drain(bar(n, kBars), n / kBars & 1);
+                    __syncwarp();
+                }
             dev::tc_fence_after();
             asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem),
                          "r"(kCols)
@@ -235,9 +245,12 @@ struct Products {
     // products n (counted from 0) and all before are done; whole warps wait, and go on together
     __device__ __forceinline__ void wait(unsigned n, int bars) {
         volatile int *abort = &sp->abort;
-        if (!dev::mbar_wait_all(bar(n, bars), n / bars & 1, abort) && !*abort) {
-            *abort = 1;
-            atomicOr(status, kErrProducts);
+        if (!dev::mbar_wait_all(bar(n, bars), n / bars & 1, abort)) {
+            ok = false;
+            if (!*abort) {
+                *abort = 1;
+                atomicOr(status, kErrProducts);
+            }
         }
         __syncwarp();
     }
@@ -436,7 +449,7 @@ __device__ void shrink_tall(const LoraArgs &a, const uint16_t *order, const Tile
         wait_copies<kShrinkStages - 2>();
         dev::fence_async_shared();
         __syncthreads();
-        if (warp == 0) {
+        if (warp == 0 && pr.ok) {
             dev::tc_fence_after();
             const uint32_t st =
                 dev::uniform(base + (pr.count + s) % kShrinkStages * kShrinkStage);
@@ -449,6 +462,7 @@ __device__ void shrink_tall(const LoraArgs &a, const uint16_t *order, const Tile
                 dev::mma_commit(bar);
             }
             __syncwarp();
+            pr.issued = pr.count + s + 1;
         }
         if (s + kShrinkStages - 1 < steps) {
             if (s > 0) pr.wait(pr.count + s - 1, kShrinkStages);
@@ -571,7 +585,7 @@ __global__ void __launch_bounds__(kShrinkThreads, kKind == kDeep ? 1 : 2) shrink
             shrink_low<kBf16>(a, p.order + t.first, t, v % lq * kLowRanks, k0, k1, smem);
         }
     }
-    if constexpr (!few) pr.end<kShrinkTmem>();
+    if constexpr (!few) pr.end<kShrinkTmem, shrink_stages(kKind)>();
 }
 
 // ---------------------------------------------------------------------------
@@ -894,10 +908,11 @@ __device__ void expand_tall(const LoraArgs &a, const uint16_t *order, const Tile
     const uint32_t idesc = product_desc<kBf16>(kTallCols), tmem = dev::uniform(pr.tmem);
     const uint32_t u_hi = dev::uniform(t_hi), u_lo = dev::uniform(t_lo), u_b = dev::uniform(b0);
     auto products = [&](int s) {  // warp 0
+        if (!pr.ok) return;
         dev::tc_fence_after();
         const unsigned n = dev::uniform(pr.count + s);
         const uint32_t st = u_b + s % kBs * b_stage(RK), d = tmem + (n & 1) * kTallCols;
-        const uint32_t bar = dev::uniform(pr.bar(n, 2));
+        const uint32_t bar = dev::uniform(pr.bar(n, kExpandBars));
         if (dev::elect_one()) {
 #pragma unroll
             for (int h = 0; h < 2; ++h)
@@ -912,6 +927,7 @@ __device__ void expand_tall(const LoraArgs &a, const uint16_t *order, const Tile
             dev::mma_commit(bar);
         }
         __syncwarp();
+        pr.issued = n + 1;
     };
     // outputs: a warp's 32 rows (its quarter of the tensor memory's lanes) and 32 columns;
     // out[i]: where row i * 8 + lane / 4 of them lies in y
@@ -955,7 +971,7 @@ __device__ void expand_tall(const LoraArgs &a, const uint16_t *order, const Tile
                 }
             __syncwarp();
         }
-        pr.wait(pr.count + s, 2);
+        pr.wait(pr.count + s, kExpandBars);
         dev::tc_fence_after();
         // this step's products are done: its B makes room
         if (s + kBs < steps) issue_b(s + kBs);
@@ -1134,7 +1150,7 @@ __global__ void __launch_bounds__(expand_threads(few), few ? 2 : 1) expand_kerne
     });
     copy_rows<kCta, kVec>(a, p.order + p.n.rows, p.n.none);
     wait_for_last();  // (for those without a step: what follows this kernel waits for it alone)
-    if constexpr (!few) pr.end<kExpandTmem>();
+    if constexpr (!few) pr.end<kExpandTmem, kExpandBars>();
 }
 
 template <bool kBf16, int RK, bool kVec, bool few>
