@@ -21,19 +21,22 @@
 //     from memory, since each of their weights is used once.
 //   * expand: y.  All steps (128 columns of a tall tile, 32 of a low one for each warp) are
 //     one sequence of which every CTA takes an equal run; B and the residual come through
-//     rings of asynchronous copies.  In calls of few rows its CTAs fit beside shrink's, so
-//     that their grouping and first copies are done when shrink ends.
+//     rings of asynchronous copies.  In calls of few rows its CTAs start wherever shrink leaves
+//     an SM room (two of shrink's CTAs take all its registers), so that their grouping and
+//     first copies are done when shrink ends.
 // Tall tiles run on tcgen05 (M = 128 rows of the tile), low ones on the warp MMA with the rows
 // as its M = 16, straight from what the asynchronous copies bring.
 //
 // What bounds it (one GB300, calls in a row in a graph).  Few rows: the chain of two kernels
 // and their dependent loads, 7.1 us for one row, rank 16, beside qkv (0.8 MB), of which the
 // grouping is 1, the loads of A 1.5, the sums' meeting 1.5, t and the outputs 1.5; 64 rows of
-// 32 adapters beside gate+up 21.8 us, of which the adapters' 46 MB are 7 to 8.  Many rows:
-// the bytes of y, 149 us for 4096 rows, rank 64, beside gate+up (643 MB, 4.3 TB/s): the
+// 32 adapters beside gate+up 21.7 us, of which the adapters' 46 MB are 7 to 8.  Many rows:
+// the bytes of y, 150 us for 4096 rows, rank 64, beside gate+up (643 MB, 4.3 TB/s): the
 // grouping, shrink 20, then expand 122, where copies alone would take about 105 and products and
 // outputs alone about 90, which one CTA per SM, in step at a barrier per 128 columns, overlaps
-// in part.  With the tall tiles on the warp MMA the same call took 189 to 221 us.
+// in part.  With the tall tiles on the warp MMA the same call took 189 to 221 us.  Columns that
+// are not multiples of 8 (or addresses of 2 bytes) are read and written 2 bytes a lane, the
+// residual with nothing ahead: the same call with 17405 + 17403 columns takes 602 us.
 //
 // t is fp32; as expand's operand it is split into two values of the 16-bit type, of a row first
 // scaled by a power of two: the value cut to the type and the rest rounded.  16 bits (bf16) or
@@ -290,7 +293,7 @@ __device__ void share_plan(const LoraArgs &a, const Plan &p) {
 }
 
 // ---------------------------------------------------------------------------
-// plan: one CTA, more than kMaxRows rows.  Bin l < L: the rows of adapter l; bin L: those
+// plan: one CTA, more than kLocalRows rows.  Bin l < L: the rows of adapter l; bin L: those
 // without one.  The order within a bin is that of an atomic counter.
 // ---------------------------------------------------------------------------
 __global__ void __launch_bounds__(kPlanThreads) plan_kernel(LoraArgs a) {
@@ -594,8 +597,8 @@ __global__ void __launch_bounds__(kShrinkThreads, kKind == kDeep ? 1 : 2) shrink
 // bytes of a row of B in shared memory (low tiles): an odd number of 32 bytes, so that rows
 // next to each other lie in other banks
 constexpr int row_pitch(int RK) { return (RK | 1) * 32; }
-// Calls of few rows: two CTAs of 8 warps per SM, so small that shrink's CTAs fit beside them
-// and they start while it runs.  Others: one of 16 warps with all of the SM.
+// Calls of few rows: two CTAs of 8 warps per SM, small enough to start beside one of shrink's
+// while it runs (two take the SM's registers).  Others: one of 16 warps with all of the SM.
 constexpr int expand_threads(bool few) { return few ? 256 : 512; }
 constexpr int kResidualStage = kTall * kTallCols * 2;
 constexpr int blocks64(int RK) { return RK > 4 ? 2 : 1; }  // of 64 of the rank

@@ -13,12 +13,14 @@
 // units of e^top where the row's largest is negative, so that their shares outlive their p;
 // below l = -745, where binary64 has no e^l either, p is 0.
 //
-// A warp has a row, each lane every 32nd logit in registers as an integer key that
-// orders as the number does.  A step finds the largest key and the lowest index that
-// holds it (two warp-wide integer reductions), and its lane strikes it out.  Bound by the
-// issue rate where there are many rows: 8192 of 256 logits, k 8, take 9.2 us in a row in a
-// graph (their 8.9 MB would take 1.3), about 500 instructions a row; one row takes 2.1, a
-// launch.  (Holders by a vote, with the second reduction only for ties: 10.2.)
+// A warp has a row, each lane every 32nd logit as an integer key that orders as the number
+// does (in registers up to 256 logits a row, in local memory above).  A step finds the largest
+// key and the lowest index that holds it (two warp-wide integer reductions), and its lane
+// strikes it out.  8192 rows of 256 logits, k 8, take 9.1 us in a row in a graph (their 8.9 MB
+// would take 1.3): 829 instructions a row, 5.4 us if every cycle issued one; 61% do, and the
+// others wait for the half-rate integer pipe, for fixed latencies and for the logits, in about
+// equal parts.  One row takes 2.1, a launch.  (Holders by a vote, with the second reduction
+// only for ties: 10.2.)
 #include "w4a16_internal.h"
 
 namespace w4a16 {
