@@ -641,7 +641,7 @@ __device__ __forceinline__ float2 unpack16(uint32_t v) {
     return __half22float2(*reinterpret_cast<const __half2 *>(&v));
 }
 // the power of two (its exponent field) that scales a row whose largest finite value is `most`
-// to at most 4 (bf16), 2^16 (fp16, whose smallest value is then 2^-38 of the largest)
+// below 8 (bf16) or 2^15 (fp16, whose smallest number is then 2^-38 of the largest)
 template <bool kBf16>
 __device__ __forceinline__ int row_exponent(float most) {
     return min(max((int)(__float_as_uint(most) >> 23) - (kBf16 ? 0 : 14), 2), 252);
